@@ -121,6 +121,11 @@ def lib():
                 [C, P, P, i64, i32, i64, P, P, P, P, P, i64, i64, P, sz, P, P, P, ctypes.POINTER(P)],
                 ctypes.c_int,
             ),
+            # structures by plain address (ctypes.byref objects or None pass as void*)
+            "engram_qk_norm_rope": ([P, i64, P, P, P, P, i64, P, P, P, P, P], ctypes.c_int),
+            "engram_kv_append": ([P, P, P, P, P, P, P, i64, P, P, P, P], ctypes.c_int),
+            "engram_paged_attention_workspace_bytes": ([P, i64, i64], sz),
+            "engram_paged_attention": ([P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -624,3 +629,243 @@ def engram_forward_host(cfg, tokens, seq_offsets, host_tables, host_scales, W_ou
         "engram_forward_host",
     )
     return n_unique
+
+
+# ------------------------------------------------------------------ attention --
+# The attention step of a decoder layer beside the Engram read: head norm and
+# rotation, the paged cache's append, attention over the cache.
+
+
+class engram_attn_config(ctypes.Structure):
+    _fields_ = [
+        ("n_heads", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32),
+        ("rope_layout", ctypes.c_uint32),
+        ("dtype", ctypes.c_uint32),
+        ("norm_eps", ctypes.c_float),
+        ("scale", ctypes.c_float),
+        ("window", ctypes.c_int32),
+    ]
+
+
+class engram_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class engram_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class engram_kv_batch(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int64),
+        ("n_query", ctypes.c_int64),
+        ("seq_offsets", ctypes.c_void_p),
+        ("kv_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
+_ATTN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def make_attn_config(n_heads, n_kv_heads, head_dim, dtype=torch.bfloat16, rope_dim=None, rope_interleaved=False,
+                     norm_eps=1e-6, scale=None, window=0):
+    """An engram_attn_config: query and key/value heads, values per head, the
+    values of a head that rotate (default all), their pairing, the heads' type
+    (bf16 or fp16), the score factor (default 1/sqrt(head_dim)) and the sliding
+    window (0: plain causal)."""
+    if dtype not in _ATTN_DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    c = engram_attn_config()
+    c.n_heads, c.n_kv_heads, c.head_dim = int(n_heads), int(n_kv_heads), int(head_dim)
+    c.rope_dim = int(head_dim if rope_dim is None else rope_dim)
+    c.rope_layout = 1 if rope_interleaved else 0
+    c.dtype = _ATTN_DTYPES[dtype]
+    c.norm_eps = float(norm_eps)
+    c.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
+    c.window = int(window)
+    c.torch_dtype = dtype
+    return c
+
+
+def rope_table(n_positions, rope_dim, theta=10000.0, device="cuda"):
+    """The rotation table fp32 [n_positions, rope_dim] (cosines, then sines) of
+    the angles position * theta^(-2i/rope_dim), computed in 64 bits."""
+    half = rope_dim // 2
+    i = torch.arange(half, dtype=torch.float64, device=device)
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * theta ** (-i / max(half, 1))
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def kv_cache(k_pages, v_pages):
+    """An engram_kv_cache over K and V pages [n_pages, page_size, n_kv_heads, head_dim] with the same
+    strides (any, the head's values contiguous: permute for other orders).  It keeps the tensors alive."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype not in _ATTN_DTYPES:
+            raise TypeError(f"{name} must be bf16 or fp16, got {t.dtype}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim] with contiguous heads")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same type, shape and strides")
+    c = engram_kv_cache()
+    c.k, c.v = k_pages.data_ptr(), v_pages.data_ptr()
+    c.n_pages, c.page_size = k_pages.shape[0], k_pages.shape[1]
+    c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
+    c.tensors = (k_pages, v_pages)
+    c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), k_pages.dtype
+    return c
+
+
+def kv_batch(seq_offsets, kv_len, block_table, n_query):
+    """An engram_kv_batch: seq_offsets int64 [n_seqs + 1], kv_len int32 [n_seqs] (lengths with the new
+    tokens), block_table int32 [n_seqs, pages], n_query new tokens in all.  It keeps the tensors alive;
+    their contents may change from step to step."""
+    _need(seq_offsets, torch.int64, "seq_offsets")
+    _need(kv_len, torch.int32, "kv_len")
+    if block_table.dtype != torch.int32:
+        raise TypeError(f"block_table must be torch.int32, got {block_table.dtype}")
+    n = kv_len.numel()
+    if not block_table.is_cuda or block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be a CUDA tensor [n_seqs, pages]")
+    if n and (block_table.stride(1) != 1 and block_table.shape[1] > 1 or block_table.stride(0) < block_table.shape[1]):
+        raise ValueError("block_table must have contiguous rows")
+    if seq_offsets.numel() != n + 1:
+        raise ValueError("seq_offsets must have one entry more than kv_len")
+    b = engram_kv_batch()
+    b.n_seqs, b.n_query = n, int(n_query)
+    b.seq_offsets, b.kv_len, b.block_table = seq_offsets.data_ptr(), kv_len.data_ptr(), block_table.data_ptr()
+    b.table_stride = block_table.shape[1] if n <= 1 else block_table.stride(0)
+    b.tensors = (seq_offsets, kv_len, block_table)
+    return b
+
+
+def _heads(t, cfg, tokens, heads, name):
+    """The engram_heads of a [tokens, heads, head_dim] tensor with contiguous heads."""
+    if t.dtype is not cfg.torch_dtype:
+        raise TypeError(f"{name} must be {cfg.torch_dtype}, got {t.dtype}")
+    if t.shape != (tokens, heads, cfg.head_dim):
+        raise ValueError(f"{name} must be {[tokens, heads, cfg.head_dim]}, got {list(t.shape)}")
+    st, sh, sc = t.stride()
+    if sc != 1 and cfg.head_dim > 1 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor with contiguous heads")
+    # the stride of a size of one is never used, and torch may give it any value
+    return engram_heads(t.data_ptr(), st if tokens > 1 else 0, sh if heads > 1 else 0)
+
+
+def _weight(w, cfg, name):
+    if w is None:
+        return None
+    _need(w, cfg.torch_dtype, name)
+    if w.numel() != cfg.head_dim:
+        raise ValueError(f"{name} must have {cfg.head_dim} values")
+    return w.data_ptr()
+
+
+def _table(table, cfg):
+    if table is None:
+        if cfg.rope_dim:
+            raise ValueError("table is needed: rope_dim is not 0")
+        return None, 0
+    _need(table, torch.float32, "table")
+    if table.dim() != 2 or table.shape[1] != cfg.rope_dim:
+        raise ValueError(f"table must be [positions, {cfg.rope_dim}]")
+    return table.data_ptr(), table.shape[0]
+
+
+def _cache_of(cache, cfg):
+    if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
+        raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.n_kv_heads, cfg.head_dim]}")
+    return ctypes.byref(cache)
+
+
+def engram_qk_norm_rope(cfg, q, k, positions, table, w_q=None, w_k=None, q_out=None, k_out=None, stream=None):
+    """(q_out, k_out): every head of q [T, n_heads, D] and k [T, n_kv_heads, D] RMS-normed (with w_q / w_k
+    [D]; None: no norm) and rotated by its token's position.  Either of q and k may be None; q_out=q and
+    k_out=k work in place."""
+    T = q.shape[0] if q is not None else k.shape[0]
+    hq = hk = ho = hko = None
+    if q is not None:
+        hq = _heads(q, cfg, T, cfg.n_heads, "q")
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        ho = ctypes.byref(_heads(q_out, cfg, T, cfg.n_heads, "q_out"))
+        hq = ctypes.byref(hq)
+    if k is not None:
+        hk = ctypes.byref(_heads(k, cfg, T, cfg.n_kv_heads, "k"))
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        hko = ctypes.byref(_heads(k_out, cfg, T, cfg.n_kv_heads, "k_out"))
+    if positions is not None:
+        _need(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError(f"positions must have {T} entries")
+    tab, rows = _table(table, cfg)
+    _check(
+        lib().engram_qk_norm_rope(ctypes.byref(cfg), T, hq, hk, _ptr(positions), tab, rows, _weight(w_q, cfg, "w_q"),
+                                  _weight(w_k, cfg, "w_k"), ho, hko, _stream(stream)),
+        "engram_qk_norm_rope",
+    )
+    return q_out, k_out
+
+
+def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
+    """The step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] into their slots of the cache.
+    With q [n_query, n_heads, D], also its norm and rotation in the same launch; returns q_out (None without)."""
+    T = batch.n_query
+    hk = ctypes.byref(_heads(k, cfg, T, cfg.n_kv_heads, "k"))
+    hv = ctypes.byref(_heads(v, cfg, T, cfg.n_kv_heads, "v"))
+    hq = ho = None
+    if q is not None:
+        hq = ctypes.byref(_heads(q, cfg, T, cfg.n_heads, "q"))
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        ho = ctypes.byref(_heads(q_out, cfg, T, cfg.n_heads, "q_out"))
+    tab, rows = _table(table, cfg)
+    _check(
+        lib().engram_kv_append(ctypes.byref(cfg), _cache_of(cache, cfg), ctypes.byref(batch), hk, hv,
+                               _weight(w_k, cfg, "w_k"), tab, rows, hq, _weight(w_q, cfg, "w_q"), ho,
+                               _stream(stream)),
+        "engram_kv_append",
+    )
+    return q_out if q is not None else None
+
+
+def engram_paged_attention_workspace_bytes(cfg, n_seqs, n_query):
+    return int(lib().engram_paged_attention_workspace_bytes(ctypes.byref(cfg), int(n_seqs), int(n_query)))
+
+
+def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
+    """out [n_query, n_heads, D]: attention of the step's tokens over the paged cache (and lse fp32
+    [n_query, n_heads] if a tensor for it is given)."""
+    T = batch.n_query
+    hq = _heads(q, cfg, T, cfg.n_heads, "q")
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    ho = _heads(out, cfg, T, cfg.n_heads, "out")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.shape != (T, cfg.n_heads):
+            raise ValueError(f"lse must be {[T, cfg.n_heads]}")
+    if workspace is None:
+        need = lib().engram_paged_attention_workspace_bytes(ctypes.byref(cfg), batch.n_seqs, T)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    else:
+        _need(workspace, torch.uint8, "workspace")
+    _check(
+        lib().engram_paged_attention(ctypes.byref(cfg), _cache_of(cache, cfg), ctypes.byref(batch), ctypes.byref(hq),
+                                     ctypes.byref(ho), lse.data_ptr() if lse is not None else None,
+                                     workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        "engram_paged_attention",
+    )
+    return out

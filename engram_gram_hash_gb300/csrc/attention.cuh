@@ -1,0 +1,267 @@
+// C entry points of the attention step (head norm + rotation, cache append,
+// paged attention): argument checks, tensor maps, launches.
+#pragma once
+
+namespace engram {
+namespace attn {
+
+static bool finite_pos(float x) { return x > 0.f && x < INFINITY; }
+
+static engram_status check_attn_config(const engram_attn_config *c) {
+    if (!c) return ENGRAM_EINVAL;
+    if (c->n_kv_heads < 1 || c->n_heads < 1 || c->n_heads % c->n_kv_heads) return ENGRAM_EINVAL;
+    if (c->n_heads / c->n_kv_heads > 128 || c->n_heads > 65536) return ENGRAM_EINVAL;
+    if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8) return ENGRAM_EINVAL;
+    if (c->rope_dim < 0 || c->rope_dim > c->head_dim || c->rope_dim % 16) return ENGRAM_EINVAL;
+    if (c->rope_layout > ENGRAM_ROPE_INTERLEAVED || c->dtype > ENGRAM_FP16) return ENGRAM_EINVAL;
+    if (!(c->norm_eps >= 0.f) || !finite_pos(c->scale) || c->window < 0) return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+static bool view_ok(const engram_heads *h) {
+    return h && h->data && aligned(h->data, 16) && h->token_stride % 8 == 0 && h->head_stride % 8 == 0;
+}
+static HeadView view(const engram_heads *h) {
+    return h ? HeadView{static_cast<uint16_t *>(h->data), h->token_stride, h->head_stride} : HeadView{nullptr, 0, 0};
+}
+
+static engram_status check_cache(const engram_attn_config *cfg, const engram_kv_cache *c) {
+    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ENGRAM_EINVAL;
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX) return ENGRAM_EINVAL;
+    if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16) return ENGRAM_EINVAL;
+    // strides positive (a size of one may still name any), so no value lies before the base
+    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s < 8 || s % 8 || s >= (INT64_C(1) << 39)) return ENGRAM_EINVAL;
+    if (c->token_stride < cfg->head_dim || c->page_stride < cfg->head_dim) return ENGRAM_EINVAL;
+    if (cfg->n_kv_heads > 1 && c->head_stride < cfg->head_dim) return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+static engram_status check_batch(const engram_kv_batch *b) {
+    if (!b || b->n_query < 0 || b->n_seqs < 0) return ENGRAM_EINVAL;
+    if (b->n_query > INT32_MAX || b->n_seqs > INT32_MAX || b->table_stride < 0) return ENGRAM_EINVAL;
+    if (b->n_query == 0) return ENGRAM_OK;
+    if (b->n_seqs < 1 || b->table_stride < 1 || b->table_stride > INT32_MAX) return ENGRAM_EINVAL;
+    if (!b->seq_offsets || !b->kv_len || !b->block_table) return ENGRAM_EINVAL;
+    if (!aligned(b->seq_offsets, 8) || !aligned(b->kv_len, 4) || !aligned(b->block_table, 4)) return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+static Batch device_batch(const engram_kv_batch *b, const engram_kv_cache *c) {
+    Batch d;
+    d.offs = b->seq_offsets;
+    d.kv_len = b->kv_len;
+    d.block_table = b->block_table;
+    d.table_stride = b->table_stride;
+    d.n_seqs = b->n_seqs;
+    d.n_query = b->n_query;
+    d.n_pages = c->n_pages;
+    d.page_size = c->page_size;
+    return d;
+}
+
+// An ordinary launch that may start while the kernel before it drains: every
+// kernel here waits for that kernel's completion before its first global
+// access, so this only hides launch latency.
+template <typename... P, typename... A>
+static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
+                                  const char *what, const A &...args) {
+    cudaLaunchConfig_t lc = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = st;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, kern, args...);
+    return e == cudaSuccess ? ENGRAM_OK : cuda_fail(e, what);
+}
+
+// ------------------------------------------------- norm, rotation, append ----
+
+template <typename E, int LPH, int U, bool APPEND>
+static engram_status head_launch_u(const engram_attn_config *cfg, HeadParams &p, cudaStream_t st) {
+    const int heads = p.n_q + p.n_k + p.n_v, per = 32 / LPH * U;
+    p.head_blocks = (heads + per - 1) / per;
+    const int64_t blocks = (p.n_tokens * p.head_blocks + 7) / 8;
+    if (blocks > INT32_MAX) return ENGRAM_EINVAL;
+    const dim3 grid((unsigned)blocks);
+    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
+        return launch_after(head_kernel<E, LPH, U, true, APPEND>, grid, 256, 0, st, "head_kernel", p);
+    return launch_after(head_kernel<E, LPH, U, false, APPEND>, grid, 256, 0, st, "head_kernel", p);
+}
+
+template <typename E, bool APPEND>
+static engram_status head_launch(const engram_attn_config *cfg, HeadParams &p, cudaStream_t st) {
+    p.head_dim = cfg->head_dim;
+    p.rope_dim = cfg->rope_dim;
+    p.eps = cfg->norm_eps;
+    // One head per lane while the batch leaves SMs idle (a shorter chain per
+    // warp), four once there are several warps per SM without it.
+    const int64_t warps1 = p.n_tokens * ((p.n_q + p.n_k + p.n_v + 3) / 4);
+    const bool wide = warps1 >= (int64_t)num_sms() * 64;
+    if (cfg->head_dim <= 64)
+        return wide ? head_launch_u<E, 4, 4, APPEND>(cfg, p, st) : head_launch_u<E, 4, 1, APPEND>(cfg, p, st);
+    return wide ? head_launch_u<E, 8, 4, APPEND>(cfg, p, st) : head_launch_u<E, 8, 1, APPEND>(cfg, p, st);
+}
+
+// ---------------------------------------------------------------- attention --
+
+// A [page][head][token][D] view of K or V pages for TMA: boxes of 64 values x
+// `rows` tokens in 128-byte swizzled rows; values past head_dim read as zeros.
+static bool page_map(CUtensorMap *m, const engram_attn_config *cfg, const engram_kv_cache *c, void *base, int rows) {
+    auto enc = tensormap_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)cfg->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)cfg->n_kv_heads,
+                          (cuuint64_t)c->n_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)c->token_stride * 2, (cuuint64_t)c->head_stride * 2,
+                             (cuuint64_t)c->page_stride * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type =
+        cfg->dtype == ENGRAM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc(m, type, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
+static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+static int padded_dim(const engram_attn_config *cfg) { return cfg->head_dim <= 64 ? 64 : 128; }
+
+static size_t rows_part_o_bytes(const engram_attn_config *cfg) {
+    return up256((size_t)num_sms() * 2 * rows::ROWS * padded_dim(cfg) * sizeof(float));
+}
+static size_t rows_workspace_bytes(const engram_attn_config *cfg) {
+    return rows_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
+}
+
+template <typename E, int DP>
+static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                 const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                 float *lse, void *workspace, cudaStream_t st) {
+    rows::Params p;
+    memset(&p, 0, sizeof(p));
+    p.b = device_batch(batch, cache);
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.q_token_stride = q->token_stride;
+    p.q_head_stride = q->head_stride;
+    p.out = static_cast<uint16_t *>(out->data);
+    p.out_token_stride = out->token_stride;
+    p.out_head_stride = out->head_stride;
+    p.lse = lse;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows_part_o_bytes(cfg));
+    p.n_heads = cfg->n_heads;
+    p.n_kv_heads = cfg->n_kv_heads;
+    p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.head_dim = cfg->head_dim;
+    p.window = cfg->window;
+    p.box = gcd(cache->page_size, rows::KT);
+    p.runs = num_sms();
+    p.scale_log2 = cfg->scale * 1.4426950408889634f;
+    CUtensorMap km, vm;
+    if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
+    constexpr int smem = rows::smem_bytes<DP>();
+    static std::atomic<bool> attr_done[64];
+    const auto kern = rows::rows_kernel<E, DP>;
+    engram_status s = ensure_smem((const void *)kern, smem, attr_done);
+    if (s != ENGRAM_OK) return s;
+    s = launch_after(kern, dim3(p.runs), rows::NUM_THREADS, smem, st, "rows_kernel", km, vm, p);
+    if (s != ENGRAM_OK || p.runs == 1) return s;
+    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, st, "rows_join_kernel", p);
+}
+
+}  // namespace attn
+}  // namespace engram
+
+extern "C" engram_status engram_qk_norm_rope(const engram_attn_config *cfg, int64_t n_tokens, const engram_heads *q,
+                                             const engram_heads *k, const int32_t *positions, const float *table,
+                                             int64_t table_rows, const void *w_q, const void *w_k,
+                                             const engram_heads *q_out, const engram_heads *k_out, void *stream) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || n_tokens < 0 || n_tokens > INT32_MAX) return ENGRAM_EINVAL;
+    if (n_tokens == 0 || (!q && !k)) return ENGRAM_OK;
+    if ((q && (!view_ok(q) || !view_ok(q_out))) || (k && (!view_ok(k) || !view_ok(k_out)))) return ENGRAM_EINVAL;
+    if (!aligned(w_q, 16) || !aligned(w_k, 16) || table_rows < 0) return ENGRAM_EINVAL;
+    if (cfg->rope_dim > 0 && (!positions || !table || !aligned(positions, 4) || !aligned(table, 16))) return ENGRAM_EINVAL;
+    HeadParams p;
+    memset(&p, 0, sizeof(p));
+    p.q = view(q);
+    p.k = view(k);
+    p.q_out = view(q ? q_out : nullptr);
+    p.k_out = view(k ? k_out : nullptr);
+    p.n_q = q ? cfg->n_heads : 0;
+    p.n_k = k ? cfg->n_kv_heads : 0;
+    p.w_q = static_cast<const uint16_t *>(w_q);
+    p.w_k = static_cast<const uint16_t *>(w_k);
+    p.positions = cfg->rope_dim > 0 ? positions : nullptr;
+    p.table = table;
+    p.table_rows = table_rows;
+    p.n_tokens = n_tokens;
+    return cfg->dtype == ENGRAM_BF16 ? head_launch<Bf16, false>(cfg, p, (cudaStream_t)stream)
+                                     : head_launch<Fp16, false>(cfg, p, (cudaStream_t)stream);
+}
+
+extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                          const engram_kv_batch *batch, const engram_heads *k, const engram_heads *v,
+                                          const void *w_k, const float *table, int64_t table_rows,
+                                          const engram_heads *q, const void *w_q, const engram_heads *q_out,
+                                          void *stream) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK) return ENGRAM_EINVAL;
+    if (batch->n_query == 0) return ENGRAM_OK;
+    if (check_cache(cfg, cache) != ENGRAM_OK || !view_ok(k) || !view_ok(v)) return ENGRAM_EINVAL;
+    if (q && (!view_ok(q) || !view_ok(q_out))) return ENGRAM_EINVAL;
+    if (!aligned(w_q, 16) || !aligned(w_k, 16) || table_rows < 0) return ENGRAM_EINVAL;
+    if (cfg->rope_dim > 0 && (!table || !aligned(table, 16))) return ENGRAM_EINVAL;
+    HeadParams p;
+    memset(&p, 0, sizeof(p));
+    p.q = view(q);
+    p.k = view(k);
+    p.v = view(v);
+    p.q_out = view(q ? q_out : nullptr);
+    p.n_q = q ? cfg->n_heads : 0;
+    p.n_k = p.n_v = cfg->n_kv_heads;
+    p.w_q = static_cast<const uint16_t *>(w_q);
+    p.w_k = static_cast<const uint16_t *>(w_k);
+    p.table = table;
+    p.table_rows = table_rows;
+    p.n_tokens = batch->n_query;
+    p.k_pages = static_cast<uint16_t *>(cache->k);
+    p.v_pages = static_cast<uint16_t *>(cache->v);
+    p.page_stride = cache->page_stride;
+    p.slot_stride = cache->token_stride;
+    p.page_head_stride = cache->head_stride;
+    p.batch = device_batch(batch, cache);
+    return cfg->dtype == ENGRAM_BF16 ? head_launch<Bf16, true>(cfg, p, (cudaStream_t)stream)
+                                     : head_launch<Fp16, true>(cfg, p, (cudaStream_t)stream);
+}
+
+extern "C" size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || n_seqs < 0 || n_query < 0) return 0;
+    return rows_workspace_bytes(cfg);
+}
+
+extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                                const engram_kv_batch *batch, const engram_heads *q,
+                                                const engram_heads *out, float *lse, void *workspace,
+                                                size_t workspace_bytes, void *stream) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK) return ENGRAM_EINVAL;
+    if (batch->n_query == 0) return ENGRAM_OK;
+    if (check_cache(cfg, cache) != ENGRAM_OK || !view_ok(q) || !view_ok(out) || !aligned(lse, 4)) return ENGRAM_EINVAL;
+    if (batch->n_query > INT32_MAX / (cfg->n_heads / cfg->n_kv_heads)) return ENGRAM_EINVAL;
+    if (!workspace || !aligned(workspace, 256)) return ENGRAM_EINVAL;
+    if (workspace_bytes < engram_paged_attention_workspace_bytes(cfg, batch->n_seqs, batch->n_query)) return ENGRAM_ENOMEM;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool bf16 = cfg->dtype == ENGRAM_BF16;
+    if (padded_dim(cfg) == 64)
+        return bf16 ? rows_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
+                    : rows_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);
+    return bf16 ? rows_launch<Bf16, 128>(cfg, cache, batch, q, out, lse, workspace, st)
+                : rows_launch<Fp16, 128>(cfg, cache, batch, q, out, lse, workspace, st);
+}

@@ -26,6 +26,9 @@
 #include "fuse3.cuh"
 #include "layer.cuh"
 #include "narrow.cuh"
+#include "attn_common.cuh"
+#include "qk_rope.cuh"
+#include "attn_rows.cuh"
 
 namespace engram {
 
@@ -2281,3 +2284,5 @@ extern "C" engram_status engram_forward_no_workspace(const engram_config *cfg, c
     if (s != ENGRAM_OK) return s;
     return fuse_launch(cfg, nullptr, X, W_out, g, h, n_query, st);
 }
+
+#include "attention.cuh"

@@ -445,6 +445,134 @@ engram_status engram_forward_host_pipelined(const engram_config *cfg, const int3
                                             int64_t *n_unique, void *stream, void *side_stream,
                                             void *const *events);
 
+/* ======================================================================= *
+ * Attention beside the Engram read.  The Engram rows are added into the
+ * residual stream between attention layers ("The architecture"); the calls
+ * below are the attention step of a decoder layer that serves from a paged
+ * cache: heads are normed and rotated, new keys and values are appended, and
+ * the new tokens attend to the cache.  Conventions are those of the head of
+ * this file (device pointers, caller-owned buffers, no allocation, argument
+ * checks before anything is enqueued, the sticky device error word).
+ *
+ * Values are bf16 or fp16 (cfg->dtype; pointers are void*); head sums, scores,
+ * softmax statistics and accumulators are fp32, each output is rounded once.
+ * ======================================================================= */
+#define ENGRAM_BF16 0
+#define ENGRAM_FP16 1
+#define ENGRAM_ROPE_HALVES 0      /* pairs (i, i + rope_dim/2) */
+#define ENGRAM_ROPE_INTERLEAVED 1 /* pairs (2i, 2i + 1) */
+
+typedef struct {
+    int32_t n_heads;      /* query heads Hq >= 1, a multiple of n_kv_heads */
+    int32_t n_kv_heads;   /* key/value heads; query head h reads head h / (Hq / Hkv); Hq / Hkv <= 128 */
+    int32_t head_dim;     /* D: a multiple of 8, 8 <= D <= 128 */
+    int32_t rope_dim;     /* the first rope_dim values of a head rotate: a multiple of 16, 0 <= rope_dim <= D */
+    uint32_t rope_layout; /* ENGRAM_ROPE_HALVES or ENGRAM_ROPE_INTERLEAVED */
+    uint32_t dtype;       /* ENGRAM_BF16 or ENGRAM_FP16 */
+    float norm_eps;       /* eps of the head norm, >= 0 */
+    float scale;          /* factor of the scores, finite and > 0 (usually 1/sqrt(D)) */
+    int32_t window;       /* 0: causal; w > 0: a token sees itself and the w - 1 positions before it */
+} engram_attn_config;
+
+/* A [tokens][heads][head_dim] view: the head's values are contiguous, strides
+ * in elements (multiples of 8; data 16-byte aligned), so q, k and v may be
+ * slices of one packed projection. */
+typedef struct {
+    void *data;
+    int64_t token_stride;
+    int64_t head_stride;
+} engram_heads;
+
+/* The paged cache of one layer: page p holds page_size tokens of every
+ * key/value head, value (p, token, head, c) at p*page_stride +
+ * token*token_stride + head*head_stride + c of `k` and of `v` (elements;
+ * strides multiples of 8, data 16-byte aligned).  Both [page][token][head][D]
+ * and [page][head][token][D] are such layouts. */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t n_pages;   /* 1 .. 2^31 - 1 */
+    int32_t page_size; /* tokens per page: a multiple of 16, at most 65536 */
+    int64_t page_stride;
+    int64_t token_stride;
+    int64_t head_stride;
+} engram_kv_cache;
+
+/* One step's batch.  Sequence s brings q_len = seq_offsets[s+1] -
+ * seq_offsets[s] new tokens (rows seq_offsets[s] - seq_offsets[0] onwards of
+ * q, k and v); with them its length is kv_len[s], so its new token i has
+ * position kv_len[s] - q_len + i.  Position p is kept in row p % page_size of
+ * page block_table[s*table_stride + p / page_size].  A token whose position
+ * is negative (a padding sequence with kv_len 0, say) is not in the sequence:
+ * it is not appended and attends to nothing. */
+typedef struct {
+    int64_t n_seqs;
+    int64_t n_query;            /* new tokens in all, seq_offsets[n_seqs] - seq_offsets[0], < 2^31 */
+    const int64_t *seq_offsets; /* int64 [n_seqs + 1], ascending (as engram_hash takes them) */
+    const int32_t *kv_len;      /* int32 [n_seqs] */
+    const int32_t *block_table; /* int32 [n_seqs][table_stride]; entries past a sequence's length are not read */
+    int64_t table_stride;       /* >= ceil(kv_len[s] / page_size) for every s (ENGRAM_ERANGE on the device) */
+} engram_kv_batch;
+
+/*
+ * RMS norm of every query and key head and the rotation of its first rope_dim
+ * values, in one pass:
+ *   n = x / sqrt(mean(x^2) + norm_eps) * w     (w NULL: n = x, no norm)
+ *   y_a = n_a cos - n_b sin,  y_b = n_b cos + n_a sin   for each pair (a, b)
+ *   of index i < rope_dim/2, y = n for the other values.
+ *   q, k        [n_tokens][n_heads / n_kv_heads][D]; either may be NULL (left out)
+ *   positions   int32 [n_tokens], each in [0, table_rows) (ENGRAM_ERANGE on
+ *               the device otherwise, and that token is not written); NULL
+ *               only if rope_dim is 0
+ *   table       fp32 [table_rows][rope_dim]: rope_dim/2 cosines, then
+ *               rope_dim/2 sines of the position's angles (16-byte aligned);
+ *               NULL only if rope_dim is 0
+ *   w_q, w_k    [D] of the heads' type (16-byte aligned) or NULL
+ *   q_out, k_out  outputs for q and k; the input's own view (in place) or one
+ *               that shares no memory with the inputs
+ */
+engram_status engram_qk_norm_rope(const engram_attn_config *cfg, int64_t n_tokens, const engram_heads *q,
+                                  const engram_heads *k, const int32_t *positions, const float *table,
+                                  int64_t table_rows, const void *w_q, const void *w_k, const engram_heads *q_out,
+                                  const engram_heads *k_out, void *stream);
+
+/*
+ * Appends a step's keys and values to the paged cache, in one launch: k is
+ * normed (w_k, or NULL for none) and rotated by its position as in
+ * engram_qk_norm_rope and written to its slot, v is copied to its slot.  With
+ * q (optional; NULL otherwise) the step's queries are normed (w_q) and
+ * rotated into q_out in the same launch.
+ * A position >= table_rows, a page id outside [0, n_pages) or a position past
+ * the block table sets ENGRAM_ERANGE and writes nothing for that token.  Two
+ * tokens that name one slot in the same call race.
+ */
+engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                               const engram_kv_batch *batch, const engram_heads *k, const engram_heads *v,
+                               const void *w_k, const float *table, int64_t table_rows, const engram_heads *q,
+                               const void *w_q, const engram_heads *q_out, void *stream);
+
+/*
+ * Attention of a step's new tokens over the paged cache: for the query at
+ * position p of head h, over the cached positions j with max(0, p - window +
+ * 1) <= j <= p (window 0: from 0),
+ *   out = sum_j softmax_j(scale * q.k_j) v_j,  lse = ln sum_j exp(scale * q.k_j).
+ *   q, out     [n_query][n_heads][D]
+ *   lse        fp32 [n_query][n_heads] or NULL
+ *   workspace  >= engram_paged_attention_workspace_bytes(cfg, n_seqs,
+ *              n_query) bytes, 256-byte aligned; scratch, nothing to clear
+ * A query without any key gets out = 0 and lse = -inf.  Cache slots at or past
+ * a sequence's length may hold anything, NaN included: they are not used.
+ * From one token per sequence to whole prompts, in any mix.  Long sequences
+ * are split over the GPU by a rule on the batch's lengths, read on the
+ * device; partial results are joined in a fixed order, so equal inputs give
+ * equal bits.  A page id outside [0, n_pages) sets ENGRAM_ERANGE and reads as
+ * zeros.  kv_len beyond the block table sets ENGRAM_ERANGE and is cut there.
+ */
+size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query);
+engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                     const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                     float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
