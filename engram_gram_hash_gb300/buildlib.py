@@ -21,7 +21,7 @@ def sources():
 
 def build_cmd(out=LIB_PATH, extra=()):
     return [
-        "nvcc", *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+        "nvcc", *ARCH, "-lineinfo", "-O3", "-std=c++17", "--split-compile=0", "-Xcompiler", "-fPIC", "-shared",
         *extra, "-o", out, MAIN_SRC,
     ]
 

@@ -174,6 +174,69 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, st, "rows_join_kernel", p);
 }
 
+// Row blocks x kv heads of a batch at most.
+static int64_t tile_items_most(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    const int64_t rows = n_query * (cfg->n_heads / cfg->n_kv_heads);
+    const int64_t seqs = n_seqs < n_query ? n_seqs : n_query;
+    return (rows / tile::ROWS + seqs) * cfg->n_kv_heads;
+}
+static int64_t tile_slots(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    return std::min<int64_t>((int64_t)num_sms() * tile::SLOTS_PER_SM,
+                             tile_items_most(cfg, n_seqs, n_query) * tile::MAX_SPLIT);
+}
+static size_t tile_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
+    return up256((size_t)slots * tile::ROWS * padded_dim(cfg) * sizeof(float));
+}
+static size_t tile_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    const int64_t slots = tile_slots(cfg, n_seqs, n_query);
+    return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float));
+}
+
+// Query rows per sequence and key/value head from which the 256-row items pay
+// (on average over the batch: the lengths themselves are on the device).
+constexpr int64_t kTileRows = 32;
+static bool use_tiles(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    return n_query * (cfg->n_heads / cfg->n_kv_heads) >= kTileRows * n_seqs;
+}
+
+template <typename E, int DP>
+static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                 const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                 float *lse, void *workspace, cudaStream_t st) {
+    tile::Params p;
+    memset(&p, 0, sizeof(p));
+    const int64_t slots = tile_slots(cfg, batch->n_seqs, batch->n_query);
+    p.b = device_batch(batch, cache);
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.q_token_stride = q->token_stride;
+    p.q_head_stride = q->head_stride;
+    p.out = static_cast<uint16_t *>(out->data);
+    p.out_token_stride = out->token_stride;
+    p.out_head_stride = out->head_stride;
+    p.lse = lse;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tile_part_o_bytes(cfg, slots));
+    p.n_heads = cfg->n_heads;
+    p.n_kv_heads = cfg->n_kv_heads;
+    p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.head_dim = cfg->head_dim;
+    p.window = cfg->window;
+    p.box = gcd(cache->page_size, tile::KT);
+    p.ctas = num_sms();
+    p.max_slots = (int32_t)slots;
+    p.scale_log2 = cfg->scale * 1.4426950408889634f;
+    CUtensorMap km, vm;
+    if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
+    constexpr int smem = tile::smem_bytes<DP>();
+    static std::atomic<bool> attr_done[64];
+    const auto kern = tile::tile_kernel<E, DP, std::is_same<E, Bf16>::value>;
+    engram_status s = ensure_smem((const void *)kern, smem, attr_done);
+    if (s != ENGRAM_OK) return s;
+    s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS, smem, st, "tile_kernel", km, vm, p);
+    if (s != ENGRAM_OK) return s;
+    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * 8), 128, 0, st, "tile_join_kernel", p);
+}
+
 }  // namespace attn
 }  // namespace engram
 
@@ -243,7 +306,7 @@ extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const e
 extern "C" size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
     using namespace engram::attn;
     if (check_attn_config(cfg) != ENGRAM_OK || n_seqs < 0 || n_query < 0) return 0;
-    return rows_workspace_bytes(cfg);
+    return use_tiles(cfg, n_seqs, n_query) ? tile_workspace_bytes(cfg, n_seqs, n_query) : rows_workspace_bytes(cfg);
 }
 
 extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
@@ -259,6 +322,13 @@ extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, c
     if (workspace_bytes < engram_paged_attention_workspace_bytes(cfg, batch->n_seqs, batch->n_query)) return ENGRAM_ENOMEM;
     cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = cfg->dtype == ENGRAM_BF16;
+    if (use_tiles(cfg, batch->n_seqs, batch->n_query)) {
+        if (padded_dim(cfg) == 64)
+            return bf16 ? tile_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
+                        : tile_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);
+        return bf16 ? tile_launch<Bf16, 128>(cfg, cache, batch, q, out, lse, workspace, st)
+                    : tile_launch<Fp16, 128>(cfg, cache, batch, q, out, lse, workspace, st);
+    }
     if (padded_dim(cfg) == 64)
         return bf16 ? rows_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
                     : rows_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);

@@ -70,6 +70,12 @@ __device__ __forceinline__ Seq load_seq(const Batch &b, int64_t s, int64_t base)
     return Seq{(int32_t)a, (int32_t)(e - a), kv < 0 ? 0 : (int32_t)kv};
 }
 
+// mbar_wait by a whole warp, with one answer for all its lanes (near the time
+// limit the lanes could differ, and the warp-wide steps that follow must not).
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 // The last sequence s with offs[s] <= base + t (a whole warp looks at 32
 // offsets at a time, so up to 32 sequences take one load and 1,024 take two).
 __device__ __forceinline__ int64_t warp_find_seq(const int64_t *offs, int64_t n_seqs, int64_t p) {

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int32_t j = walk.j; j < end; ++j, ++it) {
                 if ((int)(it & 1) != grp) continue;
                 const int st = it % C::STAGES;
-                const bool ok = mbar_wait(&sh->full[st], (it / C::STAGES) & 1, abort);
+                const bool ok = warp_wait(&sh->full[st], (it / C::STAGES) & 1, abort);
                 const int32_t key0 = (g.tile0 + j) * KT + wq * 16;
                 if (ok && key0 < g.hi && key0 + 16 > g.lo) {
                     const uint32_t kb = smem_u32(smem + st * C::STAGE_BYTES) + wq * 16 * 128;

@@ -1,0 +1,825 @@
+// Paged attention for many query rows per key/value head (prompts, chunks):
+// the same sum as the rows kernel,
+//   out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  s_j = scale * q.k_j,
+// with both products on the tcgen05 tensor cores.
+//
+// Bound: the tensor pipe (4 * 128 * 128 * D flop per 128 x 128 tile and
+// direction; the softmax of a tile fits beside the other tile's products).
+//
+// An item is 256 query rows (the pairs (token, query head of the group),
+// consecutive: all heads that share a key/value head share its tiles) as two
+// 128-row tiles, against a run of 128-key tiles.  Per CTA (one per SM,
+// persistent over items):
+//   warps 0-3, 4-7  one softmax warpgroup per row tile, a row per thread: the
+//                   row's 128 scores come from TMEM into registers, its
+//                   maximum and sum need no exchange; weights go back to
+//                   TMEM as 16-bit pairs over the scores they came from.
+//   warp 8          issues the products: S = Q K^T (shared x shared memory),
+//                   O += P V (TMEM x shared memory).  While one tile's
+//                   softmax runs, the other tile's products do.
+//   warp 9          TMA: K and V tiles in turn into a ring of 32 KB stages.
+//   warp 10         finds the CTA's next items and hands them to the others.
+// TMEM: S0 | S1 | O0 | O1, 128 columns each (512 in all at 128 values).
+//
+// The running maximum moves only when a row's new maximum exceeds it by 2^8
+// (then O and the sum are scaled): weights stay below 2^8, far inside both
+// 16-bit types, and most tiles need no pass over O.  O is complete up to the
+// tile before whenever new scores arrive (one in-order MMA queue), so the
+// softmax warps scale it themselves.
+//
+// Few items are split along the keys (by the plan below) and leave partial
+// (m, l, O) for tile_join_kernel.
+#pragma once
+
+namespace engram {
+namespace attn {
+namespace tile {
+
+constexpr int MT = 128;               // rows per tile (TMEM lanes)
+constexpr int ROWS = 2 * MT;          // rows per item
+constexpr int KT = 128;               // keys per tile
+constexpr int NUM_THREADS = 384;
+constexpr int CHUNKS = 128;           // the plan's prefix sums: sequences in this many chunks
+constexpr int MAX_SPLIT = 152;
+constexpr int SLOTS_PER_SM = 8;       // workspace for partial results
+constexpr float RESCALE_LOG2 = 8.f;
+
+// How many parts the longest item is cut into at most; the plan picks one.
+constexpr int N_CAND = 16;
+__device__ const int kSplits[N_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 38, 64, 96, 152};
+
+template <int DP>
+struct Cfg {
+    static constexpr int STAGE_BYTES = KT * DP * 2;  // K or V of a tile
+    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int Q_BYTES = MT * DP * 2;      // one row tile
+    static constexpr int O_COL = 256;                // TMEM: scores in columns 0..255, then the outputs
+    static constexpr int TMEM_COLS = 512;
+};
+
+struct PlanShared {
+    int64_t items[CHUNKS + 1];   // items before each chunk of sequences
+    int64_t parts[CHUNKS + 1];   // ... and among them the parts of split ones (workspace slots)
+    unsigned long long cand_items[N_CAND], cand_parts[N_CAND];
+    unsigned long long work, segs;
+    int max_tiles;
+    int cut;                     // tiles per part at most
+};
+
+struct Item {
+    int64_t s;           // sequence
+    int64_t slot;        // workspace slot of this part (split items)
+    Seq q;
+    int32_t head, r0, n_rows, pos0;  // n_rows 0: no more items
+    int32_t lo, hi;      // keys in reach of any row
+    int32_t tile0, n;    // this part's tiles
+    int32_t part, splits;
+};
+constexpr int ITEMS = 4;  // items found ahead
+
+template <int DP>
+struct Shared {
+    uint64_t kv_full[Cfg<DP>::STAGES];
+    uint64_t kv_empty[Cfg<DP>::STAGES];
+    uint64_t q_full[2];
+    uint64_t s_full[2];
+    uint64_t p_ready[2];
+    uint64_t o_full[2];
+    uint64_t item_full[ITEMS];
+    uint64_t item_empty[ITEMS];
+    Item items[ITEMS];
+    uint32_t tmem_base;
+    int abort;
+    PlanShared plan;
+};
+
+template <int DP>
+constexpr int smem_bytes() {
+    return 2 * Cfg<DP>::Q_BYTES + Cfg<DP>::STAGES * Cfg<DP>::STAGE_BYTES + (int)sizeof(Shared<DP>);
+}
+static_assert(smem_bytes<128>() <= 232448, "tile kernel shared memory over the per-CTA limit");
+
+struct Params {
+    Batch b;
+    const uint16_t *q;
+    int64_t q_token_stride, q_head_stride;
+    uint16_t *out;
+    int64_t out_token_stride, out_head_stride;
+    float *lse;
+    float *part_o;      // [slots][ROWS][DP]
+    float *part_ml;     // [slots][2][ROWS]
+    int32_t n_heads, n_kv_heads, group, head_dim;
+    int32_t window;
+    int32_t box;        // tokens per TMA box: gcd(page_size, KT)
+    int32_t ctas;
+    int32_t max_slots;  // 0: nothing is split
+    float scale_log2;
+};
+
+// ------------------------------------------------------------------- plan ----
+
+// A sequence's share: row blocks, the most key tiles any of them reaches, and
+// about how many they reach on average.
+struct Share {
+    int64_t segs;    // row blocks x kv heads
+    int32_t blocks;
+    int32_t tiles;
+    int32_t mean;
+};
+__device__ __forceinline__ Share share(const Params &p, const Seq &q) {
+    Share r;
+    r.blocks = (int32_t)(((int64_t)q.q_len * p.group + ROWS - 1) / ROWS);
+    r.segs = (int64_t)r.blocks * p.n_kv_heads;
+    int32_t n = (q.kv + KT - 1) / KT;
+    if (p.window > 0) {
+        const int64_t reach = (int64_t)p.window + (ROWS - 2) / p.group + 1;
+        const int64_t w = (reach + KT - 2) / KT + 1;
+        if (w < n) n = (int32_t)w;
+    }
+    const int32_t first = q.kv - q.q_len > 0 ? q.kv - q.q_len : 0;
+    const int32_t mean = (int32_t)(((int64_t)q.kv + first) / 2 / KT) + 1;
+    r.tiles = n;
+    r.mean = mean < n ? mean : n;
+    return r;
+}
+__device__ __forceinline__ int32_t splits_of(int32_t tiles, int32_t cut) {
+    return tiles > cut ? (tiles + cut - 1) / cut : 1;
+}
+
+// All threads of a block of NT >= CHUNKS threads, into sh: the cut, and the
+// items before each chunk of sequences.
+template <int NT>
+__device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t per = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
+    const int64_t s0 = tid < CHUNKS ? tid * per : p.b.n_seqs;
+    const int64_t s1 = s0 + per < p.b.n_seqs ? s0 + per : p.b.n_seqs;
+    if (tid < N_CAND) sh->cand_items[tid] = sh->cand_parts[tid] = 0;
+    if (tid == 0) {
+        sh->work = sh->segs = 0;
+        sh->max_tiles = 1;
+        sh->cut = INT32_MAX;
+    }
+    __syncthreads();
+    if (p.max_slots > 0) {
+        int64_t work = 0;
+        int32_t most = 1;
+        for (int64_t s = s0; s < s1; ++s) {
+            const Share h = share(p, load_seq(p.b, s, base));
+            work += h.segs * h.mean;
+            if (h.segs > 0 && h.tiles > most) most = h.tiles;
+        }
+        if (work) {
+            atomicAdd(&sh->work, (unsigned long long)work);
+            atomicMax(&sh->max_tiles, most);
+        }
+        __syncthreads();
+        const int32_t max_tiles = sh->max_tiles;
+        for (int64_t s = s0; s < s1; ++s) {
+            const Share h = share(p, load_seq(p.b, s, base));
+            if (h.segs == 0) continue;
+            for (int c = 0; c < N_CAND; ++c) {
+                const int32_t n = splits_of(h.tiles, (max_tiles + kSplits[c] - 1) / kSplits[c]);
+                atomicAdd(&sh->cand_items[c], (unsigned long long)(h.segs * n));
+                if (n > 1) atomicAdd(&sh->cand_parts[c], (unsigned long long)(h.segs * n));
+            }
+        }
+        __syncthreads();
+        // The time of each candidate in tiles: equal items go in rounds; items
+        // of unequal size fill each other's gaps (half the longest is left
+        // over).  An item costs about two tiles beside its own, a part about
+        // five (its partial result is written and read again).
+        if (tid < 32) {
+            float best = INFINITY;
+            int cut = INT32_MAX;
+            if (lane < N_CAND) {
+                const int32_t c = (max_tiles + kSplits[lane] - 1) / kSplits[lane];
+                const float n = (float)sh->cand_items[lane], w = (float)sh->work, g = (float)p.ctas;
+                const float rounds = ceilf(n / g);
+                const float span = n <= g ? (float)c : (w > 0.85f * n * c ? rounds * c : w / g + 0.5f * c);
+                const float each = kSplits[lane] > 1 ? 5.f : 2.f;
+                if (kSplits[lane] == 1 || sh->cand_parts[lane] <= (unsigned long long)p.max_slots) best = span + rounds * each;
+                cut = kSplits[lane] == 1 ? INT32_MAX : c;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {  // the least; of equals the first candidate (lower lane)
+                const float ob = __shfl_down_sync(0xffffffffu, best, o);
+                const int oc = __shfl_down_sync(0xffffffffu, cut, o);
+                if (ob < best) {
+                    best = ob;
+                    cut = oc;
+                }
+            }
+            if (lane == 0) sh->cut = cut;
+        }
+        __syncthreads();
+    }
+    if (tid < CHUNKS) {
+        int64_t n = 0, parts = 0;
+        for (int64_t s = s0; s < s1; ++s) {
+            const Share h = share(p, load_seq(p.b, s, base));
+            const int32_t k = splits_of(h.tiles, sh->cut);
+            n += h.segs * k;
+            if (k > 1) parts += h.segs * k;
+        }
+        sh->items[tid + 1] = n;
+        sh->parts[tid + 1] = parts;
+        if (tid == 0) sh->items[0] = sh->parts[0] = 0;
+    }
+    __syncthreads();
+    if (tid < 64) {  // inclusive sums over the chunks, 32 at a time; a warp for each array
+        int64_t *a = tid < 32 ? sh->items : sh->parts;
+        int64_t run = 0;
+        for (int c = 0; c < CHUNKS; c += 32) {
+            int64_t v = a[c + lane + 1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            a[c + lane + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// Rows and keys of segment seg = block * n_kv_heads + head of sequence it.q;
+// part it.part of it.splits.
+__device__ __forceinline__ void place(const Params &p, Item &it, int64_t seg) {
+    it.head = (int32_t)(seg % p.n_kv_heads);
+    it.r0 = (int32_t)(seg / p.n_kv_heads) * ROWS;
+    const int32_t left = it.q.q_len * p.group - it.r0;
+    it.n_rows = left < ROWS ? left : ROWS;
+    it.pos0 = it.q.kv - it.q.q_len;
+    const int32_t first = it.pos0 + it.r0 / p.group, last = it.pos0 + (it.r0 + it.n_rows - 1) / p.group;
+    it.hi = last + 1 > 0 ? last + 1 : 0;
+    it.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
+    const int32_t t0 = it.lo / KT, nt = it.hi > it.lo ? (it.hi + KT - 1) / KT - t0 : 0;
+    const int32_t a = (int32_t)((int64_t)nt * it.part / it.splits), b = (int32_t)((int64_t)nt * (it.part + 1) / it.splits);
+    it.tile0 = t0 + a;
+    it.n = b - a;
+}
+
+// Item number `index` of the plan (every thread of the caller alike).
+// Parts outermost (all heads and blocks go over the same keys at about the
+// same time and share them through L2), the longest blocks first, heads
+// innermost.
+__device__ __forceinline__ Item find_item(const Params &p, int64_t base, const PlanShared *sh, int64_t index) {
+    int lo = 0, hi = CHUNKS;  // items[lo] <= index < items[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh->items[mid] <= index) lo = mid; else hi = mid;
+    }
+    const int64_t per = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
+    Item it;
+    int64_t at = index - sh->items[lo];
+    it.slot = sh->parts[lo];
+    for (it.s = lo * per;; ++it.s) {
+        it.q = load_seq(p.b, it.s, base);
+        const Share h = share(p, it.q);
+        it.splits = splits_of(h.tiles, sh->cut);
+        const int64_t n = h.segs * it.splits;
+        if (at < n) {
+            it.part = (int32_t)(at / h.segs);
+            const int64_t k = at - it.part * h.segs;
+            const int32_t block = (int32_t)(k / p.n_kv_heads);
+            const int64_t seg = (int64_t)(h.blocks - 1 - block) * p.n_kv_heads + (k - (int64_t)block * p.n_kv_heads);
+            it.slot += seg * it.splits + it.part;
+            place(p, it, seg);
+            return it;
+        }
+        at -= n;
+        if (it.splits > 1) it.slot += n;
+    }
+}
+
+// ---------------------------------------------------------------- helpers ----
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    mma_bf16(d, a, b, idesc, accumulate);  // kind::f16: the descriptor names the type
+}
+// A from TMEM (16-bit pairs, a row per lane), B from shared memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+// kind::f16 instruction descriptor, fp32 accumulator, A K-major.
+__host__ __device__ constexpr uint32_t idesc_16(bool bf16, int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// ----------------------------------------------------------------- kernel ----
+
+template <typename E, int DP, bool BF16>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    tile_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const __grid_constant__ Params p) {
+    using C = Cfg<DP>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_smem = smem;
+    uint8_t *kv_smem = smem + 2 * C::Q_BYTES;
+    Shared<DP> *sh = reinterpret_cast<Shared<DP> *>(kv_smem + C::STAGES * C::STAGE_BYTES);
+    volatile int *abort = &sh->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
+        grid_dependency_wait();
+        if (threadIdx.x == 0) raise_error(ENGRAM_EUNSUPPORTED);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&sh->kv_full[i], 1);
+            mbar_init(&sh->kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], 4);
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->p_ready[i], 4);
+            mbar_init(&sh->o_full[i], 1);
+        }
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(&sh->item_full[i], 1);
+            mbar_init(&sh->item_empty[i], 10);  // eight softmax warps, the MMA and the load warp
+        }
+        sh->abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+    }
+    if (warp == 8) {
+        tmem_alloc(&sh->tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t base = __ldg(p.b.offs);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.b.offs + p.b.n_seqs) - base != p.b.n_query)
+        raise_error(ENGRAM_ERANGE);
+    tc_fence_before();
+    make_plan<NUM_THREADS>(p, base, &sh->plan);  // synchronises the block
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+    const int64_t n_items = sh->plan.items[CHUNKS];
+
+    // Item number i of this CTA, for a whole warp: every role takes all of them in order (null after a time-out).
+    const auto take = [&](uint32_t i) -> const Item * {
+        return warp_wait(&sh->item_full[i % ITEMS], (i / ITEMS) & 1, abort) ? &sh->items[i % ITEMS] : nullptr;
+    };
+
+    // Registers move from the load and MMA warps to the softmax warps, which hold a row of 128
+    // scores each: 256 x 208 + 128 x 88 = the launch's 384 x 168.
+    if (warp < 8) {  // ------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int t = warp >> 2;                  // row tile
+        const int row = (warp & 3) * 32 + lane;   // row of the tile: this thread's TMEM lane
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_tm = tmem + lanes + t * KT, o_tm = tmem + lanes + C::O_COL + t * DP;
+        uint32_t s_ph = 0, o_ph = 0, it = 0;
+        bool ok = true;
+
+        // the tile's query rows into shared memory, 16 bytes a lane: rows past the item's are zero
+        const auto load_q = [&](const Item &w) {
+            constexpr int PIECES = DP / 8, PER = 32 / PIECES;  // 16-byte pieces of a row, rows a warp loads at once
+            const int ch = lane % PIECES;
+#pragma unroll 4
+            for (int i = 0; i < 32; i += PER) {
+                const int r = (warp & 3) * 32 + i + lane / PIECES;
+                const int rr = w.r0 + t * MT + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (t * MT + r < w.n_rows && ch * 8 < p.head_dim) {
+                    const int32_t tok = rr / p.group, hh = rr - tok * p.group;
+                    v = *reinterpret_cast<const uint4 *>(p.q + ((int64_t)w.q.row0 + tok) * p.q_token_stride +
+                                                         (int64_t)(w.head * p.group + hh) * p.q_head_stride + ch * 8);
+                }
+                const uint32_t dst = smem_u32(q_smem) + t * C::Q_BYTES + (ch >> 3) * (MT * 128) + r * 128 +
+                                     (((ch & 7) ^ (r & 7)) << 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->q_full[t]);
+        };
+
+        const Item *w = take(0);
+        if (w && w->n > 0 && w->n_rows > t * MT) load_q(*w);
+        for (uint32_t k = 0; w && w->n_rows > 0 && ok; ++k) {
+            const bool mine = w->n_rows > t * MT;
+            const int32_t n = w->n;
+            float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
+            if (mine && n > 0) {
+                const int32_t tile0 = w->tile0, lo = w->lo, hi = w->hi;
+                const int32_t pos = w->pos0 + (w->r0 + t * MT + row) / p.group;
+                const int32_t row_lo = p.window > 0 ? pos - p.window + 1 : 0;
+                // keys in reach of every row of the tile
+                const int32_t last = (w->n_rows < (t + 1) * MT ? w->n_rows : (t + 1) * MT) - 1;
+                const int32_t full_hi = w->pos0 + (w->r0 + t * MT) / p.group + 1;
+                const int32_t full_lo = p.window > 0 ? w->pos0 + (w->r0 + last) / p.group - p.window + 1 : 0;
+                for (int32_t j = 0; j < n; ++j) {
+                    const int32_t key0 = (tile0 + j) * KT;
+                    ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t raw[4][32];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tm + c * 32, raw[c]);
+                    tmem_ld_wait();
+                    float s[KT];
+#pragma unroll
+                    for (int i = 0; i < KT; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
+                    if (key0 < full_lo || key0 + KT > full_hi) {
+                        const int32_t a = row_lo - key0, b = pos - key0;  // this row's keys: [a, b] of the tile
+#pragma unroll
+                        for (int i = 0; i < KT; ++i)
+                            if (i < a || i > b) s[i] = -INFINITY;
+                    }
+                    float mx = fmaxf(s[0], s[1]);
+#pragma unroll
+                    for (int i = 2; i < KT; i += 2) mx = max3(mx, s[i], s[i + 1]);
+                    float up = 1.f;
+                    if ((mx - m) * p.scale_log2 > RESCALE_LOG2) {  // also from -inf
+                        up = rows::exp2_approx((m - mx) * p.scale_log2);
+                        m = mx;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, up != 1.f)) {
+                        l *= up;
+#pragma unroll
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_tm + c * 16, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
+                            tmem_st_32x32b_x16(o_tm + c * 16, o);
+                        }
+                    }
+                    const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mref, -mref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, off);
+                            x.x = rows::exp2_approx(x.x);
+                            x.y = rows::exp2_approx(x.y);
+                            sum[i & 1] = add2(sum[i & 1], x);
+                            pk[i] = E::pack(x.x, x.y);  // 16-bit operands of the second product
+                        }
+                        tmem_st_32x32b_x16(s_tm + c * 16, pk);
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    tmem_st_wait();
+                    // keys that no row reaches may hold anything: their values are cleared before the product
+                    if (t == 0 && (key0 < lo || key0 + KT > hi)) {
+                        const uint32_t vi = it + 2 * j + 1;
+                        ok = warp_wait(&sh->kv_full[vi % C::STAGES], (vi / C::STAGES) & 1, abort);
+                        if (!ok) break;
+                        if (key0 + row < lo || key0 + row >= hi) {
+                            const uint32_t at = smem_u32(kv_smem) + (vi % C::STAGES) * C::STAGE_BYTES + row * 128;
+#pragma unroll
+                            for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * (KT * 128) + i * 16),
+                                                 "r"(0)
+                                                 : "memory");
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->p_ready[t]);
+                }
+                if (!ok) break;
+                ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            it += 2 * n;
+            // the next item's queries first, so that its scores are computed under this item's epilogue
+            const Item *const next = take(k + 1);
+            if (next && next->n > 0 && next->n_rows > t * MT) load_q(*next);
+            if (mine) {
+                const bool whole = w->splits == 1, live = t * MT + row < w->n_rows;
+                const int64_t slot = whole ? 0 : w->slot;
+                const int32_t rr = w->r0 + t * MT + row, tok = rr / p.group, head = w->head * p.group + rr - tok * p.group;
+                const int64_t out_row = (int64_t)w->q.row0 + tok;
+                const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+                uint16_t *dst = p.out + out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
+                float *part = p.part_o + (slot * ROWS + t * MT + row) * DP;
+#pragma unroll
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t o[32];
+                    if (n > 0) {
+                        tmem_ld_32x32b_x32(o_tm + c * 32, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
+                    if (live) {
+                        if (whole) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if (c * 32 + i * 8 < p.head_dim) {
+                                    uint32_t u[4];
+#pragma unroll
+                                    for (int h = 0; h < 4; ++h)
+                                        u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv,
+                                                       __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
+                                    *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                                }
+                            }
+                        } else if (n > 0) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4 *>(part + c * 32 + i * 4) =
+                                    make_uint4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();  // O has been read before the next item's first product is allowed
+                if (live) {
+                    const float m2 = m == -INFINITY ? -INFINITY : m * p.scale_log2;
+                    if (!whole) {
+                        p.part_ml[slot * (2 * ROWS) + t * MT + row] = m2;
+                        p.part_ml[slot * (2 * ROWS) + ROWS + t * MT + row] = l;
+                    } else if (p.lse) {
+                        p.lse[out_row * p.n_heads + head] = rows::lse_of(m2, l);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_empty[k % ITEMS]);
+            w = next;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 10) {  // --------------------------------------------- items
+            if (lane == 0) {
+                uint32_t i = 0;
+                for (int64_t index = blockIdx.x;; index += gridDim.x, ++i) {
+                    if (i >= ITEMS && !mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort)) break;
+                    if (index < n_items)
+                        sh->items[i % ITEMS] = find_item(p, base, &sh->plan, index);
+                    else
+                        sh->items[i % ITEMS].n_rows = 0;
+                    mbar_arrive(&sh->item_full[i % ITEMS]);
+                    if (index >= n_items) break;
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9) {  // --------------------------------------- K, V loads
+            const int boxes = KT / p.box;
+            const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64);
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t i = 0; ok; ++i) {
+                const Item *const item = take(i);
+                if (!item || item->n_rows == 0) break;
+                const struct {
+                    int64_t s;
+                    int32_t head, tile0, n, lo, hi;
+                } w = {item->s, item->head, item->tile0, item->n, item->lo, item->hi};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
+                int64_t window0 = -1;
+                int32_t page = -1;
+                for (int32_t j = 0; ok && j < w.n; ++j) {
+                    const int64_t b0 = (int64_t)(w.tile0 + j) * boxes;
+                    if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
+                        window0 = b0;
+                        const int64_t key = (b0 + lane) * p.box;
+                        page = -1;
+                        if (key < w.hi) {
+                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + key / p.b.page_size);
+                            if (page < 0 || page >= p.b.n_pages) {
+                                if (key + p.box > w.lo) raise_error(ENGRAM_ERANGE);
+                                page = -1;  // out of range: the copy fills zeros
+                            }
+                        }
+                    }
+                    const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
+                    const int64_t key = (b0 + lane) * p.box;
+                    const bool load = lane < boxes && key < w.hi && key + p.box > w.lo;
+                    const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+                    const int y = (int)(key % p.b.page_size);
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const int st = it % C::STAGES;
+                        if (lane == 0) {
+                            if (it >= C::STAGES) ok = mbar_wait(&sh->kv_empty[st], ((it / C::STAGES) - 1) & 1, abort);
+                            if (ok) mbar_arrive_expect_tx(&sh->kv_full[st], loads * box_bytes);
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        if (load) {
+                            uint8_t *dst = kv_smem + st * C::STAGE_BYTES + lane * p.box * 128;
+#pragma unroll
+                            for (int c = 0; c < DP / 64; ++c)
+                                rows::tma_load_4d(dst + c * KT * 128, kv ? &v_map : &k_map, &sh->kv_full[st], c * 64, y, w.head,
+                                                  mine);
+                        }
+                    }
+                }
+            }
+            if (lane == 0) {  // never leave with a copy still landing (also after an abort elsewhere)
+                int no_abort = 0;
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+                    mbar_wait(&sh->kv_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, 200000000ull);
+            }
+        } else if (warp == 8) {  // -------------------------------------------- MMAs
+            if (lane == 0) {
+                constexpr uint32_t ID_S = idesc_16(BF16, MT, KT, false), ID_O = idesc_16(BF16, MT, DP, true);
+                const uint32_t qa = smem_u32(q_smem), kva = smem_u32(kv_smem);
+                uint32_t it = 0;           // ring entries consumed
+                uint32_t q_ph = 0;         // items with work so far (q_full phases of tile 0)
+                uint32_t q1_ph = 0;        // ... of tile 1
+                uint32_t p_ph[2] = {0, 0}; // weights consumed
+                bool ok = true;
+                const auto full = [&](uint32_t i) { return mbar_wait(&sh->kv_full[i % C::STAGES], (i / C::STAGES) & 1, abort); };
+                const auto scores = [&](int t, uint32_t i) {  // S_t = Q_t K^T, K in ring entry i
+                    const uint32_t a = qa + t * C::Q_BYTES, b = kva + (i % C::STAGES) * C::STAGE_BYTES;
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        const uint32_t off = (k >> 2) * (KT * 128) + (k & 3) * 32;
+                        mma_ss(tmem + t * KT, smem_desc(a + off, 16, 1024, kSwizzle128B),
+                               smem_desc(b + off, 16, 1024, kSwizzle128B), ID_S, k != 0);
+                    }
+                    mma_commit(&sh->s_full[t]);
+                };
+                for (uint32_t i = 0; ok; ++i) {
+                    ok = mbar_wait(&sh->item_full[i % ITEMS], (i / ITEMS) & 1, abort);
+                    const Item *const item = &sh->items[i % ITEMS];
+                    if (!ok || item->n_rows == 0) break;
+                    const int32_t n = item->n;
+                    const int tiles = item->n_rows > MT ? 2 : 1;
+                    mbar_arrive(&sh->item_empty[i % ITEMS]);
+                    if (n == 0) continue;
+                    ok = mbar_wait(&sh->q_full[0], q_ph++ & 1, abort) &&
+                         (tiles == 1 || mbar_wait(&sh->q_full[1], q1_ph++ & 1, abort)) && full(it);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int t = 0; t < tiles; ++t) scores(t, it);
+                    mma_commit(&sh->kv_empty[it % C::STAGES]);
+                    ++it;
+                    for (int32_t j = 0; ok && j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        ok = full(it) && (!more || full(it + 1));
+                        const uint32_t v = kva + (it % C::STAGES) * C::STAGE_BYTES;
+                        for (int t = 0; ok && t < tiles; ++t) {
+                            ok = mbar_wait(&sh->p_ready[t], p_ph[t]++ & 1, abort);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < KT / 16; ++k)
+                                mma_ts(tmem + C::O_COL + t * DP, tmem + t * KT + k * 8,
+                                       smem_desc(v + k * 2048, KT * 128, 1024, kSwizzle128B), ID_O, (j | k) != 0);
+                            if (more)
+                                scores(t, it + 1);
+                            else
+                                mma_commit(&sh->o_full[t]);
+                        }
+                        mma_commit(&sh->kv_empty[it % C::STAGES]);
+                        if (more) mma_commit(&sh->kv_empty[(it + 1) % C::STAGES]);
+                        it += more ? 2 : 1;
+                    }
+                }
+                // Leave only when every MMA and the arrivals that follow them are done: the last ring entry's
+                // release, or after an abort one more commit (whichever phase the barrier is in).
+                int no_abort = 0;
+                if (ok) {
+                    if (it) mbar_wait(&sh->kv_empty[(it - 1) % C::STAGES], ((it - 1) / C::STAGES) & 1, &no_abort, 200000000ull);
+                } else {
+                    mma_commit(&sh->o_full[0]);
+                    mbar_wait(&sh->o_full[0], 0, &no_abort, 200000000ull);
+                    mbar_wait(&sh->o_full[0], 1, &no_abort, 200000000ull);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Adds up the parts of split items, in order: a warp takes one row at a time,
+// its lanes 4 values each.
+template <typename E, int DP>
+__global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ Params p) {
+    __shared__ PlanShared plan;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t base = __ldg(p.b.offs);
+    make_plan<128>(p, base, &plan);
+    if (plan.cut == INT32_MAX) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = (int64_t)gridDim.x * 4, wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    int64_t slot0 = 0, rows0 = 0;  // slots and rows before sequence s
+    for (int64_t s = 0; s < p.b.n_seqs; ++s) {
+        Item it;
+        it.s = s;
+        it.q = load_seq(p.b, s, base);
+        const Share h = share(p, it.q);
+        it.splits = splits_of(h.tiles, plan.cut);
+        if (it.splits == 1) continue;
+        const int64_t n_rows = h.segs * ROWS;
+        // this warp's rows of the sequence: numbers congruent to wid over all split sequences' rows
+        for (int64_t x = (wid + warps - rows0 % warps) % warps; x < n_rows; x += warps) {
+            const int64_t seg = x / ROWS;
+            const int r = (int)(x - seg * ROWS);
+            it.part = 0;
+            place(p, it, seg);
+            if (r >= it.n_rows) continue;
+            const int64_t slot = slot0 + seg * it.splits;
+            const float *ml = p.part_ml + slot * (2 * ROWS) + r;
+            float m = -INFINITY;
+            for (int k = lane; k < it.splits; k += 32) m = fmaxf(m, __ldcg(ml + (int64_t)k * (2 * ROWS)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < it.splits; k0 += 32) {
+                float mk = -INFINITY, wk = 0.f;
+                if (k0 + lane < it.splits) {
+                    mk = __ldcg(ml + (int64_t)(k0 + lane) * (2 * ROWS));
+                    wk = rows::weight(mk, m);
+                    l += wk * __ldcg(ml + (int64_t)(k0 + lane) * (2 * ROWS) + ROWS);
+                }
+                const int n = it.splits - k0 < 32 ? it.splits - k0 : 32;
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) {
+                    const float x_k = __shfl_sync(0xffffffffu, wk, k);
+                    // a part without keys for this row left no sum (and, without any tile, no O)
+                    const bool some = __shfl_sync(0xffffffffu, mk, k) != -INFINITY;
+                    if (some && lane * 4 < DP) {
+                        const float4 v =
+                            __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((slot + k0 + k) * ROWS + r) * DP) + lane);
+                        acc.x = fmaf(x_k, v.x, acc.x);
+                        acc.y = fmaf(x_k, v.y, acc.y);
+                        acc.z = fmaf(x_k, v.z, acc.z);
+                        acc.w = fmaf(x_k, v.w, acc.w);
+                    }
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+            const int32_t tok = (it.r0 + r) / p.group, hh = (it.r0 + r) - tok * p.group, head = it.head * p.group + hh;
+            const int64_t row = (int64_t)it.q.row0 + tok;
+            if (lane * 4 < p.head_dim)
+                *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + (int64_t)head * p.out_head_stride + lane * 4) =
+                    make_uint2(E::pack(acc.x * inv, acc.y * inv), E::pack(acc.z * inv, acc.w * inv));
+            if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = rows::lse_of(m, l);
+        }
+        slot0 += h.segs * it.splits;
+        rows0 += n_rows;
+    }
+}
+
+}  // namespace tile
+}  // namespace attn
+}  // namespace engram

@@ -15,6 +15,7 @@
 #include <map>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 #include <cstdlib>
 #include <cstring>
 
@@ -29,6 +30,7 @@
 #include "attn_common.cuh"
 #include "qk_rope.cuh"
 #include "attn_rows.cuh"
+#include "attn_tile.cuh"
 
 namespace engram {
 
