@@ -85,6 +85,7 @@ struct Shared {
     uint64_t s_full[2];
     uint64_t p_ready[2];
     uint64_t o_full[2];
+    uint64_t drained;
     uint64_t item_full[ITEMS];
     uint64_t item_empty[ITEMS];
     Item items[ITEMS];
@@ -326,6 +327,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -374,6 +384,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(&sh->p_ready[i], 4);
             mbar_init(&sh->o_full[i], 1);
         }
+        mbar_init(&sh->drained, 1);
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(&sh->item_full[i], 1);
             mbar_init(&sh->item_empty[i], 10);  // eight softmax warps, the MMA and the load warp
@@ -470,9 +481,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int i = 0; i < KT; ++i)
                             if (i < a || i > b) s[i] = -INFINITY;
                     }
-                    float mx = fmaxf(s[0], s[1]);
+                    float part[8];  // independent chains: one alone would wait out each maximum's latency
 #pragma unroll
-                    for (int i = 2; i < KT; i += 2) mx = max3(mx, s[i], s[i + 1]);
+                    for (int i = 0; i < 8; ++i) part[i] = fmaxf(s[i], s[i + 8]);
+#pragma unroll
+                    for (int i = 16; i < KT; i += 2) part[(i >> 1) & 7] = max3(part[(i >> 1) & 7], s[i], s[i + 1]);
+                    const float mx = fmaxf(max3(max3(part[0], part[1], part[2]), part[3], part[4]), max3(part[5], part[6], part[7]));
                     float up = 1.f;
                     if ((mx - m) * p.scale_log2 > RESCALE_LOG2) {  // also from -inf
                         up = rows::exp2_approx((m - mx) * p.scale_log2);
@@ -668,72 +682,85 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     mbar_wait(&sh->kv_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, 200000000ull);
             }
         } else if (warp == 8) {  // -------------------------------------------- MMAs
-            if (lane == 0) {
-                constexpr uint32_t ID_S = idesc_16(BF16, MT, KT, false), ID_O = idesc_16(BF16, MT, DP, true);
-                const uint32_t qa = smem_u32(q_smem), kva = smem_u32(kv_smem);
-                uint32_t it = 0;           // ring entries consumed
-                uint32_t q_ph = 0;         // items with work so far (q_full phases of tile 0)
-                uint32_t q1_ph = 0;        // ... of tile 1
-                uint32_t p_ph[2] = {0, 0}; // weights consumed
-                bool ok = true;
-                const auto full = [&](uint32_t i) { return mbar_wait(&sh->kv_full[i % C::STAGES], (i / C::STAGES) & 1, abort); };
-                const auto scores = [&](int t, uint32_t i) {  // S_t = Q_t K^T, K in ring entry i
-                    const uint32_t a = qa + t * C::Q_BYTES, b = kva + (i % C::STAGES) * C::STAGE_BYTES;
+            // The whole warp walks the tiles with warp-uniform values (the instruction takes its
+            // descriptors from uniform registers) and one elected lane issues.
+            constexpr uint32_t ID_S = idesc_16(BF16, MT, KT, false), ID_O = idesc_16(BF16, MT, DP, true);
+            const bool leader = elect_one();
+            const uint32_t qa = smem_u32(q_smem), kva = smem_u32(kv_smem);
+            const uint64_t q_desc = smem_desc(qa, 16, 1024, kSwizzle128B);
+            const uint64_t k_desc = smem_desc(kva, 16, 1024, kSwizzle128B);
+            const uint64_t v_desc = smem_desc(kva, KT * 128, 1024, kSwizzle128B);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t st = 0, st_ph = 0;  // ring entry to consume next, and its phase
+            uint32_t q_ph = 0;           // items with work so far (q_full phases), a bit per row tile
+            uint32_t p_ph = 0;           // weights consumed, a bit per row tile
+            bool ok = true;
+            // S_t = Q_t K^T, K in ring entry e
+            const auto scores = [&](int t, uint32_t e) {
+                const uint64_t a = q_desc + t * (C::Q_BYTES >> 4), k0 = k_desc + e * (C::STAGE_BYTES >> 4);
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) {
-                        const uint32_t off = (k >> 2) * (KT * 128) + (k & 3) * 32;
-                        mma_ss(tmem + t * KT, smem_desc(a + off, 16, 1024, kSwizzle128B),
-                               smem_desc(b + off, 16, 1024, kSwizzle128B), ID_S, k != 0);
+                        const uint32_t off = ((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4;
+                        mma_ss(tm + t * KT, a + off, k0 + off, ID_S, k != 0);
                     }
                     mma_commit(&sh->s_full[t]);
-                };
-                for (uint32_t i = 0; ok; ++i) {
-                    ok = mbar_wait(&sh->item_full[i % ITEMS], (i / ITEMS) & 1, abort);
-                    const Item *const item = &sh->items[i % ITEMS];
-                    if (!ok || item->n_rows == 0) break;
-                    const int32_t n = item->n;
-                    const int tiles = item->n_rows > MT ? 2 : 1;
-                    mbar_arrive(&sh->item_empty[i % ITEMS]);
-                    if (n == 0) continue;
-                    ok = mbar_wait(&sh->q_full[0], q_ph++ & 1, abort) &&
-                         (tiles == 1 || mbar_wait(&sh->q_full[1], q1_ph++ & 1, abort)) && full(it);
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (int t = 0; t < tiles; ++t) scores(t, it);
-                    mma_commit(&sh->kv_empty[it % C::STAGES]);
-                    ++it;
-                    for (int32_t j = 0; ok && j < n; ++j) {
-                        const bool more = j + 1 < n;
-                        ok = full(it) && (!more || full(it + 1));
-                        const uint32_t v = kva + (it % C::STAGES) * C::STAGE_BYTES;
-                        for (int t = 0; ok && t < tiles; ++t) {
-                            ok = mbar_wait(&sh->p_ready[t], p_ph[t]++ & 1, abort);
-                            if (!ok) break;
-                            tc_fence_after();
+                }
+            };
+            for (uint32_t i = 0; ok; ++i) {
+                const Item *const item = take(i);
+                ok = item != nullptr;
+                if (!ok) break;
+                const int32_t n_rows = __shfl_sync(0xffffffffu, item->n_rows, 0);
+                const int32_t n = __shfl_sync(0xffffffffu, item->n, 0);
+                if (n_rows == 0) break;
+                __syncwarp();
+                if (leader) mbar_arrive(&sh->item_empty[i % ITEMS]);
+                if (n == 0) continue;
+                const int tiles = n_rows > MT ? 2 : 1;
+                for (int t = 0; ok && t < tiles; ++t) {
+                    ok = warp_wait(&sh->q_full[t], (q_ph >> t) & 1, abort);
+                    q_ph ^= 1u << t;
+                }
+                if (!ok || !(ok = warp_wait(&sh->kv_full[st], st_ph, abort))) break;
+                tc_fence_after();
+                for (int t = 0; t < tiles; ++t) scores(t, st);
+                if (leader) mma_commit(&sh->kv_empty[st]);
+                if (++st == C::STAGES) st = 0, st_ph ^= 1;
+                for (int32_t j = 0; ok && j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const uint32_t v = st, v_ph = st_ph;
+                    if (++st == C::STAGES) st = 0, st_ph ^= 1;
+                    ok = warp_wait(&sh->kv_full[v], v_ph, abort) && (!more || warp_wait(&sh->kv_full[st], st_ph, abort));
+                    const uint64_t v0 = v_desc + v * (C::STAGE_BYTES >> 4);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok || t >= tiles) break;
+                        ok = warp_wait(&sh->p_ready[t], (p_ph >> t) & 1, abort);
+                        if (!ok) break;
+                        p_ph ^= 1u << t;
+                        tc_fence_after();
+                        if (leader) {
 #pragma unroll
                             for (int k = 0; k < KT / 16; ++k)
-                                mma_ts(tmem + C::O_COL + t * DP, tmem + t * KT + k * 8,
-                                       smem_desc(v + k * 2048, KT * 128, 1024, kSwizzle128B), ID_O, (j | k) != 0);
-                            if (more)
-                                scores(t, it + 1);
-                            else
-                                mma_commit(&sh->o_full[t]);
+                                mma_ts(tm + C::O_COL + t * DP, tm + t * KT + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                            if (!more) mma_commit(&sh->o_full[t]);
                         }
-                        mma_commit(&sh->kv_empty[it % C::STAGES]);
-                        if (more) mma_commit(&sh->kv_empty[(it + 1) % C::STAGES]);
-                        it += more ? 2 : 1;
+                        if (more) scores(t, st);
                     }
+                    if (leader) {
+                        mma_commit(&sh->kv_empty[v]);
+                        if (more) mma_commit(&sh->kv_empty[st]);
+                    }
+                    if (more && ++st == C::STAGES) st = 0, st_ph ^= 1;
                 }
-                // Leave only when every MMA and the arrivals that follow them are done: the last ring entry's
-                // release, or after an abort one more commit (whichever phase the barrier is in).
+            }
+            // Leave only when every MMA and the arrivals that follow them are done: one more commit of the
+            // issuing lane, on a barrier that nothing else uses.
+            if (leader) {
                 int no_abort = 0;
-                if (ok) {
-                    if (it) mbar_wait(&sh->kv_empty[(it - 1) % C::STAGES], ((it - 1) / C::STAGES) & 1, &no_abort, 200000000ull);
-                } else {
-                    mma_commit(&sh->o_full[0]);
-                    mbar_wait(&sh->o_full[0], 0, &no_abort, 200000000ull);
-                    mbar_wait(&sh->o_full[0], 1, &no_abort, 200000000ull);
-                }
+                mma_commit(&sh->drained);
+                mbar_wait(&sh->drained, 0, &no_abort, 200000000ull);
             }
             __syncwarp();
         }
