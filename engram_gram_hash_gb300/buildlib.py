@@ -1,11 +1,11 @@
-"""Builds libengram.so in-tree with nvcc for sm_103a (one translation unit)."""
+"""Builds libengram.so in-tree with nvcc for sm_103a (two translation units, compiled side by side)."""
 
 import os
 import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
-MAIN_SRC = os.path.join(SRC_DIR, "engram_core.cu")
+MAIN_SRCS = [os.path.join(SRC_DIR, f) for f in ("engram_core.cu", "attention.cu")]
 LIB_PATH = os.path.join(HERE, "libengram.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -19,11 +19,12 @@ def sources():
     return out
 
 
-def build_cmd(out=LIB_PATH, extra=()):
-    return [
-        "nvcc", *ARCH, "-lineinfo", "-O3", "-std=c++17", "--split-compile=0", "-Xcompiler", "-fPIC", "-shared",
-        *extra, "-o", out, MAIN_SRC,
-    ]
+def compile_cmd(src, obj, extra=()):
+    return ["nvcc", *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", *extra, "-c", "-o", obj, src]
+
+
+def link_cmd(objs, out=LIB_PATH):
+    return ["nvcc", *ARCH, "-shared", "-o", out, *objs]
 
 
 def build(force=False, verbose=False):
@@ -33,8 +34,15 @@ def build(force=False, verbose=False):
         t = os.path.getmtime(LIB_PATH)
         stale = any(os.path.getmtime(s) > t for s in sources())
     if stale:
-        cmd = build_cmd()
+        objs = [os.path.splitext(s)[0] + ".o" for s in MAIN_SRCS]
+        cmds = [compile_cmd(s, o) for s, o in zip(MAIN_SRCS, objs)]
         if verbose:
-            print(" ".join(cmd))
-        subprocess.check_call(cmd)
+            for cmd in cmds:
+                print(" ".join(cmd))
+        procs = [subprocess.Popen(cmd) for cmd in cmds]
+        codes = [p.wait() for p in procs]
+        for cmd, code in zip(cmds, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.check_call(link_cmd(objs))
     return LIB_PATH

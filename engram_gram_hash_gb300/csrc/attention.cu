@@ -1,9 +1,25 @@
-// C entry points of the attention step (head norm + rotation, cache append,
-// paged attention): argument checks, tensor maps, launches.
-#pragma once
+// The attention step (head norm + rotation, cache append, paged attention): C
+// entry points, argument checks, tensor maps, launches.  A translation unit of
+// its own: it shares no device code with the Engram read but the helpers of
+// common.cuh, and the two compile side by side.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <initializer_list>
+#include <type_traits>
+
+#include "common.cuh"
+#include "host.cuh"
+
+#include "attn_common.cuh"
+#include "attn_rows.cuh"
+#include "attn_tile.cuh"
+#include "qk_rope.cuh"
 
 namespace engram {
 namespace attn {
+
+cudaError_t take_error(unsigned int *w) { return take_error_word(w); }
 
 static bool finite_pos(float x) { return x > 0.f && x < INFINITY; }
 
@@ -239,6 +255,8 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
 
 }  // namespace attn
 }  // namespace engram
+
+using namespace engram;
 
 extern "C" engram_status engram_qk_norm_rope(const engram_attn_config *cfg, int64_t n_tokens, const engram_heads *q,
                                              const engram_heads *k, const int32_t *positions, const float *table,

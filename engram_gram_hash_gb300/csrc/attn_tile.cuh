@@ -83,7 +83,8 @@ struct Shared {
     uint64_t kv_empty[Cfg<DP>::STAGES];
     uint64_t q_full[2];
     uint64_t s_full[2];
-    uint64_t p_ready[2];
+    uint64_t p_half[2];   // weights of the first half of the keys
+    uint64_t p_ready[2];  // all weights
     uint64_t o_full[2];
     uint64_t turn[2];
     uint64_t drained[2];
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 4);
             mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->p_half[i], 4);
             mbar_init(&sh->p_ready[i], 4);
             mbar_init(&sh->turn[i], 1);
             mbar_init(&sh->drained[i], 1);
@@ -470,25 +472,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
+                    // the second half of the scores arrives under the first half's maximum
                     uint32_t raw[4][32];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tm + c * 32, raw[c]);
+                    tmem_ld_32x32b_x32(s_tm, raw[0]);
+                    tmem_ld_32x32b_x32(s_tm + 32, raw[1]);
                     tmem_ld_wait();
+                    tmem_ld_32x32b_x32(s_tm + 64, raw[2]);
+                    tmem_ld_32x32b_x32(s_tm + 96, raw[3]);
+                    const bool edge = key0 < full_lo || key0 + KT > full_hi;
+                    const int32_t a = row_lo - key0, b = pos - key0;  // this row's keys: [a, b] of the tile
                     float s[KT];
+                    float part[4];  // independent chains: one alone would wait out each maximum's latency
 #pragma unroll
-                    for (int i = 0; i < KT; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
-                    if (key0 < full_lo || key0 + KT > full_hi) {
-                        const int32_t a = row_lo - key0, b = pos - key0;  // this row's keys: [a, b] of the tile
+                    for (int h = 0; h < 2; ++h) {
+                        if (h) tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < KT; ++i)
-                            if (i < a || i > b) s[i] = -INFINITY;
+                        for (int i = h * 64; i < h * 64 + 64; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
+                        if (edge) {
+#pragma unroll
+                            for (int i = h * 64; i < h * 64 + 64; ++i)
+                                if (i < a || i > b) s[i] = -INFINITY;
+                        }
+#pragma unroll
+                        for (int i = h * 64; i < h * 64 + 64; i += 2)
+                            part[(i >> 1) & 3] = i < 8 ? fmaxf(s[i], s[i + 1]) : max3(part[(i >> 1) & 3], s[i], s[i + 1]);
                     }
-                    float part[8];  // independent chains: one alone would wait out each maximum's latency
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) part[i] = fmaxf(s[i], s[i + 8]);
-#pragma unroll
-                    for (int i = 16; i < KT; i += 2) part[(i >> 1) & 7] = max3(part[(i >> 1) & 7], s[i], s[i + 1]);
-                    const float mx = fmaxf(max3(max3(part[0], part[1], part[2]), part[3], part[4]), max3(part[5], part[6], part[7]));
+                    const float mx = fmaxf(max3(part[0], part[1], part[2]), part[3]);
                     float up = 1.f;
                     if ((mx - m) * p.scale_log2 > RESCALE_LOG2) {  // also from -inf
                         up = rows::exp2_approx((m - mx) * p.scale_log2);
@@ -506,24 +515,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             tmem_st_32x32b_x16(o_tm + c * 16, o);
                         }
                     }
-                    const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
-                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mref, -mref);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, off);
-                            x.x = rows::exp2_approx(x.x);
-                            x.y = rows::exp2_approx(x.y);
-                            sum[i & 1] = add2(sum[i & 1], x);
-                            pk[i] = E::pack(x.x, x.y);  // 16-bit operands of the second product
-                        }
-                        tmem_st_32x32b_x16(s_tm + c * 16, pk);
-                    }
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                    tmem_st_wait();
                     // keys that no row reaches may hold anything: their values are cleared before the product
                     // (by both row tiles, each before its own)
                     if (key0 < lo || key0 + KT > hi) {
@@ -542,9 +533,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                         fence_proxy_async_smem();
                     }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh->p_ready[t]);
+                    const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
+                    const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mref, -mref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, off);
+                            x.x = rows::exp2_approx(x.x);
+                            x.y = rows::exp2_approx(x.y);
+                            sum[i & 1] = add2(sum[i & 1], x);
+                            pk[i] = E::pack(x.x, x.y);  // 16-bit operands of the second product
+                        }
+                        tmem_st_32x32b_x16(s_tm + c * 16, pk);
+                        if (c & 1) {  // half of the weights are there: the second product starts on the first half
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(c == 1 ? &sh->p_half[t] : &sh->p_ready[t]);
+                        }
+                    }
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
                 if (!ok) break;
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
@@ -614,7 +625,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (warp == 10) {  // --------------------------------------------- items
             if (lane == 0) {
                 uint32_t i = 0;
-                for (int64_t index = blockIdx.x;; index += gridDim.x, ++i) {
+                // Rounds of one item per CTA, every other one in reverse: the items come longest first,
+                // and the CTAs at one end would get the longer one of every round.
+                for (;; ++i) {
+                    const int64_t index = (int64_t)i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                     if (i >= ITEMS && !mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort)) break;
                     if (index < n_items)
                         sh->items[i % ITEMS] = find_item(p, base, &sh->plan, index);
@@ -758,14 +772,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = warp_wait(&sh->kv_full[v], st_ph, abort);
                     advance();
                     ok = ok && (!more || warp_wait(&sh->kv_full[st], st_ph, abort)) &&
-                         warp_wait(&sh->p_ready[t], p_ph, abort) && my_turn(both);
+                         warp_wait(&sh->p_half[t], p_ph, abort) && my_turn(both);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < KT / 32; ++k)
+                            mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                    }
+                    ok = warp_wait(&sh->p_ready[t], p_ph, abort);
                     if (!ok) break;
                     p_ph ^= 1;
                     tc_fence_after();
                     if (leader) {
 #pragma unroll
-                        for (int k = 0; k < KT / 16; ++k)
-                            mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                        for (int k = KT / 32; k < KT / 16; ++k)
+                            mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, 1);
                         if (more)
                             scores();
                         else

@@ -20,10 +20,10 @@ constexpr int kRowBytes = 256;
 constexpr int kMem = 512;
 constexpr uint64_t kGolden = 0x9E3779B97F4A7C15ull;
 
-// One sticky word per device (each device that loads the library gets its
-// own copy).  Bit k set = status k was seen.  Only ever OR-ed on the device.
-// (libengram is one translation unit, so this header defines it.)
-__device__ unsigned int g_error_word = 0;
+// One sticky word per device and translation unit (each device that loads the
+// library gets its own copies; engram_last_error reads them all).  Bit k set =
+// status k was seen.  Only ever OR-ed on the device.
+static __device__ unsigned int g_error_word = 0;
 
 __device__ __forceinline__ void raise_error(engram_status st) { atomicOr(&g_error_word, 1u << (int)st); }
 

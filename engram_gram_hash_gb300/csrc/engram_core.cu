@@ -15,22 +15,18 @@
 #include <map>
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 #include <cstdlib>
 #include <cstring>
 
 #include <cudaTypedefs.h>
 
 #include "common.cuh"
+#include "host.cuh"
 #include "fuse.cuh"
 #include "fuse2.cuh"
 #include "fuse3.cuh"
 #include "layer.cuh"
 #include "narrow.cuh"
-#include "attn_common.cuh"
-#include "qk_rope.cuh"
-#include "attn_rows.cuh"
-#include "attn_tile.cuh"
 
 namespace engram {
 
@@ -889,25 +885,6 @@ __global__ void cache_reset_kernel(int64_t *__restrict__ tags, uint32_t *__restr
 
 // ================================================================ host side ==
 
-// Per-device host caches below are relaxed atomics: host threads that reach a
-// first call together compute and store the same value.
-int num_sms() {
-    static std::atomic<int> sms[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return 148;
-    int n = sms[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        int v = 0;
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        n = v > 0 ? v : 148;
-        sms[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
-}
-
-static bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
 engram_status check_config(const engram_config *cfg) {
     if (!cfg) return ENGRAM_EINVAL;
     if (cfg->vocab < 1 || cfg->rows < 1 || cfg->d_model < 0) return ENGRAM_EINVAL;
@@ -924,31 +901,6 @@ static int64_t row_stride(const engram_config *cfg) { return records(cfg) ? ENGR
 static const float *scales_arg(const engram_config *cfg, const float *scales) { return records(cfg) ? nullptr : scales; }
 static bool scales_ok(const engram_config *cfg, const float *scales) {
     return records(cfg) || (scales && (reinterpret_cast<uintptr_t>(scales) % 4) == 0);
-}
-
-// With ENGRAM_DEBUG set in the environment, failed CUDA calls are reported on
-// stderr with the call site (the status returned is the same either way).
-static engram_status cuda_fail(cudaError_t e, const char *what) {
-    static const bool debug = getenv("ENGRAM_DEBUG") != nullptr;
-    if (debug) fprintf(stderr, "libengram: %s failed: %s\n", what, cudaGetErrorString(e));
-    return ENGRAM_ECUDA;
-}
-
-// Opt a kernel in to `bytes` of dynamic shared memory once per device.
-static engram_status ensure_smem(const void *kern, int bytes, std::atomic<bool> *attr_done) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_relaxed)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(smem)");
-        if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_relaxed);
-    }
-    return ENGRAM_OK;
-}
-
-engram_status launch_status() {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? ENGRAM_OK : cuda_fail(e, "kernel launch");
 }
 
 static void fill_hash_params(HashParams &a, const engram_config *cfg, const int32_t *tokens, const int64_t *offs,
@@ -1079,19 +1031,6 @@ engram_status stage_launch(const uint8_t *host_tables, const float *host_scales,
 
 
 // ----------------------------------------------------------- fuse launcher --
-
-static PFN_cuTensorMapEncodeTiled_v12000 tensormap_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
 
 // 2-D bf16 tensor [outer][inner] (inner contiguous), box [box_outer][box_inner],
 // 128-byte swizzle (a box row of 64 bf16 is one swizzle span) or 64-byte
@@ -1560,10 +1499,9 @@ extern "C" const char *engram_status_string(engram_status st) {
 
 extern "C" engram_status engram_last_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return ENGRAM_ECUDA;
-    unsigned int w = 0;
-    if (cudaMemcpyFromSymbol(&w, g_error_word, sizeof(w)) != cudaSuccess) return ENGRAM_ECUDA;
-    const unsigned int zero = 0;
-    if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess) return ENGRAM_ECUDA;
+    unsigned int w = 0, attention = 0;
+    if (take_error_word(&w) != cudaSuccess || attn::take_error(&attention) != cudaSuccess) return ENGRAM_ECUDA;
+    w |= attention;
     for (int k = 1; k < 32; ++k)
         if (w & (1u << k)) return (engram_status)k;
     return ENGRAM_OK;
@@ -2286,5 +2224,3 @@ extern "C" engram_status engram_forward_no_workspace(const engram_config *cfg, c
     if (s != ENGRAM_OK) return s;
     return fuse_launch(cfg, nullptr, X, W_out, g, h, n_query, st);
 }
-
-#include "attention.cuh"
