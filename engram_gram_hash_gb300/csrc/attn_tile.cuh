@@ -40,6 +40,7 @@ constexpr int ROWS = 2 * MT;          // rows per item
 constexpr int KT = 128;               // keys per tile
 constexpr int NUM_THREADS = 384;
 constexpr int CHUNKS = 128;           // the plan's prefix sums: sequences in this many chunks
+constexpr int P_PARTS = 2;            // a tile's weights are handed over in this many parts
 constexpr int MAX_SPLIT = 152;
 constexpr int SLOTS_PER_SM = 8;       // workspace for partial results
 constexpr float RESCALE_LOG2 = 8.f;
@@ -83,8 +84,7 @@ struct Shared {
     uint64_t kv_empty[Cfg<DP>::STAGES];
     uint64_t q_full[2];
     uint64_t s_full[2];
-    uint64_t p_half[2];   // weights of the first half of the keys
-    uint64_t p_ready[2];  // all weights
+    uint64_t p_ready[2][P_PARTS];
     uint64_t o_full[2];
     uint64_t turn[2];
     uint64_t drained[2];
@@ -383,8 +383,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->q_full[i], 4);
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_half[i], 4);
-            mbar_init(&sh->p_ready[i], 4);
+            for (int c = 0; c < P_PARTS; ++c) mbar_init(&sh->p_ready[i][c], 4);
             mbar_init(&sh->turn[i], 1);
             mbar_init(&sh->drained[i], 1);
             mbar_init(&sh->o_full[i], 1);
@@ -548,11 +547,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             pk[i] = E::pack(x.x, x.y);  // 16-bit operands of the second product
                         }
                         tmem_st_32x32b_x16(s_tm + c * 16, pk);
-                        if (c & 1) {  // half of the weights are there: the second product starts on the first half
+                        if ((c + 1) % (4 / P_PARTS) == 0) {  // the second product may start on these keys
                             tmem_st_wait();
                             tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) mbar_arrive(c == 1 ? &sh->p_half[t] : &sh->p_ready[t]);
+                            if (lane == 0) mbar_arrive(&sh->p_ready[t][c * P_PARTS / 4]);
                         }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
@@ -772,22 +771,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = warp_wait(&sh->kv_full[v], st_ph, abort);
                     advance();
                     ok = ok && (!more || warp_wait(&sh->kv_full[st], st_ph, abort)) &&
-                         warp_wait(&sh->p_half[t], p_ph, abort) && my_turn(both);
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (leader) {
+                         warp_wait(&sh->p_ready[t][0], p_ph, abort) && my_turn(both);
 #pragma unroll
-                        for (int k = 0; k < KT / 32; ++k)
-                            mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                    for (int c = 0; c < P_PARTS; ++c) {
+                        if (c) ok = ok && warp_wait(&sh->p_ready[t][c], p_ph, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = c * (KT / 16 / P_PARTS); k < (c + 1) * (KT / 16 / P_PARTS); ++k)
+                                mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                        }
                     }
-                    ok = warp_wait(&sh->p_ready[t], p_ph, abort);
                     if (!ok) break;
                     p_ph ^= 1;
-                    tc_fence_after();
                     if (leader) {
-#pragma unroll
-                        for (int k = KT / 32; k < KT / 16; ++k)
-                            mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, 1);
                         if (more)
                             scores();
                         else
