@@ -329,6 +329,8 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// The bits x, x + 1, ..., 31 (all for x <= 0, none for x > 31).
+__device__ __forceinline__ uint32_t bits_from(int32_t x) { return x <= 0 ? ~0u : x > 31 ? 0u : ~0u << x; }
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
     asm volatile(
@@ -428,23 +430,30 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t s_ph = 0, o_ph = 0, it = 0;
         bool ok = true;
 
-        // the tile's query rows into shared memory, 16 bytes a lane: rows past the item's are zero
-        const auto load_q = [&](const Item &w) {
-            constexpr int PIECES = DP / 8, PER = 32 / PIECES;  // 16-byte pieces of a row, rows a warp loads at once
-            const int ch = lane % PIECES;
-#pragma unroll 4
-            for (int i = 0; i < 32; i += PER) {
-                const int r = (warp & 3) * 32 + i + lane / PIECES;
-                const int rr = w.r0 + t * MT + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (t * MT + r < w.n_rows && ch * 8 < p.head_dim) {
-                    const int32_t tok = rr / p.group, hh = rr - tok * p.group;
-                    v = *reinterpret_cast<const uint4 *>(p.q + ((int64_t)w.q.row0 + tok) * p.q_token_stride +
-                                                         (int64_t)(w.head * p.group + hh) * p.q_head_stride + ch * 8);
+        // The tile's query rows, 16 bytes a lane and round (rows past the item's are zero): into
+        // registers, all rounds in flight, and from there into shared memory.
+        constexpr int PIECES = DP / 8, PER = 32 / PIECES;  // 16-byte pieces of a row, rows a warp loads at once
+        constexpr int ROUNDS = 32 / PER;
+        const int q_ch = lane % PIECES, q_row = (warp & 3) * 32 + lane / PIECES;
+        const auto load_q = [&](const Item &w, uint4 (&v)[ROUNDS]) {
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int r = t * MT + q_row + i * PER;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (r < w.n_rows && q_ch * 8 < p.head_dim) {
+                    const int32_t tok = (w.r0 + r) / p.group, hh = w.r0 + r - tok * p.group;
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)w.q.row0 + tok) * p.q_token_stride +
+                                                                 (int64_t)(w.head * p.group + hh) * p.q_head_stride + q_ch * 8));
                 }
-                const uint32_t dst = smem_u32(q_smem) + t * C::Q_BYTES + (ch >> 3) * (MT * 128) + r * 128 +
-                                     (((ch & 7) ^ (r & 7)) << 4);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+            }
+        };
+        const auto store_q = [&](const uint4 (&v)[ROUNDS]) {
+            const uint32_t base_row = smem_u32(q_smem) + t * C::Q_BYTES + (q_ch >> 3) * (MT * 128);
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int r = q_row + i * PER;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base_row + r * 128 + (((q_ch & 7) ^ (r & 7)) << 4)),
+                             "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
                              : "memory");
             }
             fence_proxy_async_smem();
@@ -453,7 +462,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         };
 
         const Item *w = take(0);
-        if (w && w->n > 0 && w->n_rows > t * MT) load_q(*w);
+        if (w && w->n > 0 && w->n_rows > t * MT) {
+            uint4 v[ROUNDS];
+            load_q(*w, v);
+            store_q(v);
+        }
         for (uint32_t k = 0; w && w->n_rows > 0 && ok; ++k) {
             const bool mine = w->n_rows > t * MT;
             const int32_t n = w->n;
@@ -489,8 +502,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int i = h * 64; i < h * 64 + 64; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
                         if (edge) {
 #pragma unroll
-                            for (int i = h * 64; i < h * 64 + 64; ++i)
-                                if (i < a || i > b) s[i] = -INFINITY;
+                            for (int c = h * 2; c < h * 2 + 2; ++c) {
+                                const uint32_t in = bits_from(a - c * 32) & ~bits_from(b - c * 32 + 1);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(in & (1u << i))) s[c * 32 + i] = -INFINITY;
+                            }
                         }
 #pragma unroll
                         for (int i = h * 64; i < h * 64 + 64; i += 2)
@@ -557,14 +574,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 }
                 if (!ok) break;
+            }
+            it += 2 * n;
+            if (mine && n > 0) {
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
             }
-            it += 2 * n;
             // the next item's queries first, so that its scores are computed under this item's epilogue
             const Item *const next = take(k + 1);
-            if (next && next->n > 0 && next->n_rows > t * MT) load_q(*next);
+            if (next && next->n > 0 && next->n_rows > t * MT) {
+                uint4 v[ROUNDS];
+                load_q(*next, v);
+                store_q(v);
+            }
             if (mine) {
                 const bool whole = w->splits == 1, live = t * MT + row < w->n_rows;
                 const int64_t slot = whole ? 0 : w->slot;
@@ -622,22 +645,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 10) {  // --------------------------------------------- items
-            if (lane == 0) {
-                uint32_t i = 0;
-                // Rounds of one item per CTA, every other one in reverse: the items come longest first,
-                // and the CTAs at one end would get the longer one of every round.
-                for (;; ++i) {
-                    const int64_t index = (int64_t)i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                    if (i >= ITEMS && !mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort)) break;
-                    if (index < n_items)
-                        sh->items[i % ITEMS] = find_item(p, base, &sh->plan, index);
-                    else
-                        sh->items[i % ITEMS].n_rows = 0;
-                    mbar_arrive(&sh->item_full[i % ITEMS]);
-                    if (index >= n_items) break;
+            // Rounds of one item per CTA, every other one in reverse: the items come longest first, and
+            // the CTAs at one end would get the longer one of every round.  A lane finds one of the
+            // next 32 items (several divisions each), then they are handed out in order.
+            bool ok = true, more = true;
+            for (uint32_t i0 = 0; ok && more; i0 += 32) {
+                const uint32_t i = i0 + lane;
+                const int64_t index = (int64_t)i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item mine;
+                mine.n_rows = 0;
+                if (index < n_items) mine = find_item(p, base, &sh->plan, index);
+                for (int k = 0; ok && more && k < 32; ++k) {
+                    if (lane == k) {
+                        if (i >= ITEMS) ok = mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort);
+                        if (ok) {
+                            sh->items[i % ITEMS] = mine;
+                            mbar_arrive(&sh->item_full[i % ITEMS]);
+                        }
+                        more = mine.n_rows != 0;
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, k);
+                    more = __shfl_sync(0xffffffffu, more, k);
                 }
             }
-            __syncwarp();
         } else if (warp == 9) {  // --------------------------------------- K, V loads
             const int boxes = KT / p.box;
             const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64);
