@@ -173,6 +173,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.n_heads = cfg->n_heads;
     p.n_kv_heads = cfg->n_kv_heads;
     p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.by_group = Divisor(p.group);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, rows::KT);
@@ -235,6 +236,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.n_heads = cfg->n_heads;
     p.n_kv_heads = cfg->n_kv_heads;
     p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.by_group = Divisor(p.group);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, tile::KT);

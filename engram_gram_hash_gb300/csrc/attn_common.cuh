@@ -34,6 +34,22 @@ struct Fp16 {
     }
 };
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a multiplication (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", 1994):
+// with 2^l >= d and m = floor(2^(31+l) / d) + 1, m d - 2^(31+l) <= 2^l, so
+// floor(n m / 2^(31+l)) = floor(n / d).
+struct Divisor {
+    uint32_t d, m, l;
+    Divisor() = default;
+    explicit Divisor(uint32_t d_) : d(d_), l(0) {
+        while ((1u << l) < d) ++l;
+        m = (uint32_t)((UINT64_C(1) << (31 + l)) / d + 1);
+    }
+    __device__ __forceinline__ int32_t quotient(int32_t n) const {
+        return d == 1 ? n : (int32_t)(__umulhi((uint32_t)n, m) >> (l - 1));
+    }
+};
+
 // engram_kv_batch with the cache's page geometry.
 struct Batch {
     const int64_t *offs;

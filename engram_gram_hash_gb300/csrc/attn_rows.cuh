@@ -74,6 +74,7 @@ struct Params {
     float *part_o;      // [grid][2][ROWS][DP]
     float *part_ml;     // [grid][2][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
+    Divisor by_group;
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t runs;       // CTAs of the attention launch
@@ -203,7 +204,7 @@ __device__ __forceinline__ Segment segment(const Params &p, const Walk &w) {
     const int32_t left = w.q.q_len * p.group - g.r0;
     g.n_rows = left < ROWS ? left : ROWS;
     g.pos0 = w.q.kv - w.q.q_len;
-    const int32_t first = g.pos0 + g.r0 / p.group, last = g.pos0 + (g.r0 + g.n_rows - 1) / p.group;
+    const int32_t first = g.pos0 + p.by_group.quotient(g.r0), last = g.pos0 + p.by_group.quotient(g.r0 + g.n_rows - 1);
     g.hi = last + 1;  // <= kv
     g.full_hi = first + 1;
     g.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 const int r = qr + i * 8;
                 const bool live = r < g.n_rows;
-                const int32_t tok = (g.r0 + r) / p.group, hh = (g.r0 + r) - tok * p.group;
+                const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
                 const int32_t pos = g.pos0 + tok;
                 row_hi[i] = live ? pos : -1;
                 row_lo[i] = p.window > 0 ? pos - p.window + 1 : 0;
@@ -536,7 +537,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 row_total(sh, r, mm, ll);
                 const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
                 if (c < p.head_dim) {
-                    const int32_t tok = (g.r0 + r) / p.group, hh = (g.r0 + r) - tok * p.group;
+                    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
                     uint16_t *dst = p.out + (int64_t)w_row(walk, tok) * p.out_token_stride +
                                     (int64_t)(g.head * p.group + hh) * p.out_head_stride + c;
                     *reinterpret_cast<uint2 *>(dst) = make_uint2(E::pack(v.x * inv, v.y * inv), E::pack(v.z * inv, v.w * inv));
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     p.part_ml[slot * (2 * ROWS) + r] = mm;
                     p.part_ml[slot * (2 * ROWS) + ROWS + r] = ll;
                 } else if (p.lse) {
-                    const int32_t tok = (g.r0 + r) / p.group, hh = (g.r0 + r) - tok * p.group;
+                    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
                     p.lse[(int64_t)w_row(walk, tok) * p.n_heads + g.head * p.group + hh] = lse_of(mm, ll);
                 }
             }
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-    const int32_t tok = (g.r0 + r) / p.group, hh = (g.r0 + r) - tok * p.group, head = g.head * p.group + hh;
+    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group, head = g.head * p.group + hh;
     const int64_t row = w_row(w, tok);
     if (lane * 4 < p.head_dim)
         *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + head * p.out_head_stride + lane * 4) =

@@ -112,6 +112,7 @@ struct Params {
     float *part_o;      // [slots][ROWS][DP]
     float *part_ml;     // [slots][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
+    Divisor by_group;
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t ctas;
@@ -255,7 +256,7 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int64_t seg) {
     const int32_t left = it.q.q_len * p.group - it.r0;
     it.n_rows = left < ROWS ? left : ROWS;
     it.pos0 = it.q.kv - it.q.q_len;
-    const int32_t first = it.pos0 + it.r0 / p.group, last = it.pos0 + (it.r0 + it.n_rows - 1) / p.group;
+    const int32_t first = it.pos0 + p.by_group.quotient(it.r0), last = it.pos0 + p.by_group.quotient(it.r0 + it.n_rows - 1);
     it.hi = last + 1 > 0 ? last + 1 : 0;
     it.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
     const int32_t t0 = it.lo / KT, nt = it.hi > it.lo ? (it.hi + KT - 1) / KT - t0 : 0;
@@ -436,15 +437,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         constexpr int ROUNDS = 32 / PER;
         const int q_ch = lane % PIECES, q_row = (warp & 3) * 32 + lane / PIECES;
         const auto load_q = [&](const Item &w, uint4 (&v)[ROUNDS]) {
+            const int32_t rr = w.r0 + t * MT + row, tok = p.by_group.quotient(rr), n_rows = w.n_rows;
+            const int64_t mine = ((int64_t)w.q.row0 + tok) * p.q_token_stride +
+                                 (int64_t)(w.head * p.group + rr - tok * p.group) * p.q_head_stride;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                const int r = t * MT + q_row + i * PER;
+                const int r = q_row + i * PER;
+                const int64_t at = __shfl_sync(0xffffffffu, mine, r & 31);
                 v[i] = make_uint4(0, 0, 0, 0);
-                if (r < w.n_rows && q_ch * 8 < p.head_dim) {
-                    const int32_t tok = (w.r0 + r) / p.group, hh = w.r0 + r - tok * p.group;
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + ((int64_t)w.q.row0 + tok) * p.q_token_stride +
-                                                                 (int64_t)(w.head * p.group + hh) * p.q_head_stride + q_ch * 8));
-                }
+                if (t * MT + r < n_rows && q_ch * 8 < p.head_dim)
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + at + q_ch * 8));
             }
         };
         const auto store_q = [&](const uint4 (&v)[ROUNDS]) {
@@ -473,12 +475,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
             if (mine && n > 0) {
                 const int32_t tile0 = w->tile0, lo = w->lo, hi = w->hi;
-                const int32_t pos = w->pos0 + (w->r0 + t * MT + row) / p.group;
+                const int32_t pos = w->pos0 + p.by_group.quotient(w->r0 + t * MT + row);
                 const int32_t row_lo = p.window > 0 ? pos - p.window + 1 : 0;
                 // keys in reach of every row of the tile
                 const int32_t last = (w->n_rows < (t + 1) * MT ? w->n_rows : (t + 1) * MT) - 1;
-                const int32_t full_hi = w->pos0 + (w->r0 + t * MT) / p.group + 1;
-                const int32_t full_lo = p.window > 0 ? w->pos0 + (w->r0 + last) / p.group - p.window + 1 : 0;
+                const int32_t full_hi = w->pos0 + p.by_group.quotient(w->r0 + t * MT) + 1;
+                const int32_t full_lo = p.window > 0 ? w->pos0 + p.by_group.quotient(w->r0 + last) - p.window + 1 : 0;
                 for (int32_t j = 0; j < n; ++j) {
                     const int32_t key0 = (tile0 + j) * KT;
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
@@ -581,21 +583,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (!ok) break;
                 tc_fence_after();
             }
-            // the next item's queries first, so that its scores are computed under this item's epilogue
-            const Item *const next = take(k + 1);
-            if (next && next->n > 0 && next->n_rows > t * MT) {
-                uint4 v[ROUNDS];
-                load_q(*next, v);
-                store_q(v);
-            }
+            // The item's rows leave through the query tile's shared memory (every product on it is done;
+            // each warp uses its own 32 rows): a thread holds a whole row, and its 16-byte stores
+            // alone would touch a line each.
             if (mine) {
                 const bool whole = w->splits == 1, live = t * MT + row < w->n_rows;
                 const int64_t slot = whole ? 0 : w->slot;
-                const int32_t rr = w->r0 + t * MT + row, tok = rr / p.group, head = w->head * p.group + rr - tok * p.group;
+                const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
                 const int64_t out_row = (int64_t)w->q.row0 + tok;
                 const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-                uint16_t *dst = p.out + out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
+                const int64_t dst = out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
                 float *part = p.part_o + (slot * ROWS + t * MT + row) * DP;
+                const uint32_t stage = smem_u32(q_smem) + t * C::Q_BYTES;
 #pragma unroll
                 for (int c = 0; c < DP / 32; ++c) {
                     uint32_t o[32];
@@ -606,25 +605,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
-                    if (live) {
-                        if (whole) {
+                    if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if (c * 32 + i * 8 < p.head_dim) {
-                                    uint32_t u[4];
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = c * 4 + i;  // 16-byte piece of the row
+                            uint32_t u[4];
 #pragma unroll
-                                    for (int h = 0; h < 4; ++h)
-                                        u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv,
-                                                       __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
-                                    *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(u[0], u[1], u[2], u[3]);
-                                }
-                            }
-                        } else if (n > 0) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4 *>(part + c * 32 + i * 4) =
-                                    make_uint4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
+                            for (int h = 0; h < 4; ++h)
+                                u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv, __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                             stage + (ch >> 3) * (MT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
+                                         "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
+                                         : "memory");
                         }
+                    } else if (live && n > 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(part + c * 32 + i * 4) =
+                                make_uint4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
                     }
                 }
                 tc_fence_before();  // O has been read before the next item's first product is allowed
@@ -637,6 +635,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         p.lse[out_row * p.n_heads + head] = rows::lse_of(m2, l);
                     }
                 }
+                if (whole) {
+                    const int32_t n_rows = w->n_rows;
+                    __syncwarp();
+#pragma unroll 4
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        const int r = q_row + i * PER;
+                        const int64_t at = __shfl_sync(0xffffffffu, dst, r & 31);
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(stage + (q_ch >> 3) * (MT * 128) + r * 128 + (((q_ch & 7) ^ (r & 7)) << 4))
+                                     : "memory");
+                        if (t * MT + r < n_rows && q_ch * 8 < p.head_dim) *reinterpret_cast<uint4 *>(p.out + at + q_ch * 8) = v;
+                    }
+                    __syncwarp();
+                }
+            }
+            const Item *const next = take(k + 1);
+            if (next && next->n > 0 && next->n_rows > t * MT) {
+                uint4 v[ROUNDS];
+                load_q(*next, v);
+                store_q(v);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->item_empty[k % ITEMS]);
@@ -648,6 +668,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // Rounds of one item per CTA, every other one in reverse: the items come longest first, and
             // the CTAs at one end would get the longer one of every round.  A lane finds one of the
             // next 32 items (several divisions each), then they are handed out in order.
+            const auto prefetch_q = [&](const Item &w) {  // an item's queries on their way into L2
+                const int64_t row0 = w.q.row0;
+                const int32_t r0 = w.r0, n_rows = w.n > 0 ? w.n_rows : 0, head0 = w.head * p.group;
+                for (int r = lane; r < n_rows; r += 32) {
+                    const int32_t tok = p.by_group.quotient(r0 + r), hh = r0 + r - tok * p.group;
+                    const uint16_t *q = p.q + (row0 + tok) * p.q_token_stride + (int64_t)(head0 + hh) * p.q_head_stride;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                    if (p.head_dim > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+                }
+            };
             bool ok = true, more = true;
             for (uint32_t i0 = 0; ok && more; i0 += 32) {
                 const uint32_t i = i0 + lane;
@@ -666,6 +696,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                     ok = __shfl_sync(0xffffffffu, ok, k);
                     more = __shfl_sync(0xffffffffu, more, k);
+                    if (ok && more) prefetch_q(sh->items[(i0 + k) % ITEMS]);
                 }
             }
         } else if (warp == 9) {  // --------------------------------------- K, V loads
@@ -906,7 +937,7 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-            const int32_t tok = (it.r0 + r) / p.group, hh = (it.r0 + r) - tok * p.group, head = it.head * p.group + hh;
+            const int32_t tok = p.by_group.quotient(it.r0 + r), hh = (it.r0 + r) - tok * p.group, head = it.head * p.group + hh;
             const int64_t row = (int64_t)it.q.row0 + tok;
             if (lane * 4 < p.head_dim)
                 *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + (int64_t)head * p.out_head_stride + lane * 4) =
