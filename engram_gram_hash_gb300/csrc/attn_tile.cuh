@@ -431,33 +431,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t s_ph = 0, o_ph = 0, it = 0;
         bool ok = true;
 
-        // The tile's query rows, 16 bytes a lane and round (rows past the item's are zero): into
-        // registers, all rounds in flight, and from there into shared memory.
+        // The tile's query rows into shared memory by asynchronous copies, 16 bytes a lane and round
+        // (rows past the item's are zero): fetch_q starts them, hand_q waits for them and tells the
+        // MMA warp.
         constexpr int PIECES = DP / 8, PER = 32 / PIECES;  // 16-byte pieces of a row, rows a warp loads at once
-        constexpr int ROUNDS = 32 / PER;
-        const int q_ch = lane % PIECES, q_row = (warp & 3) * 32 + lane / PIECES;
-        const auto load_q = [&](const Item &w, uint4 (&v)[ROUNDS]) {
+        const auto fetch_q = [&](const Item &w) {
+            const int ch = lane % PIECES;
             const int32_t rr = w.r0 + t * MT + row, tok = p.by_group.quotient(rr), n_rows = w.n_rows;
             const int64_t mine = ((int64_t)w.q.row0 + tok) * p.q_token_stride +
                                  (int64_t)(w.head * p.group + rr - tok * p.group) * p.q_head_stride;
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int r = q_row + i * PER;
+            const uint32_t dst = smem_u32(q_smem) + t * C::Q_BYTES + (ch >> 3) * (MT * 128);
+#pragma unroll 4
+            for (int i = 0; i < 32; i += PER) {
+                const int r = (warp & 3) * 32 + i + lane / PIECES;
                 const int64_t at = __shfl_sync(0xffffffffu, mine, r & 31);
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (t * MT + r < n_rows && q_ch * 8 < p.head_dim)
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + at + q_ch * 8));
-            }
-        };
-        const auto store_q = [&](const uint4 (&v)[ROUNDS]) {
-            const uint32_t base_row = smem_u32(q_smem) + t * C::Q_BYTES + (q_ch >> 3) * (MT * 128);
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int r = q_row + i * PER;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base_row + r * 128 + (((q_ch & 7) ^ (r & 7)) << 4)),
-                             "r"(v[i].x), "r"(v[i].y), "r"(v[i].z), "r"(v[i].w)
+                const bool in = t * MT + r < n_rows && ch * 8 < p.head_dim;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                             "l"(p.q + (in ? at + ch * 8 : 0)), "r"(in ? 16 : 0)
                              : "memory");
             }
+        };
+        const auto hand_q = [&] {
+            asm volatile("cp.async.wait_all;" ::: "memory");
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->q_full[t]);
@@ -465,13 +460,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
         const Item *w = take(0);
         if (w && w->n > 0 && w->n_rows > t * MT) {
-            uint4 v[ROUNDS];
-            load_q(*w, v);
-            store_q(v);
+            fetch_q(*w);
+            hand_q();
         }
         for (uint32_t k = 0; w && w->n_rows > 0 && ok; ++k) {
             const bool mine = w->n_rows > t * MT;
             const int32_t n = w->n;
+            const Item *next = nullptr;
+            bool next_mine = false;
             float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
             if (mine && n > 0) {
                 const int32_t tile0 = w->tile0, lo = w->lo, hi = w->hi;
@@ -486,6 +482,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
+                    if (j + 1 == n) {
+                        // The last scores are there, so the queries' memory is free: the next item's are
+                        // fetched now, and its scores computed under this item's epilogue.
+                        next = take(k + 1);
+                        next_mine = next && next->n > 0 && next->n_rows > t * MT;
+                        if (next_mine) fetch_q(*next);
+                    }
                     // the second half of the scores arrives under the first half's maximum
                     uint32_t raw[4][32];
                     tmem_ld_32x32b_x32(s_tm, raw[0]);
@@ -579,22 +582,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             it += 2 * n;
             if (mine && n > 0) {
+                if (next_mine) hand_q();
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
+            } else {
+                next = take(k + 1);
+                if (next && next->n > 0 && next->n_rows > t * MT) {
+                    fetch_q(*next);
+                    hand_q();
+                }
             }
-            // The item's rows leave through the query tile's shared memory (every product on it is done;
-            // each warp uses its own 32 rows): a thread holds a whole row, and its 16-byte stores
-            // alone would touch a line each.
             if (mine) {
                 const bool whole = w->splits == 1, live = t * MT + row < w->n_rows;
                 const int64_t slot = whole ? 0 : w->slot;
                 const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
                 const int64_t out_row = (int64_t)w->q.row0 + tok;
                 const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-                const int64_t dst = out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
+                uint16_t *dst = p.out + out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
                 float *part = p.part_o + (slot * ROWS + t * MT + row) * DP;
-                const uint32_t stage = smem_u32(q_smem) + t * C::Q_BYTES;
 #pragma unroll
                 for (int c = 0; c < DP / 32; ++c) {
                     uint32_t o[32];
@@ -605,20 +611,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
+                    if (!live) continue;
                     if (whole) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int ch = c * 4 + i;  // 16-byte piece of the row
-                            uint32_t u[4];
+                        for (int i = 0; i < 4; ++i)
+                            if (c * 32 + i * 8 < p.head_dim) {
+                                uint32_t u[4];
 #pragma unroll
-                            for (int h = 0; h < 4; ++h)
-                                u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv, __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
-                            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                             stage + (ch >> 3) * (MT * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)),
-                                         "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
-                                         : "memory");
-                        }
-                    } else if (live && n > 0) {
+                                for (int h = 0; h < 4; ++h)
+                                    u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv, __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
+                                *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(u[0], u[1], u[2], u[3]);
+                            }
+                    } else if (n > 0) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             *reinterpret_cast<uint4 *>(part + c * 32 + i * 4) =
@@ -635,28 +639,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         p.lse[out_row * p.n_heads + head] = rows::lse_of(m2, l);
                     }
                 }
-                if (whole) {
-                    const int32_t n_rows = w->n_rows;
-                    __syncwarp();
-#pragma unroll 4
-                    for (int i = 0; i < ROUNDS; ++i) {
-                        const int r = q_row + i * PER;
-                        const int64_t at = __shfl_sync(0xffffffffu, dst, r & 31);
-                        uint4 v;
-                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(stage + (q_ch >> 3) * (MT * 128) + r * 128 + (((q_ch & 7) ^ (r & 7)) << 4))
-                                     : "memory");
-                        if (t * MT + r < n_rows && q_ch * 8 < p.head_dim) *reinterpret_cast<uint4 *>(p.out + at + q_ch * 8) = v;
-                    }
-                    __syncwarp();
-                }
-            }
-            const Item *const next = take(k + 1);
-            if (next && next->n > 0 && next->n_rows > t * MT) {
-                uint4 v[ROUNDS];
-                load_q(*next, v);
-                store_q(v);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh->item_empty[k % ITEMS]);
