@@ -696,7 +696,9 @@ def make_attn_config(n_heads, n_kv_heads, head_dim, dtype=torch.bfloat16, rope_d
     c.norm_eps = float(norm_eps)
     c.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
     c.window = int(window)
-    c.torch_dtype = dtype
+    # what the calls below look at on every step, as plain Python values
+    c.torch_dtype, c.dim, c.q_heads, c.kv_heads, c.rope = dtype, c.head_dim, c.n_heads, c.n_kv_heads, c.rope_dim
+    c.ref = ctypes.byref(c)
     return c
 
 
@@ -727,6 +729,7 @@ def kv_cache(k_pages, v_pages):
     c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
     c.tensors = (k_pages, v_pages)
     c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), k_pages.dtype
+    c.ref = ctypes.byref(c)
     return c
 
 
@@ -750,71 +753,88 @@ def kv_batch(seq_offsets, kv_len, block_table, n_query):
     b.seq_offsets, b.kv_len, b.block_table = seq_offsets.data_ptr(), kv_len.data_ptr(), block_table.data_ptr()
     b.table_stride = block_table.shape[1] if n <= 1 else block_table.stride(0)
     b.tensors = (seq_offsets, kv_len, block_table)
+    b.ref = ctypes.byref(b)
     return b
 
 
-def _heads(t, cfg, tokens, heads, name):
+def _heads(t, cfg, shape, name):
     """The engram_heads of a [tokens, heads, head_dim] tensor with contiguous heads."""
     if t.dtype is not cfg.torch_dtype:
         raise TypeError(f"{name} must be {cfg.torch_dtype}, got {t.dtype}")
-    if t.shape != (tokens, heads, cfg.head_dim):
-        raise ValueError(f"{name} must be {[tokens, heads, cfg.head_dim]}, got {list(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     st, sh, sc = t.stride()
-    if sc != 1 and cfg.head_dim > 1 or not t.is_cuda:
+    if sc != 1 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor with contiguous heads")
     # the stride of a size of one is never used, and torch may give it any value
-    return engram_heads(t.data_ptr(), st if tokens > 1 else 0, sh if heads > 1 else 0)
+    return ctypes.byref(engram_heads(t.data_ptr(), st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0))
+
+
+def _heads_out(out, like, cfg, shape, name):
+    """(the output tensor, its engram_heads): a new contiguous one if none is given."""
+    if out is not None:
+        return out, _heads(out, cfg, shape, name)
+    out = torch.empty(shape, dtype=cfg.torch_dtype, device=like.device)
+    return out, ctypes.byref(engram_heads(out.data_ptr(), shape[1] * shape[2], shape[2]))
 
 
 def _weight(w, cfg, name):
     if w is None:
         return None
-    _need(w, cfg.torch_dtype, name)
-    if w.numel() != cfg.head_dim:
-        raise ValueError(f"{name} must have {cfg.head_dim} values")
+    if w.dtype is not cfg.torch_dtype:
+        raise TypeError(f"{name} must be {cfg.torch_dtype}, got {w.dtype}")
+    if w.numel() != cfg.dim or not w.is_contiguous() or not w.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {cfg.dim} values")
     return w.data_ptr()
 
 
 def _table(table, cfg):
     if table is None:
-        if cfg.rope_dim:
+        if cfg.rope:
             raise ValueError("table is needed: rope_dim is not 0")
         return None, 0
-    _need(table, torch.float32, "table")
-    if table.dim() != 2 or table.shape[1] != cfg.rope_dim:
-        raise ValueError(f"table must be [positions, {cfg.rope_dim}]")
+    if table.dtype is not torch.float32:
+        raise TypeError(f"table must be torch.float32, got {table.dtype}")
+    if table.dim() != 2 or table.shape[1] != cfg.rope or not table.is_contiguous() or not table.is_cuda:
+        raise ValueError(f"table must be a contiguous CUDA tensor [positions, {cfg.rope}]")
     return table.data_ptr(), table.shape[0]
 
 
 def _cache_of(cache, cfg):
-    if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
-        raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.n_kv_heads, cfg.head_dim]}")
-    return ctypes.byref(cache)
+    if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.kv_heads, cfg.dim):
+        raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.kv_heads, cfg.dim]}")
+    return cache.ref
+
+
+def _stream_of(t, stream):
+    """The handle of `stream`, or of the current stream on t's device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def engram_qk_norm_rope(cfg, q, k, positions, table, w_q=None, w_k=None, q_out=None, k_out=None, stream=None):
     """(q_out, k_out): every head of q [T, n_heads, D] and k [T, n_kv_heads, D] RMS-normed (with w_q / w_k
     [D]; None: no norm) and rotated by its token's position.  Either of q and k may be None; q_out=q and
     k_out=k work in place."""
-    T = q.shape[0] if q is not None else k.shape[0]
-    hq = hk = ho = hko = None
+    some = q if q is not None else k
+    T = some.shape[0]
+    hq = hk = ho = hko = pos = None
     if q is not None:
-        hq = _heads(q, cfg, T, cfg.n_heads, "q")
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        ho = ctypes.byref(_heads(q_out, cfg, T, cfg.n_heads, "q_out"))
-        hq = ctypes.byref(hq)
+        shape = (T, cfg.q_heads, cfg.dim)
+        hq = _heads(q, cfg, shape, "q")
+        q_out, ho = _heads_out(q_out, q, cfg, shape, "q_out")
     if k is not None:
-        hk = ctypes.byref(_heads(k, cfg, T, cfg.n_kv_heads, "k"))
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        hko = ctypes.byref(_heads(k_out, cfg, T, cfg.n_kv_heads, "k_out"))
+        shape = (T, cfg.kv_heads, cfg.dim)
+        hk = _heads(k, cfg, shape, "k")
+        k_out, hko = _heads_out(k_out, k, cfg, shape, "k_out")
     if positions is not None:
         _need(positions, torch.int32, "positions")
         if positions.numel() != T:
             raise ValueError(f"positions must have {T} entries")
+        pos = positions.data_ptr()
     tab, rows = _table(table, cfg)
     _check(
-        lib().engram_qk_norm_rope(ctypes.byref(cfg), T, hq, hk, _ptr(positions), tab, rows, _weight(w_q, cfg, "w_q"),
-                                  _weight(w_k, cfg, "w_k"), ho, hko, _stream(stream)),
+        lib().engram_qk_norm_rope(cfg.ref, T, hq, hk, pos, tab, rows, _weight(w_q, cfg, "w_q"),
+                                  _weight(w_k, cfg, "w_k"), ho, hko, _stream_of(some, stream)),
         "engram_qk_norm_rope",
     )
     return q_out, k_out
@@ -824,18 +844,18 @@ def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None,
     """The step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] into their slots of the cache.
     With q [n_query, n_heads, D], also its norm and rotation in the same launch; returns q_out (None without)."""
     T = batch.n_query
-    hk = ctypes.byref(_heads(k, cfg, T, cfg.n_kv_heads, "k"))
-    hv = ctypes.byref(_heads(v, cfg, T, cfg.n_kv_heads, "v"))
+    shape = (T, cfg.kv_heads, cfg.dim)
+    hk = _heads(k, cfg, shape, "k")
+    hv = _heads(v, cfg, shape, "v")
     hq = ho = None
     if q is not None:
-        hq = ctypes.byref(_heads(q, cfg, T, cfg.n_heads, "q"))
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        ho = ctypes.byref(_heads(q_out, cfg, T, cfg.n_heads, "q_out"))
+        shape = (T, cfg.q_heads, cfg.dim)
+        hq = _heads(q, cfg, shape, "q")
+        q_out, ho = _heads_out(q_out, q, cfg, shape, "q_out")
     tab, rows = _table(table, cfg)
     _check(
-        lib().engram_kv_append(ctypes.byref(cfg), _cache_of(cache, cfg), ctypes.byref(batch), hk, hv,
-                               _weight(w_k, cfg, "w_k"), tab, rows, hq, _weight(w_q, cfg, "w_q"), ho,
-                               _stream(stream)),
+        lib().engram_kv_append(cfg.ref, _cache_of(cache, cfg), batch.ref, hk, hv, _weight(w_k, cfg, "w_k"), tab, rows,
+                               hq, _weight(w_q, cfg, "w_q"), ho, _stream_of(k, stream)),
         "engram_kv_append",
     )
     return q_out if q is not None else None
@@ -849,23 +869,24 @@ def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=N
     """out [n_query, n_heads, D]: attention of the step's tokens over the paged cache (and lse fp32
     [n_query, n_heads] if a tensor for it is given)."""
     T = batch.n_query
-    hq = _heads(q, cfg, T, cfg.n_heads, "q")
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    ho = _heads(out, cfg, T, cfg.n_heads, "out")
+    shape = (T, cfg.q_heads, cfg.dim)
+    hq = _heads(q, cfg, shape, "q")
+    out, ho = _heads_out(out, q, cfg, shape, "out")
     if lse is not None:
         _need(lse, torch.float32, "lse")
-        if lse.shape != (T, cfg.n_heads):
-            raise ValueError(f"lse must be {[T, cfg.n_heads]}")
+        if lse.shape != shape[:2]:
+            raise ValueError(f"lse must be {list(shape[:2])}")
+    L = lib()
     if workspace is None:
-        need = lib().engram_paged_attention_workspace_bytes(ctypes.byref(cfg), batch.n_seqs, T)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        need = L.engram_paged_attention_workspace_bytes(cfg.ref, batch.n_seqs, T)
+        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
     else:
         _need(workspace, torch.uint8, "workspace")
+        need = workspace.numel()
     _check(
-        lib().engram_paged_attention(ctypes.byref(cfg), _cache_of(cache, cfg), ctypes.byref(batch), ctypes.byref(hq),
-                                     ctypes.byref(ho), lse.data_ptr() if lse is not None else None,
-                                     workspace.data_ptr(), workspace.numel(), _stream(stream)),
+        L.engram_paged_attention(cfg.ref, _cache_of(cache, cfg), batch.ref, hq, ho,
+                                 lse.data_ptr() if lse is not None else None, workspace.data_ptr(), need,
+                                 _stream_of(q, stream)),
         "engram_paged_attention",
     )
     return out

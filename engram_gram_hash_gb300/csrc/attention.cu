@@ -154,6 +154,20 @@ static size_t rows_workspace_bytes(const engram_attn_config *cfg) {
     return rows_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
 }
 
+// Whether segments stay whole (their tiles at most, by the block table's room): a cut one costs the
+// join, about 7 us a call, a whole one about 0.55 us a tile of 64 keys on its one SM.  32 heads of 128
+// (8 key/value heads), us whole / cut: 1 sequence of 500 tokens 11.0 / 11.8, 1,000: 15.8 / 13.4;
+// 16 sequences (about one segment an SM) of 500: 11.5 / 19.5, 2,000: 27.7 / 35.2; 64 sequences of
+// 500: 35.7 / 43.0, 1,000: 55.2 / 60.9, but there unequal lengths would wait for the longest.
+static int32_t rows_whole(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const int64_t tiles = (batch->table_stride * cache->page_size + rows::KT - 1) / rows::KT;
+    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
+    const int64_t segs = cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
+                                                    (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);  // at most
+    if (tiles <= 8 || (tiles <= 32 && segs * 2 >= num_sms() && segs <= num_sms())) return (int32_t)tiles;
+    return 0;
+}
+
 template <typename E, int DP>
 static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_cache *cache,
                                  const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
@@ -178,6 +192,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.window = cfg->window;
     p.box = gcd(cache->page_size, rows::KT);
     p.runs = num_sms();
+    p.whole = rows_whole(cfg, cache, batch);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     CUtensorMap km, vm;
     if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
@@ -187,7 +202,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.runs), rows::NUM_THREADS, smem, st, "rows_kernel", km, vm, p);
-    if (s != ENGRAM_OK || p.runs == 1) return s;
+    if (s != ENGRAM_OK || p.runs == 1 || p.whole > 0) return s;
     return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, st, "rows_join_kernel", p);
 }
 

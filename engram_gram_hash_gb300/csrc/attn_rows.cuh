@@ -31,7 +31,6 @@ constexpr int ROWS = 16;            // query rows per segment
 constexpr int KT = 64;              // keys per tile
 constexpr int CONSUMERS = 8;        // two groups of four warps
 constexpr int NUM_THREADS = 32 * (CONSUMERS + 1);
-constexpr int MIN_TILES = 1;        // tiles per CTA at least
 
 template <int DP>
 struct Cfg {
@@ -78,6 +77,7 @@ struct Params {
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t runs;       // CTAs of the attention launch
+    int32_t whole;      // > 0: every segment is given this many tiles and none is cut (no join follows)
     float scale_log2;   // scale * log2(e)
 };
 
@@ -86,6 +86,7 @@ struct Params {
 // Key tiles that a segment of sequence q is given on the line (at least one,
 // so that rows without keys are written too), and its segments per kv head.
 __device__ __forceinline__ int32_t seg_tiles(const Params &p, const Seq &q) {
+    if (p.whole > 0) return p.whole;
     int32_t n = (q.kv + KT - 1) / KT;
     if (p.window > 0) {
         const int32_t tokens = (ROWS - 2) / p.group + 2;  // most tokens that 16 consecutive rows touch
@@ -135,7 +136,8 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
         r.total += scan[w];
     }
     r.run = (r.total + p.runs - 1) / p.runs;
-    if (r.run < MIN_TILES) r.run = MIN_TILES;
+    if (p.whole > 0) r.run = (r.run + p.whole - 1) / p.whole * p.whole;
+    if (r.run < 1) r.run = 1;
     const int64_t f = index * r.run;
     if (f >= before && f < before + sum) {
         int64_t at = before;
@@ -568,11 +570,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <typename E, int DP>
 __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ Params p) {
     __shared__ int64_t scan[4], find_s, find_before;
-    grid_dependency_wait();
-    allow_dependent_launch();
+    // The plan reads the batch only, which was final before the attention kernel let this one start
+    // (it does so after its own wait); the partial results need the wait below.
     const int64_t base = __ldg(p.b.offs);
     const int64_t cut = (int64_t)blockIdx.x + 1;
     const Plan plan = plan_find<128>(p, base, cut, scan, &find_s, &find_before);
+    grid_dependency_wait();
+    allow_dependent_launch();
     const int64_t f = cut * plan.run;
     if (f >= plan.total) return;
     Walk w;
