@@ -100,11 +100,10 @@ static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, in
 
 template <typename E, int LPH, int U, bool APPEND>
 static engram_status head_launch_u(const engram_attn_config *cfg, HeadParams &p, cudaStream_t st) {
-    const int heads = p.n_q + p.n_k + p.n_v, per = 32 / LPH * U;
-    p.head_blocks = (heads + per - 1) / per;
-    const int64_t blocks = (p.n_tokens * p.head_blocks + 7) / 8;
-    if (blocks > INT32_MAX) return ENGRAM_EINVAL;
-    const dim3 grid((unsigned)blocks);
+    constexpr int per = 32 / LPH * U;  // heads per warp; a block takes 8 tokens
+    const int64_t blocks = (p.n_tokens + 7) / 8;
+    const dim3 grid((unsigned)blocks, (p.n_q + per - 1) / per + (p.n_k + p.n_v + per - 1) / per);
+    if (grid.y > 65535) return ENGRAM_EINVAL;
     if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
         return launch_after(head_kernel<E, LPH, U, true, APPEND>, grid, 256, 0, st, "head_kernel", p);
     return launch_after(head_kernel<E, LPH, U, false, APPEND>, grid, 256, 0, st, "head_kernel", p);
@@ -115,13 +114,15 @@ static engram_status head_launch(const engram_attn_config *cfg, HeadParams &p, c
     p.head_dim = cfg->head_dim;
     p.rope_dim = cfg->rope_dim;
     p.eps = cfg->norm_eps;
-    // One head per lane while the batch leaves SMs idle (a shorter chain per
-    // warp), four once there are several warps per SM without it.
+    p.inv_dim = 1.f / (float)cfg->head_dim;
+    // One head per lane while the batch leaves SMs idle (a shorter chain per warp), two once there are
+    // 64 warps per SM without it: 32,768 tokens of 32 + 8 heads of 128 take 117 us with two, 140 with
+    // one, 117 to 145 with four (more registers, fewer warps); 64 tokens 1.8 us with one or two.
     const int64_t warps1 = p.n_tokens * ((p.n_q + p.n_k + p.n_v + 3) / 4);
     const bool wide = warps1 >= (int64_t)num_sms() * 64;
     if (cfg->head_dim <= 64)
-        return wide ? head_launch_u<E, 4, 4, APPEND>(cfg, p, st) : head_launch_u<E, 4, 1, APPEND>(cfg, p, st);
-    return wide ? head_launch_u<E, 8, 4, APPEND>(cfg, p, st) : head_launch_u<E, 8, 1, APPEND>(cfg, p, st);
+        return wide ? head_launch_u<E, 4, 2, APPEND>(cfg, p, st) : head_launch_u<E, 4, 1, APPEND>(cfg, p, st);
+    return wide ? head_launch_u<E, 8, 2, APPEND>(cfg, p, st) : head_launch_u<E, 8, 1, APPEND>(cfg, p, st);
 }
 
 // ---------------------------------------------------------------- attention --
@@ -334,6 +335,7 @@ extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const e
     p.slot_stride = cache->token_stride;
     p.page_head_stride = cache->head_stride;
     p.batch = device_batch(batch, cache);
+    p.by_page = Divisor(cache->page_size);
     return cfg->dtype == ENGRAM_BF16 ? head_launch<Bf16, true>(cfg, p, (cudaStream_t)stream)
                                      : head_launch<Fp16, true>(cfg, p, (cudaStream_t)stream);
 }
