@@ -116,7 +116,7 @@ static engram_status head_launch(const engram_attn_config *cfg, HeadParams &p, c
     p.eps = cfg->norm_eps;
     p.inv_dim = 1.f / (float)cfg->head_dim;
     // One head per lane while the batch leaves SMs idle (a shorter chain per warp), two once there are
-    // 64 warps per SM without it: 32,768 tokens of 32 + 8 heads of 128 take 117 us with two, 140 with
+    // 64 warps per SM without it: 32,768 tokens of 32 + 8 heads of 128 take 120 us with two, 140 with
     // one, 117 to 145 with four (more registers, fewer warps); 64 tokens 1.8 us with one or two.
     const int64_t warps1 = p.n_tokens * ((p.n_q + p.n_k + p.n_v + 3) / 4);
     const bool wide = warps1 >= (int64_t)num_sms() * 64;
@@ -213,7 +213,11 @@ static int64_t tile_items_most(const engram_attn_config *cfg, int64_t n_seqs, in
     const int64_t seqs = n_seqs < n_query ? n_seqs : n_query;
     return (rows / tile::ROWS + seqs) * cfg->n_kv_heads;
 }
+// Slots for partial results.  With six items a SM or more nothing is split (the last round is at most
+// a sixth of the time, and the parts cost about as much), so none are needed and no join follows.
 static int64_t tile_slots(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    const int64_t least = (n_query * (cfg->n_heads / cfg->n_kv_heads) + tile::ROWS - 1) / tile::ROWS * cfg->n_kv_heads;
+    if (least >= (int64_t)num_sms() * 6) return 0;
     return std::min<int64_t>((int64_t)num_sms() * tile::SLOTS_PER_SM,
                              tile_items_most(cfg, n_seqs, n_query) * tile::MAX_SPLIT);
 }
@@ -222,7 +226,7 @@ static size_t tile_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
 }
 static size_t tile_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
     const int64_t slots = tile_slots(cfg, n_seqs, n_query);
-    return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float));
+    return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
 
 // Query rows per sequence and key/value head from which the 256-row items pay
@@ -258,6 +262,9 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.box = gcd(cache->page_size, tile::KT);
     p.ctas = num_sms();
     p.max_slots = (int32_t)slots;
+    p.cut = slots == 0 ? nullptr
+                       : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
+                                                     tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query) - 256);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     CUtensorMap km, vm;
     if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
@@ -267,7 +274,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS, smem, st, "tile_kernel", km, vm, p);
-    if (s != ENGRAM_OK) return s;
+    if (s != ENGRAM_OK || slots == 0) return s;
     return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * 8), 128, 0, st, "tile_join_kernel", p);
 }
 

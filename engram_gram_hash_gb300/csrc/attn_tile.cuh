@@ -39,7 +39,7 @@ constexpr int MT = 128;               // rows per tile (TMEM lanes)
 constexpr int ROWS = 2 * MT;          // rows per item
 constexpr int KT = 128;               // keys per tile
 constexpr int NUM_THREADS = 384;
-constexpr int CHUNKS = 128;           // the plan's prefix sums: sequences in this many chunks
+constexpr int CHUNKS = 64;            // the plan's prefix sums: sequences in this many chunks
 constexpr int P_PARTS = 2;            // a tile's weights are handed over in this many parts
 constexpr int MAX_SPLIT = 152;
 constexpr int SLOTS_PER_SM = 8;       // workspace for partial results
@@ -62,7 +62,7 @@ struct PlanShared {
     int64_t items[CHUNKS + 1];   // items before each chunk of sequences
     int64_t parts[CHUNKS + 1];   // ... and among them the parts of split ones (workspace slots)
     unsigned long long cand_items[N_CAND], cand_parts[N_CAND];
-    unsigned long long work, segs;
+    unsigned long long work;
     int max_tiles;
     int cut;                     // tiles per part at most
 };
@@ -117,6 +117,7 @@ struct Params {
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t ctas;
     int32_t max_slots;  // 0: nothing is split
+    int32_t *cut;       // the plan's cut, for the join
     float scale_log2;
 };
 
@@ -150,17 +151,56 @@ __device__ __forceinline__ int32_t splits_of(int32_t tiles, int32_t cut) {
     return tiles > cut ? (tiles + cut - 1) / cut : 1;
 }
 
-// All threads of a block of NT >= CHUNKS threads, into sh: the cut, and the
-// items before each chunk of sequences.
+// The sums over the chunks of sequences, by all threads of a block of at least
+// CHUNKS threads: a[c + 1] and b[c + 1] from per(s), a pair of counts.
+template <typename F>
+__device__ __forceinline__ void chunk_sums(const Params &p, int64_t *a, int64_t *b, const F &per) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int64_t size = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
+    if (tid < CHUNKS) {
+        const int64_t s0 = tid * size, s1 = s0 + size < p.b.n_seqs ? s0 + size : p.b.n_seqs;
+        int64_t x = 0, y = 0;
+        for (int64_t s = s0; s < s1; ++s) per(s, x, y);
+        a[tid + 1] = x;
+        b[tid + 1] = y;
+        if (tid == 0) a[0] = b[0] = 0;
+    }
+    __syncthreads();
+    if (tid < 64) {  // inclusive, 32 at a time; a warp for each array
+        int64_t *v = tid < 32 ? a : b;
+        int64_t run = 0;
+        for (int c = 0; c < CHUNKS; c += 32) {
+            int64_t x = v[c + lane + 1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += u;
+            }
+            v[c + lane + 1] = run + x;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+    }
+    __syncthreads();
+}
+
+// The chunk whose range of v (sums over the chunks) holds x.
+__device__ __forceinline__ int find_chunk(const int64_t *v, int64_t x) {
+    int lo = 0, hi = CHUNKS;  // v[lo] <= x < v[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// All threads of a block of NT threads, into sh: the cut, and the items before
+// each chunk of sequences.
 template <int NT>
 __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
     const int tid = threadIdx.x, lane = tid & 31;
-    const int64_t per = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
-    const int64_t s0 = tid < CHUNKS ? tid * per : p.b.n_seqs;
-    const int64_t s1 = s0 + per < p.b.n_seqs ? s0 + per : p.b.n_seqs;
     if (tid < N_CAND) sh->cand_items[tid] = sh->cand_parts[tid] = 0;
     if (tid == 0) {
-        sh->work = sh->segs = 0;
+        sh->work = 0;
         sh->max_tiles = 1;
         sh->cut = INT32_MAX;
     }
@@ -168,7 +208,7 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
     if (p.max_slots > 0) {
         int64_t work = 0;
         int32_t most = 1;
-        for (int64_t s = s0; s < s1; ++s) {
+        for (int64_t s = tid; s < p.b.n_seqs; s += NT) {
             const Share h = share(p, load_seq(p.b, s, base));
             work += h.segs * h.mean;
             if (h.segs > 0 && h.tiles > most) most = h.tiles;
@@ -178,15 +218,20 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
             atomicMax(&sh->max_tiles, most);
         }
         __syncthreads();
-        const int32_t max_tiles = sh->max_tiles;
-        for (int64_t s = s0; s < s1; ++s) {
+        // a candidate per lane, two sequences per warp and round
+        static_assert(N_CAND == 16, "a half warp of candidates");
+        const int c = lane & 15;
+        const int32_t max_tiles = sh->max_tiles, cut_c = (max_tiles + kSplits[c] - 1) / kSplits[c];
+        unsigned long long items = 0, parts = 0;
+        for (int64_t s = (tid >> 4); s < p.b.n_seqs; s += NT / 16) {
             const Share h = share(p, load_seq(p.b, s, base));
-            if (h.segs == 0) continue;
-            for (int c = 0; c < N_CAND; ++c) {
-                const int32_t n = splits_of(h.tiles, (max_tiles + kSplits[c] - 1) / kSplits[c]);
-                atomicAdd(&sh->cand_items[c], (unsigned long long)(h.segs * n));
-                if (n > 1) atomicAdd(&sh->cand_parts[c], (unsigned long long)(h.segs * n));
-            }
+            const int32_t n = splits_of(h.tiles, cut_c);
+            items += h.segs * n;
+            if (n > 1) parts += h.segs * n;
+        }
+        if (items) {
+            atomicAdd(&sh->cand_items[c], items);
+            atomicAdd(&sh->cand_parts[c], parts);
         }
         __syncthreads();
         // The time of each candidate in tiles: equal items go in rounds; items
@@ -197,13 +242,12 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
             float best = INFINITY;
             int cut = INT32_MAX;
             if (lane < N_CAND) {
-                const int32_t c = (max_tiles + kSplits[lane] - 1) / kSplits[lane];
                 const float n = (float)sh->cand_items[lane], w = (float)sh->work, g = (float)p.ctas;
                 const float rounds = ceilf(n / g);
-                const float span = n <= g ? (float)c : (w > 0.85f * n * c ? rounds * c : w / g + 0.5f * c);
+                const float span = n <= g ? (float)cut_c : (w > 0.85f * n * cut_c ? rounds * cut_c : w / g + 0.5f * cut_c);
                 const float each = kSplits[lane] > 1 ? 5.f : 2.f;
                 if (kSplits[lane] == 1 || sh->cand_parts[lane] <= (unsigned long long)p.max_slots) best = span + rounds * each;
-                cut = kSplits[lane] == 1 ? INT32_MAX : c;
+                cut = kSplits[lane] == 1 ? INT32_MAX : cut_c;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {  // the least; of equals the first candidate (lower lane)
@@ -218,34 +262,13 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
         }
         __syncthreads();
     }
-    if (tid < CHUNKS) {
-        int64_t n = 0, parts = 0;
-        for (int64_t s = s0; s < s1; ++s) {
-            const Share h = share(p, load_seq(p.b, s, base));
-            const int32_t k = splits_of(h.tiles, sh->cut);
-            n += h.segs * k;
-            if (k > 1) parts += h.segs * k;
-        }
-        sh->items[tid + 1] = n;
-        sh->parts[tid + 1] = parts;
-        if (tid == 0) sh->items[0] = sh->parts[0] = 0;
-    }
-    __syncthreads();
-    if (tid < 64) {  // inclusive sums over the chunks, 32 at a time; a warp for each array
-        int64_t *a = tid < 32 ? sh->items : sh->parts;
-        int64_t run = 0;
-        for (int c = 0; c < CHUNKS; c += 32) {
-            int64_t v = a[c + lane + 1];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-                if (lane >= o) v += u;
-            }
-            a[c + lane + 1] = run + v;
-            run += __shfl_sync(0xffffffffu, v, 31);
-        }
-    }
-    __syncthreads();
+    const int32_t cut = sh->cut;
+    chunk_sums(p, sh->items, sh->parts, [&](int64_t s, int64_t &n, int64_t &parts) {
+        const Share h = share(p, load_seq(p.b, s, base));
+        const int32_t k = splits_of(h.tiles, cut);
+        n += h.segs * k;
+        if (k > 1) parts += h.segs * k;
+    });
 }
 
 // Rows and keys of segment seg = block * n_kv_heads + head of sequence it.q;
@@ -270,11 +293,7 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int64_t seg) {
 // same time and share them through L2), the longest blocks first, heads
 // innermost.
 __device__ __forceinline__ Item find_item(const Params &p, int64_t base, const PlanShared *sh, int64_t index) {
-    int lo = 0, hi = CHUNKS;  // items[lo] <= index < items[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (sh->items[mid] <= index) lo = mid; else hi = mid;
-    }
+    const int lo = find_chunk(sh->items, index);
     const int64_t per = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
     Item it;
     int64_t at = index - sh->items[lo];
@@ -414,6 +433,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
     const int64_t n_items = sh->plan.items[CHUNKS];
+    if (blockIdx.x == 0 && threadIdx.x == 0 && p.cut) *p.cut = sh->plan.cut;
 
     // Item number i of this CTA, for a whole warp: every role takes all of them in order (null after a time-out).
     const auto take = [&](uint32_t i) -> const Item * {
@@ -857,77 +877,120 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
 }
 
-// Adds up the parts of split items, in order: a warp takes one row at a time,
-// its lanes 4 values each.
+// Adds up the parts of split items, in order.  A block takes 16 rows of a
+// segment at a time, a warp 4 of them (their loads together), its lanes 4
+// values of each.
 template <typename E, int DP>
 __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ Params p) {
-    __shared__ PlanShared plan;
+    constexpr int R = 4;
+    __shared__ int64_t segs[CHUNKS + 1], parts[CHUNKS + 1];
     grid_dependency_wait();
     allow_dependent_launch();
+    const int32_t cut = __ldcg(p.cut);
+    if (cut == INT32_MAX) return;
     const int64_t base = __ldg(p.b.offs);
-    make_plan<128>(p, base, &plan);
-    if (plan.cut == INT32_MAX) return;
+    chunk_sums(p, segs, parts, [&](int64_t s, int64_t &n, int64_t &k_sum) {
+        const Share h = share(p, load_seq(p.b, s, base));
+        const int32_t k = splits_of(h.tiles, cut);
+        if (k > 1) {
+            n += h.segs;
+            k_sum += h.segs * k;
+        }
+    });
     const int lane = threadIdx.x & 31;
-    const int64_t warps = (int64_t)gridDim.x * 4, wid = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    int64_t slot0 = 0, rows0 = 0;  // slots and rows before sequence s
-    for (int64_t s = 0; s < p.b.n_seqs; ++s) {
+    const bool on = lane * 4 < DP;
+    const int64_t per = (p.b.n_seqs + CHUNKS - 1) / CHUNKS;
+    for (int64_t x = blockIdx.x; x < segs[CHUNKS] * (ROWS / 16); x += gridDim.x) {
+        // the segment: the sequence whose split segments hold number x / 16
+        const int c = find_chunk(segs, x / (ROWS / 16));
+        int64_t at = x / (ROWS / 16) - segs[c], slot = parts[c];
         Item it;
-        it.s = s;
-        it.q = load_seq(p.b, s, base);
-        const Share h = share(p, it.q);
-        it.splits = splits_of(h.tiles, plan.cut);
-        if (it.splits == 1) continue;
-        const int64_t n_rows = h.segs * ROWS;
-        // this warp's rows of the sequence: numbers congruent to wid over all split sequences' rows
-        for (int64_t x = (wid + warps - rows0 % warps) % warps; x < n_rows; x += warps) {
-            const int64_t seg = x / ROWS;
-            const int r = (int)(x - seg * ROWS);
-            it.part = 0;
-            place(p, it, seg);
-            if (r >= it.n_rows) continue;
-            const int64_t slot = slot0 + seg * it.splits;
-            const float *ml = p.part_ml + slot * (2 * ROWS) + r;
-            float m = -INFINITY;
-            for (int k = lane; k < it.splits; k += 32) m = fmaxf(m, __ldcg(ml + (int64_t)k * (2 * ROWS)));
+        for (it.s = c * per;; ++it.s) {
+            it.q = load_seq(p.b, it.s, base);
+            const Share h = share(p, it.q);
+            it.splits = splits_of(h.tiles, cut);
+            if (it.splits == 1) continue;
+            if (at < h.segs) break;
+            at -= h.segs;
+            slot += h.segs * it.splits;
+        }
+        it.part = 0;
+        place(p, it, at);
+        slot += at * it.splits;
+        const int r0 = (int)(x % (ROWS / 16)) * 16 + (threadIdx.x >> 5) * R;
+        if (r0 >= it.n_rows) continue;
+
+        float m[R], l[R];
+        float4 acc[R];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            float l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k0 = 0; k0 < it.splits; k0 += 32) {
-                float mk = -INFINITY, wk = 0.f;
-                if (k0 + lane < it.splits) {
-                    mk = __ldcg(ml + (int64_t)(k0 + lane) * (2 * ROWS));
-                    wk = rows::weight(mk, m);
-                    l += wk * __ldcg(ml + (int64_t)(k0 + lane) * (2 * ROWS) + ROWS);
-                }
-                const int n = it.splits - k0 < 32 ? it.splits - k0 : 32;
-#pragma unroll 4
-                for (int k = 0; k < n; ++k) {
-                    const float x_k = __shfl_sync(0xffffffffu, wk, k);
+        for (int q = 0; q < R; ++q) {
+            m[q] = -INFINITY;
+            l[q] = 0.f;
+            acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float *ml = p.part_ml + slot * (2 * ROWS) + r0;  // 4 rows: one 16-byte load
+        for (int k = lane; k < it.splits; k += 32) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(ml + (int64_t)k * (2 * ROWS)));
+            m[0] = fmaxf(m[0], v.x);
+            m[1] = fmaxf(m[1], v.y);
+            m[2] = fmaxf(m[2], v.z);
+            m[3] = fmaxf(m[3], v.w);
+        }
+#pragma unroll
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m[q] = fmaxf(m[q], __shfl_xor_sync(0xffffffffu, m[q], o));
+        for (int k0 = 0; k0 < it.splits; k0 += 32) {
+            float mk[R], wk[R];
+#pragma unroll
+            for (int q = 0; q < R; ++q) mk[q] = -INFINITY, wk[q] = 0.f;
+            if (k0 + lane < it.splits) {
+                const float *a = ml + (int64_t)(k0 + lane) * (2 * ROWS);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(a)), u = __ldcg(reinterpret_cast<const float4 *>(a + ROWS));
+                mk[0] = v.x, mk[1] = v.y, mk[2] = v.z, mk[3] = v.w;
+                const float lk[R] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    if (r0 + q < it.n_rows) {
+                        wk[q] = rows::weight(mk[q], m[q]);
+                        l[q] += wk[q] * lk[q];
+                    }
+            }
+            const int n = it.splits - k0 < 32 ? it.splits - k0 : 32;
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+                float4 v[R];
+                const float *o = p.part_o + ((slot + k0 + k) * ROWS + r0) * DP + lane * 4;
+#pragma unroll
+                for (int q = 0; q < R; ++q)
+                    v[q] = on ? __ldcg(reinterpret_cast<const float4 *>(o + q * DP)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < R; ++q) {
+                    const float f = __shfl_sync(0xffffffffu, wk[q], k);
                     // a part without keys for this row left no sum (and, without any tile, no O)
-                    const bool some = __shfl_sync(0xffffffffu, mk, k) != -INFINITY;
-                    if (some && lane * 4 < DP) {
-                        const float4 v =
-                            __ldcg(reinterpret_cast<const float4 *>(p.part_o + ((slot + k0 + k) * ROWS + r) * DP) + lane);
-                        acc.x = fmaf(x_k, v.x, acc.x);
-                        acc.y = fmaf(x_k, v.y, acc.y);
-                        acc.z = fmaf(x_k, v.z, acc.z);
-                        acc.w = fmaf(x_k, v.w, acc.w);
+                    if (__shfl_sync(0xffffffffu, mk[q], k) != -INFINITY) {
+                        acc[q].x = fmaf(f, v[q].x, acc[q].x);
+                        acc[q].y = fmaf(f, v[q].y, acc[q].y);
+                        acc[q].z = fmaf(f, v[q].z, acc[q].z);
+                        acc[q].w = fmaf(f, v[q].w, acc[q].w);
                     }
                 }
             }
+        }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-            const int32_t tok = p.by_group.quotient(it.r0 + r), hh = (it.r0 + r) - tok * p.group, head = it.head * p.group + hh;
+        for (int q = 0; q < R; ++q) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], o);
+            const int r = r0 + q;
+            if (r >= it.n_rows) continue;
+            const float inv = l[q] > 0.f ? 1.f / l[q] : (l[q] == 0.f ? 0.f : l[q]);
+            const int32_t tok = p.by_group.quotient(it.r0 + r), head = it.head * p.group + it.r0 + r - tok * p.group;
             const int64_t row = (int64_t)it.q.row0 + tok;
             if (lane * 4 < p.head_dim)
                 *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + (int64_t)head * p.out_head_stride + lane * 4) =
-                    make_uint2(E::pack(acc.x * inv, acc.y * inv), E::pack(acc.z * inv, acc.w * inv));
-            if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = rows::lse_of(m, l);
+                    make_uint2(E::pack(acc[q].x * inv, acc[q].y * inv), E::pack(acc[q].z * inv, acc[q].w * inv));
+            if (p.lse && lane == 0) p.lse[row * p.n_heads + head] = rows::lse_of(m[q], l[q]);
         }
-        slot0 += h.segs * it.splits;
-        rows0 += n_rows;
     }
 }
 

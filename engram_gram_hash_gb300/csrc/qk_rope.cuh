@@ -7,8 +7,8 @@
 //
 // Bound: memory.  Every value is read once and written once in 16-byte pieces;
 // the fp32 table row of a token (rope_dim * 4 bytes) is read once per warp and
-// serves all its heads.  32,768 tokens of 32 + 8 heads of 128: 117 us, 5.9 TB/s
-// (87 % of the copy rate); 15,026 tokens' keys and values into pages 27 us,
+// serves all its heads.  32,768 tokens of 32 + 8 heads of 128: 120 us, 5.7 TB/s
+// (84 % of the copy rate); 15,026 tokens' keys and values into pages 27 us,
 // 4.8 TB/s (the chain offsets -> length -> page -> slot bounds it).
 // Layout: a lane holds two 8-value pieces of a head, chosen so that both
 // values of every pair are in the same lane (HALVES: piece l and the piece
