@@ -183,6 +183,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.out_token_stride = out->token_stride;
     p.out_head_stride = out->head_stride;
     p.lse = lse;
+    p.values = ValuePages{static_cast<const uint16_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows_part_o_bytes(cfg));
     p.n_heads = cfg->n_heads;
@@ -251,6 +252,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.out_token_stride = out->token_stride;
     p.out_head_stride = out->head_stride;
     p.lse = lse;
+    p.values = ValuePages{static_cast<const uint16_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tile_part_o_bytes(cfg, slots));
     p.n_heads = cfg->n_heads;

@@ -6,6 +6,11 @@ namespace engram {
 namespace attn {
 
 struct Bf16 {
+    // two values times zero onto acc: NaN from then on if either is an infinity or NaN
+    static __device__ __forceinline__ void spot(uint32_t &acc, uint32_t w) {
+        asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+    }
+    static constexpr uint32_t EXPONENT = 0x7F80u;
     static __device__ __forceinline__ float2 unpack(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -18,6 +23,10 @@ struct Bf16 {
 };
 
 struct Fp16 {
+    static __device__ __forceinline__ void spot(uint32_t &acc, uint32_t w) {
+        asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
+    }
+    static constexpr uint32_t EXPONENT = 0x7C00u;
     static __device__ __forceinline__ float2 unpack(uint32_t w) {
         return __half22float2(*reinterpret_cast<__half2 *>(&w));
     }
@@ -90,6 +99,89 @@ __device__ __forceinline__ Seq load_seq(const Batch &b, int64_t s, int64_t base)
 // limit the lanes could differ, and the warp-wide steps that follow must not).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
+// Infinities and NaN among the values.  A key that is hidden from a row has
+// weight 0 there, but 0 times an infinity is NaN, and the products run over
+// whole tiles.  So in tiles that some row sees only part of ("edge" tiles) such
+// values are cleared before the product (clear_nonfinite) and, where any was
+// found, added to the rows that do see their key afterwards (add_nonfinite):
+// the sum over the visible keys is infinite or NaN exactly where it should be.
+
+// The infinities and NaN of the two values in w are set to zero.
+template <typename E>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    if ((w & E::EXPONENT) == E::EXPONENT) w &= 0xFFFF0000u;
+    if (((w >> 16) & E::EXPONENT) == E::EXPONENT) w &= 0x0000FFFFu;
+    return w;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// N 16-byte pieces of shared memory, `at(i)` the address of the i-th: whether
+// they hold an infinity or NaN (false if !keep), and their clearing: all of
+// them if !keep, else the infinities and NaN.
+template <typename E, int N, typename F>
+__device__ __forceinline__ bool holds_nonfinite(bool keep, const F &at) {
+    uint32_t acc = 0;
+    if (keep) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint4 v = lds16(at(i));
+            E::spot(acc, v.x);
+            E::spot(acc, v.y);
+            E::spot(acc, v.z);
+            E::spot(acc, v.w);
+        }
+    }
+    return acc != 0u;
+}
+template <typename E, int N, typename F>
+__device__ __forceinline__ void clear_nonfinite(bool keep, const F &at) {
+#pragma unroll 1
+    for (int i = 0; i < N; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (keep) {
+            v = lds16(at(i));
+            v = make_uint4(finite_only<E>(v.x), finite_only<E>(v.y), finite_only<E>(v.z), finite_only<E>(v.w));
+        }
+        sts16(at(i), v);
+    }
+}
+
+// The cached values as plain memory.
+struct ValuePages {
+    const uint16_t *v;
+    int64_t page_stride, slot_stride, head_stride;
+};
+// o[i] += the infinities and NaN among values c + i < dim, i < N, of keys
+// [key_lo, key_hi) of sequence s.
+template <typename E, int N>
+__device__ __forceinline__ void add_nonfinite(const Batch &b, const ValuePages &pages, int64_t s, int32_t head, int32_t key_lo,
+                                              int32_t key_hi, int c, int dim, float (&o)[N]) {
+#pragma unroll 1
+    for (int32_t key = key_lo; key < key_hi; ++key) {
+        const int32_t page = __ldg(b.block_table + s * b.table_stride + key / b.page_size);
+        if (page < 0 || page >= b.n_pages) continue;
+        const uint16_t *v = pages.v + page * pages.page_stride + (key % b.page_size) * pages.slot_stride +
+                            head * pages.head_stride + c;
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            if (c + i >= dim) break;
+            const uint32_t w = *reinterpret_cast<const uint32_t *>(v + i);
+            const float2 f = E::unpack(w);
+            if ((w & E::EXPONENT) == E::EXPONENT) o[i] += f.x;
+            if (((w >> 16) & E::EXPONENT) == E::EXPONENT) o[i + 1] += f.y;
+        }
+    }
 }
 
 // The last sequence s with offs[s] <= base + t (a whole warp looks at 32

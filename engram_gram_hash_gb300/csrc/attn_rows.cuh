@@ -53,6 +53,7 @@ struct Shared {
     int64_t scan[NUM_THREADS / 32];
     int64_t find_s;       // plan_find's answer
     int64_t find_before;
+    int32_t bad_lo[2], bad_hi[2];  // tiles in which infinities or NaN were cleared; two segments in turn
     int abort;
 };
 
@@ -70,6 +71,7 @@ struct Params {
     uint16_t *out;
     int64_t out_token_stride, out_head_stride;
     float *lse;         // [n_query][n_heads] or null
+    ValuePages values;
     float *part_o;      // [grid][2][ROWS][DP]
     float *part_ml;     // [grid][2][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
@@ -277,6 +279,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(&sh->empty[i], 4);
         }
         sh->abort = 0;
+        sh->bad_lo[0] = sh->bad_lo[1] = INT32_MAX;
+        sh->bad_hi[0] = sh->bad_hi[1] = -1;
         fence_mbar_init();
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
@@ -355,7 +359,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {  // ------------------------------------------------------ consumers
         const int grp = warp >> 2, wq = warp & 3;
         const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's rows qr, qr + 8 and first column
-        for (int64_t f = f0; f < f1;) {
+        int turn = 0;  // segments alternate
+        for (int64_t f = f0; f < f1; turn ^= 1) {
             const Segment g = segment(p, walk);
             const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
             const int32_t end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
@@ -409,7 +414,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                     }
                     // keys outside [full_lo, full_hi) are hidden from some row; keys outside
-                    // [lo, hi) may hold anything, so their values are cleared as well
+                    // [lo, hi) may hold anything
                     const bool edge = key0 < g.full_lo || key0 + 16 > g.full_hi;
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
@@ -421,14 +426,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 if (key > row_hi[c >> 1] || key < row_lo[c >> 1]) s[t][c] = -INFINITY;
                             }
                         }
-                    uint32_t vmask[2] = {0xffffffffu, 0xffffffffu};
-                    if (edge) {
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const int32_t key = key0 + t * 8 + qc;
-                            vmask[t] = (key >= g.lo && key < g.hi ? 0x0000ffffu : 0u) |
-                                       (key + 1 >= g.lo && key + 1 < g.hi ? 0xffff0000u : 0u);
+                    if (edge) {  // half a key's values per lane: this warp's 16 keys are read by no other
+                        const int key = lane >> 1, c0 = (lane & 1) * (DP / 16);
+                        const uint32_t vrow = kb + C::KV_BYTES + key * 128;
+                        const auto at = [&](int i) {
+                            const int ch = c0 + i;
+                            return vrow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4);
+                        };
+                        const bool keep = key0 + key >= g.lo && key0 + key < g.hi, bad = holds_nonfinite<E, DP / 16>(keep, at);
+                        if (bad) {
+                            atomicMin(&sh->bad_lo[turn], g.tile0 + j);
+                            atomicMax(&sh->bad_hi[turn], g.tile0 + j);
                         }
+                        if (bad || !keep) clear_nonfinite<E, DP / 16>(keep, at);
+                        fence_proxy_async_smem();  // before the ring's next copy over it
+                        __syncwarp();
                     }
                     float up[2];
                     bool same = true;
@@ -472,8 +484,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             const int ch = nn * 2 + (lane >> 4);
                             uint32_t b[4];
                             ldmatrix_x4_trans(b, vrow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4));
-                            E::mma(o[nn * 2], pa, b[0] & vmask[0], b[1] & vmask[1]);
-                            E::mma(o[nn * 2 + 1], pa, b[2] & vmask[0], b[3] & vmask[1]);
+                            E::mma(o[nn * 2], pa, b[0], b[1]);
+                            E::mma(o[nn * 2 + 1], pa, b[2], b[3]);
                         }
                     }
                 }
@@ -492,6 +504,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             consumers_sync();
+            if (threadIdx.x == 0) {  // the segment before is done with its turn
+                sh->bad_lo[turn ^ 1] = INT32_MAX;
+                sh->bad_hi[turn ^ 1] = -1;
+            }
             float all[2], fac[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -530,6 +546,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 for (int w = 1; w < 4; ++w) {
                     const float4 t = *reinterpret_cast<const float4 *>(join + w * (ROWS * DP) + e);
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+                }
+                if (sh->bad_hi[turn] >= 0 && c < p.head_dim) {
+                    const int32_t pos = g.pos0 + p.by_group.quotient(g.r0 + r);
+                    const int32_t lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+                    float x[4] = {v.x, v.y, v.z, v.w};
+                    add_nonfinite<E, 4>(p.b, p.values, walk.s, g.head, max(lo, sh->bad_lo[turn] * KT),
+                                        min(pos + 1, (sh->bad_hi[turn] + 1) * KT), c, p.head_dim, x);
+                    v = make_float4(x[0], x[1], x[2], x[3]);
                 }
                 if (!whole) {
                     *reinterpret_cast<float4 *>(p.part_o + (int64_t)slot * (ROWS * DP) + e) = v;

@@ -75,6 +75,8 @@ struct Item {
     int32_t lo, hi;      // keys in reach of any row
     int32_t tile0, n;    // this part's tiles
     int32_t part, splits;
+    int32_t full_lo, full_hi;  // keys in reach of every row
+    int32_t bad_lo, bad_hi;    // this part's tiles in which infinities or NaN were cleared
 };
 constexpr int ITEMS = 4;  // items found ahead
 
@@ -109,6 +111,7 @@ struct Params {
     uint16_t *out;
     int64_t out_token_stride, out_head_stride;
     float *lse;
+    ValuePages values;
     float *part_o;      // [slots][ROWS][DP]
     float *part_ml;     // [slots][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
@@ -282,6 +285,10 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int64_t seg) {
     const int32_t first = it.pos0 + p.by_group.quotient(it.r0), last = it.pos0 + p.by_group.quotient(it.r0 + it.n_rows - 1);
     it.hi = last + 1 > 0 ? last + 1 : 0;
     it.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
+    it.full_hi = first + 1;
+    it.full_lo = p.window > 0 ? last - p.window + 1 : 0;
+    it.bad_lo = INT32_MAX;
+    it.bad_hi = -1;
     const int32_t t0 = it.lo / KT, nt = it.hi > it.lo ? (it.hi + KT - 1) / KT - t0 : 0;
     const int32_t a = (int32_t)((int64_t)nt * it.part / it.splits), b = (int32_t)((int64_t)nt * (it.part + 1) / it.splits);
     it.tile0 = t0 + a;
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool next_mine = false;
             float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
             if (mine && n > 0) {
-                const int32_t tile0 = w->tile0, lo = w->lo, hi = w->hi;
+                const int32_t tile0 = w->tile0;
                 const int32_t pos = w->pos0 + p.by_group.quotient(w->r0 + t * MT + row);
                 const int32_t row_lo = p.window > 0 ? pos - p.window + 1 : 0;
                 // keys in reach of every row of the tile
@@ -556,21 +563,25 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             tmem_st_32x32b_x16(o_tm + c * 16, o);
                         }
                     }
-                    // keys that no row reaches may hold anything: their values are cleared before the product
-                    // (by both row tiles, each before its own)
-                    if (key0 < lo || key0 + KT > hi) {
+                    // Values that must not meet a weight of zero leave the tile before the products: those
+                    // of keys that no row reaches (they may be anything), infinities and NaN of keys that
+                    // some row does not see.  Both row tiles do it, each before its own products; who clears
+                    // one first notes it, so either's epilogue adds it to the rows that see it.
+                    if (key0 < w->full_lo || key0 + KT > w->full_hi) {
                         const uint32_t vi = it + 2 * j + 1;
                         ok = warp_wait(&sh->kv_full[vi % C::STAGES], (vi / C::STAGES) & 1, abort);
                         if (!ok) break;
-                        if (key0 + row < lo || key0 + row >= hi) {
-                            const uint32_t at = smem_u32(kv_smem) + (vi % C::STAGES) * C::STAGE_BYTES + row * 128;
-#pragma unroll
-                            for (int c = 0; c < DP / 64; ++c)
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + c * (KT * 128) + i * 16),
-                                                 "r"(0)
-                                                 : "memory");
+                        const uint32_t vrow = smem_u32(kv_smem) + (vi % C::STAGES) * C::STAGE_BYTES + row * 128;
+                        const auto at = [&](int i) { return vrow + (i >> 3) * (KT * 128) + (((i ^ row) & 7) << 4); };
+                        const bool keep = key0 + row >= w->lo && key0 + row < w->hi;
+                        if (holds_nonfinite<E, DP / 8>(keep, at)) {
+                            Item *const note = const_cast<Item *>(w);
+                            atomicMin(&note->bad_lo, j);
+                            atomicMax(&note->bad_hi, j);
+                            __threadfence_block();
+                            clear_nonfinite<E, DP / 8>(true, at);
+                        } else if (!keep) {
+                            clear_nonfinite<E, DP / 8>(false, at);
                         }
                         fence_proxy_async_smem();
                     }
@@ -632,6 +643,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
                     if (!live) continue;
+                    if (w->bad_hi >= 0) {
+                        const int32_t pos = w->pos0 + tok, lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+                        add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(lo, (w->tile0 + w->bad_lo) * KT),
+                                             min(pos + 1, (w->tile0 + w->bad_hi + 1) * KT), c * 32, p.head_dim, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
+                    }
                     if (whole) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i)

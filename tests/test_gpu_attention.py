@@ -136,6 +136,58 @@ def test_attention_window_ignores_nan_before_it(eg):
     assert torch.equal(eg.engram_paged_attention(cfg, st.cache, st.batch, st.q), ref)
 
 
+def _slot(st, s, j):
+    return st.block_table[s, j // st.page].long(), j % st.page
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("shape", [
+    dict(dtype=BF16, heads=8, kv_heads=2, dim=128, page=64, new=[40, 1, 130], total=[100, 70, 500]),  # tiles
+    dict(dtype=FP16, heads=6, kv_heads=2, dim=72, page=48, new=[300, 7], total=[300, 200]),  # tiles
+    dict(dtype=BF16, heads=4, kv_heads=2, dim=64, page=16, new=[3, 1, 2], total=[60, 130, 2]),  # few rows
+    dict(dtype=FP16, heads=4, kv_heads=4, dim=128, page=32, new=[5, 1], total=[700, 1900]),  # few rows, cut
+])
+def test_attention_infinities_stay_with_the_rows_that_see_them(eg, shape, window):
+    """Infinities and NaN among cached keys and values: a row that does not see the position is as if they
+    were finite, a row that does is infinite or NaN in that column (value) or as a whole (key)."""
+    st = Step(eg, seed=21, **shape)
+    g = torch.Generator().manual_seed(5)
+    clean_k, clean_v = st.k_pages.clone(), st.v_pages.clone()
+    bad_v, bad_k = [], []
+    for s, (a, b) in enumerate(zip(st.new, st.total)):
+        at = {b - 1, b - a, max(b - a - 60, 0), int(torch.randint(0, b, (1,), generator=g))}
+        for i, j in enumerate(sorted(at)):
+            h, c = int(torch.randint(0, st.kv_heads, (1,), generator=g)), int(torch.randint(0, st.dim, (1,), generator=g))
+            x = (math.inf, -math.inf, math.nan)[(i + s) % 3]
+            st.v_pages[(*_slot(st, s, j), h, c)] = x
+            bad_v.append((s, j, h, c, x))
+    s, j, h = 0, st.total[0] - 1, 0
+    st.k_pages[(*_slot(st, s, j), h, 3)] = math.nan
+    bad_k.append((s, j, h))
+    cfg = eg.make_attn_config(st.heads, st.kv_heads, st.dim, dtype=st.dtype, rope_dim=0, window=window)
+    got = eg.engram_paged_attention(cfg, st.cache, st.batch, st.q).double()
+    assert eg.engram_last_error() == 0
+    finite_v = torch.where(torch.isfinite(st.v_pages), st.v_pages, torch.where(torch.isnan(clean_v), clean_v, 0))
+    ref, _, bound, _ = plain.attention(st.q, clean_k, finite_v, st.block_table, st.new, st.total, st.kv_heads, cfg.scale, window)
+    expect = torch.zeros_like(ref)
+    pos = plain.positions_of(st.new, st.total)
+    seq = torch.repeat_interleave(torch.arange(len(st.new)), torch.tensor(st.new))
+    group = st.heads // st.kv_heads
+
+    def rows_seeing(s, j):
+        return ((seq == s) & (pos >= j) & ((pos < j + window) if window else (pos >= 0))).cuda()
+
+    for s, j, h, c, x in bad_v:
+        expect[rows_seeing(s, j), h * group:(h + 1) * group, c] += x
+    for s, j, h in bad_k:
+        expect[rows_seeing(s, j), h * group:(h + 1) * group] = math.nan
+    touched = expect != 0
+    assert touched.any() and not touched.all()
+    assert ((got - ref).abs() <= bound)[~touched].all()
+    # a weight can underflow to zero, and zero times an infinity is NaN: both are accepted where p is tiny
+    assert not torch.isfinite(got[touched]).any()
+
+
 def test_attention_large_scores(eg):
     """Scores of several hundred: the running maximum moves far and weights underflow."""
     st = Step(eg, BF16, 4, 1, 128, 64, [1, 40], [777, 640], seed=5)
