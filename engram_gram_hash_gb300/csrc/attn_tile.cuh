@@ -516,6 +516,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         next_mine = next && next->n > 0 && next->n_rows > t * MT;
                         if (next_mine) fetch_q(*next);
                     }
+                    // Values that must not meet a weight of zero leave the tile before the products: those
+                    // of keys that no row reaches (they may be anything), infinities and NaN of keys that
+                    // some row does not see.  Both row tiles do it, each before its own products; who clears
+                    // one first notes it, so either's epilogue adds it to the rows that see it.
+                    if (key0 < w->full_lo || key0 + KT > w->full_hi) {
+                        const uint32_t vi = it + 2 * j + 1;
+                        ok = warp_wait(&sh->kv_full[vi % C::STAGES], (vi / C::STAGES) & 1, abort);
+                        if (!ok) break;
+                        const uint32_t vrow = smem_u32(kv_smem) + (vi % C::STAGES) * C::STAGE_BYTES + row * 128;
+                        const auto at = [&](int i) { return vrow + (i >> 3) * (KT * 128) + (((i ^ row) & 7) << 4); };
+                        const bool keep = key0 + row >= w->lo && key0 + row < w->hi;
+                        if (holds_nonfinite<E, DP / 8>(keep, at)) {
+                            Item *const note = const_cast<Item *>(w);
+                            atomicMin(&note->bad_lo, j);
+                            atomicMax(&note->bad_hi, j);
+                            __threadfence_block();
+                            clear_nonfinite<E, DP / 8>(true, at);
+                        } else if (!keep) {
+                            clear_nonfinite<E, DP / 8>(false, at);
+                        }
+                        fence_proxy_async_smem();
+                    }
                     // the second half of the scores arrives under the first half's maximum
                     uint32_t raw[4][32];
                     tmem_ld_32x32b_x32(s_tm, raw[0]);
@@ -562,28 +584,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
                             tmem_st_32x32b_x16(o_tm + c * 16, o);
                         }
-                    }
-                    // Values that must not meet a weight of zero leave the tile before the products: those
-                    // of keys that no row reaches (they may be anything), infinities and NaN of keys that
-                    // some row does not see.  Both row tiles do it, each before its own products; who clears
-                    // one first notes it, so either's epilogue adds it to the rows that see it.
-                    if (key0 < w->full_lo || key0 + KT > w->full_hi) {
-                        const uint32_t vi = it + 2 * j + 1;
-                        ok = warp_wait(&sh->kv_full[vi % C::STAGES], (vi / C::STAGES) & 1, abort);
-                        if (!ok) break;
-                        const uint32_t vrow = smem_u32(kv_smem) + (vi % C::STAGES) * C::STAGE_BYTES + row * 128;
-                        const auto at = [&](int i) { return vrow + (i >> 3) * (KT * 128) + (((i ^ row) & 7) << 4); };
-                        const bool keep = key0 + row >= w->lo && key0 + row < w->hi;
-                        if (holds_nonfinite<E, DP / 8>(keep, at)) {
-                            Item *const note = const_cast<Item *>(w);
-                            atomicMin(&note->bad_lo, j);
-                            atomicMax(&note->bad_hi, j);
-                            __threadfence_block();
-                            clear_nonfinite<E, DP / 8>(true, at);
-                        } else if (!keep) {
-                            clear_nonfinite<E, DP / 8>(false, at);
-                        }
-                        fence_proxy_async_smem();
                     }
                     const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
                     const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mref, -mref);
