@@ -30,7 +30,7 @@ namespace rows {
 constexpr int ROWS = 16;            // query rows per segment
 constexpr int KT = 64;              // keys per tile
 constexpr int CONSUMERS = 8;        // two groups of four warps
-constexpr int NUM_THREADS = 32 * (CONSUMERS + 1);
+constexpr int NUM_THREADS = 384;    // the consumers, and the producer's warpgroup (three idle warps)
 
 template <int DP>
 struct Cfg {
@@ -302,61 +302,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     walk.start(p, base, sh->find_s, f0 - sh->find_before);
     uint32_t it = 0;  // tiles through the ring
 
-    if (warp == CONSUMERS) {  // ------------------------------------ producer
-        const int boxes = KT / p.box;
-        const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64) * 2u;
-        for (int64_t f = f0; f < f1;) {
-            const Segment g = segment(p, walk);
-            const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
-            const int32_t end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
-            int64_t window0 = -1;  // first box whose page lane 0 holds
-            int32_t page = -1;
-            for (int32_t j = walk.j; j < end; ++j, ++it) {
-                const int32_t tile = g.tile0 + j;
-                const int64_t b0 = (int64_t)tile * boxes;
-                if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
-                    window0 = b0;
+    // Registers move to the consumers, which hold 16 rows' queries and outputs: 256 x 192 + 128 x 120 =
+    // the launch's 384 x 168.
+    if (warp >= CONSUMERS) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        if (warp == CONSUMERS) {  // ------------------------------------ producer
+            const int boxes = KT / p.box;
+            const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64) * 2u;
+            for (int64_t f = f0; f < f1;) {
+                const Segment g = segment(p, walk);
+                const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
+                const int32_t end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
+                int64_t window0 = -1;  // first box whose page lane 0 holds
+                int32_t page = -1;
+                for (int32_t j = walk.j; j < end; ++j, ++it) {
+                    const int32_t tile = g.tile0 + j;
+                    const int64_t b0 = (int64_t)tile * boxes;
+                    if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
+                        window0 = b0;
+                        const int64_t key = (b0 + lane) * p.box;
+                        page = -1;
+                        if (key < g.hi) {
+                            page = __ldg(p.b.block_table + walk.s * p.b.table_stride + key / p.b.page_size);
+                            if (page < 0 || page >= p.b.n_pages) {
+                                if (key + p.box > g.lo) raise_error(ENGRAM_ERANGE);
+                                page = -1;  // out of range: the copy fills zeros
+                            }
+                        }
+                    }
+                    const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
                     const int64_t key = (b0 + lane) * p.box;
-                    page = -1;
-                    if (key < g.hi) {
-                        page = __ldg(p.b.block_table + walk.s * p.b.table_stride + key / p.b.page_size);
-                        if (page < 0 || page >= p.b.n_pages) {
-                            if (key + p.box > g.lo) raise_error(ENGRAM_ERANGE);
-                            page = -1;  // out of range: the copy fills zeros
+                    const bool load = lane < boxes && key < g.hi && key + p.box > g.lo;
+                    const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+                    const int st = it % C::STAGES;
+                    bool ok = true;
+                    if (lane == 0) {
+                        if (it >= C::STAGES) ok = mbar_wait(&sh->empty[st], ((it / C::STAGES) - 1) & 1, abort);
+                        if (ok) mbar_arrive_expect_tx(&sh->full[st], loads * box_bytes);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (ok && load) {
+                        uint8_t *dst = smem + st * C::STAGE_BYTES + lane * p.box * 128;
+                        const int y = (int)(key % p.b.page_size);
+#pragma unroll
+                        for (int c = 0; c < DP / 64; ++c) {
+                            tma_load_4d(dst + c * KT * 128, &k_map, &sh->full[st], c * 64, y, g.head, mine);
+                            tma_load_4d(dst + C::KV_BYTES + c * KT * 128, &v_map, &sh->full[st], c * 64, y, g.head, mine);
                         }
                     }
                 }
-                const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
-                const int64_t key = (b0 + lane) * p.box;
-                const bool load = lane < boxes && key < g.hi && key + p.box > g.lo;
-                const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-                const int st = it % C::STAGES;
-                bool ok = true;
-                if (lane == 0) {
-                    if (it >= C::STAGES) ok = mbar_wait(&sh->empty[st], ((it / C::STAGES) - 1) & 1, abort);
-                    if (ok) mbar_arrive_expect_tx(&sh->full[st], loads * box_bytes);
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (ok && load) {
-                    uint8_t *dst = smem + st * C::STAGE_BYTES + lane * p.box * 128;
-                    const int y = (int)(key % p.b.page_size);
-#pragma unroll
-                    for (int c = 0; c < DP / 64; ++c) {
-                        tma_load_4d(dst + c * KT * 128, &k_map, &sh->full[st], c * 64, y, g.head, mine);
-                        tma_load_4d(dst + C::KV_BYTES + c * KT * 128, &v_map, &sh->full[st], c * 64, y, g.head, mine);
-                    }
-                }
+                f += n;
+                if (f < f1) walk.next(p, base);
             }
-            f += n;
-            if (f < f1) walk.next(p, base);
-        }
-        // never leave with a copy still landing (also after an abort elsewhere)
-        if (lane == 0) {
-            int no_abort = 0;
-            for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
-                mbar_wait(&sh->full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, 200000000ull);
+            // never leave with a copy still landing (also after an abort elsewhere)
+            if (lane == 0) {
+                int no_abort = 0;
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i)
+                    mbar_wait(&sh->full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, 200000000ull);
+            }
         }
     } else {  // ------------------------------------------------------ consumers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int grp = warp >> 2, wq = warp & 3;
         const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's rows qr, qr + 8 and first column
         int turn = 0;  // segments alternate
@@ -400,32 +406,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int32_t key0 = (g.tile0 + j) * KT + wq * 16;
                 if (ok && key0 < g.hi && key0 + 16 > g.lo) {
                     const uint32_t kb = smem_u32(smem + st * C::STAGE_BYTES) + wq * 16 * 128;
-                    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    {
-                        const int key = ((lane >> 4) << 3) + (lane & 7);
-                        const uint32_t krow = kb + key * 128;
-#pragma unroll
-                        for (int kk = 0; kk < DP / 16; ++kk) {
-                            const int ch = kk * 2 + ((lane >> 3) & 1);  // 16-byte piece of the key's row
-                            uint32_t b[4];
-                            ldmatrix_x4(b, krow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4));
-                            E::mma(s[0], qf[kk], b[0], b[1]);
-                            E::mma(s[1], qf[kk], b[2], b[3]);
-                        }
-                    }
                     // keys outside [full_lo, full_hi) are hidden from some row; keys outside
                     // [lo, hi) may hold anything
                     const bool edge = key0 < g.full_lo || key0 + 16 > g.full_hi;
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            s[t][c] *= p.scale_log2;
-                            if (edge) {
-                                const int32_t key = key0 + t * 8 + qc + (c & 1);
-                                if (key > row_hi[c >> 1] || key < row_lo[c >> 1]) s[t][c] = -INFINITY;
-                            }
-                        }
                     if (edge) {  // half a key's values per lane: this warp's 16 keys are read by no other
                         const int key = lane >> 1, c0 = (lane & 1) * (DP / 16);
                         const uint32_t vrow = kb + C::KV_BYTES + key * 128;
@@ -442,6 +425,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         fence_proxy_async_smem();  // before the ring's next copy over it
                         __syncwarp();
                     }
+                    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    {
+                        const int key = ((lane >> 4) << 3) + (lane & 7);
+                        const uint32_t krow = kb + key * 128;
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk) {
+                            const int ch = kk * 2 + ((lane >> 3) & 1);  // 16-byte piece of the key's row
+                            uint32_t b[4];
+                            ldmatrix_x4(b, krow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4));
+                            E::mma(s[0], qf[kk], b[0], b[1]);
+                            E::mma(s[1], qf[kk], b[2], b[3]);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            s[t][c] *= p.scale_log2;
+                            if (edge) {
+                                const int32_t key = key0 + t * 8 + qc + (c & 1);
+                                if (key > row_hi[c >> 1] || key < row_lo[c >> 1]) s[t][c] = -INFINITY;
+                            }
+                        }
                     float up[2];
                     bool same = true;
 #pragma unroll
