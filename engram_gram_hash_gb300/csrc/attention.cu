@@ -80,10 +80,13 @@ static Batch device_batch(const engram_kv_batch *b, const engram_kv_cache *c) {
 // kernel here waits for that kernel's completion before its first global
 // access, so this only hides launch latency.
 template <typename... P, typename... A>
-static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, cudaStream_t st,
+static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
                                   const char *what, const A &...args) {
     cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.gridDim = grid;
@@ -91,7 +94,7 @@ static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, in
     lc.dynamicSmemBytes = smem;
     lc.stream = st;
     lc.attrs = attr;
-    lc.numAttrs = 1;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&lc, kern, args...);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail(e, what);
 }
@@ -105,8 +108,8 @@ static engram_status head_launch_u(const engram_attn_config *cfg, HeadParams &p,
     const dim3 grid((unsigned)blocks, (p.n_q + per - 1) / per + (p.n_k + p.n_v + per - 1) / per);
     if (grid.y > 65535) return ENGRAM_EINVAL;
     if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
-        return launch_after(head_kernel<E, LPH, U, true, APPEND>, grid, 256, 0, st, "head_kernel", p);
-    return launch_after(head_kernel<E, LPH, U, false, APPEND>, grid, 256, 0, st, "head_kernel", p);
+        return launch_after(head_kernel<E, LPH, U, true, APPEND>, grid, 256, 0, 1, st, "head_kernel", p);
+    return launch_after(head_kernel<E, LPH, U, false, APPEND>, grid, 256, 0, 1, st, "head_kernel", p);
 }
 
 template <typename E, bool APPEND>
@@ -155,18 +158,37 @@ static size_t rows_workspace_bytes(const engram_attn_config *cfg) {
     return rows_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
 }
 
-// Whether segments stay whole (their tiles at most, by the block table's room): a cut one costs the
-// join, about 7 us a call, a whole one about 0.55 us a tile of 64 keys on its one SM.  32 heads of 128
-// (8 key/value heads), us whole / cut: 1 sequence of 500 tokens 11.0 / 11.8, 1,000: 15.8 / 13.4;
-// 16 sequences (about one segment an SM) of 500: 11.5 / 19.5, 2,000: 27.7 / 35.2; 64 sequences of
-// 500: 35.7 / 43.0, 1,000: 55.2 / 60.9, but there unequal lengths would wait for the longest.
-static int32_t rows_whole(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    const int64_t tiles = (batch->table_stride * cache->page_size + rows::KT - 1) / rows::KT;
-    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
+// How a segment's tiles are shared out.  The lengths are on the device; what is known here is the room
+// of the block tables (tiles at most) and how many segments there are at most.
+//   cluster of 8 or 4: few segments and short tables, one launch.  15 clusters of 8 and 36 of 4 fit the
+//     GPU at once.
+//   whole: no cut, no join; about one segment an SM, or so short that a cut cannot pay.
+//   cut: equal runs of tiles for every SM, then the join (a launch and about 5 us).
+// Measured, 8 key/value heads of 128, us a call in a CUDA graph, cluster of 8 / of 4 / whole or cut:
+//   1 sequence of 500 tokens 9.8 / 10.1 / 11.6, 2,000: 11.5 / 13.6 / 12.6, 4,000: 13.7 / 18.3 / 16.9,
+//     8,000: 18.5 / - / 16.5;  2 of 2,000: - / 13.6 / 12.9 (17.5 with the second launch's host time);
+//   4 of 2,000: - / 13.8 / 18.3, 4,000: - / 18.5 / 21.1;  16 of 500 whole 12.1, cut 19.5, 2,000: 27 / 33;
+//   64 of 1,000: cut 58, whole 55 with equal lengths, but unequal ones would wait for the longest.
+static void rows_shares(rows::Params &p, const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const int64_t tiles = (batch->table_stride * cache->page_size + rows::KT - 1) / rows::KT;  // of a segment at most
+    const int64_t group = p.group, seqs = std::min(batch->n_seqs, batch->n_query);
     const int64_t segs = cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
                                                     (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);  // at most
-    if (tiles <= 8 || (tiles <= 32 && segs * 2 >= num_sms() && segs <= num_sms())) return (int32_t)tiles;
-    return 0;
+    const int sms = num_sms();
+    p.cluster = 1;
+    p.whole = 0;
+    p.runs = sms;
+    if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
+        p.cluster = 8;
+    } else if (tiles > 2 && tiles <= (segs >= 24 ? 64 : 32) && segs * 4 <= sms - 8) {
+        p.cluster = 4;
+    } else if (tiles <= 8 || (tiles <= 32 && segs * 2 >= sms && segs <= sms)) {
+        p.whole = (int32_t)tiles;
+    }
+    if (p.cluster > 1) {
+        p.whole = 1;
+        p.runs = (int32_t)segs;
+    }
 }
 
 template <typename E, int DP>
@@ -193,8 +215,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, rows::KT);
-    p.runs = num_sms();
-    p.whole = rows_whole(cfg, cache, batch);
+    rows_shares(p, cfg, cache, batch);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     CUtensorMap km, vm;
     if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
@@ -203,9 +224,9 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     const auto kern = rows::rows_kernel<E, DP>;
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
-    s = launch_after(kern, dim3(p.runs), rows::NUM_THREADS, smem, st, "rows_kernel", km, vm, p);
+    s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows_kernel", km, vm, p);
     if (s != ENGRAM_OK || p.runs == 1 || p.whole > 0) return s;
-    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, st, "rows_join_kernel", p);
+    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
 // Row blocks x kv heads of a batch at most.
@@ -275,9 +296,9 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     const auto kern = tile::tile_kernel<E, DP, std::is_same<E, Bf16>::value>;
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
-    s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS, smem, st, "tile_kernel", km, vm, p);
+    s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS, smem, 1, st, "tile_kernel", km, vm, p);
     if (s != ENGRAM_OK || slots == 0) return s;
-    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * 8), 128, 0, st, "tile_join_kernel", p);
+    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * 8), 128, 0, 1, st, "tile_join_kernel", p);
 }
 
 }  // namespace attn

@@ -12,7 +12,10 @@
 // form one line that is cut into equal runs, one per CTA (one CTA per SM):
 // the load is even whatever the lengths are.  A segment inside one run is
 // finished there; a cut one leaves partial (m, l, O) in the workspace, which
-// rows_join_kernel adds up in order.
+// rows_join_kernel adds up in order.  With few segments and short tables the
+// join's launch would cost as much as the attention: then a cluster of CTAs
+// takes a segment, a share of its tiles each, and they join through
+// distributed shared memory.
 //
 // Per CTA: a TMA producer warp fills a ring of tiles (K and V of 64 keys,
 // 128-byte swizzle, 32 KB at 128 values; the ring holds what HBM latency
@@ -53,6 +56,8 @@ struct Shared {
     int64_t scan[NUM_THREADS / 32];
     int64_t find_s;       // plan_find's answer
     int64_t find_before;
+    uint64_t ready, done;  // cluster: every CTA's share is in its shared memory; every CTA has read the others'
+    float tm[ROWS], tl[ROWS];      // cluster: this CTA's maximum and sum of each row
     int32_t bad_lo[2], bad_hi[2];  // tiles in which infinities or NaN were cleared; two segments in turn
     int abort;
 };
@@ -79,6 +84,7 @@ struct Params {
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t runs;       // CTAs of the attention launch
+    int32_t cluster;    // CTAs that share a segment through distributed shared memory (1: none; then whole = 1)
     int32_t whole;      // > 0: every segment is given this many tiles and none is cut (no join follows)
     float scale_log2;   // scale * log2(e)
 };
@@ -261,7 +267,35 @@ __device__ __forceinline__ void row_total(const Shared<DP> *sh, int r, float &m,
     for (int w = 0; w < CONSUMERS; ++w) l += sh->l[w][r] * weight(sh->m[w][r], m);
 }
 
+__device__ __forceinline__ float ld_shared_cluster_f1(uint32_t cluster_saddr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_saddr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_saddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_saddr)
+                 : "memory");
+    return v;
+}
+
 // ---------------------------------------------------------------- kernel ----
+
+// Values c .. c + 3 of row r of the segment, v / l, and the row's lse.
+template <typename E>
+__device__ __forceinline__ void write_out(const Params &p, const Walk &w, const Segment &g, int r, int c, float4 v, float l) {
+    if (c >= p.head_dim) return;
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
+    uint16_t *dst = p.out + (int64_t)w_row(w, tok) * p.out_token_stride + (int64_t)(g.head * p.group + hh) * p.out_head_stride + c;
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(E::pack(v.x * inv, v.y * inv), E::pack(v.z * inv, v.w * inv));
+}
+__device__ __forceinline__ void write_lse(const Params &p, const Walk &w, const Segment &g, int r, float m, float l) {
+    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
+    p.lse[(int64_t)w_row(w, tok) * p.n_heads + g.head * p.group + hh] = lse_of(m, l);
+}
 
 template <typename E, int DP>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -281,10 +315,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         sh->abort = 0;
         sh->bad_lo[0] = sh->bad_lo[1] = INT32_MAX;
         sh->bad_hi[0] = sh->bad_hi[1] = -1;
+        mbar_init(&sh->ready, p.cluster);
+        mbar_init(&sh->done, p.cluster);
         fence_mbar_init();
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
     }
+    if (p.cluster > 1) cluster_sync_all();  // the others' barriers are there before anyone arrives on them
     grid_dependency_wait();
     allow_dependent_launch();
     if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
@@ -294,13 +331,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int64_t base = __ldg(p.b.offs);
     if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.b.offs + p.b.n_seqs) - base != p.b.n_query)
         raise_error(ENGRAM_ERANGE);
-    const Plan plan = plan_find<NUM_THREADS>(p, base, blockIdx.x, sh->scan, &sh->find_s, &sh->find_before);
-    const int64_t f0 = (int64_t)blockIdx.x * plan.run;
+    const int64_t index = blockIdx.x / p.cluster;
+    const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
+    const Plan plan = plan_find<NUM_THREADS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+    const int64_t f0 = index * plan.run;
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
     Walk walk;
     walk.start(p, base, sh->find_s, f0 - sh->find_before);
     uint32_t it = 0;  // tiles through the ring
+    // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
+    const auto tiles_of = [&](const Segment &g, int64_t f, int32_t &first, int32_t &end) -> int32_t {
+        if (p.cluster > 1) {
+            first = (int32_t)((int64_t)g.n_tiles * rank / p.cluster);
+            end = (int32_t)((int64_t)g.n_tiles * (rank + 1) / p.cluster);
+            return 1;
+        }
+        const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
+        first = walk.j;
+        end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
+        return n;
+    };
 
     // Registers move to the consumers, which hold 16 rows' queries and outputs: 256 x 192 + 128 x 120 =
     // the launch's 384 x 168.
@@ -311,11 +362,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64) * 2u;
             for (int64_t f = f0; f < f1;) {
                 const Segment g = segment(p, walk);
-                const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
-                const int32_t end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
+                int32_t first, end;
+                const int32_t n = tiles_of(g, f, first, end);
                 int64_t window0 = -1;  // first box whose page lane 0 holds
                 int32_t page = -1;
-                for (int32_t j = walk.j; j < end; ++j, ++it) {
+                for (int32_t j = first; j < end; ++j, ++it) {
                     const int32_t tile = g.tile0 + j;
                     const int64_t b0 = (int64_t)tile * boxes;
                     if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
@@ -366,10 +417,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int grp = warp >> 2, wq = warp & 3;
         const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's rows qr, qr + 8 and first column
         int turn = 0;  // segments alternate
+        uint32_t exchange_ph = 0;
         for (int64_t f = f0; f < f1; turn ^= 1) {
             const Segment g = segment(p, walk);
-            const int32_t n = (int32_t)(f1 - f < walk.tiles - walk.j ? f1 - f : walk.tiles - walk.j);
-            const int32_t end = walk.j + n < g.n_tiles ? walk.j + n : g.n_tiles;
+            int32_t first, end;
+            const int32_t n = tiles_of(g, f, first, end);
 
             // the 16 query rows as A fragments, and each row's reach
             uint32_t qf[DP / 16][4];
@@ -399,7 +451,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-            for (int32_t j = walk.j; j < end; ++j, ++it) {
+            for (int32_t j = first; j < end; ++j, ++it) {
                 if ((int)(it & 1) != grp) continue;
                 const int st = it % C::STAGES;
                 const bool ok = warp_wait(&sh->full[st], (it / C::STAGES) & 1, abort);
@@ -561,31 +613,60 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                         min(pos + 1, (sh->bad_hi[turn] + 1) * KT), c, p.head_dim, x);
                     v = make_float4(x[0], x[1], x[2], x[3]);
                 }
+                if (p.cluster > 1) {
+                    *reinterpret_cast<float4 *>(join + e) = v;  // read by this thread alone so far
+                    continue;
+                }
                 if (!whole) {
                     *reinterpret_cast<float4 *>(p.part_o + (int64_t)slot * (ROWS * DP) + e) = v;
                     continue;
                 }
                 float mm, ll;
                 row_total(sh, r, mm, ll);
-                const float inv = ll > 0.f ? 1.f / ll : (ll == 0.f ? 0.f : ll);
-                if (c < p.head_dim) {
-                    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
-                    uint16_t *dst = p.out + (int64_t)w_row(walk, tok) * p.out_token_stride +
-                                    (int64_t)(g.head * p.group + hh) * p.out_head_stride + c;
-                    *reinterpret_cast<uint2 *>(dst) = make_uint2(E::pack(v.x * inv, v.y * inv), E::pack(v.z * inv, v.w * inv));
-                }
+                write_out<E>(p, walk, g, r, c, v, ll);
             }
             if (threadIdx.x < g.n_rows) {
                 const int r = threadIdx.x;
                 float mm, ll;
                 row_total(sh, r, mm, ll);
-                if (!whole) {
+                if (p.cluster > 1) {
+                    sh->tm[r] = mm;
+                    sh->tl[r] = ll;
+                } else if (!whole) {
                     p.part_ml[slot * (2 * ROWS) + r] = mm;
                     p.part_ml[slot * (2 * ROWS) + ROWS + r] = ll;
                 } else if (p.lse) {
-                    const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
-                    p.lse[(int64_t)w_row(walk, tok) * p.n_heads + g.head * p.group + hh] = lse_of(mm, ll);
+                    write_lse(p, walk, g, r, mm, ll);
                 }
+            }
+            if (p.cluster > 1) {  // each CTA joins its share of the values from all shares of the keys, in rank order
+                consumers_sync();
+                if (threadIdx.x == 0) mbar_arrive_cluster_ranks(smem_u32(&sh->ready), p.cluster);
+                const bool ok = mbar_wait_cluster(&sh->ready, exchange_ph, abort);
+                const int share = ROWS * DP / p.cluster;
+                for (int e = rank * share + threadIdx.x * 4; ok && e < (rank + 1) * share; e += 32 * CONSUMERS * 4) {
+                    const int r = e / DP, c = e - r * DP;
+                    if (r >= g.n_rows) continue;
+                    float mm = -INFINITY, ll = 0.f;
+                    for (int k = 0; k < p.cluster; ++k) mm = fmaxf(mm, ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tm[r]), k)));
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int k = 0; k < p.cluster; ++k) {
+                        const float w = weight(ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tm[r]), k)), mm);
+                        const float4 x = ld_shared_cluster_f4(mapa_shared(smem_u32(join + e), k));
+                        ll = fmaf(w, ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tl[r]), k)), ll);
+                        v.x = fmaf(w, x.x, v.x);
+                        v.y = fmaf(w, x.y, v.y);
+                        v.z = fmaf(w, x.z, v.z);
+                        v.w = fmaf(w, x.w, v.w);
+                    }
+                    write_out<E>(p, walk, g, r, c, v, ll);
+                    if (p.lse && c == 0) write_lse(p, walk, g, r, mm, ll);
+                }
+                consumers_sync();
+                if (threadIdx.x == 0) mbar_arrive_cluster_ranks(smem_u32(&sh->done), p.cluster);
+                mbar_wait_cluster(&sh->done, exchange_ph, abort);  // nobody reads this CTA's memory any more
+                exchange_ph ^= 1;
             }
             consumers_sync();  // the join's memory is free again
             f += n;
