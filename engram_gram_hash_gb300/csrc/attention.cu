@@ -212,6 +212,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.n_kv_heads = cfg->n_kv_heads;
     p.group = cfg->n_heads / cfg->n_kv_heads;
     p.by_group = Divisor(p.group);
+    p.by_heads = Divisor(cfg->n_kv_heads);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, rows::KT);
@@ -280,6 +281,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.n_kv_heads = cfg->n_kv_heads;
     p.group = cfg->n_heads / cfg->n_kv_heads;
     p.by_group = Divisor(p.group);
+    p.by_heads = Divisor(cfg->n_kv_heads);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, tile::KT);
@@ -384,7 +386,7 @@ extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, c
     if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK) return ENGRAM_EINVAL;
     if (batch->n_query == 0) return ENGRAM_OK;
     if (check_cache(cfg, cache) != ENGRAM_OK || !view_ok(q) || !view_ok(out) || !aligned(lse, 4)) return ENGRAM_EINVAL;
-    if (batch->n_query > INT32_MAX / (cfg->n_heads / cfg->n_kv_heads)) return ENGRAM_EINVAL;
+    if (batch->n_query > INT32_MAX / cfg->n_heads) return ENGRAM_EINVAL;
     if (!workspace || !aligned(workspace, 256)) return ENGRAM_EINVAL;
     if (workspace_bytes < engram_paged_attention_workspace_bytes(cfg, batch->n_seqs, batch->n_query)) return ENGRAM_ENOMEM;
     cudaStream_t st = (cudaStream_t)stream;

@@ -33,6 +33,7 @@ namespace rows {
 constexpr int ROWS = 16;            // query rows per segment
 constexpr int KT = 64;              // keys per tile
 constexpr int CONSUMERS = 8;        // two groups of four warps
+constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment
 constexpr int NUM_THREADS = 384;    // the consumers, and the producer's warpgroup (three idle warps)
 
 template <int DP>
@@ -46,6 +47,12 @@ struct Cfg {
     static_assert(STAGES % 2 == 0, "each ring stage must belong to one consumer group");
     static constexpr int JOIN_FLOATS = 4 * ROWS * DP;
 };
+
+// Float c of row r in a join buffer: the rows' eight-float groups are rotated, so
+// that the accumulators' layout (8 rows x 4 pairs of columns a store) meets
+// different banks.
+template <int DP>
+__device__ __forceinline__ int join_at(int r, int c) { return r * DP + (c ^ ((r & 3) * 8)); }
 
 template <int DP>
 struct Shared {
@@ -80,7 +87,7 @@ struct Params {
     float *part_o;      // [grid][2][ROWS][DP]
     float *part_ml;     // [grid][2][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
-    Divisor by_group;
+    Divisor by_group, by_heads;  // the query heads of a kv head; the kv heads
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t runs;       // CTAs of the attention launch
@@ -113,6 +120,12 @@ struct Plan {
     int64_t run;    // tiles per CTA
 };
 
+__device__ __forceinline__ int64_t run_of(const Params &p, int64_t total) {
+    int64_t run = total < INT32_MAX - p.runs ? ((int32_t)total + p.runs - 1) / p.runs : (total + p.runs - 1) / p.runs;
+    if (p.whole > 1) run = (run + p.whole - 1) / p.whole * p.whole;
+    return run < 1 ? 1 : run;
+}
+
 // All threads of a block of NT: the length of the line, the tiles per CTA,
 // and for f(run) = the place asked for the sequence it lies in (sh_s, with
 // the tiles before that sequence in sh_before; sh_s = -1 past the end).
@@ -143,9 +156,7 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
         if (w < warp) before += scan[w];
         r.total += scan[w];
     }
-    r.run = (r.total + p.runs - 1) / p.runs;
-    if (p.whole > 0) r.run = (r.run + p.whole - 1) / p.whole * p.whole;
-    if (r.run < 1) r.run = 1;
+    r.run = run_of(p, r.total);
     const int64_t f = index * r.run;
     if (f >= before && f < before + sum) {
         int64_t at = before;
@@ -164,11 +175,36 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
     return r;
 }
 
+// The same for at most 32 sequences, by every warp for itself: one round of
+// loads and no block barrier.
+__device__ __forceinline__ Plan plan_find_small(const Params &p, int64_t base, int64_t index, int64_t &s, int64_t &before) {
+    const int lane = threadIdx.x & 31;
+    int64_t cost = 0;
+    if (lane < p.b.n_seqs) {
+        const Seq q = load_seq(p.b, lane, base);
+        cost = (int64_t)seg_rows(p, q) * p.n_kv_heads * seg_tiles(p, q);
+    }
+    int64_t incl = cost;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    Plan r;
+    r.total = __shfl_sync(0xffffffffu, incl, 31);
+    r.run = run_of(p, r.total);
+    const int64_t f = index * r.run;
+    const uint32_t in = __ballot_sync(0xffffffffu, f >= incl - cost && f < incl);
+    s = __ffs(in) - 1;  // -1 past the end
+    before = __shfl_sync(0xffffffffu, incl - cost, in ? (int)s : 0);
+    return r;
+}
+
 // A place on the line: the segment and the tile within it.
 struct Walk {
     int64_t s;       // sequence
-    int64_t seg;     // segment within the sequence: row tile * n_kv_heads + kv head
-    int64_t n_segs;
+    int32_t seg;     // segment within the sequence: row tile * n_kv_heads + kv head
+    int32_t n_segs;  // (n_query * n_heads < 2^31)
     int32_t tiles;   // tiles per segment of this sequence
     int32_t j;       // tile within the segment
     Seq q;
@@ -177,12 +213,12 @@ struct Walk {
         s = s_;
         q = load_seq(p.b, s, base);
         tiles = seg_tiles(p, q);
-        n_segs = (int64_t)seg_rows(p, q) * p.n_kv_heads;
+        n_segs = seg_rows(p, q) * p.n_kv_heads;
     }
     __device__ __forceinline__ void start(const Params &p, int64_t base, int64_t s_, int64_t offset) {
         enter(p, base, s_);
-        seg = offset / tiles;
-        j = (int32_t)(offset - seg * tiles);
+        seg = (int32_t)(offset < INT32_MAX ? (int32_t)offset / tiles : offset / tiles);
+        j = (int32_t)(offset - (int64_t)seg * tiles);
     }
     // to the first tile of the next segment (the line has one)
     __device__ __forceinline__ void next(const Params &p, int64_t base) {
@@ -209,8 +245,9 @@ struct Segment {
 
 __device__ __forceinline__ Segment segment(const Params &p, const Walk &w) {
     Segment g;
-    g.head = (int32_t)(w.seg % p.n_kv_heads);
-    g.r0 = (int32_t)(w.seg / p.n_kv_heads) * ROWS;
+    const int32_t block = p.by_heads.quotient(w.seg);
+    g.head = w.seg - block * p.n_kv_heads;
+    g.r0 = block * ROWS;
     const int32_t left = w.q.q_len * p.group - g.r0;
     g.n_rows = left < ROWS ? left : ROWS;
     g.pos0 = w.q.kv - w.q.q_len;
@@ -267,6 +304,12 @@ __device__ __forceinline__ void row_total(const Shared<DP> *sh, int r, float &m,
     for (int w = 0; w < CONSUMERS; ++w) l += sh->l[w][r] * weight(sh->m[w][r], m);
 }
 
+// One arrival on this barrier's counterpart in CTA `rank` of the cluster,
+// after this thread's earlier accesses (and those it has synchronised with).
+__device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_shared(smem_u32(bar), rank))
+                 : "memory");
+}
 __device__ __forceinline__ float ld_shared_cluster_f1(uint32_t cluster_saddr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_saddr) : "memory");
@@ -333,12 +376,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         raise_error(ENGRAM_ERANGE);
     const int64_t index = blockIdx.x / p.cluster;
     const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
-    const Plan plan = plan_find<NUM_THREADS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+    Plan plan;
+    int64_t at_s, at_before;
+    if (p.b.n_seqs <= 32) {
+        plan = plan_find_small(p, base, index, at_s, at_before);
+        __syncthreads();  // the barriers are initialised
+    } else {
+        plan = plan_find<NUM_THREADS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+        at_s = sh->find_s;
+        at_before = sh->find_before;
+    }
     const int64_t f0 = index * plan.run;
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
     Walk walk;
-    walk.start(p, base, sh->find_s, f0 - sh->find_before);
+    walk.start(p, base, at_s, f0 - at_before);
     uint32_t it = 0;  // tiles through the ring
     // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
     const auto tiles_of = [&](const Segment &g, int64_t f, int32_t &first, int32_t &end) -> int32_t {
@@ -582,7 +634,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int nn = 0; nn < DP / 8; ++nn)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float2 *at = reinterpret_cast<float2 *>(mine + (qr + i * 8) * DP + nn * 8 + qc);
+                            float2 *at = reinterpret_cast<float2 *>(mine + join_at<DP>(qr + i * 8, nn * 8 + qc));
                             float2 v = make_float2(o[nn][2 * i] * fac[i], o[nn][2 * i + 1] * fac[i]);
                             if (half == 0) {
                                 v.x += at->x;
@@ -599,10 +651,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int e = threadIdx.x * 4; e < ROWS * DP; e += 32 * CONSUMERS * 4) {
                 const int r = e / DP, c = e - r * DP;
                 if (r >= g.n_rows) continue;
-                float4 v = *reinterpret_cast<const float4 *>(join + e);
+                const int at = join_at<DP>(r, c);
+                float4 v = *reinterpret_cast<const float4 *>(join + at);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) {
-                    const float4 t = *reinterpret_cast<const float4 *>(join + w * (ROWS * DP) + e);
+                    const float4 t = *reinterpret_cast<const float4 *>(join + w * (ROWS * DP) + at);
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
                 if (sh->bad_hi[turn] >= 0 && c < p.head_dim) {
@@ -614,7 +667,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     v = make_float4(x[0], x[1], x[2], x[3]);
                 }
                 if (p.cluster > 1) {
-                    *reinterpret_cast<float4 *>(join + e) = v;  // read by this thread alone so far
+                    *reinterpret_cast<float4 *>(join + at) = v;  // read by this thread alone so far
                     continue;
                 }
                 if (!whole) {
@@ -641,30 +694,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             if (p.cluster > 1) {  // each CTA joins its share of the values from all shares of the keys, in rank order
                 consumers_sync();
-                if (threadIdx.x == 0) mbar_arrive_cluster_ranks(smem_u32(&sh->ready), p.cluster);
+                if (threadIdx.x < p.cluster) arrive_at(&sh->ready, threadIdx.x);
                 const bool ok = mbar_wait_cluster(&sh->ready, exchange_ph, abort);
                 const int share = ROWS * DP / p.cluster;
                 for (int e = rank * share + threadIdx.x * 4; ok && e < (rank + 1) * share; e += 32 * CONSUMERS * 4) {
                     const int r = e / DP, c = e - r * DP;
                     if (r >= g.n_rows) continue;
-                    float mm = -INFINITY, ll = 0.f;
-                    for (int k = 0; k < p.cluster; ++k) mm = fmaxf(mm, ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tm[r]), k)));
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int k = 0; k < p.cluster; ++k) {
-                        const float w = weight(ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tm[r]), k)), mm);
-                        const float4 x = ld_shared_cluster_f4(mapa_shared(smem_u32(join + e), k));
-                        ll = fmaf(w, ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tl[r]), k)), ll);
-                        v.x = fmaf(w, x.x, v.x);
-                        v.y = fmaf(w, x.y, v.y);
-                        v.z = fmaf(w, x.z, v.z);
-                        v.w = fmaf(w, x.w, v.w);
+                    float mk[MAX_CLUSTER], lk[MAX_CLUSTER], mm = -INFINITY, ll = 0.f;
+                    float4 x[MAX_CLUSTER], v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < MAX_CLUSTER; ++k) {
+                        mk[k] = -INFINITY;
+                        lk[k] = 0.f;
+                        x[k] = v;
+                        if (k < p.cluster) {
+                            mk[k] = ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tm[r]), k));
+                            lk[k] = ld_shared_cluster_f1(mapa_shared(smem_u32(&sh->tl[r]), k));
+                            x[k] = ld_shared_cluster_f4(mapa_shared(smem_u32(join + join_at<DP>(r, c)), k));
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < MAX_CLUSTER; ++k) mm = fmaxf(mm, mk[k]);
+#pragma unroll
+                    for (int k = 0; k < MAX_CLUSTER; ++k) {
+                        const float w = weight(mk[k], mm);
+                        ll = fmaf(w, lk[k], ll);
+                        v.x = fmaf(w, x[k].x, v.x);
+                        v.y = fmaf(w, x[k].y, v.y);
+                        v.z = fmaf(w, x[k].z, v.z);
+                        v.w = fmaf(w, x[k].w, v.w);
                     }
                     write_out<E>(p, walk, g, r, c, v, ll);
                     if (p.lse && c == 0) write_lse(p, walk, g, r, mm, ll);
                 }
                 consumers_sync();
-                if (threadIdx.x == 0) mbar_arrive_cluster_ranks(smem_u32(&sh->done), p.cluster);
+                if (threadIdx.x < p.cluster) arrive_at(&sh->done, threadIdx.x);
                 mbar_wait_cluster(&sh->done, exchange_ph, abort);  // nobody reads this CTA's memory any more
                 exchange_ph ^= 1;
             }
@@ -685,13 +749,21 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     // (it does so after its own wait); the partial results need the wait below.
     const int64_t base = __ldg(p.b.offs);
     const int64_t cut = (int64_t)blockIdx.x + 1;
-    const Plan plan = plan_find<128>(p, base, cut, scan, &find_s, &find_before);
+    Plan plan;
+    int64_t at_s, at_before;
+    if (p.b.n_seqs <= 32) {
+        plan = plan_find_small(p, base, cut, at_s, at_before);
+    } else {
+        plan = plan_find<128>(p, base, cut, scan, &find_s, &find_before);
+        at_s = find_s;
+        at_before = find_before;
+    }
     grid_dependency_wait();
     allow_dependent_launch();
     const int64_t f = cut * plan.run;
     if (f >= plan.total) return;
     Walk w;
-    w.start(p, base, find_s, f - find_before);
+    w.start(p, base, at_s, f - at_before);
     const int64_t first = f - w.j;  // the segment's first tile on the line
     if (w.j == 0 || (cut - 1) * plan.run > first) return;
     const Segment g = segment(p, w);

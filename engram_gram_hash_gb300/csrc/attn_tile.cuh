@@ -115,7 +115,7 @@ struct Params {
     float *part_o;      // [slots][ROWS][DP]
     float *part_ml;     // [slots][2][ROWS]
     int32_t n_heads, n_kv_heads, group, head_dim;
-    Divisor by_group;
+    Divisor by_group, by_heads;  // the query heads of a kv head; the kv heads
     int32_t window;
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t ctas;
@@ -276,9 +276,10 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
 
 // Rows and keys of segment seg = block * n_kv_heads + head of sequence it.q;
 // part it.part of it.splits.
-__device__ __forceinline__ void place(const Params &p, Item &it, int64_t seg) {
-    it.head = (int32_t)(seg % p.n_kv_heads);
-    it.r0 = (int32_t)(seg / p.n_kv_heads) * ROWS;
+__device__ __forceinline__ void place(const Params &p, Item &it, int32_t seg) {
+    const int32_t block = p.by_heads.quotient(seg);
+    it.head = seg - block * p.n_kv_heads;
+    it.r0 = block * ROWS;
     const int32_t left = it.q.q_len * p.group - it.r0;
     it.n_rows = left < ROWS ? left : ROWS;
     it.pos0 = it.q.kv - it.q.q_len;
@@ -312,10 +313,10 @@ __device__ __forceinline__ Item find_item(const Params &p, int64_t base, const P
         const int64_t n = h.segs * it.splits;
         if (at < n) {
             it.part = (int32_t)(at / h.segs);
-            const int64_t k = at - it.part * h.segs;
-            const int32_t block = (int32_t)(k / p.n_kv_heads);
-            const int64_t seg = (int64_t)(h.blocks - 1 - block) * p.n_kv_heads + (k - (int64_t)block * p.n_kv_heads);
-            it.slot += seg * it.splits + it.part;
+            const int32_t k = (int32_t)(at - it.part * h.segs);  // < segs, an int32 (n_query * n_heads < 2^31)
+            const int32_t block = p.by_heads.quotient(k);
+            const int32_t seg = (h.blocks - 1 - block) * p.n_kv_heads + k - block * p.n_kv_heads;
+            it.slot += (int64_t)seg * it.splits + it.part;
             place(p, it, seg);
             return it;
         }
@@ -936,7 +937,7 @@ __global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ 
             slot += h.segs * it.splits;
         }
         it.part = 0;
-        place(p, it, at);
+        place(p, it, (int32_t)at);
         slot += at * it.splits;
         const int r0 = (int)(x % (ROWS / 16)) * 16 + (threadIdx.x >> 5) * R;
         if (r0 >= it.n_rows) continue;

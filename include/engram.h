@@ -557,6 +557,7 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  * 1) <= j <= p (window 0: from 0),
  *   out = sum_j softmax_j(scale * q.k_j) v_j,  lse = ln sum_j exp(scale * q.k_j).
  *   q, out     [n_query][n_heads][D]
+ *              (n_query * n_heads < 2^31)
  *   lse        fp32 [n_query][n_heads] or NULL
  *   workspace  >= engram_paged_attention_workspace_bytes(cfg, n_seqs,
  *              n_query) bytes, 256-byte aligned; scratch, nothing to clear
