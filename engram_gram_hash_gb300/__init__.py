@@ -124,7 +124,7 @@ def lib():
             # structures by plain address (ctypes.byref objects or None pass as void*)
             "engram_qk_norm_rope": ([P, i64, P, P, P, P, i64, P, P, P, P, P], ctypes.c_int),
             "engram_kv_append": ([P, P, P, P, P, P, P, i64, P, P, P, P], ctypes.c_int),
-            "engram_paged_attention_workspace_bytes": ([P, i64, i64], sz),
+            "engram_paged_attention_workspace_bytes": ([P, P, P], sz),
             "engram_paged_attention": ([P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
@@ -861,8 +861,9 @@ def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None,
     return q_out if q is not None else None
 
 
-def engram_paged_attention_workspace_bytes(cfg, n_seqs, n_query):
-    return int(lib().engram_paged_attention_workspace_bytes(ctypes.byref(cfg), int(n_seqs), int(n_query)))
+def engram_paged_attention_workspace_bytes(cfg, cache, batch):
+    """Bytes of workspace that engram_paged_attention needs for this batch (0: none)."""
+    return int(lib().engram_paged_attention_workspace_bytes(cfg.ref, cache.ref, batch.ref))
 
 
 def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
@@ -876,17 +877,19 @@ def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=N
         _need(lse, torch.float32, "lse")
         if lse.shape != shape[:2]:
             raise ValueError(f"lse must be {list(shape[:2])}")
-    L = lib()
+    L, pages = lib(), _cache_of(cache, cfg)
+    ws = None
     if workspace is None:
-        need = L.engram_paged_attention_workspace_bytes(cfg.ref, batch.n_seqs, T)
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+        need = L.engram_paged_attention_workspace_bytes(cfg.ref, pages, batch.ref)
+        if need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     else:
         _need(workspace, torch.uint8, "workspace")
-        need = workspace.numel()
+        need, ws = workspace.numel(), workspace.data_ptr()
     _check(
-        L.engram_paged_attention(cfg.ref, _cache_of(cache, cfg), batch.ref, hq, ho,
-                                 lse.data_ptr() if lse is not None else None, workspace.data_ptr(), need,
-                                 _stream_of(q, stream)),
+        L.engram_paged_attention(cfg.ref, pages, batch.ref, hq, ho, lse.data_ptr() if lse is not None else None, ws,
+                                 need, _stream_of(q, stream)),
         "engram_paged_attention",
     )
     return out

@@ -169,15 +169,17 @@ static size_t rows_workspace_bytes(const engram_attn_config *cfg) {
 //     8,000: 18.5 / - / 16.5;  2 of 2,000: - / 13.6 / 12.9 (17.5 with the second launch's host time);
 //   4 of 2,000: - / 13.8 / 18.3, 4,000: - / 18.5 / 21.1;  16 of 500 whole 12.1, cut 19.5, 2,000: 27 / 33;
 //   64 of 1,000: cut 58, whole 55 with equal lengths, but unequal ones would wait for the longest.
-static void rows_shares(rows::Params &p, const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+struct RowsShares {
+    int32_t cluster, whole, runs;
+    bool cut() const { return whole == 0 && runs > 1; }
+};
+static RowsShares rows_shares(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     const int64_t tiles = (batch->table_stride * cache->page_size + rows::KT - 1) / rows::KT;  // of a segment at most
-    const int64_t group = p.group, seqs = std::min(batch->n_seqs, batch->n_query);
+    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
     const int64_t segs = cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
                                                     (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);  // at most
     const int sms = num_sms();
-    p.cluster = 1;
-    p.whole = 0;
-    p.runs = sms;
+    RowsShares p = {1, 0, sms};
     if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
         p.cluster = 8;
     } else if (tiles > 2 && tiles <= (segs >= 24 ? 64 : 32) && segs * 4 <= sms - 8) {
@@ -189,6 +191,7 @@ static void rows_shares(rows::Params &p, const engram_attn_config *cfg, const en
         p.whole = 1;
         p.runs = (int32_t)segs;
     }
+    return p;
 }
 
 template <typename E, int DP>
@@ -216,7 +219,10 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.box = gcd(cache->page_size, rows::KT);
-    rows_shares(p, cfg, cache, batch);
+    const RowsShares shares = rows_shares(cfg, cache, batch);
+    p.cluster = shares.cluster;
+    p.whole = shares.whole;
+    p.runs = shares.runs;
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     CUtensorMap km, vm;
     if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
@@ -226,7 +232,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows_kernel", km, vm, p);
-    if (s != ENGRAM_OK || p.runs == 1 || p.whole > 0) return s;
+    if (s != ENGRAM_OK || !shares.cut()) return s;
     return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
@@ -249,6 +255,7 @@ static size_t tile_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
 }
 static size_t tile_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
     const int64_t slots = tile_slots(cfg, n_seqs, n_query);
+    if (slots == 0) return 0;
     return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
 
@@ -372,10 +379,21 @@ extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const e
                                      : head_launch<Fp16, true>(cfg, p, (cudaStream_t)stream);
 }
 
-extern "C" size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+namespace engram {
+namespace attn {
+static size_t workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    if (use_tiles(cfg, batch->n_seqs, batch->n_query)) return tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query);
+    return rows_shares(cfg, cache, batch).cut() ? rows_workspace_bytes(cfg) : 0;
+}
+}  // namespace attn
+}  // namespace engram
+
+extern "C" size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                                         const engram_kv_batch *batch) {
     using namespace engram::attn;
-    if (check_attn_config(cfg) != ENGRAM_OK || n_seqs < 0 || n_query < 0) return 0;
-    return use_tiles(cfg, n_seqs, n_query) ? tile_workspace_bytes(cfg, n_seqs, n_query) : rows_workspace_bytes(cfg);
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK || batch->n_query == 0) return 0;
+    if (check_cache(cfg, cache) != ENGRAM_OK) return 0;
+    return workspace_bytes(cfg, cache, batch);
 }
 
 extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
@@ -387,8 +405,9 @@ extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, c
     if (batch->n_query == 0) return ENGRAM_OK;
     if (check_cache(cfg, cache) != ENGRAM_OK || !view_ok(q) || !view_ok(out) || !aligned(lse, 4)) return ENGRAM_EINVAL;
     if (batch->n_query > INT32_MAX / cfg->n_heads) return ENGRAM_EINVAL;
-    if (!workspace || !aligned(workspace, 256)) return ENGRAM_EINVAL;
-    if (workspace_bytes < engram_paged_attention_workspace_bytes(cfg, batch->n_seqs, batch->n_query)) return ENGRAM_ENOMEM;
+    const size_t need = engram::attn::workspace_bytes(cfg, cache, batch);
+    if (need > 0 && (!workspace || !aligned(workspace, 256))) return ENGRAM_EINVAL;
+    if (workspace_bytes < need) return ENGRAM_ENOMEM;
     cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = cfg->dtype == ENGRAM_BF16;
     if (use_tiles(cfg, batch->n_seqs, batch->n_query)) {

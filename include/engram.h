@@ -559,8 +559,10 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  *   q, out     [n_query][n_heads][D]
  *              (n_query * n_heads < 2^31)
  *   lse        fp32 [n_query][n_heads] or NULL
- *   workspace  >= engram_paged_attention_workspace_bytes(cfg, n_seqs,
- *              n_query) bytes, 256-byte aligned; scratch, nothing to clear
+ *   workspace  >= engram_paged_attention_workspace_bytes(cfg, cache, batch)
+ *              bytes, 256-byte aligned; scratch, nothing to clear.  The size
+ *              follows from the descriptions alone (nothing on the device is
+ *              read); where it is 0, NULL will do
  * A query without any key gets out = 0 and lse = -inf.  Cache slots at or past
  * a sequence's length may hold anything, NaN included: they are not used.
  * From one token per sequence to whole prompts, in any mix.  Long sequences
@@ -569,7 +571,8 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  * equal bits.  A page id outside [0, n_pages) sets ENGRAM_ERANGE and reads as
  * zeros.  kv_len beyond the block table sets ENGRAM_ERANGE and is cut there.
  */
-size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query);
+size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache,
+                                              const engram_kv_batch *batch);
 engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
                                      const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
                                      float *lse, void *workspace, size_t workspace_bytes, void *stream);

@@ -85,7 +85,7 @@ BAD_CONFIGS = [
 def test_bad_configs(eg, bad):
     c = _cfg(eg, **bad)
     assert qk(eg, cfg=c) == 1 and append(eg, cfg=c) == 1 and attend(eg, cfg=c) == 1
-    assert eg.engram_paged_attention_workspace_bytes(c, 2, 5) == 0
+    assert eg.lib().engram_paged_attention_workspace_bytes(_ref(c), _ref(_cache(eg)), _ref(_batch(eg))) == 0
 
 
 @pytest.mark.parametrize("bad", [
@@ -117,8 +117,9 @@ def test_bad_views_and_pointers(eg):
     assert qk(eg, pos=None) == 1 and qk(eg, table=None) == 1 and append(eg, table=None) == 1
     assert qk(eg, table=A + 8) == 1 and append(eg, table=A + 4) == 1 and qk(eg, w=A + 8) == 1 and append(eg, w=A + 2) == 1
     assert qk(eg, n=-1) == 1 and qk(eg, rows=-1) == 1 and append(eg, rows=-1) == 1
-    assert attend(eg, lse=A + 2) == 1 and attend(eg, ws=None) == 1 and attend(eg, ws=A + 16) == 1
-    assert attend(eg, ws_bytes=16) == 6
+    long = _batch(eg, n_seqs=5, table_stride=1 << 20)  # needs a workspace
+    assert attend(eg, lse=A + 2) == 1 and attend(eg, batch=long, ws=None) == 1 and attend(eg, batch=long, ws=A + 16) == 1
+    assert attend(eg, batch=long, ws_bytes=16) == 6
 
 
 def test_rows_times_group_must_fit(eg):
@@ -132,11 +133,18 @@ def test_empty_calls_are_no_ops(eg):
     assert qk(eg, n=0, q=None, k=None) == 0 and qk(eg, q=None, k=None) == 0
 
 
-def test_workspace_does_not_grow_with_the_cache(eg):
-    c = _cfg(eg)
-    n = eg.engram_paged_attention_workspace_bytes(c, 1, 1)
-    assert 0 < n <= 64 << 20
-    assert eg.engram_paged_attention_workspace_bytes(c, -1, 1) == 0
+def test_workspace_size(eg):
+    """Follows from the descriptions; none for short block tables, bounded for the longest."""
+    def size(**kw):
+        return eg.lib().engram_paged_attention_workspace_bytes(_ref(_cfg(eg)), _ref(_cache(eg)), _ref(_batch(eg, **kw)))
+
+    assert size(table_stride=4) == 0 and attend(eg, ws=None, ws_bytes=0, batch=_batch(eg, n_query=0)) == 0
+    long = size(n_seqs=5, table_stride=1 << 20)
+    assert 0 < long <= 16 << 20 and size(n_seqs=5, table_stride=1 << 24) == long
+    chunk = size(n_query=2000, table_stride=1 << 20)
+    assert 0 < chunk <= 256 << 20
+    assert size(n_query=1 << 20, table_stride=1 << 20) == 0  # many row blocks: nothing is split
+    assert size(n_query=-1) == 0 and size(n_query=0) == 0
 
 
 def test_binding_checks(eg):

@@ -227,13 +227,19 @@ def test_attention_seq_offsets_base(eg):
     assert torch.equal(a, b)
 
 
-def test_attention_graph_streams_workspace(eg):
+@pytest.mark.parametrize("new, total", [
+    ([1, 1, 1], [500, 70, 3000]),  # clusters, no workspace
+    ([1, 1, 1], [500, 70, 5000]),  # cut and joined
+    ([1, 100, 1], [500, 170, 5000]),  # tiles, split
+])
+def test_attention_graph_streams_workspace(eg, new, total):
     """Captured in a CUDA graph and replayed after the lengths changed; on a stream of its own; with a
     caller's workspace full of NaN."""
-    st = Step(eg, BF16, 8, 2, 128, 16, [1, 1, 1], [500, 70, 3000], seed=10)
+    st = Step(eg, BF16, 8, 2, 128, 16, new, total, seed=10)
     cfg = eg.make_attn_config(8, 2, 128, rope_dim=0)
     full, _ = check_attention(eg, st)
-    n = eg.engram_paged_attention_workspace_bytes(cfg, 3, 3)
+    n = eg.engram_paged_attention_workspace_bytes(cfg, st.cache, st.batch)
+    assert (n > 0) == (total[2] == 5000)
     ws = torch.full((n // 4,), math.nan, device="cuda").view(torch.uint8)
     out = torch.empty_like(full)
     side = torch.cuda.Stream()
@@ -245,7 +251,7 @@ def test_attention_graph_streams_workspace(eg):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         eg.engram_paged_attention(cfg, st.cache, st.batch, st.q, out=out, workspace=ws)
-    st.total = [123, 70, 1]
+    st.total = [123, total[1], 1]
     st.kv_len.copy_(torch.tensor(st.total, dtype=torch.int32))
     graph.replay()
     torch.cuda.synchronize()
