@@ -158,6 +158,21 @@ static size_t rows_workspace_bytes(const engram_attn_config *cfg) {
     return rows_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
 }
 
+// Segments of the rows kernel (row tile x kv head) at most, and the 32 KB key tiles that the block table
+// has room for (in a window's reach).
+static int64_t rows_segs_most(const engram_attn_config *cfg, const engram_kv_batch *batch) {
+    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
+    return cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
+                                      (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);
+}
+static int64_t keys_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const int64_t room = batch->table_stride * cache->page_size;
+    return cfg->window > 0 ? std::min<int64_t>(room, cfg->window + 256) : room;
+}
+static int64_t rows_tiles_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    return (keys_most(cfg, cache, batch) * padded_dim(cfg) + 8191) / 8192;
+}
+
 // How a segment's tiles are shared out.  The lengths are on the device; what is known here is the room
 // of the block tables (tiles at most) and how many segments there are at most.
 //   cluster of 8 or 4: few segments and short tables, one launch.  15 clusters of 8 and 36 of 4 fit the
@@ -174,10 +189,7 @@ struct RowsShares {
     bool cut() const { return whole == 0 && runs > 1; }
 };
 static RowsShares rows_shares(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    const int64_t tiles = (batch->table_stride * cache->page_size + rows::KT - 1) / rows::KT;  // of a segment at most
-    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
-    const int64_t segs = cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
-                                                    (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);  // at most
+    const int64_t tiles = rows_tiles_most(cfg, cache, batch), segs = rows_segs_most(cfg, batch);
     const int sms = num_sms();
     RowsShares p = {1, 0, sms};
     if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
@@ -218,7 +230,8 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.by_heads = Divisor(cfg->n_kv_heads);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
-    p.box = gcd(cache->page_size, rows::KT);
+    p.kt_log2 = rows::Cfg<DP>::KT_LOG2;
+    p.box = gcd(cache->page_size, rows::Cfg<DP>::KT);
     const RowsShares shares = rows_shares(cfg, cache, batch);
     p.cluster = shares.cluster;
     p.whole = shares.whole;
@@ -259,11 +272,21 @@ static size_t tile_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs
     return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
 
-// Query rows per sequence and key/value head from which the 256-row items pay
-// (on average over the batch: the lengths themselves are on the device).
-constexpr int64_t kTileRows = 32;
-static bool use_tiles(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
-    return n_query * (cfg->n_heads / cfg->n_kv_heads) >= kTileRows * n_seqs;
+// Rows kernel or tile kernel: the one whose estimate, in us on this GPU, is less.  A segment of 16 rows
+// costs about 2.5 and 0.6 a 32 KB tile of keys, an item of 256 rows 3 and 1.5 a tile of 128 keys; the tile
+// kernel starts later (14, or 23 with its items split and joined) but has 16 times the rows a tile.
+// Measured, 32 heads of 128 with 8 key/value heads, us rows kernel / tile kernel, new tokens over cached
+// ones: 16 over 4,000 16 / 26, over 16,000 42 / 34; 8 over 16,000 28 / 33; 64 over 4,000 42 / 33; prompts
+// of 64 7.5 / 16.7, 128 13.2 / 18.7, 256 26.5 / 20.4, 512 60.9 / 23.6; 8 sequences of 8 over 2,000 28 / 33,
+// of 16 over 2,000 45 / 33; 64 heads' groups of 4 rows over 4,000 keys (64 values) 130 / 196.
+static bool use_tiles(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const double sms = num_sms();
+    const double segs = (double)rows_segs_most(cfg, batch), items = (double)tile_items_most(cfg, batch->n_seqs, batch->n_query);
+    const double seg_us = 2.5 + 0.6 * (double)rows_tiles_most(cfg, cache, batch);
+    const double item_us = 1.5 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
+    const double rows_us = std::min(7.0 + segs * seg_us / sms, 5.0 + ceil(segs / sms) * seg_us);
+    const double tile_us = std::min(23.0 + items * item_us / sms, 14.0 + ceil(items / sms) * (3.0 + item_us));
+    return tile_us < rows_us;
 }
 
 template <typename E, int DP>
@@ -382,7 +405,7 @@ extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const e
 namespace engram {
 namespace attn {
 static size_t workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    if (use_tiles(cfg, batch->n_seqs, batch->n_query)) return tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query);
+    if (use_tiles(cfg, cache, batch)) return tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query);
     return rows_shares(cfg, cache, batch).cut() ? rows_workspace_bytes(cfg) : 0;
 }
 }  // namespace attn
@@ -410,7 +433,7 @@ extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, c
     if (workspace_bytes < need) return ENGRAM_ENOMEM;
     cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = cfg->dtype == ENGRAM_BF16;
-    if (use_tiles(cfg, batch->n_seqs, batch->n_query)) {
+    if (use_tiles(cfg, cache, batch)) {
         if (padded_dim(cfg) == 64)
             return bf16 ? tile_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
                         : tile_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);

@@ -8,7 +8,7 @@
 // Bound: the bytes of K and V (each is read once, for all the query heads
 // that share it).  A "segment" is one 16-row tile (rows are the pairs (token,
 // query head of the group), consecutive) of one sequence and one key/value
-// head, its work the 64-key tiles in its reach.  The tiles of all segments
+// head, its work the key tiles in its reach.  The tiles of all segments
 // form one line that is cut into equal runs, one per CTA (one CTA per SM):
 // the load is even whatever the lengths are.  A segment inside one run is
 // finished there; a cut one leaves partial (m, l, O) in the workspace, which
@@ -17,10 +17,10 @@
 // takes a segment, a share of its tiles each, and they join through
 // distributed shared memory.
 //
-// Per CTA: a TMA producer warp fills a ring of tiles (K and V of 64 keys,
-// 128-byte swizzle, 32 KB at 128 values; the ring holds what HBM latency
-// needs in flight per SM) and runs ahead across segments; two groups of four
-// warps take tiles in turn, each warp 16 keys of its tile with mma.sync
+// Per CTA: two TMA producer warps (K, V) fill a ring of 32 KB tiles (64 keys of
+// 128 values or 128 of 64, 128-byte swizzle; the ring holds what HBM latency
+// needs in flight per SM) and run ahead across segments; two groups of four
+// warps take tiles in turn, each warp a quarter of its tile's keys with mma.sync
 // m16n8k16 (16 rows need no larger instruction, and the tensor time is a
 // fifth of the tile's memory time), its own m, l and O in registers; the
 // eight warps join through shared memory at the end of the segment.
@@ -31,13 +31,15 @@ namespace attn {
 namespace rows {
 
 constexpr int ROWS = 16;            // query rows per segment
-constexpr int KT = 64;              // keys per tile
 constexpr int CONSUMERS = 8;        // two groups of four warps
 constexpr int MAX_CLUSTER = 8;      // CTAs that share a segment
 constexpr int NUM_THREADS = 384;    // the consumers, and the producer's warpgroup (three idle warps)
 
 template <int DP>
 struct Cfg {
+    static constexpr int KT_LOG2 = DP == 64 ? 7 : 6;
+    static constexpr int KT = 1 << KT_LOG2;       // keys per tile: 32 KB of K and V
+    static constexpr int KPW = KT / 4;            // keys per warp
     static constexpr int KV_BYTES = KT * DP * 2;  // K (or V) of a tile
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     // Even: the two consumer groups take tiles in turn, so a stage then belongs to one group.
@@ -89,6 +91,7 @@ struct Params {
     int32_t n_heads, n_kv_heads, group, head_dim;
     Divisor by_group, by_heads;  // the query heads of a kv head; the kv heads
     int32_t window;
+    int32_t kt_log2;    // Cfg<DP>::KT_LOG2
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
     int32_t runs;       // CTAs of the attention launch
     int32_t cluster;    // CTAs that share a segment through distributed shared memory (1: none; then whole = 1)
@@ -102,11 +105,12 @@ struct Params {
 // so that rows without keys are written too), and its segments per kv head.
 __device__ __forceinline__ int32_t seg_tiles(const Params &p, const Seq &q) {
     if (p.whole > 0) return p.whole;
-    int32_t n = (q.kv + KT - 1) / KT;
+    const int32_t kt = 1 << p.kt_log2;
+    int32_t n = (q.kv + kt - 1) >> p.kt_log2;
     if (p.window > 0) {
         const int32_t tokens = (ROWS - 2) / p.group + 2;  // most tokens that 16 consecutive rows touch
         const int64_t reach = (int64_t)p.window + tokens - 1;
-        const int64_t w = (reach + KT - 2) / KT + 1;
+        const int64_t w = ((reach + kt - 2) >> p.kt_log2) + 1;
         if (w < n) n = (int32_t)w;
     }
     return n > 0 ? n : 1;
@@ -257,8 +261,8 @@ __device__ __forceinline__ Segment segment(const Params &p, const Walk &w) {
     g.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
     g.full_lo = p.window > 0 && last - p.window + 1 > 0 ? last - p.window + 1 : 0;
     if (g.hi < 0) g.hi = 0;
-    g.tile0 = g.lo / KT;
-    g.n_tiles = g.hi > g.lo ? (g.hi + KT - 1) / KT - g.tile0 : 0;
+    g.tile0 = g.lo >> p.kt_log2;
+    g.n_tiles = g.hi > g.lo ? ((g.hi + (1 << p.kt_log2) - 1) >> p.kt_log2) - g.tile0 : 0;
     return g;
 }
 
@@ -345,6 +349,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ Params p) {
     using C = Cfg<DP>;
+    constexpr int KT = C::KT, KPW = C::KPW;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *join = reinterpret_cast<float *>(smem + C::STAGES * C::STAGE_BYTES);
     Shared<DP> *sh = reinterpret_cast<Shared<DP> *>(join + C::JOIN_FLOATS);
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&sh->full[i], 1);
+            mbar_init(&sh->full[i], 2);  // K and V
             mbar_init(&sh->empty[i], 4);
         }
         sh->abort = 0;
@@ -409,9 +414,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // the launch's 384 x 168.
     if (warp >= CONSUMERS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        if (warp == CONSUMERS) {  // ------------------------------------ producer
+        if (warp < CONSUMERS + 2) {  // ---------------------- producers: one warp loads K, the next V
+            const bool is_v = warp == CONSUMERS + 1;
+            const CUtensorMap *const map = is_v ? &v_map : &k_map;
             const int boxes = KT / p.box;
-            const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64) * 2u;
+            const uint32_t box_bytes = (uint32_t)p.box * 128u * (DP / 64);
             for (int64_t f = f0; f < f1;) {
                 const Segment g = segment(p, walk);
                 int32_t first, end;
@@ -445,13 +452,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok && load) {
-                        uint8_t *dst = smem + st * C::STAGE_BYTES + lane * p.box * 128;
+                        uint8_t *dst = smem + st * C::STAGE_BYTES + (is_v ? C::KV_BYTES : 0) + lane * p.box * 128;
                         const int y = (int)(key % p.b.page_size);
 #pragma unroll
-                        for (int c = 0; c < DP / 64; ++c) {
-                            tma_load_4d(dst + c * KT * 128, &k_map, &sh->full[st], c * 64, y, g.head, mine);
-                            tma_load_4d(dst + C::KV_BYTES + c * KT * 128, &v_map, &sh->full[st], c * 64, y, g.head, mine);
-                        }
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_4d(dst + c * KT * 128, map, &sh->full[st], c * 64, y, g.head, mine);
                     }
                 }
                 f += n;
@@ -507,43 +512,49 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if ((int)(it & 1) != grp) continue;
                 const int st = it % C::STAGES;
                 const bool ok = warp_wait(&sh->full[st], (it / C::STAGES) & 1, abort);
-                const int32_t key0 = (g.tile0 + j) * KT + wq * 16;
-                if (ok && key0 < g.hi && key0 + 16 > g.lo) {
-                    const uint32_t kb = smem_u32(smem + st * C::STAGE_BYTES) + wq * 16 * 128;
+                const int32_t key0 = (g.tile0 + j) * KT + wq * KPW;
+                if (ok && key0 < g.hi && key0 + KPW > g.lo) {
+                    const uint32_t kb = smem_u32(smem + st * C::STAGE_BYTES) + wq * KPW * 128;
                     // keys outside [full_lo, full_hi) are hidden from some row; keys outside
                     // [lo, hi) may hold anything
-                    const bool edge = key0 < g.full_lo || key0 + 16 > g.full_hi;
-                    if (edge) {  // half a key's values per lane: this warp's 16 keys are read by no other
-                        const int key = lane >> 1, c0 = (lane & 1) * (DP / 16);
+                    const bool edge = key0 < g.full_lo || key0 + KPW > g.full_hi;
+                    if (edge) {  // this warp's keys are read by no other
+                        constexpr int LANES = 32 / KPW, PIECES = DP / 8 / LANES;  // lanes per key, 16-byte pieces per lane
+                        const int key = lane / LANES, c0 = (lane % LANES) * PIECES;
                         const uint32_t vrow = kb + C::KV_BYTES + key * 128;
                         const auto at = [&](int i) {
                             const int ch = c0 + i;
                             return vrow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4);
                         };
-                        const bool keep = key0 + key >= g.lo && key0 + key < g.hi, bad = holds_nonfinite<E, DP / 16>(keep, at);
+                        const bool keep = key0 + key >= g.lo && key0 + key < g.hi, bad = holds_nonfinite<E, PIECES>(keep, at);
                         if (bad) {
                             atomicMin(&sh->bad_lo[turn], g.tile0 + j);
                             atomicMax(&sh->bad_hi[turn], g.tile0 + j);
                         }
-                        if (bad || !keep) clear_nonfinite<E, DP / 16>(keep, at);
+                        if (bad || !keep) clear_nonfinite<E, PIECES>(keep, at);
                         fence_proxy_async_smem();  // before the ring's next copy over it
                         __syncwarp();
                     }
-                    float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                    float s[KPW / 8][4];  // rows qr (0, 1) and qr + 8 (2, 3), keys 8 t + qc, + 1
+#pragma unroll
+                    for (int t = 0; t < KPW / 8; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
                     {
                         const int key = ((lane >> 4) << 3) + (lane & 7);
                         const uint32_t krow = kb + key * 128;
 #pragma unroll
                         for (int kk = 0; kk < DP / 16; ++kk) {
                             const int ch = kk * 2 + ((lane >> 3) & 1);  // 16-byte piece of the key's row
-                            uint32_t b[4];
-                            ldmatrix_x4(b, krow + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4));
-                            E::mma(s[0], qf[kk], b[0], b[1]);
-                            E::mma(s[1], qf[kk], b[2], b[3]);
+#pragma unroll
+                            for (int b16 = 0; b16 < KPW / 16; ++b16) {
+                                uint32_t b[4];
+                                ldmatrix_x4(b, krow + b16 * 16 * 128 + (ch >> 3) * (KT * 128) + (((ch & 7) ^ (key & 7)) << 4));
+                                E::mma(s[2 * b16], qf[kk], b[0], b[1]);
+                                E::mma(s[2 * b16 + 1], qf[kk], b[2], b[3]);
+                            }
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < KPW / 8; ++t)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             s[t][c] *= p.scale_log2;
@@ -556,7 +567,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     bool same = true;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+                        float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
+#pragma unroll
+                        for (int t = 1; t < KPW / 8; ++t) mx = fmaxf(mx, fmaxf(s[t][2 * i], s[t][2 * i + 1]));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                         mx = fmaxf(mx, m[i]);
@@ -576,19 +589,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
+                    for (int t = 0; t < KPW / 8; ++t)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             s[t][c] = weight(s[t][c], m[c >> 1]);
                             l[c >> 1] += s[t][c];
                         }
-                    // the weights rounded to the values' type: the matrix instruction takes 16-bit
-                    // operands, and a weight's relative error there is the output's own rounding
-                    const uint32_t pa[4] = {E::pack(s[0][0], s[0][1]), E::pack(s[0][2], s[0][3]),
-                                            E::pack(s[1][0], s[1][1]), E::pack(s[1][2], s[1][3])};
-                    {
-                        const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
-                        const uint32_t vrow = kb + C::KV_BYTES + key * 128;
+                    const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+                    for (int b16 = 0; b16 < KPW / 16; ++b16) {
+                        // the weights rounded to the values' type: the matrix instruction takes 16-bit
+                        // operands, and a weight's relative error there is the output's own rounding
+                        const float(&u)[4] = s[2 * b16], (&v)[4] = s[2 * b16 + 1];
+                        const uint32_t pa[4] = {E::pack(u[0], u[1]), E::pack(u[2], u[3]), E::pack(v[0], v[1]), E::pack(v[2], v[3])};
+                        const uint32_t vrow = kb + C::KV_BYTES + (b16 * 16 + key) * 128;
 #pragma unroll
                         for (int nn = 0; nn < DP / 16; ++nn) {
                             const int ch = nn * 2 + (lane >> 4);
