@@ -121,6 +121,7 @@ struct Params {
     int32_t ctas;
     int32_t max_slots;  // 0: nothing is split
     int32_t *cut;       // the plan's cut, for the join
+    int32_t out_by_32;  // output rows are 32-byte aligned
     float scale_log2;
 };
 
@@ -367,6 +368,12 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(is));
     return is != 0;
+}
+// 32 bytes in one store: a thread that holds a row touches each of its lines half as often.
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -655,20 +662,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
                     }
                     if (whole) {
+                        uint32_t u[16];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (c * 32 + i * 8 < p.head_dim) {
-                                uint32_t u[4];
+                        for (int h = 0; h < 16; ++h)
+                            u[h] = E::pack(__uint_as_float(o[2 * h]) * inv, __uint_as_float(o[2 * h + 1]) * inv);
+                        uint16_t *const at = dst + c * 32;
+                        if (p.out_by_32 && c * 32 + 32 <= p.head_dim) {
+                            st_global_v8(at, u);
+                            st_global_v8(at + 16, u + 8);
+                        } else {
 #pragma unroll
-                                for (int h = 0; h < 4; ++h)
-                                    u[h] = E::pack(__uint_as_float(o[i * 8 + 2 * h]) * inv, __uint_as_float(o[i * 8 + 2 * h + 1]) * inv);
-                                *reinterpret_cast<uint4 *>(dst + c * 32 + i * 8) = make_uint4(u[0], u[1], u[2], u[3]);
-                            }
+                            for (int i = 0; i < 4; ++i)
+                                if (c * 32 + i * 8 < p.head_dim)
+                                    *reinterpret_cast<uint4 *>(at + i * 8) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                        }
                     } else if (n > 0) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            *reinterpret_cast<uint4 *>(part + c * 32 + i * 4) =
-                                make_uint4(o[i * 4], o[i * 4 + 1], o[i * 4 + 2], o[i * 4 + 3]);
+                        for (int i = 0; i < 4; ++i) st_global_v8(part + c * 32 + i * 8, o + i * 8);
                     }
                 }
                 tc_fence_before();  // O has been read before the next item's first product is allowed
