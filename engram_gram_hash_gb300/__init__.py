@@ -12,7 +12,7 @@ import os
 
 import torch
 
-from .buildlib import LIB_PATH, build  # noqa: F401
+from .buildlib import LIB_PATH, STEP_PATH, build  # noqa: F401
 
 N_TABLES = 48
 ROW_BYTES = 256
@@ -696,9 +696,7 @@ def make_attn_config(n_heads, n_kv_heads, head_dim, dtype=torch.bfloat16, rope_d
     c.norm_eps = float(norm_eps)
     c.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
     c.window = int(window)
-    # what the calls below look at on every step, as plain Python values
-    c.torch_dtype, c.dim, c.q_heads, c.kv_heads, c.rope = dtype, c.head_dim, c.n_heads, c.n_kv_heads, c.rope_dim
-    c.ref = ctypes.byref(c)
+    c.torch_dtype, c.address = dtype, ctypes.addressof(c)
     return c
 
 
@@ -729,7 +727,7 @@ def kv_cache(k_pages, v_pages):
     c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
     c.tensors = (k_pages, v_pages)
     c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), k_pages.dtype
-    c.ref = ctypes.byref(c)
+    c.address = ctypes.addressof(c)
     return c
 
 
@@ -753,143 +751,57 @@ def kv_batch(seq_offsets, kv_len, block_table, n_query):
     b.seq_offsets, b.kv_len, b.block_table = seq_offsets.data_ptr(), kv_len.data_ptr(), block_table.data_ptr()
     b.table_stride = block_table.shape[1] if n <= 1 else block_table.stride(0)
     b.tensors = (seq_offsets, kv_len, block_table)
-    b.ref = ctypes.byref(b)
+    b.address = ctypes.addressof(b)
     return b
 
 
-def _heads(t, cfg, shape, name):
-    """The engram_heads of a [tokens, heads, head_dim] tensor with contiguous heads."""
-    if t.dtype is not cfg.torch_dtype:
-        raise TypeError(f"{name} must be {cfg.torch_dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    st, sh, sc = t.stride()
-    if sc != 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor with contiguous heads")
-    # the stride of a size of one is never used, and torch may give it any value
-    return ctypes.byref(engram_heads(t.data_ptr(), st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0))
+_step_module = None
 
 
-def _heads_out(out, like, cfg, shape, name):
-    """(the output tensor, its engram_heads): a new contiguous one if none is given."""
-    if out is not None:
-        return out, _heads(out, cfg, shape, name)
-    out = torch.empty(shape, dtype=cfg.torch_dtype, device=like.device)
-    return out, ctypes.byref(engram_heads(out.data_ptr(), shape[1] * shape[2], shape[2]))
+def _step():
+    """The marshalling module of the calls below (csrc/step_binding.cpp; raises if it was never built)."""
+    global _step_module
+    if _step_module is None:
+        import importlib.util
 
-
-def _weight(w, cfg, name):
-    if w is None:
-        return None
-    if w.dtype is not cfg.torch_dtype:
-        raise TypeError(f"{name} must be {cfg.torch_dtype}, got {w.dtype}")
-    if w.numel() != cfg.dim or not w.is_contiguous() or not w.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {cfg.dim} values")
-    return w.data_ptr()
-
-
-def _table(table, cfg):
-    if table is None:
-        if cfg.rope:
-            raise ValueError("table is needed: rope_dim is not 0")
-        return None, 0
-    if table.dtype is not torch.float32:
-        raise TypeError(f"table must be torch.float32, got {table.dtype}")
-    if table.dim() != 2 or table.shape[1] != cfg.rope or not table.is_contiguous() or not table.is_cuda:
-        raise ValueError(f"table must be a contiguous CUDA tensor [positions, {cfg.rope}]")
-    return table.data_ptr(), table.shape[0]
+        if not os.path.exists(STEP_PATH):
+            raise RuntimeError(f"_step.so not built at {STEP_PATH}; run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location(__name__ + "._step", STEP_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(EngramError, *[ctypes.cast(f, ctypes.c_void_p).value
+                              for f in (L.engram_qk_norm_rope, L.engram_kv_append, L.engram_paged_attention,
+                                        L.engram_paged_attention_workspace_bytes)])
+        _step_module = m
+    return _step_module
 
 
 def _cache_of(cache, cfg):
-    if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.kv_heads, cfg.dim):
-        raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.kv_heads, cfg.dim]}")
-    return cache.ref
-
-
-def _stream_of(t, stream):
-    """The handle of `stream`, or of the current stream on t's device."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
+        raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.n_kv_heads, cfg.head_dim]}")
+    return cache.address
 
 
 def engram_qk_norm_rope(cfg, q, k, positions, table, w_q=None, w_k=None, q_out=None, k_out=None, stream=None):
     """(q_out, k_out): every head of q [T, n_heads, D] and k [T, n_kv_heads, D] RMS-normed (with w_q / w_k
     [D]; None: no norm) and rotated by its token's position.  Either of q and k may be None; q_out=q and
     k_out=k work in place."""
-    some = q if q is not None else k
-    T = some.shape[0]
-    hq = hk = ho = hko = pos = None
-    if q is not None:
-        shape = (T, cfg.q_heads, cfg.dim)
-        hq = _heads(q, cfg, shape, "q")
-        q_out, ho = _heads_out(q_out, q, cfg, shape, "q_out")
-    if k is not None:
-        shape = (T, cfg.kv_heads, cfg.dim)
-        hk = _heads(k, cfg, shape, "k")
-        k_out, hko = _heads_out(k_out, k, cfg, shape, "k_out")
-    if positions is not None:
-        _need(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError(f"positions must have {T} entries")
-        pos = positions.data_ptr()
-    tab, rows = _table(table, cfg)
-    _check(
-        lib().engram_qk_norm_rope(cfg.ref, T, hq, hk, pos, tab, rows, _weight(w_q, cfg, "w_q"),
-                                  _weight(w_k, cfg, "w_k"), ho, hko, _stream_of(some, stream)),
-        "engram_qk_norm_rope",
-    )
-    return q_out, k_out
+    return _step().qk_norm_rope(cfg.address, q, k, positions, table, w_q, w_k, q_out, k_out, stream)
 
 
 def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
     """The step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] into their slots of the cache.
     With q [n_query, n_heads, D], also its norm and rotation in the same launch; returns q_out (None without)."""
-    T = batch.n_query
-    shape = (T, cfg.kv_heads, cfg.dim)
-    hk = _heads(k, cfg, shape, "k")
-    hv = _heads(v, cfg, shape, "v")
-    hq = ho = None
-    if q is not None:
-        shape = (T, cfg.q_heads, cfg.dim)
-        hq = _heads(q, cfg, shape, "q")
-        q_out, ho = _heads_out(q_out, q, cfg, shape, "q_out")
-    tab, rows = _table(table, cfg)
-    _check(
-        lib().engram_kv_append(cfg.ref, _cache_of(cache, cfg), batch.ref, hk, hv, _weight(w_k, cfg, "w_k"), tab, rows,
-                               hq, _weight(w_q, cfg, "w_q"), ho, _stream_of(k, stream)),
-        "engram_kv_append",
-    )
-    return q_out if q is not None else None
+    return _step().kv_append(cfg.address, _cache_of(cache, cfg), batch.address, k, v, table, w_k, q, w_q, q_out, stream)
 
 
 def engram_paged_attention_workspace_bytes(cfg, cache, batch):
     """Bytes of workspace that engram_paged_attention needs for this batch (0: none)."""
-    return int(lib().engram_paged_attention_workspace_bytes(cfg.ref, cache.ref, batch.ref))
+    return int(lib().engram_paged_attention_workspace_bytes(cfg.address, cache.address, batch.address))
 
 
 def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
     """out [n_query, n_heads, D]: attention of the step's tokens over the paged cache (and lse fp32
     [n_query, n_heads] if a tensor for it is given)."""
-    T = batch.n_query
-    shape = (T, cfg.q_heads, cfg.dim)
-    hq = _heads(q, cfg, shape, "q")
-    out, ho = _heads_out(out, q, cfg, shape, "out")
-    if lse is not None:
-        _need(lse, torch.float32, "lse")
-        if lse.shape != shape[:2]:
-            raise ValueError(f"lse must be {list(shape[:2])}")
-    L, pages = lib(), _cache_of(cache, cfg)
-    ws = None
-    if workspace is None:
-        need = L.engram_paged_attention_workspace_bytes(cfg.ref, pages, batch.ref)
-        if need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-            ws = workspace.data_ptr()
-    else:
-        _need(workspace, torch.uint8, "workspace")
-        need, ws = workspace.numel(), workspace.data_ptr()
-    _check(
-        L.engram_paged_attention(cfg.ref, pages, batch.ref, hq, ho, lse.data_ptr() if lse is not None else None, ws,
-                                 need, _stream_of(q, stream)),
-        "engram_paged_attention",
-    )
-    return out
+    return _step().paged_attention(cfg.address, _cache_of(cache, cfg), batch.address, q, out, lse, workspace, stream)

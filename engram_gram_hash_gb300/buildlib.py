@@ -1,12 +1,16 @@
-"""Builds libengram.so in-tree with nvcc for sm_103a (two translation units, compiled side by side)."""
+"""Builds libengram.so in-tree with nvcc for sm_103a (two translation units, compiled side by side) and, with
+the host compiler, the binding's marshalling module for the decode-step calls (against torch's headers)."""
 
 import os
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 MAIN_SRCS = [os.path.join(SRC_DIR, f) for f in ("engram_core.cu", "attention.cu")]
 LIB_PATH = os.path.join(HERE, "libengram.so")
+STEP_SRC = os.path.join(SRC_DIR, "step_binding.cpp")
+STEP_PATH = os.path.join(HERE, "_step.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -19,6 +23,26 @@ def sources():
     return out
 
 
+def _stale(path, srcs):
+    if not os.path.exists(path):
+        return True
+    t = os.path.getmtime(path)
+    return any(os.path.getmtime(s) > t for s in srcs)
+
+
+def step_cmd():
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{d}" for d in include], "-o", STEP_PATH, STEP_SRC, f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
 def compile_cmd(src, obj, extra=()):
     return ["nvcc", *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", *extra, "-c", "-o", obj, src]
 
@@ -28,21 +52,21 @@ def link_cmd(objs, out=LIB_PATH):
 
 
 def build(force=False, verbose=False):
-    """Compile if any source is newer than the library; returns its path."""
-    stale = force or not os.path.exists(LIB_PATH)
-    if not stale:
-        t = os.path.getmtime(LIB_PATH)
-        stale = any(os.path.getmtime(s) > t for s in sources())
-    if stale:
+    """Compile what is older than its sources; returns the library's path."""
+    cmds, objs = [], []
+    if force or _stale(LIB_PATH, sources()):
         objs = [os.path.splitext(s)[0] + ".o" for s in MAIN_SRCS]
-        cmds = [compile_cmd(s, o) for s, o in zip(MAIN_SRCS, objs)]
-        if verbose:
-            for cmd in cmds:
-                print(" ".join(cmd))
-        procs = [subprocess.Popen(cmd) for cmd in cmds]
-        codes = [p.wait() for p in procs]
-        for cmd, code in zip(cmds, codes):
-            if code:
-                raise subprocess.CalledProcessError(code, cmd)
+        cmds += [compile_cmd(s, o) for s, o in zip(MAIN_SRCS, objs)]
+    if force or _stale(STEP_PATH, [STEP_SRC, os.path.join(os.path.dirname(HERE), "include", "engram.h")]):
+        cmds.append(step_cmd())
+    if verbose:
+        for cmd in cmds:
+            print(" ".join(cmd))
+    procs = [subprocess.Popen(cmd) for cmd in cmds]
+    codes = [p.wait() for p in procs]
+    for cmd, code in zip(cmds, codes):
+        if code:
+            raise subprocess.CalledProcessError(code, cmd)
+    if objs:
         subprocess.check_call(link_cmd(objs))
     return LIB_PATH

@@ -166,6 +166,10 @@ def test_binding_checks(eg):
         eg.engram_qk_norm_rope(cfg, q.float(), None, pos, table)
     with pytest.raises(ValueError):
         eg.engram_qk_norm_rope(cfg, q[:, :4], None, pos, table)
+    with pytest.raises(ValueError):
+        eg.engram_qk_norm_rope(cfg, None, None, pos, table)
+    with pytest.raises(TypeError):
+        eg.engram_qk_norm_rope(cfg, [1.0], None, pos, table)
 
 
 def test_rope_table(eg):

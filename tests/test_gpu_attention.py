@@ -283,6 +283,61 @@ def test_attention_device_errors(eg):
     assert eg.engram_last_error() == 0
 
 
+def test_refusals_of_the_binding(eg):
+    """Wrong types, shapes, devices and sizes raise before anything is enqueued; a status raises EngramError."""
+    st = Step(eg, BF16, 8, 2, 128, 16, [1, 1], [30, 20], seed=13)
+    cfg, table = eg.make_attn_config(8, 2, 128), eg.rope_table(64, 128)
+    f16 = eg.make_attn_config(8, 2, 128, dtype=FP16)
+    w = torch.ones(128, device="cuda", dtype=BF16)
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    cases = [
+        (TypeError, lambda: eg.engram_qk_norm_rope(f16, st.q, None, pos, table)),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.k, None, pos, table)),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q[:1], st.k, pos, table)),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos[:1], table)),
+        (TypeError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos.long(), table)),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, table[:, :64].contiguous())),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, None)),
+        (TypeError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, table.half())),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, table, w_q=w[:64])),
+        (TypeError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, table, w_q=w.float())),
+        (ValueError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, pos, table, q_out=torch.empty_like(st.q)[:1])),
+        (eg.EngramError, lambda: eg.engram_qk_norm_rope(cfg, st.q, None, None, table)),
+        (ValueError, lambda: eg.engram_kv_append(f16, st.cache, st.batch, st.k, st.v, table)),
+        (ValueError, lambda: eg.engram_kv_append(cfg, st.cache, st.batch, st.k[:1], st.v, table)),
+        (ValueError, lambda: eg.engram_kv_append(cfg, st.cache, st.batch, st.k, None, table)),
+        (ValueError, lambda: eg.engram_paged_attention(cfg, st.cache, st.batch, st.q[:1])),
+        (ValueError, lambda: eg.engram_paged_attention(cfg, st.cache, st.batch, st.q.cpu())),
+        (ValueError, lambda: eg.engram_paged_attention(cfg, st.cache, st.batch, st.q, lse=torch.empty(2, 4, device="cuda"))),
+        (TypeError, lambda: eg.engram_paged_attention(cfg, st.cache, st.batch, st.q, workspace=torch.empty(9, device="cuda"))),
+    ]
+    for i, (error, call) in enumerate(cases):
+        with pytest.raises(error):
+            call()
+            pytest.fail(f"case {i} was accepted")
+    wide = eg.kv_batch(st.seq_offsets, st.kv_len, torch.zeros((2, 1 << 14), dtype=torch.int32, device="cuda"), 2)
+    with pytest.raises(eg.EngramError) as e:
+        eg.engram_paged_attention(cfg, st.cache, wide, st.q, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 6  # ENGRAM_ENOMEM
+    assert eg.engram_last_error() == 0
+
+
+def test_calls_on_another_stream(eg):
+    """With stream= the outputs and workspace made by the call belong to that stream: many calls there give
+    the bits of the current stream's, with other work allocating in between."""
+    st = Step(eg, BF16, 8, 2, 128, 16, [1, 60, 1], [500, 170, 6000], seed=14)
+    cfg = eg.make_attn_config(8, 2, 128, rope_dim=0)
+    ref = eg.engram_paged_attention(cfg, st.cache, st.batch, st.q)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for _ in range(20):
+        outs.append(eg.engram_paged_attention(cfg, st.cache, st.batch, st.q, stream=side))
+        torch.full((1 << 20,), math.nan, device="cuda")
+    side.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
 # ------------------------------------------------------------ norm, rotation ----
 
 HEADS = [  # dtype, heads, kv_heads, dim, rope
