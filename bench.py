@@ -102,11 +102,14 @@ def _code_only(src):
 
 
 def kernel_source_hash():
-    """sha256 prefix of the kernel sources' code (comments and spacing aside):
+    """sha256 prefix of the code of the Engram read's kernel sources (comments
+    and spacing aside; the attention step is a translation unit of its own):
     the DRAM-traffic figures under profiles/ are used only while it matches."""
     h = hashlib.sha256()
     d = os.path.join(ROOT, "engram_gram_hash_gb300", "csrc")
     for f in sorted(os.listdir(d)):
+        if not f.endswith((".cu", ".cuh")) or f.startswith(("attn_", "attention", "qk_rope")):
+            continue
         with open(os.path.join(d, f), encoding="utf-8") as fh:
             h.update(f.encode() + b"\0" + _code_only(fh.read()).encode())
     return h.hexdigest()[:16]

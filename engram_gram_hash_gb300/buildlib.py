@@ -9,6 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 MAIN_SRCS = [os.path.join(SRC_DIR, f) for f in ("engram_core.cu", "attention.cu")]
 LIB_PATH = os.path.join(HERE, "libengram.so")
+OBJ_DIR = os.path.join(HERE, "_build")
 STEP_SRC = os.path.join(SRC_DIR, "step_binding.cpp")
 STEP_PATH = os.path.join(HERE, "_step.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,7 +56,8 @@ def build(force=False, verbose=False):
     """Compile what is older than its sources; returns the library's path."""
     cmds, objs = [], []
     if force or _stale(LIB_PATH, sources()):
-        objs = [os.path.splitext(s)[0] + ".o" for s in MAIN_SRCS]
+        os.makedirs(OBJ_DIR, exist_ok=True)
+        objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in MAIN_SRCS]
         cmds += [compile_cmd(s, o) for s, o in zip(MAIN_SRCS, objs)]
     if force or _stale(STEP_PATH, [STEP_SRC, os.path.join(os.path.dirname(HERE), "include", "engram.h")]):
         cmds.append(step_cmd())
