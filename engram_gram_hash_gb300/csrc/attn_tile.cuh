@@ -155,6 +155,34 @@ __device__ __forceinline__ int32_t splits_of(int32_t tiles, int32_t cut) {
     return tiles > cut ? (tiles + cut - 1) / cut : 1;
 }
 
+// The candidate that takes the least time, by a warp: lane c < N_CAND with the
+// items and parts of candidate c and its cut.  Times are in tiles: equal items
+// go in rounds; items of unequal size fill each other's gaps (half the longest
+// is left over).  An item costs about two tiles beside its own, a part about
+// five (its partial result is written and read again).
+__device__ __forceinline__ int32_t best_cut(const Params &p, float items, float parts, float work, int32_t cut_c) {
+    const int lane = threadIdx.x & 31;
+    float best = INFINITY;
+    int32_t cut = INT32_MAX;
+    if (lane < N_CAND) {
+        const float g = (float)p.ctas, rounds = ceilf(items / g);
+        const float span = items <= g ? (float)cut_c : (work > 0.85f * items * cut_c ? rounds * cut_c : work / g + 0.5f * cut_c);
+        const bool whole = kSplits[lane] == 1;
+        if (whole || parts <= (float)p.max_slots) best = span + rounds * (whole ? 2.f : 5.f);
+        cut = whole ? INT32_MAX : cut_c;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {  // of equals the first candidate (lower lane)
+        const float ob = __shfl_down_sync(0xffffffffu, best, o);
+        const int32_t oc = __shfl_down_sync(0xffffffffu, cut, o);
+        if (ob < best) {
+            best = ob;
+            cut = oc;
+        }
+    }
+    return __shfl_sync(0xffffffffu, cut, 0);
+}
+
 // The sums over the chunks of sequences, by all threads of a block of at least
 // CHUNKS threads: a[c + 1] and b[c + 1] from per(s), a pair of counts.
 template <typename F>
@@ -238,30 +266,8 @@ __device__ void make_plan(const Params &p, int64_t base, PlanShared *sh) {
             atomicAdd(&sh->cand_parts[c], parts);
         }
         __syncthreads();
-        // The time of each candidate in tiles: equal items go in rounds; items
-        // of unequal size fill each other's gaps (half the longest is left
-        // over).  An item costs about two tiles beside its own, a part about
-        // five (its partial result is written and read again).
         if (tid < 32) {
-            float best = INFINITY;
-            int cut = INT32_MAX;
-            if (lane < N_CAND) {
-                const float n = (float)sh->cand_items[lane], w = (float)sh->work, g = (float)p.ctas;
-                const float rounds = ceilf(n / g);
-                const float span = n <= g ? (float)cut_c : (w > 0.85f * n * cut_c ? rounds * cut_c : w / g + 0.5f * cut_c);
-                const float each = kSplits[lane] > 1 ? 5.f : 2.f;
-                if (kSplits[lane] == 1 || sh->cand_parts[lane] <= (unsigned long long)p.max_slots) best = span + rounds * each;
-                cut = kSplits[lane] == 1 ? INT32_MAX : cut_c;
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {  // the least; of equals the first candidate (lower lane)
-                const float ob = __shfl_down_sync(0xffffffffu, best, o);
-                const int oc = __shfl_down_sync(0xffffffffu, cut, o);
-                if (ob < best) {
-                    best = ob;
-                    cut = oc;
-                }
-            }
+            const int32_t cut = best_cut(p, (float)sh->cand_items[c], (float)sh->cand_parts[c], (float)sh->work, cut_c);
             if (lane == 0) sh->cut = cut;
         }
         __syncthreads();
@@ -297,6 +303,17 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int32_t seg) {
     it.n = b - a;
 }
 
+// Item `at` of sequence it.s, of segs x it.splits (it.q, it.splits and it.slot,
+// the parts before the sequence, are set).
+__device__ __forceinline__ void locate(const Params &p, Item &it, int64_t at, int32_t segs, int32_t blocks) {
+    it.part = (int32_t)(at < INT32_MAX ? (int32_t)at / segs : at / segs);
+    const int32_t k = (int32_t)(at - (int64_t)it.part * segs);  // < segs, an int32 (n_query * n_heads < 2^31)
+    const int32_t block = p.by_heads.quotient(k);
+    const int32_t seg = (blocks - 1 - block) * p.n_kv_heads + k - block * p.n_kv_heads;
+    it.slot += (int64_t)seg * it.splits + it.part;
+    place(p, it, seg);
+}
+
 // Item number `index` of the plan (every thread of the caller alike).
 // Parts outermost (all heads and blocks go over the same keys at about the
 // same time and share them through L2), the longest blocks first, heads
@@ -313,17 +330,86 @@ __device__ __forceinline__ Item find_item(const Params &p, int64_t base, const P
         it.splits = splits_of(h.tiles, sh->cut);
         const int64_t n = h.segs * it.splits;
         if (at < n) {
-            it.part = (int32_t)(at / h.segs);
-            const int32_t k = (int32_t)(at - it.part * h.segs);  // < segs, an int32 (n_query * n_heads < 2^31)
-            const int32_t block = p.by_heads.quotient(k);
-            const int32_t seg = (h.blocks - 1 - block) * p.n_kv_heads + k - block * p.n_kv_heads;
-            it.slot += (int64_t)seg * it.splits + it.part;
-            place(p, it, seg);
+            locate(p, it, at, (int32_t)h.segs, h.blocks);
             return it;
         }
         at -= n;
         if (it.splits > 1) it.slot += n;
     }
+}
+
+// The same plan for at most 32 sequences, by one warp (the one that finds the
+// items: no block barrier, and no other role waits for it).  Here the sequences
+// go longest parts first, too.
+struct WarpPlan {
+    int64_t total;   // items in all
+    int32_t cut;
+    // of this lane's sequence: the items before it and its own, the parts before it
+    int64_t before, items, slots;
+    int32_t segs, blocks, splits;
+};
+__device__ __forceinline__ WarpPlan plan_warp(const Params &p, int64_t base) {
+    const int lane = threadIdx.x & 31, n = (int)p.b.n_seqs;
+    WarpPlan w;
+    Share h = {0, 0, 0, 0};
+    if (lane < n) h = share(p, load_seq(p.b, lane, base));
+    w.segs = (int32_t)h.segs;
+    w.blocks = h.blocks;
+    w.cut = INT32_MAX;
+    if (p.max_slots > 0) {
+        int64_t work = h.segs * h.mean;
+        int32_t most = h.segs > 0 && h.tiles > 1 ? h.tiles : 1;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            work += __shfl_xor_sync(0xffffffffu, work, o);
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+        }
+        const int32_t cut_c = (most + kSplits[lane & 15] - 1) / kSplits[lane & 15];
+        float items = 0.f, parts = 0.f;
+        for (int i = 0; 2 * i < n; ++i) {  // a candidate per lane, the sequences by halves of the warp
+            const int s = 2 * i + (lane >> 4);
+            const int32_t segs = __shfl_sync(0xffffffffu, w.segs, s & 31), tiles = __shfl_sync(0xffffffffu, h.tiles, s & 31);
+            if (s >= n) continue;
+            const int32_t k = splits_of(tiles, cut_c);
+            items += (float)segs * k;
+            if (k > 1) parts += (float)segs * k;
+        }
+        items += __shfl_xor_sync(0xffffffffu, items, 16);
+        parts += __shfl_xor_sync(0xffffffffu, parts, 16);
+        w.cut = best_cut(p, items, parts, (float)work, cut_c);
+    }
+    w.splits = splits_of(h.tiles, w.cut);
+    w.items = h.segs * w.splits;
+    const int32_t size = (h.tiles + w.splits - 1) / w.splits;  // tiles of a part
+    w.total = w.before = w.slots = 0;
+    for (int s = 0; s < n; ++s) {
+        const int64_t items = __shfl_sync(0xffffffffu, w.items, s);
+        const int32_t other = __shfl_sync(0xffffffffu, size, s), k = __shfl_sync(0xffffffffu, w.splits, s);
+        w.total += items;
+        if (other > size || (other == size && s < lane)) w.before += items;
+        if (s < lane && k > 1) w.slots += items;
+    }
+    return w;
+}
+// Item number `index` < total of the plan, each lane its own (the whole warp calls).
+__device__ __forceinline__ Item find_item_warp(const Params &p, int64_t base, const WarpPlan &w, int64_t index) {
+    int cur = 0;
+    for (int s = 0; s < (int)p.b.n_seqs; ++s) {
+        const int64_t b = __shfl_sync(0xffffffffu, w.before, s), n = __shfl_sync(0xffffffffu, w.items, s);
+        if (index >= b && index < b + n) cur = s;
+    }
+    Item it;
+    it.s = cur;
+    it.slot = __shfl_sync(0xffffffffu, w.slots, cur);
+    it.splits = __shfl_sync(0xffffffffu, w.splits, cur);
+    const int64_t at = index - __shfl_sync(0xffffffffu, w.before, cur);
+    const int32_t segs = __shfl_sync(0xffffffffu, w.segs, cur), blocks = __shfl_sync(0xffffffffu, w.blocks, cur);
+    it.n_rows = 0;
+    if (index < w.total) {
+        it.q = load_seq(p.b, cur, base);
+        locate(p, it, at, segs, blocks);
+    }
+    return it;
 }
 
 // ---------------------------------------------------------------- helpers ----
@@ -444,11 +530,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.b.offs + p.b.n_seqs) - base != p.b.n_query)
         raise_error(ENGRAM_ERANGE);
     tc_fence_before();
-    make_plan<NUM_THREADS>(p, base, &sh->plan);  // synchronises the block
+    const bool few = p.b.n_seqs <= 32;  // then the items' warp plans alone, below
+    if (few) {
+        __syncthreads();
+    } else {
+        make_plan<NUM_THREADS>(p, base, &sh->plan);  // synchronises the block
+        if (blockIdx.x == 0 && threadIdx.x == 0 && p.cut) *p.cut = sh->plan.cut;
+    }
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
-    const int64_t n_items = sh->plan.items[CHUNKS];
-    if (blockIdx.x == 0 && threadIdx.x == 0 && p.cut) *p.cut = sh->plan.cut;
 
     // Item number i of this CTA, for a whole warp: every role takes all of them in order (null after a time-out).
     const auto take = [&](uint32_t i) -> const Item * {
@@ -712,13 +802,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (p.head_dim > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
                 }
             };
+            WarpPlan plan;
+            if (few) {
+                plan = plan_warp(p, base);
+                if (blockIdx.x == 0 && lane == 0 && p.cut) *p.cut = plan.cut;
+            } else {
+                plan.total = sh->plan.items[CHUNKS];
+            }
             bool ok = true, more = true;
             for (uint32_t i0 = 0; ok && more; i0 += 32) {
                 const uint32_t i = i0 + lane;
                 const int64_t index = (int64_t)i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
                 Item mine;
                 mine.n_rows = 0;
-                if (index < n_items) mine = find_item(p, base, &sh->plan, index);
+                if (few)
+                    mine = find_item_warp(p, base, plan, index);
+                else if (index < plan.total)
+                    mine = find_item(p, base, &sh->plan, index);
                 for (int k = 0; ok && more && k < 32; ++k) {
                     if (lane == k) {
                         if (i >= ITEMS) ok = mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort);
