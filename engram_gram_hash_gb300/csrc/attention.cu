@@ -255,9 +255,12 @@ static int64_t tile_items_most(const engram_attn_config *cfg, int64_t n_seqs, in
     const int64_t seqs = n_seqs < n_query ? n_seqs : n_query;
     return (rows / tile::ROWS + seqs) * cfg->n_kv_heads;
 }
-// Slots for partial results.  With six items a SM or more nothing is split (the last round is at most
-// a sixth of the time, and the parts cost about as much), so none are needed and no join follows.
-static int64_t tile_slots(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+// Slots for partial results.  Nothing is split, none are needed and no join follows with six items a SM
+// or more (the last round is at most a sixth of the time, and the parts cost about as much) or with at
+// most six tiles of keys (a part costs about five).
+static int64_t tile_slots(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const int64_t n_seqs = batch->n_seqs, n_query = batch->n_query;
+    if (keys_most(cfg, cache, batch) <= 6 * tile::KT) return 0;
     const int64_t least = (n_query * (cfg->n_heads / cfg->n_kv_heads) + tile::ROWS - 1) / tile::ROWS * cfg->n_kv_heads;
     if (least >= (int64_t)num_sms() * 6) return 0;
     return std::min<int64_t>((int64_t)num_sms() * tile::SLOTS_PER_SM,
@@ -266,8 +269,8 @@ static int64_t tile_slots(const engram_attn_config *cfg, int64_t n_seqs, int64_t
 static size_t tile_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
     return up256((size_t)slots * tile::ROWS * padded_dim(cfg) * sizeof(float));
 }
-static size_t tile_workspace_bytes(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
-    const int64_t slots = tile_slots(cfg, n_seqs, n_query);
+static size_t tile_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    const int64_t slots = tile_slots(cfg, cache, batch);
     if (slots == 0) return 0;
     return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
@@ -295,7 +298,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
                                  float *lse, void *workspace, cudaStream_t st) {
     tile::Params p;
     memset(&p, 0, sizeof(p));
-    const int64_t slots = tile_slots(cfg, batch->n_seqs, batch->n_query);
+    const int64_t slots = tile_slots(cfg, cache, batch);
     p.b = device_batch(batch, cache);
     p.q = static_cast<const uint16_t *>(q->data);
     p.q_token_stride = q->token_stride;
@@ -320,7 +323,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.out_by_32 = aligned(out->data, 32) && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
     p.cut = slots == 0 ? nullptr
                        : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
-                                                     tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query) - 256);
+                                                     tile_workspace_bytes(cfg, cache, batch) - 256);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     CUtensorMap km, vm;
     if (!page_map(&km, cfg, cache, cache->k, p.box) || !page_map(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
@@ -406,7 +409,7 @@ extern "C" engram_status engram_kv_append(const engram_attn_config *cfg, const e
 namespace engram {
 namespace attn {
 static size_t workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    if (use_tiles(cfg, cache, batch)) return tile_workspace_bytes(cfg, batch->n_seqs, batch->n_query);
+    if (use_tiles(cfg, cache, batch)) return tile_workspace_bytes(cfg, cache, batch);
     return rows_shares(cfg, cache, batch).cut() ? rows_workspace_bytes(cfg) : 0;
 }
 }  // namespace attn
