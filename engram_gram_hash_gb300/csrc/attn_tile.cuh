@@ -24,8 +24,8 @@
 // The running maximum moves only when a row's new maximum exceeds it by 2^8
 // (then O and the sum are scaled): weights stay below 2^8, far inside both
 // 16-bit types, and most tiles need no pass over O.  O is complete up to the
-// tile before whenever new scores arrive (one in-order MMA queue), so the
-// softmax warps scale it themselves.
+// tile before whenever new scores arrive (one in-order MMA queue; APART: when
+// pv_done says so), so the softmax warps scale it themselves.
 //
 // Few items are split along the keys (by the plan below) and leave partial
 // (m, l, O) for tile_join_kernel.
@@ -56,6 +56,12 @@ struct Cfg {
     static constexpr int Q_BYTES = MT * DP * 2;      // one row tile
     static constexpr int O_COL = 256;                // TMEM: scores in columns 0..255, then the outputs
     static constexpr int TMEM_COLS = 512;
+    // Up to 64 values TMEM has room for the weights beside the scores: the next scores are then
+    // computed while a tile's weights are.  Weights over the scores there: 7 sequences of 440 new
+    // tokens over 8,001 294 us instead of 283, one of 4,096 over 28,672 1,294 instead of 1,234 (32/4
+    // heads of 64).  With 128 values O takes the columns that this needs.
+    static constexpr bool APART = DP == 64;
+    static constexpr int P_COL = APART ? O_COL + 2 * DP : 0;  // weights: 64 columns a row tile, or over the scores
 };
 
 struct PlanShared {
@@ -87,6 +93,8 @@ struct Shared {
     uint64_t q_full[2];
     uint64_t s_full[2];
     uint64_t p_ready[2][P_PARTS];
+    uint64_t s_free[2];   // APART: the scores have been read
+    uint64_t pv_done[2];  // APART: the weights have been used, O is up to date
     uint64_t o_full[2];
     uint64_t turn[2];
     uint64_t drained[2];
@@ -507,6 +515,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_init(&sh->q_full[i], 4);
             mbar_init(&sh->s_full[i], 1);
             for (int c = 0; c < P_PARTS; ++c) mbar_init(&sh->p_ready[i][c], 4);
+            mbar_init(&sh->s_free[i], 4);
+            mbar_init(&sh->pv_done[i], 1);
             mbar_init(&sh->turn[i], 1);
             mbar_init(&sh->drained[i], 1);
             mbar_init(&sh->o_full[i], 1);
@@ -553,7 +563,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int row = (warp & 3) * 32 + lane;   // row of the tile: this thread's TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + t * KT, o_tm = tmem + lanes + C::O_COL + t * DP;
-        uint32_t s_ph = 0, o_ph = 0, it = 0;
+        const uint32_t p_tm = C::APART ? tmem + lanes + C::P_COL + t * 64 : s_tm;
+        uint32_t s_ph = 0, o_ph = 0, it = 0, pv_ph = 0;
         bool ok = true;
 
         // The tile's query rows into shared memory by asynchronous copies, 16 bytes a lane and round
@@ -649,7 +660,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     float part[4];  // independent chains: one alone would wait out each maximum's latency
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        if (h) tmem_ld_wait();
+                        if (h) {
+                            tmem_ld_wait();
+                            if (C::APART) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&sh->s_free[t]);
+                            }
+                        }
 #pragma unroll
                         for (int i = h * 64; i < h * 64 + 64; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
                         if (edge) {
@@ -666,6 +684,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             part[(i >> 1) & 3] = i < 8 ? fmaxf(s[i], s[i + 1]) : max3(part[(i >> 1) & 3], s[i], s[i + 1]);
                     }
                     const float mx = fmaxf(max3(part[0], part[1], part[2]), part[3]);
+                    if (C::APART) {  // the tile before is in O, its weights are used (before the first there is none)
+                        ok = warp_wait(&sh->pv_done[t], pv_ph ^ 1, abort);
+                        pv_ph ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                     float up = 1.f;
                     if ((mx - m) * p.scale_log2 > RESCALE_LOG2) {  // also from -inf
                         up = rows::exp2_approx((m - mx) * p.scale_log2);
@@ -697,7 +721,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             sum[i & 1] = add2(sum[i & 1], x);
                             pk[i] = E::pack(x.x, x.y);  // 16-bit operands of the second product
                         }
-                        tmem_st_32x32b_x16(s_tm + c * 16, pk);
+                        tmem_st_32x32b_x16(p_tm + c * 16, pk);
                         if ((c + 1) % (4 / P_PARTS) == 0) {  // the second product may start on these keys
                             tmem_st_wait();
                             tc_fence_before();
@@ -908,8 +932,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const uint64_t v_desc = smem_desc(kva, KT * 128, 1024, kSwizzle128B);
             const uint32_t s_tm = __shfl_sync(0xffffffffu, tmem, 0) + t * KT;
             const uint32_t o_tm = __shfl_sync(0xffffffffu, tmem, 0) + C::O_COL + t * DP;
+            const uint32_t p_tm = C::APART ? __shfl_sync(0xffffffffu, tmem, 0) + C::P_COL + t * 64 : s_tm;
             uint32_t st = 0, st_ph = 0;  // ring entry to consume next, and its phase
-            uint32_t q_ph = 0, p_ph = 0, turn_ph = 0;
+            uint32_t q_ph = 0, p_ph = 0, turn_ph = 0, s_ph = 0;
             bool ok = true;
             const auto advance = [&] {
                 if (++st == C::STAGES) st = 0, st_ph ^= 1;
@@ -926,9 +951,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             };
             // Row tile 0 has the first turn: its first wait finds the phase before the first complete.
             const auto my_turn = [&](bool both) {
-                if (!both) return true;
+                if (C::APART || !both) return true;
                 const bool r = warp_wait(&sh->turn[t], turn_ph ^ (t == 0), abort);
                 turn_ph ^= 1;
+                return r;
+            };
+            // APART: the scores before have been read (before the first there are none).
+            const auto scores_free = [&] {
+                if (!C::APART) return true;
+                const bool r = warp_wait(&sh->s_free[t], s_ph ^ 1, abort);
+                s_ph ^= 1;
                 return r;
             };
             for (uint32_t i = 0; ok; ++i) {
@@ -950,13 +982,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     }
                     continue;
                 }
-                ok = warp_wait(&sh->q_full[t], q_ph, abort) && warp_wait(&sh->kv_full[st], st_ph, abort) && my_turn(both);
+                ok = warp_wait(&sh->q_full[t], q_ph, abort) && warp_wait(&sh->kv_full[st], st_ph, abort) && scores_free() &&
+                     my_turn(both);
                 if (!ok) break;
                 q_ph ^= 1;
                 tc_fence_after();
                 if (leader) {
                     scores();
-                    if (both) mbar_arrive(&sh->turn[t ^ 1]);
+                    if (!C::APART && both) mbar_arrive(&sh->turn[t ^ 1]);
                 }
                 advance();
                 for (int32_t j = 0; j < n; ++j) {
@@ -965,8 +998,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const uint64_t v0 = v_desc + v * (C::STAGE_BYTES >> 4);
                     ok = warp_wait(&sh->kv_full[v], st_ph, abort);
                     advance();
-                    ok = ok && (!more || warp_wait(&sh->kv_full[st], st_ph, abort)) &&
-                         warp_wait(&sh->p_ready[t][0], p_ph, abort) && my_turn(both);
+                    ok = ok && (!more || warp_wait(&sh->kv_full[st], st_ph, abort));
+                    if (C::APART && more && ok) {
+                        ok = scores_free();
+                        tc_fence_after();
+                        if (ok && leader) scores();
+                    }
+                    ok = ok && warp_wait(&sh->p_ready[t][0], p_ph, abort) && my_turn(both);
 #pragma unroll
                     for (int c = 0; c < P_PARTS; ++c) {
                         if (c) ok = ok && warp_wait(&sh->p_ready[t][c], p_ph, abort);
@@ -975,17 +1013,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         if (leader) {
 #pragma unroll
                             for (int k = c * (KT / 16 / P_PARTS); k < (c + 1) * (KT / 16 / P_PARTS); ++k)
-                                mma_ts(o_tm, s_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                                mma_ts(o_tm, p_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
                         }
                     }
                     if (!ok) break;
                     p_ph ^= 1;
                     if (leader) {
-                        if (more)
-                            scores();
-                        else
+                        if (C::APART) mma_commit(&sh->pv_done[t]);
+                        if (!more)
                             mma_commit(&sh->o_full[t]);
-                        if (both) mbar_arrive(&sh->turn[t ^ 1]);
+                        else if (!C::APART)
+                            scores();
+                        if (!C::APART && both) mbar_arrive(&sh->turn[t ^ 1]);
                         mma_commit(&sh->kv_empty[v]);
                     }
                     if (more) advance();
