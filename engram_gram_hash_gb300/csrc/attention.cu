@@ -275,20 +275,24 @@ static size_t tile_workspace_bytes(const engram_attn_config *cfg, const engram_k
     return tile_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
 
-// Rows kernel or tile kernel: the one whose estimate, in us on this GPU, is less.  A segment of 16 rows
-// costs about 2.5 and 0.6 a 32 KB tile of keys, an item of 256 rows 3 and 1.5 a tile of 128 keys; the tile
-// kernel starts later (14, or 23 with its items split and joined) but has 16 times the rows a tile.
-// Measured, 32 heads of 128 with 8 key/value heads, us rows kernel / tile kernel, new tokens over cached
-// ones: 16 over 4,000 16 / 26, over 16,000 42 / 34; 8 over 16,000 28 / 33; 64 over 4,000 42 / 33; prompts
-// of 64 7.5 / 16.7, 128 13.2 / 18.7, 256 26.5 / 20.4, 512 60.9 / 23.6; 8 sequences of 8 over 2,000 28 / 33,
-// of 16 over 2,000 45 / 33; 64 heads' groups of 4 rows over 4,000 keys (64 values) 130 / 196.
+// Rows kernel or tile kernel: the one whose estimate, in us on this GPU, is less.  Both count the parts of
+// sequences of the mean number of rows (the lengths are on the device): a segment of 16 rows costs 2.5 and
+// 0.6 a 32 KB tile of keys, an item of 256 rows 3.7 and 1.6 a tile of 128 keys; whole rounds of them, or
+// equal shares after a later start (split and joined).  Fitted to 197 measured pairs (8, 4 and 32 key/value
+// heads, 1 to 40 sequences of 2 to 256 new tokens over 1 to 16,000): the choice costs 0.1 % over the better
+// kernel in the mean and 13 % at worst.  Of them, 32 heads of 128 with 8 key/value heads, us rows kernel /
+// tile kernel, new tokens over cached ones: 8 over 16,000 28 / 33, 16 42 / 34; 64 over 4,000 42 / 30; prompts
+// of 64 7.6 / 10.6, 128 13.3 / 12.9, 256 27 / 15; 8 sequences of 4 over 16,000 88 / 115, of 8 over 2,000
+// 28 / 31, of 16 45 / 32; 40 of 4 over 2,000 63 / 102, of 16 185 / 103.
 static bool use_tiles(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     const double sms = num_sms();
-    const double segs = (double)rows_segs_most(cfg, batch), items = (double)tile_items_most(cfg, batch->n_seqs, batch->n_query);
+    const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
+    const double mean = (double)rows / (double)seqs, parts = (double)seqs * cfg->n_kv_heads;
+    const double segs = parts * ceil(mean / rows::ROWS), items = parts * ceil(mean / tile::ROWS);
     const double seg_us = 2.5 + 0.6 * (double)rows_tiles_most(cfg, cache, batch);
-    const double item_us = 1.5 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
-    const double rows_us = std::min(7.0 + segs * seg_us / sms, 5.0 + ceil(segs / sms) * seg_us);
-    const double tile_us = std::min(23.0 + items * item_us / sms, 14.0 + ceil(items / sms) * (3.0 + item_us));
+    const double item_us = 3.7 + 1.6 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
+    const double rows_us = std::min(9.0 + segs * seg_us / sms, 3.5 + ceil(segs / sms) * seg_us);
+    const double tile_us = tile_slots(cfg, cache, batch) > 0 ? 24.0 + items * item_us / sms : 4.0 + ceil(items / sms) * item_us;
     return tile_us < rows_us;
 }
 
