@@ -79,7 +79,7 @@ struct Item {
     Seq q;
     int32_t head, r0, n_rows, pos0;  // n_rows 0: no more items
     int32_t lo, hi;      // keys in reach of any row
-    int32_t tile0, n;    // this part's tiles
+    int32_t key0, n;     // this part's first key and tiles
     int32_t part, splits;
     int32_t full_lo, full_hi;  // keys in reach of every row
     int32_t bad_lo, bad_hi;    // this part's tiles in which infinities or NaN were cleared
@@ -150,7 +150,7 @@ __device__ __forceinline__ Share share(const Params &p, const Seq &q) {
     int32_t n = (q.kv + KT - 1) / KT;
     if (p.window > 0) {
         const int64_t reach = (int64_t)p.window + (ROWS - 2) / p.group + 1;
-        const int64_t w = (reach + KT - 2) / KT + 1;
+        const int64_t w = (reach + p.box + KT - 2) / KT;
         if (w < n) n = (int32_t)w;
     }
     const int32_t first = q.kv - q.q_len > 0 ? q.kv - q.q_len : 0;
@@ -305,9 +305,11 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int32_t seg) {
     it.full_lo = p.window > 0 ? last - p.window + 1 : 0;
     it.bad_lo = INT32_MAX;
     it.bad_hi = -1;
-    const int32_t t0 = it.lo / KT, nt = it.hi > it.lo ? (it.hi + KT - 1) / KT - t0 : 0;
+    // Tiles start at the box of the first key: with a window, on multiples of KT an item would meet half a
+    // tile more (128 keys, groups of 4: 2.5 tiles an item instead of 2).
+    const int32_t k0 = it.lo - it.lo % p.box, nt = it.hi > it.lo ? (it.hi - k0 + KT - 1) / KT : 0;
     const int32_t a = (int32_t)((int64_t)nt * it.part / it.splits), b = (int32_t)((int64_t)nt * (it.part + 1) / it.splits);
-    it.tile0 = t0 + a;
+    it.key0 = k0 + a * KT;
     it.n = b - a;
 }
 
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             bool next_mine = false;
             float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
             if (mine && n > 0) {
-                const int32_t tile0 = w->tile0;
+                const int32_t item_key0 = w->key0;
                 const int32_t pos = w->pos0 + p.by_group.quotient(w->r0 + t * MT + row);
                 const int32_t row_lo = p.window > 0 ? pos - p.window + 1 : 0;
                 // keys in reach of every row of the tile
@@ -614,7 +616,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int32_t full_hi = w->pos0 + p.by_group.quotient(w->r0 + t * MT) + 1;
                 const int32_t full_lo = p.window > 0 ? w->pos0 + p.by_group.quotient(w->r0 + last) - p.window + 1 : 0;
                 for (int32_t j = 0; j < n; ++j) {
-                    const int32_t key0 = (tile0 + j) * KT;
+                    const int32_t key0 = item_key0 + j * KT;
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
@@ -770,8 +772,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         float x[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
-                        add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(lo, (w->tile0 + w->bad_lo) * KT),
-                                             min(pos + 1, (w->tile0 + w->bad_hi + 1) * KT), c * 32, p.head_dim, x);
+                        add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(lo, w->key0 + w->bad_lo * KT),
+                                             min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c * 32, p.head_dim, x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
                     }
@@ -867,14 +869,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (!item || item->n_rows == 0) break;
                 const struct {
                     int64_t s;
-                    int32_t head, tile0, n, lo, hi;
-                } w = {item->s, item->head, item->tile0, item->n, item->lo, item->hi};
+                    int32_t head, key0, n, lo, hi;
+                } w = {item->s, item->head, item->key0, item->n, item->lo, item->hi};
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
                 int64_t window0 = -1;
                 int32_t page = -1;
                 for (int32_t j = 0; ok && j < w.n; ++j) {
-                    const int64_t b0 = (int64_t)(w.tile0 + j) * boxes;
+                    const int64_t b0 = w.key0 / p.box + (int64_t)j * boxes;
                     if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
                         window0 = b0;
                         const int64_t key = (b0 + lane) * p.box;
