@@ -324,7 +324,6 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     p.box = gcd(cache->page_size, tile::KT);
     p.ctas = num_sms();
     p.max_slots = (int32_t)slots;
-    p.out_by_32 = aligned(out->data, 32) && out->token_stride % 16 == 0 && out->head_stride % 16 == 0;
     p.cut = slots == 0 ? nullptr
                        : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
                                                      tile_workspace_bytes(cfg, cache, batch) - 256);

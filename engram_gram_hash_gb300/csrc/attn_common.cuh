@@ -146,14 +146,15 @@ __device__ __forceinline__ bool holds_nonfinite(bool keep, const F &at) {
 }
 template <typename E, int N, typename F>
 __device__ __forceinline__ void clear_nonfinite(bool keep, const F &at) {
+    if (!keep) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sts16(at(i), make_uint4(0, 0, 0, 0));
+        return;
+    }
 #pragma unroll 1
     for (int i = 0; i < N; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (keep) {
-            v = lds16(at(i));
-            v = make_uint4(finite_only<E>(v.x), finite_only<E>(v.y), finite_only<E>(v.z), finite_only<E>(v.w));
-        }
-        sts16(at(i), v);
+        const uint4 v = lds16(at(i));
+        sts16(at(i), make_uint4(finite_only<E>(v.x), finite_only<E>(v.y), finite_only<E>(v.z), finite_only<E>(v.w)));
     }
 }
 

@@ -52,8 +52,9 @@ __device__ const int kSplits[N_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 
 template <int DP>
 struct Cfg {
     static constexpr int STAGE_BYTES = KT * DP * 2;  // K or V of a tile
-    static constexpr int STAGES = DP == 128 ? 5 : 8;
+    static constexpr int STAGES = DP == 128 ? 4 : 8;
     static constexpr int Q_BYTES = MT * DP * 2;      // one row tile
+    static constexpr int SWAP_BYTES = 8 * 32 * 128;  // a softmax warp's rows on their way out, 128 bytes of each
     static constexpr int O_COL = 256;                // TMEM: scores in columns 0..255, then the outputs
     static constexpr int TMEM_COLS = 512;
     // Up to 64 values TMEM has room for the weights beside the scores: the next scores are then
@@ -108,7 +109,7 @@ struct Shared {
 
 template <int DP>
 constexpr int smem_bytes() {
-    return 2 * Cfg<DP>::Q_BYTES + Cfg<DP>::STAGES * Cfg<DP>::STAGE_BYTES + (int)sizeof(Shared<DP>);
+    return 2 * Cfg<DP>::Q_BYTES + Cfg<DP>::STAGES * Cfg<DP>::STAGE_BYTES + Cfg<DP>::SWAP_BYTES + (int)sizeof(Shared<DP>);
 }
 static_assert(smem_bytes<128>() <= 232448, "tile kernel shared memory over the per-CTA limit");
 
@@ -129,7 +130,6 @@ struct Params {
     int32_t ctas;
     int32_t max_slots;  // 0: nothing is split
     int32_t *cut;       // the plan's cut, for the join
-    int32_t out_by_32;  // output rows are 32-byte aligned
     float scale_log2;
 };
 
@@ -465,12 +465,6 @@ __device__ __forceinline__ bool elect_one() {
         : "=r"(is));
     return is != 0;
 }
-// 32 bytes in one store: a thread that holds a row touches each of its lines half as often.
-__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
-                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -500,7 +494,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_smem = smem;
     uint8_t *kv_smem = smem + 2 * C::Q_BYTES;
-    Shared<DP> *sh = reinterpret_cast<Shared<DP> *>(kv_smem + C::STAGES * C::STAGE_BYTES);
+    uint8_t *swap_smem = kv_smem + C::STAGES * C::STAGE_BYTES;
+    Shared<DP> *sh = reinterpret_cast<Shared<DP> *>(swap_smem + C::SWAP_BYTES);
     volatile int *abort = &sh->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
@@ -605,7 +600,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const bool mine = w->n_rows > t * MT;
             const int32_t n = w->n;
             const Item *next = nullptr;
-            bool next_mine = false;
             float m = -INFINITY, l = 0.f;  // m: the maximum that the weights refer to, in scores
             if (mine && n > 0) {
                 const int32_t item_key0 = w->key0;
@@ -620,13 +614,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    if (j + 1 == n) {
-                        // The last scores are there, so the queries' memory is free: the next item's are
-                        // fetched now, and its scores computed under this item's epilogue.
-                        next = take(k + 1);
-                        next_mine = next && next->n > 0 && next->n_rows > t * MT;
-                        if (next_mine) fetch_q(*next);
-                    }
                     // Values that must not meet a weight of zero leave the tile before the products: those
                     // of keys that no row reaches (they may be anything), infinities and NaN of keys that
                     // some row does not see.  Both row tiles do it, each before its own products; who clears
@@ -737,9 +724,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
             it += 2 * n;
             if (mine && n > 0) {
-                if (next_mine) hand_q();
+                // The last scores were there, so the queries' memory is free: the next item's are fetched
+                // under this item's last product, and its scores computed under this item's epilogue.
+                next = take(k + 1);
+                const bool next_mine = next && next->n > 0 && next->n_rows > t * MT;
+                if (next_mine) fetch_q(*next);
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
                 if (!ok) break;
+                if (next_mine) hand_q();
                 tc_fence_after();
             } else {
                 next = take(k + 1);
@@ -754,47 +746,72 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
                 const int64_t out_row = (int64_t)w->q.row0 + tok;
                 const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
-                uint16_t *dst = p.out + out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
-                float *part = p.part_o + (slot * ROWS + t * MT + row) * DP;
-#pragma unroll
-                for (int c = 0; c < DP / 32; ++c) {
-                    uint32_t o[32];
+                // A lane has a row in TMEM, but lanes that store to 32 rows at once cost an access to L1 each:
+                // the rows change hands in shared memory, 128 bytes of each at a time (the pieces permuted,
+                // so neither way meets a bank twice), and eight lanes store a row's piece.
+                const uint32_t swap = smem_u32(swap_smem) + warp * (32 * 128);
+                const int64_t dst = out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
+                float *part = p.part_o + (slot * ROWS + t * MT + row - lane) * DP;
+                const int32_t warp_rows = w->n_rows - (t * MT + row - lane);  // this warp's rows of the item
+                const auto read_o = [&](int c, uint32_t (&o)[32]) {  // 32 columns of this lane's row
                     if (n > 0) {
-                        tmem_ld_32x32b_x32(o_tm + c * 32, o);
+                        tmem_ld_32x32b_x32(o_tm + c, o);
                         tmem_ld_wait();
                     } else {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
-                    if (!live) continue;
-                    if (w->bad_hi >= 0) {
+                    if (w->bad_hi >= 0 && live) {
                         const int32_t pos = w->pos0 + tok, lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
                         float x[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
                         add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(lo, w->key0 + w->bad_lo * KT),
-                                             min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c * 32, p.head_dim, x);
+                                             min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c, p.head_dim, x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
                     }
-                    if (whole) {
-                        uint32_t u[16];
+                };
+                const auto put = [&](int i, const uint32_t *v) {
+                    sts16(swap + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                };
+                const auto get = [&](int r) { return lds16(swap + r * 128 + (((lane ^ r) & 7) << 4)); };
+                if (whole) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 64) {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t o[32], u[16];
+                            read_o(c + half * 32, o);
 #pragma unroll
-                        for (int h = 0; h < 16; ++h)
-                            u[h] = E::pack(__uint_as_float(o[2 * h]) * inv, __uint_as_float(o[2 * h + 1]) * inv);
-                        uint16_t *const at = dst + c * 32;
-                        if (p.out_by_32 && c * 32 + 32 <= p.head_dim) {
-                            st_global_v8(at, u);
-                            st_global_v8(at + 16, u + 8);
-                        } else {
+                            for (int h = 0; h < 16; ++h)
+                                u[h] = E::pack(__uint_as_float(o[2 * h]) * inv, __uint_as_float(o[2 * h + 1]) * inv);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (c * 32 + i * 8 < p.head_dim)
-                                    *reinterpret_cast<uint4 *>(at + i * 8) = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+                            for (int i = 0; i < 4; ++i) put(half * 4 + i, u + 4 * i);
                         }
-                    } else if (n > 0) {
+                        __syncwarp();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) st_global_v8(part + c * 32 + i * 8, o + i * 8);
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = k * 4 + (lane >> 3), at = c + (lane & 7) * 8;
+                            const int64_t to = __shfl_sync(0xffffffffu, dst, r);
+                            if (r < warp_rows && at < p.head_dim) *reinterpret_cast<uint4 *>(p.out + to + at) = get(r);
+                        }
+                        __syncwarp();
+                    }
+                } else if (n > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        read_o(c, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) put(i, o + 4 * i);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = k * 4 + (lane >> 3);
+                            if (r < warp_rows) *reinterpret_cast<uint4 *>(part + r * DP + c + (lane & 7) * 4) = get(r);
+                        }
+                        __syncwarp();
                     }
                 }
                 tc_fence_before();  // O has been read before the next item's first product is allowed
@@ -882,7 +899,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const int64_t key = (b0 + lane) * p.box;
                         page = -1;
                         if (key < w.hi) {
-                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + key / p.b.page_size);
+                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + (uint32_t)key / (uint32_t)p.b.page_size);
                             if (page < 0 || page >= p.b.n_pages) {
                                 if (key + p.box > w.lo) raise_error(ENGRAM_ERANGE);
                                 page = -1;  // out of range: the copy fills zeros
@@ -893,7 +910,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     const int64_t key = (b0 + lane) * p.box;
                     const bool load = lane < boxes && key < w.hi && key + p.box > w.lo;
                     const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-                    const int y = (int)(key % p.b.page_size);
+                    const int y = (int)((uint32_t)key % (uint32_t)p.b.page_size);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         const int st = it % C::STAGES;
