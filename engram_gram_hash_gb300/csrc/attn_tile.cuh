@@ -149,7 +149,7 @@ __device__ __forceinline__ Share share(const Params &p, const Seq &q) {
     r.segs = (int64_t)r.blocks * p.n_kv_heads;
     int32_t n = (q.kv + KT - 1) / KT;
     if (p.window > 0) {
-        const int64_t reach = (int64_t)p.window + (ROWS - 2) / p.group + 1;
+        const int64_t reach = (int64_t)p.window + p.by_group.quotient(ROWS - 2) + 1;
         const int64_t w = (reach + p.box + KT - 2) / KT;
         if (w < n) n = (int32_t)w;
     }
@@ -308,16 +308,19 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int32_t seg) {
     // Tiles start at the box of the first key: with a window, on multiples of KT an item would meet half a
     // tile more (128 keys, groups of 4: 2.5 tiles an item instead of 2).
     const int32_t k0 = it.lo - it.lo % p.box, nt = it.hi > it.lo ? (it.hi - k0 + KT - 1) / KT : 0;
-    const int32_t a = (int32_t)((int64_t)nt * it.part / it.splits), b = (int32_t)((int64_t)nt * (it.part + 1) / it.splits);
+    // nt * (splits + 1) stays under 2^32: 2^24 tiles, 152 parts
+    const int32_t a = (int32_t)((uint32_t)nt * it.part / (uint32_t)it.splits),
+                  b = (int32_t)((uint32_t)nt * (it.part + 1) / (uint32_t)it.splits);
     it.key0 = k0 + a * KT;
     it.n = b - a;
 }
 
 // Item `at` of sequence it.s, of segs x it.splits (it.q, it.splits and it.slot,
 // the parts before the sequence, are set).
-__device__ __forceinline__ void locate(const Params &p, Item &it, int64_t at, int32_t segs, int32_t blocks) {
+template <typename I>
+__device__ __forceinline__ void locate(const Params &p, Item &it, I at, int32_t segs, int32_t blocks) {
     it.part = (int32_t)(at < INT32_MAX ? (int32_t)at / segs : at / segs);
-    const int32_t k = (int32_t)(at - (int64_t)it.part * segs);  // < segs, an int32 (n_query * n_heads < 2^31)
+    const int32_t k = (int32_t)(at - (I)it.part * segs);  // < segs, an int32 (n_query * n_heads < 2^31)
     const int32_t block = p.by_heads.quotient(k);
     const int32_t seg = (blocks - 1 - block) * p.n_kv_heads + k - block * p.n_kv_heads;
     it.slot += (int64_t)seg * it.splits + it.part;
@@ -351,11 +354,13 @@ __device__ __forceinline__ Item find_item(const Params &p, int64_t base, const P
 // The same plan for at most 32 sequences, by one warp (the one that finds the
 // items: no block barrier, and no other role waits for it).  Here the sequences
 // go longest parts first, too.
+// Counts fit 32 bits: a row block has 256 of fewer than 2^31 rows x heads, and parts beyond those are
+// bounded by the workspace.  (64-bit divisions here were most of the 10 us before the first item.)
 struct WarpPlan {
-    int64_t total;   // items in all
+    int32_t total;   // items in all
     int32_t cut;
     // of this lane's sequence: the items before it and its own, the parts before it
-    int64_t before, items, slots;
+    int32_t before, items, slots;
     int32_t segs, blocks, splits;
 };
 __device__ __forceinline__ WarpPlan plan_warp(const Params &p, int64_t base) {
@@ -367,8 +372,8 @@ __device__ __forceinline__ WarpPlan plan_warp(const Params &p, int64_t base) {
     w.blocks = h.blocks;
     w.cut = INT32_MAX;
     if (p.max_slots > 0) {
-        int64_t work = h.segs * h.mean;
-        int32_t most = h.segs > 0 && h.tiles > 1 ? h.tiles : 1;
+        float work = (float)w.segs * (float)h.mean;
+        int32_t most = w.segs > 0 && h.tiles > 1 ? h.tiles : 1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             work += __shfl_xor_sync(0xffffffffu, work, o);
@@ -376,24 +381,26 @@ __device__ __forceinline__ WarpPlan plan_warp(const Params &p, int64_t base) {
         }
         const int32_t cut_c = (most + kSplits[lane & 15] - 1) / kSplits[lane & 15];
         float items = 0.f, parts = 0.f;
+#pragma unroll 1
         for (int i = 0; 2 * i < n; ++i) {  // a candidate per lane, the sequences by halves of the warp
             const int s = 2 * i + (lane >> 4);
             const int32_t segs = __shfl_sync(0xffffffffu, w.segs, s & 31), tiles = __shfl_sync(0xffffffffu, h.tiles, s & 31);
             if (s >= n) continue;
             const int32_t k = splits_of(tiles, cut_c);
-            items += (float)segs * k;
-            if (k > 1) parts += (float)segs * k;
+            items += (float)segs * (float)k;
+            if (k > 1) parts += (float)segs * (float)k;
         }
         items += __shfl_xor_sync(0xffffffffu, items, 16);
         parts += __shfl_xor_sync(0xffffffffu, parts, 16);
-        w.cut = best_cut(p, items, parts, (float)work, cut_c);
+        w.cut = best_cut(p, items, parts, work, cut_c);
     }
     w.splits = splits_of(h.tiles, w.cut);
-    w.items = h.segs * w.splits;
+    w.items = w.segs * w.splits;
     const int32_t size = (h.tiles + w.splits - 1) / w.splits;  // tiles of a part
     w.total = w.before = w.slots = 0;
+#pragma unroll 1
     for (int s = 0; s < n; ++s) {
-        const int64_t items = __shfl_sync(0xffffffffu, w.items, s);
+        const int32_t items = __shfl_sync(0xffffffffu, w.items, s);
         const int32_t other = __shfl_sync(0xffffffffu, size, s), k = __shfl_sync(0xffffffffu, w.splits, s);
         w.total += items;
         if (other > size || (other == size && s < lane)) w.before += items;
@@ -402,17 +409,19 @@ __device__ __forceinline__ WarpPlan plan_warp(const Params &p, int64_t base) {
     return w;
 }
 // Item number `index` < total of the plan, each lane its own (the whole warp calls).
-__device__ __forceinline__ Item find_item_warp(const Params &p, int64_t base, const WarpPlan &w, int64_t index) {
+__device__ __forceinline__ Item find_item_warp(const Params &p, int64_t base, const WarpPlan &w, int64_t index64) {
+    const int32_t index = index64 < w.total ? (int32_t)index64 : w.total;
     int cur = 0;
+#pragma unroll 1
     for (int s = 0; s < (int)p.b.n_seqs; ++s) {
-        const int64_t b = __shfl_sync(0xffffffffu, w.before, s), n = __shfl_sync(0xffffffffu, w.items, s);
+        const int32_t b = __shfl_sync(0xffffffffu, w.before, s), n = __shfl_sync(0xffffffffu, w.items, s);
         if (index >= b && index < b + n) cur = s;
     }
     Item it;
     it.s = cur;
     it.slot = __shfl_sync(0xffffffffu, w.slots, cur);
     it.splits = __shfl_sync(0xffffffffu, w.splits, cur);
-    const int64_t at = index - __shfl_sync(0xffffffffu, w.before, cur);
+    const int32_t at = index - __shfl_sync(0xffffffffu, w.before, cur);
     const int32_t segs = __shfl_sync(0xffffffffu, w.segs, cur), blocks = __shfl_sync(0xffffffffu, w.blocks, cur);
     it.n_rows = 0;
     if (index < w.total) {
