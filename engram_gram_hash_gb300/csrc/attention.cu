@@ -257,7 +257,7 @@ static int64_t tile_items_most(const engram_attn_config *cfg, int64_t n_seqs, in
 }
 // Slots for partial results.  Nothing is split, none are needed and no join follows with six items a SM
 // or more (the last round is at most a sixth of the time, and the parts cost about as much) or with at
-// most six tiles of keys (a part costs about five).
+// most six tiles of keys (a part costs about six).
 static int64_t tile_slots(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     const int64_t n_seqs = batch->n_seqs, n_query = batch->n_query;
     if (keys_most(cfg, cache, batch) <= 6 * tile::KT) return 0;
@@ -279,11 +279,11 @@ static size_t tile_workspace_bytes(const engram_attn_config *cfg, const engram_k
 // sequences of the mean number of rows (the lengths are on the device): a segment of 16 rows costs 2.5 and
 // 0.6 a 32 KB tile of keys, an item of 256 rows 3.7 and 1.6 a tile of 128 keys; whole rounds of them, or
 // equal shares after a later start (split and joined).  Fitted to 197 measured pairs (8, 4 and 32 key/value
-// heads, 1 to 40 sequences of 2 to 256 new tokens over 1 to 16,000): the choice costs 0.1 % over the better
-// kernel in the mean and 13 % at worst.  Of them, 32 heads of 128 with 8 key/value heads, us rows kernel /
-// tile kernel, new tokens over cached ones: 8 over 16,000 28 / 33, 16 42 / 34; 64 over 4,000 42 / 30; prompts
-// of 64 7.6 / 10.6, 128 13.3 / 12.9, 256 27 / 15; 8 sequences of 4 over 16,000 88 / 115, of 8 over 2,000
-// 28 / 31, of 16 45 / 32; 40 of 4 over 2,000 63 / 102, of 16 185 / 103.
+// heads, 1 to 40 sequences of 2 to 256 new tokens over 1 to 16,000): the choice costs 0.2 % over the better
+// kernel in the mean and 15 % at worst.  Of them, 32 heads of 128 with 8 key/value heads, us rows kernel /
+// tile kernel, new tokens over cached ones: 8 over 16,000 27 / 32, 16 42 / 33; 64 over 4,000 42 / 28; prompts
+// of 64 7.4 / 9.0, 128 12.4 / 11.4, 256 25 / 13; 8 sequences of 4 over 16,000 90 / 119, of 8 over 2,000
+// 28 / 32, of 16 44 / 32; 40 of 4 over 2,000 64 / 98, of 16 182 / 100.
 static bool use_tiles(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     const double sms = num_sms();
     const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
@@ -337,7 +337,7 @@ static engram_status tile_launch(const engram_attn_config *cfg, const engram_kv_
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS, smem, 1, st, "tile_kernel", km, vm, p);
     if (s != ENGRAM_OK || slots == 0) return s;
-    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * 8), 128, 0, 1, st, "tile_join_kernel", p);
+    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * tile::JOIN_PER_SM), 128, 0, 1, st, "tile_join_kernel", p);
 }
 
 }  // namespace attn

@@ -43,6 +43,9 @@ constexpr int CHUNKS = 64;            // the plan's prefix sums: sequences in th
 constexpr int P_PARTS = 2;            // a tile's weights are handed over in this many parts
 constexpr int MAX_SPLIT = 152;
 constexpr int SLOTS_PER_SM = 8;       // workspace for partial results
+// The join's blocks of an SM, all resident at 80 registers: 8 came in two waves (69 us instead of 70.5 for
+// a mixed step), 8 at 64 registers spill (78).
+constexpr int JOIN_PER_SM = 6;
 constexpr float RESCALE_LOG2 = 8.f;
 
 // How many parts the longest item is cut into at most; the plan picks one.
@@ -167,7 +170,8 @@ __device__ __forceinline__ int32_t splits_of(int32_t tiles, int32_t cut) {
 // items and parts of candidate c and its cut.  Times are in tiles: equal items
 // go in rounds; items of unequal size fill each other's gaps (half the longest
 // is left over).  An item costs about two tiles beside its own, a part about
-// five (its partial result is written and read again).
+// six (its partial result is written, read again and joined; taken for five,
+// a mixed step of 9 sequences was split: 69 us instead of 60).
 __device__ __forceinline__ int32_t best_cut(const Params &p, float items, float parts, float work, int32_t cut_c) {
     const int lane = threadIdx.x & 31;
     float best = INFINITY;
@@ -176,7 +180,7 @@ __device__ __forceinline__ int32_t best_cut(const Params &p, float items, float 
         const float g = (float)p.ctas, rounds = ceilf(items / g);
         const float span = items <= g ? (float)cut_c : (work > 0.85f * items * cut_c ? rounds * cut_c : work / g + 0.5f * cut_c);
         const bool whole = kSplits[lane] == 1;
-        if (whole || parts <= (float)p.max_slots) best = span + rounds * (whole ? 2.f : 5.f);
+        if (whole || parts <= (float)p.max_slots) best = span + rounds * (whole ? 2.f : 6.f);
         cut = whole ? INT32_MAX : cut_c;
     }
 #pragma unroll
@@ -1080,7 +1084,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // segment at a time, a warp 4 of them (their loads together), its lanes 4
 // values of each.
 template <typename E, int DP>
-__global__ void __launch_bounds__(128) tile_join_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(128, JOIN_PER_SM) tile_join_kernel(const __grid_constant__ Params p) {
     constexpr int R = 4;
     __shared__ int64_t segs[CHUNKS + 1], parts[CHUNKS + 1];
     grid_dependency_wait();
