@@ -13,13 +13,19 @@
 //   warps 0-3, 4-7  one softmax warpgroup per row tile, a row per thread: the
 //                   row's 128 scores come from TMEM into registers, its
 //                   maximum and sum need no exchange; weights go back to
-//                   TMEM as 16-bit pairs over the scores they came from.
+//                   TMEM as 16-bit pairs over the scores they came from (up
+//                   to 64 values: beside them).  At an item's end the rows
+//                   change hands in shared memory and leave in 128-byte pieces.
 //   warps 8, 11     issue the products of a row tile each: S = Q K^T (shared x
 //                   shared memory), O += P V (TMEM x shared memory).  While one tile's
 //                   softmax runs, the other tile's products do.
-//   warp 9          TMA: K and V tiles in turn into a ring of 32 KB stages.
+//   warp 9          TMA: K and V tiles in turn into a ring (4 stages of 32 KB,
+//                   8 of 16 KB up to 64 values).
 //   warp 10         finds the CTA's next items and hands them to the others.
 // TMEM: S0 | S1 | O0 | O1, 128 columns each (512 in all at 128 values).
+// What runs once an item or less is kept in loops and 32 bits: with few tiles
+// an item the instruction cache binds (kernel code of 216 KB: a window of 128
+// keys over 8 prompts 152 us; 169 KB: 135; 150 KB: 132).
 //
 // The running maximum moves only when a row's new maximum exceeds it by 2^8
 // (then O and the sum are scaled): weights stay below 2^8, far inside both
@@ -55,9 +61,11 @@ __device__ const int kSplits[N_CAND] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 24, 
 template <int DP>
 struct Cfg {
     static constexpr int STAGE_BYTES = KT * DP * 2;  // K or V of a tile
+    // 128 values: 4 leave room for the rows on their way out; a fifth stage was worth nothing (a chunk of
+    // 2,048 over 63,488 tokens 1,550 us with either).
     static constexpr int STAGES = DP == 128 ? 4 : 8;
     static constexpr int Q_BYTES = MT * DP * 2;      // one row tile
-    static constexpr int SWAP_BYTES = 8 * 32 * 128;  // a softmax warp's rows on their way out, 128 bytes of each
+    static constexpr int SWAP_BYTES = 8 * 32 * 128;  // the softmax warps' rows on their way out, 128 bytes of each
     static constexpr int O_COL = 256;                // TMEM: scores in columns 0..255, then the outputs
     static constexpr int TMEM_COLS = 512;
     // Up to 64 values TMEM has room for the weights beside the scores: the next scores are then
