@@ -167,7 +167,14 @@ static int64_t rows_segs_most(const engram_attn_config *cfg, const engram_kv_bat
 }
 static int64_t keys_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     const int64_t room = batch->table_stride * cache->page_size;
-    return cfg->window > 0 ? std::min<int64_t>(room, cfg->window + 256) : room;
+    return cfg->window > 0 ? std::min<int64_t>(room, (int64_t)cfg->window + 256) : room;
+}
+// The configuration with a window that hides nothing taken for plain causal attention (0): no position
+// reaches the block table's room or 2^31 - 1, so a window of that many tokens ends before every sequence.
+static engram_attn_config effective(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
+    engram_attn_config c = *cfg;
+    if (c.window >= std::min<int64_t>(batch->table_stride * cache->page_size, INT32_MAX)) c.window = 0;
+    return c;
 }
 static int64_t rows_tiles_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     return (keys_most(cfg, cache, batch) * padded_dim(cfg) + 8191) / 8192;
@@ -423,7 +430,8 @@ extern "C" size_t engram_paged_attention_workspace_bytes(const engram_attn_confi
     using namespace engram::attn;
     if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK || batch->n_query == 0) return 0;
     if (check_cache(cfg, cache) != ENGRAM_OK) return 0;
-    return workspace_bytes(cfg, cache, batch);
+    const engram_attn_config eff = effective(cfg, cache, batch);
+    return workspace_bytes(&eff, cache, batch);
 }
 
 extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, const engram_kv_cache *cache,
@@ -435,6 +443,8 @@ extern "C" engram_status engram_paged_attention(const engram_attn_config *cfg, c
     if (batch->n_query == 0) return ENGRAM_OK;
     if (check_cache(cfg, cache) != ENGRAM_OK || !view_ok(q) || !view_ok(out) || !aligned(lse, 4)) return ENGRAM_EINVAL;
     if (batch->n_query > INT32_MAX / cfg->n_heads) return ENGRAM_EINVAL;
+    const engram_attn_config eff = effective(cfg, cache, batch);
+    cfg = &eff;
     const size_t need = engram::attn::workspace_bytes(cfg, cache, batch);
     if (need > 0 && (!workspace || !aligned(workspace, 256))) return ENGRAM_EINVAL;
     if (workspace_bytes < need) return ENGRAM_ENOMEM;

@@ -95,6 +95,13 @@ __device__ __forceinline__ Seq load_seq(const Batch &b, int64_t s, int64_t base)
     return Seq{(int32_t)a, (int32_t)(e - a), kv < 0 ? 0 : (int32_t)kv};
 }
 
+// The first position that a token at `pos` sees (0: plain causal).  Compared
+// before subtracted: with a padded token (pos < 0) and a window near 2^31 the
+// difference would leave 32 bits.
+__device__ __forceinline__ int32_t first_seen(int32_t pos, int32_t window) {
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
+
 // mbar_wait by a whole warp, with one answer for all its lanes (near the time
 // limit the lanes could differ, and the warp-wide steps that follow must not).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {

@@ -258,8 +258,8 @@ __device__ __forceinline__ Segment segment(const Params &p, const Walk &w) {
     const int32_t first = g.pos0 + p.by_group.quotient(g.r0), last = g.pos0 + p.by_group.quotient(g.r0 + g.n_rows - 1);
     g.hi = last + 1;  // <= kv
     g.full_hi = first + 1;
-    g.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
-    g.full_lo = p.window > 0 && last - p.window + 1 > 0 ? last - p.window + 1 : 0;
+    g.lo = first_seen(first, p.window);
+    g.full_lo = first_seen(last, p.window);
     if (g.hi < 0) g.hi = 0;
     g.tile0 = g.lo >> p.kt_log2;
     g.n_tiles = g.hi > g.lo ? ((g.hi + (1 << p.kt_log2) - 1) >> p.kt_log2) - g.tile0 : 0;
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
                 const int32_t pos = g.pos0 + tok;
                 row_hi[i] = live ? pos : -1;
-                row_lo[i] = p.window > 0 ? pos - p.window + 1 : 0;
+                row_lo[i] = first_seen(pos, p.window);
                 const uint16_t *src = p.q + (int64_t)(w_row(walk, tok)) * p.q_token_stride +
                                       (int64_t)(g.head * p.group + hh) * p.q_head_stride;
 #pragma unroll
@@ -674,9 +674,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 if (sh->bad_hi[turn] >= 0 && c < p.head_dim) {
                     const int32_t pos = g.pos0 + p.by_group.quotient(g.r0 + r);
-                    const int32_t lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
                     float x[4] = {v.x, v.y, v.z, v.w};
-                    add_nonfinite<E, 4>(p.b, p.values, walk.s, g.head, max(lo, sh->bad_lo[turn] * KT),
+                    add_nonfinite<E, 4>(p.b, p.values, walk.s, g.head, max(first_seen(pos, p.window), sh->bad_lo[turn] * KT),
                                         min(pos + 1, (sh->bad_hi[turn] + 1) * KT), c, p.head_dim, x);
                     v = make_float4(x[0], x[1], x[2], x[3]);
                 }

@@ -312,9 +312,9 @@ __device__ __forceinline__ void place(const Params &p, Item &it, int32_t seg) {
     it.pos0 = it.q.kv - it.q.q_len;
     const int32_t first = it.pos0 + p.by_group.quotient(it.r0), last = it.pos0 + p.by_group.quotient(it.r0 + it.n_rows - 1);
     it.hi = last + 1 > 0 ? last + 1 : 0;
-    it.lo = p.window > 0 && first - p.window + 1 > 0 ? first - p.window + 1 : 0;
+    it.lo = first_seen(first, p.window);
     it.full_hi = first + 1;
-    it.full_lo = p.window > 0 ? last - p.window + 1 : 0;
+    it.full_lo = first_seen(last, p.window);
     it.bad_lo = INT32_MAX;
     it.bad_hi = -1;
     // Tiles start at the box of the first key: with a window, on multiples of KT an item would meet half a
@@ -625,11 +625,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (mine && n > 0) {
                 const int32_t item_key0 = w->key0;
                 const int32_t pos = w->pos0 + p.by_group.quotient(w->r0 + t * MT + row);
-                const int32_t row_lo = p.window > 0 ? pos - p.window + 1 : 0;
+                const int32_t row_lo = first_seen(pos, p.window);
                 // keys in reach of every row of the tile
                 const int32_t last = (w->n_rows < (t + 1) * MT ? w->n_rows : (t + 1) * MT) - 1;
                 const int32_t full_hi = w->pos0 + p.by_group.quotient(w->r0 + t * MT) + 1;
-                const int32_t full_lo = p.window > 0 ? w->pos0 + p.by_group.quotient(w->r0 + last) - p.window + 1 : 0;
+                const int32_t full_lo = first_seen(w->pos0 + p.by_group.quotient(w->r0 + last), p.window);
                 for (int32_t j = 0; j < n; ++j) {
                     const int32_t key0 = item_key0 + j * KT;
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
@@ -783,11 +783,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
                     if (w->bad_hi >= 0 && live) {
-                        const int32_t pos = w->pos0 + tok, lo = p.window > 0 && pos - p.window + 1 > 0 ? pos - p.window + 1 : 0;
+                        const int32_t pos = w->pos0 + tok;
                         float x[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
-                        add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(lo, w->key0 + w->bad_lo * KT),
+                        add_nonfinite<E, 32>(p.b, p.values, w->s, w->head, max(first_seen(pos, p.window), w->key0 + w->bad_lo * KT),
                                              min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c, p.head_dim, x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
