@@ -5,7 +5,15 @@
 namespace engram {
 namespace attn {
 
+// LIFT: the softmax weights are kept times 2^LIFT at most (numerator and sum alike, so it cancels) before
+// they are rounded to the type for the second product.  bf16 has fp32's exponents and needs none.  fp16
+// loses bits below 2^-14: with its weights up to 2^15 only those under 2^-29 of the row's largest do, 2^-25
+// in the tile kernel (without, those under 2^-14: a key 14 nats above the others, whose value is zero, left
+// 1.6e-2 relative error).
+// RESCALE: the tile kernel's running maximum may lag the true one by 2^RESCALE.  fp16, a prompt of 8,192
+// tokens with 1 / 2 / 4 / 8: 405, 398, 363, 364 us.
 struct Bf16 {
+    static constexpr float LIFT = 0.f, RESCALE = 8.f;
     // two values times zero onto acc: NaN from then on if either is an infinity or NaN
     static __device__ __forceinline__ void spot(uint32_t &acc, uint32_t w) {
         asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
@@ -23,6 +31,7 @@ struct Bf16 {
 };
 
 struct Fp16 {
+    static constexpr float LIFT = 15.f, RESCALE = 4.f;
     static __device__ __forceinline__ void spot(uint32_t &acc, uint32_t w) {
         asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w), "r"(0u));
     }

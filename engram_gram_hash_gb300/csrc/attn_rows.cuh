@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                 if (key > row_hi[c >> 1] || key < row_lo[c >> 1]) s[t][c] = -INFINITY;
                             }
                         }
-                    float up[2];
+                    float up[2], ref[2];
                     bool same = true;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -576,6 +576,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         up[i] = weight(m[i], mx);
                         same = same && mx == m[i];
                         m[i] = mx;
+                        ref[i] = mx - E::LIFT;
                     }
                     if (!__all_sync(0xffffffffu, same)) {
 #pragma unroll
@@ -592,14 +593,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     for (int t = 0; t < KPW / 8; ++t)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            s[t][c] = weight(s[t][c], m[c >> 1]);
+                            s[t][c] = weight(s[t][c], ref[c >> 1]);
                             l[c >> 1] += s[t][c];
                         }
                     const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
                     for (int b16 = 0; b16 < KPW / 16; ++b16) {
                         // the weights rounded to the values' type: the matrix instruction takes 16-bit
-                        // operands, and a weight's relative error there is the output's own rounding
+                        // operands, and a weight's relative error there is the output's own rounding (LIFT)
                         const float(&u)[4] = s[2 * b16], (&v)[4] = s[2 * b16 + 1];
                         const uint32_t pa[4] = {E::pack(u[0], u[1]), E::pack(u[2], u[3]), E::pack(v[0], v[1]), E::pack(v[2], v[3])};
                         const uint32_t vrow = kb + C::KV_BYTES + (b16 * 16 + key) * 128;
@@ -617,9 +618,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (lane == 0) mbar_arrive(&sh->empty[st]);
             }
 
-            // the eight warps' parts of the segment, joined in warp order
+            // the eight warps' parts of the segment, joined in warp order; from here on m is what the weights refer to
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                m[i] -= E::LIFT;
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
                 if ((lane & 3) == 0) {

@@ -27,9 +27,9 @@
 // an item the instruction cache binds (kernel code of 216 KB: a window of 128
 // keys over 8 prompts 152 us; 169 KB: 135; 150 KB: 132).
 //
-// The running maximum moves only when a row's new maximum exceeds it by 2^8
-// (then O and the sum are scaled): weights stay below 2^8, far inside both
-// 16-bit types, and most tiles need no pass over O.  O is complete up to the
+// The running maximum moves only when a row's new maximum exceeds it by
+// 2^E::RESCALE (then O and the sum are scaled): weights stay below 2^8 in bf16,
+// 2^15 (lifted) in fp16, inside the types, and most tiles need no pass over O.  O is complete up to the
 // tile before whenever new scores arrive (one in-order MMA queue; APART: when
 // pv_done says so), so the softmax warps scale it themselves.
 //
@@ -52,7 +52,6 @@ constexpr int SLOTS_PER_SM = 8;       // workspace for partial results
 // The join's blocks of an SM, all resident at 80 registers: 8 came in two waves (69 us instead of 70.5 for
 // a mixed step), 8 at 64 registers spill (78).
 constexpr int JOIN_PER_SM = 6;
-constexpr float RESCALE_LOG2 = 8.f;
 
 // How many parts the longest item is cut into at most; the plan picks one.
 constexpr int N_CAND = 16;
@@ -582,6 +581,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + t * KT, o_tm = tmem + lanes + C::O_COL + t * DP;
         const uint32_t p_tm = C::APART ? tmem + lanes + C::P_COL + t * 64 : s_tm;
+        constexpr float LIFT = E::LIFT > 0.f ? E::LIFT - E::RESCALE : 0.f;  // of a weight at the running maximum
         uint32_t s_ph = 0, o_ph = 0, it = 0, pv_ph = 0;
         bool ok = true;
 
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         tc_fence_after();
                     }
                     float up = 1.f;
-                    if ((mx - m) * p.scale_log2 > RESCALE_LOG2) {  // also from -inf
+                    if ((mx - m) * p.scale_log2 > E::RESCALE) {  // also from -inf
                         up = rows::exp2_approx((m - mx) * p.scale_log2);
                         m = mx;
                     }
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             tmem_st_32x32b_x16(o_tm + c * 16, o);
                         }
                     }
-                    const float mref = m == -INFINITY ? 0.f : m * p.scale_log2;
+                    const float mref = m == -INFINITY ? 0.f : fmaf(m, p.scale_log2, -LIFT);
                     const float2 sc = make_float2(p.scale_log2, p.scale_log2), off = make_float2(-mref, -mref);
                     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 tc_fence_before();  // O has been read before the next item's first product is allowed
                 if (live) {
-                    const float m2 = m == -INFINITY ? -INFINITY : m * p.scale_log2;
+                    const float m2 = m == -INFINITY ? -INFINITY : fmaf(m, p.scale_log2, -LIFT);
                     if (!whole) {
                         p.part_ml[slot * (2 * ROWS) + t * MT + row] = m2;
                         p.part_ml[slot * (2 * ROWS) + ROWS + t * MT + row] = l;
