@@ -742,15 +742,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     write_out<E>(p, walk, g, r, c, v, ll);
                     if (p.lse && c == 0) write_lse(p, walk, g, r, mm, ll);
                 }
-                consumers_sync();
-                if (threadIdx.x < p.cluster) arrive_at(&sh->done, threadIdx.x);
-                mbar_wait_cluster(&sh->done, exchange_ph, abort);  // nobody reads this CTA's memory any more
+                if (f + n < f1) {  // (more segments than clusters only with offsets that overlap)
+                    consumers_sync();
+                    if (threadIdx.x < p.cluster) arrive_at(&sh->done, threadIdx.x);
+                    mbar_wait_cluster(&sh->done, exchange_ph, abort);  // nobody reads this CTA's memory any more
+                }
                 exchange_ph ^= 1;
             }
             consumers_sync();  // the join's memory is free again
             f += n;
             if (f < f1) walk.next(p, base);
         }
+    }
+    if (p.cluster > 1) {  // no CTA leaves while another may read its memory or arrive on its barriers, after a time-out either
+        __syncwarp();
+        cluster_sync_all();
     }
 }
 

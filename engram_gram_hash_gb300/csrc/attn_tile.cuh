@@ -850,6 +850,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) mbar_arrive(&sh->item_empty[k % ITEMS]);
             w = next;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // after a time-out queries may still be on their way
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 10) {  // --------------------------------------------- items
