@@ -674,6 +674,7 @@ class engram_kv_batch(ctypes.Structure):
         ("kv_len", ctypes.c_void_p),
         ("block_table", ctypes.c_void_p),
         ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int64),
     ]
 
 
@@ -733,7 +734,7 @@ def kv_cache(k_pages, v_pages):
 
 def kv_batch(seq_offsets, kv_len, block_table, n_query):
     """An engram_kv_batch: seq_offsets int64 [n_seqs + 1], kv_len int32 [n_seqs] (lengths with the new
-    tokens), block_table int32 [n_seqs, pages], n_query new tokens in all.  It keeps the tensors alive;
+    tokens), block_table int32 [n_seqs, pages] (a slice of a wider one will do), n_query new tokens in all.  It keeps the tensors alive;
     their contents may change from step to step."""
     _need(seq_offsets, torch.int64, "seq_offsets")
     _need(kv_len, torch.int32, "kv_len")
@@ -749,7 +750,8 @@ def kv_batch(seq_offsets, kv_len, block_table, n_query):
     b = engram_kv_batch()
     b.n_seqs, b.n_query = n, int(n_query)
     b.seq_offsets, b.kv_len, b.block_table = seq_offsets.data_ptr(), kv_len.data_ptr(), block_table.data_ptr()
-    b.table_stride = block_table.shape[1] if n <= 1 else block_table.stride(0)
+    b.table_width = block_table.shape[1]
+    b.table_stride = b.table_width if n <= 1 else block_table.stride(0)
     b.tensors = (seq_offsets, kv_len, block_table)
     b.address = ctypes.addressof(b)
     return b

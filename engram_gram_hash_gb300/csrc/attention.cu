@@ -58,10 +58,14 @@ static engram_status check_batch(const engram_kv_batch *b) {
     if (b->n_query > INT32_MAX || b->n_seqs > INT32_MAX || b->table_stride < 0) return ENGRAM_EINVAL;
     if (b->n_query == 0) return ENGRAM_OK;
     if (b->n_seqs < 1 || b->table_stride < 1 || b->table_stride > INT32_MAX) return ENGRAM_EINVAL;
+    if (b->table_width < 0 || b->table_width > b->table_stride) return ENGRAM_EINVAL;
     if (!b->seq_offsets || !b->kv_len || !b->block_table) return ENGRAM_EINVAL;
     if (!aligned(b->seq_offsets, 8) || !aligned(b->kv_len, 4) || !aligned(b->block_table, 4)) return ENGRAM_EINVAL;
     return ENGRAM_OK;
 }
+
+// Entries of a sequence's row of the block table.
+static int64_t table_width(const engram_kv_batch *b) { return b->table_width > 0 ? b->table_width : b->table_stride; }
 
 static Batch device_batch(const engram_kv_batch *b, const engram_kv_cache *c) {
     Batch d;
@@ -69,6 +73,7 @@ static Batch device_batch(const engram_kv_batch *b, const engram_kv_cache *c) {
     d.kv_len = b->kv_len;
     d.block_table = b->block_table;
     d.table_stride = b->table_stride;
+    d.table_width = table_width(b);
     d.n_seqs = b->n_seqs;
     d.n_query = b->n_query;
     d.n_pages = c->n_pages;
@@ -166,14 +171,14 @@ static int64_t rows_segs_most(const engram_attn_config *cfg, const engram_kv_bat
                                       (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);
 }
 static int64_t keys_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    const int64_t room = batch->table_stride * cache->page_size;
+    const int64_t room = table_width(batch) * cache->page_size;
     return cfg->window > 0 ? std::min<int64_t>(room, (int64_t)cfg->window + 256) : room;
 }
 // The configuration with a window that hides nothing taken for plain causal attention (0): no position
 // reaches the block table's room or 2^31 - 1, so a window of that many tokens ends before every sequence.
 static engram_attn_config effective(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     engram_attn_config c = *cfg;
-    if (c.window >= std::min<int64_t>(batch->table_stride * cache->page_size, INT32_MAX)) c.window = 0;
+    if (c.window >= std::min<int64_t>(table_width(batch) * cache->page_size, INT32_MAX)) c.window = 0;
     return c;
 }
 static int64_t rows_tiles_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {

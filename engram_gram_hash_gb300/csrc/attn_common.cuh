@@ -73,7 +73,7 @@ struct Batch {
     const int64_t *offs;
     const int32_t *kv_len;
     const int32_t *block_table;
-    int64_t table_stride;
+    int64_t table_stride, table_width;
     int64_t n_seqs;
     int64_t n_query;
     int64_t n_pages;
@@ -93,7 +93,7 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const Batch &b, int64_t s, int64_t base) {
     int64_t a = __ldg(b.offs + s) - base, e = __ldg(b.offs + s + 1) - base;
     int64_t kv = __ldg(b.kv_len + s);
-    const int64_t cap = b.table_stride * b.page_size;
+    const int64_t cap = b.table_width * b.page_size;
     const bool bad = a < 0 || e < a || e > b.n_query || kv > cap;
     if (bad) {
         raise_error(ENGRAM_ERANGE);

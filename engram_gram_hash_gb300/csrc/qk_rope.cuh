@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ He
         if (pos < 0) return;  // padding
         const int32_t entry = p.by_page.quotient((int32_t)pos);  // pos < kv_len, an int32
         int32_t page = -1;
-        if (entry < p.batch.table_stride) page = __ldg(p.batch.block_table + s * p.batch.table_stride + entry);
+        if (entry < p.batch.table_width) page = __ldg(p.batch.block_table + s * p.batch.table_stride + entry);
         if (page < 0 || page >= p.batch.n_pages) {
             if (lane == 0) raise_error(ENGRAM_ERANGE);
             return;

@@ -511,7 +511,10 @@ typedef struct {
     const int64_t *seq_offsets; /* int64 [n_seqs + 1], ascending (as engram_hash takes them) */
     const int32_t *kv_len;      /* int32 [n_seqs] */
     const int32_t *block_table; /* int32 [n_seqs][table_stride]; entries past a sequence's length are not read */
-    int64_t table_stride;       /* >= ceil(kv_len[s] / page_size) for every s (ENGRAM_ERANGE on the device) */
+    int64_t table_stride;       /* entries from one sequence's row to the next */
+    int64_t table_width;        /* entries of a row, 1 .. table_stride (0: table_stride; less where the table is a
+                                 * slice of a wider one), >= ceil(kv_len[s] / page_size) for every s
+                                 * (ENGRAM_ERANGE on the device) */
 } engram_kv_batch;
 
 /*
