@@ -80,10 +80,13 @@ struct Batch {
     int32_t page_size;
 };
 
+constexpr int64_t MAX_KV = INT32_MAX - 1023;
+
 // Sequence s of a step: its first row among the step's tokens, its new
 // tokens and its length with them.  Offsets that descend or leave the step's
 // rows, and lengths past the block table, are cut to what is there (rows and
-// table entries stay in bounds) and flagged.
+// table entries stay in bounds) and flagged; so are lengths past MAX_KV, which
+// a tile's end, rounded up, would take out of 32 bits.
 struct Seq {
     int32_t row0;
     int32_t q_len;
@@ -93,7 +96,7 @@ struct Seq {
 __device__ __forceinline__ Seq load_seq(const Batch &b, int64_t s, int64_t base) {
     int64_t a = __ldg(b.offs + s) - base, e = __ldg(b.offs + s + 1) - base;
     int64_t kv = __ldg(b.kv_len + s);
-    const int64_t cap = b.table_width * b.page_size;
+    const int64_t room = b.table_width * b.page_size, cap = room < MAX_KV ? room : MAX_KV;
     const bool bad = a < 0 || e < a || e > b.n_query || kv > cap;
     if (bad) {
         raise_error(ENGRAM_ERANGE);

@@ -509,7 +509,7 @@ typedef struct {
     int64_t n_seqs;
     int64_t n_query;            /* new tokens in all, seq_offsets[n_seqs] - seq_offsets[0], < 2^31 */
     const int64_t *seq_offsets; /* int64 [n_seqs + 1], ascending (as engram_hash takes them) */
-    const int32_t *kv_len;      /* int32 [n_seqs] */
+    const int32_t *kv_len;      /* int32 [n_seqs], at most 2^31 - 1024 */
     const int32_t *block_table; /* int32 [n_seqs][table_stride]; entries past a sequence's length are not read */
     int64_t table_stride;       /* entries from one sequence's row to the next */
     int64_t table_width;        /* entries of a row, 1 .. table_stride (0: table_stride; less where the table is a
@@ -572,7 +572,8 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  * are split over the GPU by a rule on the batch's lengths, read on the
  * device; partial results are joined in a fixed order, so equal inputs give
  * equal bits.  A page id outside [0, n_pages) sets ENGRAM_ERANGE and reads as
- * zeros.  kv_len beyond the block table sets ENGRAM_ERANGE and is cut there.
+ * zeros.  kv_len beyond the block table or 2^31 - 1024 sets ENGRAM_ERANGE and is
+ * cut there.
  */
 size_t engram_paged_attention_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache *cache,
                                               const engram_kv_batch *batch);
