@@ -114,6 +114,13 @@ __device__ __forceinline__ int32_t first_seen(int32_t pos, int32_t window) {
     return window > 0 && pos >= window ? pos - window + 1 : 0;
 }
 
+// What the weighted sum of the row at `pos` is multiplied by: 1 / l.  l is 0 (no
+// weight was above zero) for a row before the sequence's start, which has no
+// key and gets 0, and for one whose scores are all -inf, whose softmax is NaN.
+__device__ __forceinline__ float inverse(float l, int32_t pos) {
+    return l > 0.f ? 1.f / l : (l == 0.f ? (pos < 0 ? 0.f : NAN) : l);
+}
+
 // mbar_wait by a whole warp, with one answer for all its lanes (near the time
 // limit the lanes could differ, and the warp-wide steps that follow must not).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {

@@ -334,8 +334,8 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_saddr) {
 template <typename E>
 __device__ __forceinline__ void write_out(const Params &p, const Walk &w, const Segment &g, int r, int c, float4 v, float l) {
     if (c >= p.head_dim) return;
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
+    const float inv = inverse(l, g.pos0 + tok);
     uint16_t *dst = p.out + (int64_t)w_row(w, tok) * p.out_token_stride + (int64_t)(g.head * p.group + hh) * p.out_head_stride + c;
     *reinterpret_cast<uint2 *>(dst) = make_uint2(E::pack(v.x * inv, v.y * inv), E::pack(v.z * inv, v.w * inv));
 }
@@ -824,8 +824,8 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group, head = g.head * p.group + hh;
+    const float inv = inverse(l, g.pos0 + tok);
     const int64_t row = w_row(w, tok);
     if (lane * 4 < p.head_dim)
         *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + head * p.out_head_stride + lane * 4) =

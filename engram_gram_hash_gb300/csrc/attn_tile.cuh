@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 const int64_t slot = whole ? 0 : w->slot;
                 const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
                 const int64_t out_row = (int64_t)w->q.row0 + tok;
-                const float inv = whole ? (l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l)) : 1.f;
+                const float inv = whole ? inverse(l, w->pos0 + tok) : 1.f;
                 // A lane has a row in TMEM, but lanes that store to 32 rows at once cost an access to L1 each:
                 // the rows change hands in shared memory, 128 bytes of each at a time (the pieces permuted,
                 // so neither way meets a bank twice), and eight lanes store a row's piece.
@@ -1195,8 +1195,8 @@ __global__ void __launch_bounds__(128, JOIN_PER_SM) tile_join_kernel(const __gri
             for (int o = 16; o > 0; o >>= 1) l[q] += __shfl_xor_sync(0xffffffffu, l[q], o);
             const int r = r0 + q;
             if (r >= it.n_rows) continue;
-            const float inv = l[q] > 0.f ? 1.f / l[q] : (l[q] == 0.f ? 0.f : l[q]);
             const int32_t tok = p.by_group.quotient(it.r0 + r), head = it.head * p.group + it.r0 + r - tok * p.group;
+            const float inv = inverse(l[q], it.pos0 + tok);
             const int64_t row = (int64_t)it.q.row0 + tok;
             if (lane * 4 < p.head_dim)
                 *reinterpret_cast<uint2 *>(p.out + row * p.out_token_stride + (int64_t)head * p.out_head_stride + lane * 4) =

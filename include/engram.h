@@ -566,8 +566,9 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  *              bytes, 256-byte aligned; scratch, nothing to clear.  The size
  *              follows from the descriptions alone (nothing on the device is
  *              read); where it is 0, NULL will do
- * A query without any key gets out = 0 and lse = -inf.  Cache slots at or past
- * a sequence's length may hold anything, NaN included: they are not used.
+ * A query without any key gets out = 0 and lse = -inf; one whose scores are all
+ * -inf (infinite keys) out = NaN and lse = -inf.  Cache slots at or past a
+ * sequence's length may hold anything, NaN included: they are not used.
  * From one token per sequence to whole prompts, in any mix.  Long sequences
  * are split over the GPU by a rule on the batch's lengths, read on the
  * device; partial results are joined in a fixed order, so equal inputs give
