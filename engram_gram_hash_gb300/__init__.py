@@ -650,6 +650,11 @@ class engram_attn_config(ctypes.Structure):
     ]
 
 
+    @property
+    def torch_dtype(self):
+        return _ATTN_TYPES[self.dtype]
+
+
 class engram_heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
@@ -678,7 +683,8 @@ class engram_kv_batch(ctypes.Structure):
     ]
 
 
-_ATTN_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_ATTN_TYPES = (torch.bfloat16, torch.float16)
+_ATTN_DTYPES = {t: i for i, t in enumerate(_ATTN_TYPES)}
 
 
 def make_attn_config(n_heads, n_kv_heads, head_dim, dtype=torch.bfloat16, rope_dim=None, rope_interleaved=False,
@@ -697,7 +703,6 @@ def make_attn_config(n_heads, n_kv_heads, head_dim, dtype=torch.bfloat16, rope_d
     c.norm_eps = float(norm_eps)
     c.scale = float(head_dim) ** -0.5 if scale is None else float(scale)
     c.window = int(window)
-    c.torch_dtype, c.address = dtype, ctypes.addressof(c)
     return c
 
 
@@ -728,7 +733,6 @@ def kv_cache(k_pages, v_pages):
     c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
     c.tensors = (k_pages, v_pages)
     c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), k_pages.dtype
-    c.address = ctypes.addressof(c)
     return c
 
 
@@ -753,7 +757,6 @@ def kv_batch(seq_offsets, kv_len, block_table, n_query):
     b.table_width = block_table.shape[1]
     b.table_stride = b.table_width if n <= 1 else block_table.stride(0)
     b.tensors = (seq_offsets, kv_len, block_table)
-    b.address = ctypes.addressof(b)
     return b
 
 
@@ -782,28 +785,28 @@ def _step():
 def _cache_of(cache, cfg):
     if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
         raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.n_kv_heads, cfg.head_dim]}")
-    return cache.address
+    return cache
 
 
 def engram_qk_norm_rope(cfg, q, k, positions, table, w_q=None, w_k=None, q_out=None, k_out=None, stream=None):
     """(q_out, k_out): every head of q [T, n_heads, D] and k [T, n_kv_heads, D] RMS-normed (with w_q / w_k
     [D]; None: no norm) and rotated by its token's position.  Either of q and k may be None; q_out=q and
     k_out=k work in place."""
-    return _step().qk_norm_rope(cfg.address, q, k, positions, table, w_q, w_k, q_out, k_out, stream)
+    return _step().qk_norm_rope(cfg, q, k, positions, table, w_q, w_k, q_out, k_out, stream)
 
 
 def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
     """The step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] into their slots of the cache.
     With q [n_query, n_heads, D], also its norm and rotation in the same launch; returns q_out (None without)."""
-    return _step().kv_append(cfg.address, _cache_of(cache, cfg), batch.address, k, v, table, w_k, q, w_q, q_out, stream)
+    return _step().kv_append(cfg, _cache_of(cache, cfg), batch, k, v, table, w_k, q, w_q, q_out, stream)
 
 
 def engram_paged_attention_workspace_bytes(cfg, cache, batch):
     """Bytes of workspace that engram_paged_attention needs for this batch (0: none)."""
-    return int(lib().engram_paged_attention_workspace_bytes(cfg.address, cache.address, batch.address))
+    return int(lib().engram_paged_attention_workspace_bytes(*(ctypes.byref(x) for x in (cfg, cache, batch))))
 
 
 def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
     """out [n_query, n_heads, D]: attention of the step's tokens over the paged cache (and lse fp32
     [n_query, n_heads] if a tensor for it is given)."""
-    return _step().paged_attention(cfg.address, _cache_of(cache, cfg), batch.address, q, out, lse, workspace, stream)
+    return _step().paged_attention(cfg, _cache_of(cache, cfg), batch, q, out, lse, workspace, stream)

@@ -105,6 +105,22 @@ T *address(PyObject *o) {
     return static_cast<T *>(p);
 }
 
+// One of engram.h's structures as its ctypes object's own memory (never a kept
+// address: copies of the object would bring the first one's along).
+template <typename T>
+const T *structure(PyObject *o, const char *name) {
+    Py_buffer view;
+    if (PyObject_GetBuffer(o, &view, PyBUF_SIMPLE) != 0) {
+        PyErr_Clear();
+        view.buf = nullptr;
+        view.len = 0;
+    } else {
+        PyBuffer_Release(&view);  // the caller's argument keeps the memory
+    }
+    if (view.len != (Py_ssize_t)sizeof(T)) fail(PyExc_TypeError, std::string(name) + " must be its engram.h structure");
+    return static_cast<const T *>(view.buf);
+}
+
 // The device of the call's tensors and its stream (a torch.cuda.Stream, or None
 // for the current one on that device), both current while this lives: what is
 // allocated here belongs to the stream that uses it.
@@ -163,7 +179,7 @@ PyObject *guarded(Py_ssize_t got, Py_ssize_t want, const F &body) {
 // (cfg, q, k, positions, table, w_q, w_k, q_out, k_out, stream) -> (q_out, k_out)
 PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 10, [&]() -> PyObject * {
-        const auto *c = address<engram_attn_config>(a[0]);
+        const auto *c = structure<engram_attn_config>(a[0], "cfg");
         const at::Tensor *q = tensor(a[1], "q"), *k = tensor(a[2], "k"), *pos = tensor(a[3], "positions");
         const at::Tensor *some = q ? q : k;
         if (!some) fail(PyExc_ValueError, "q or k is needed");
@@ -203,9 +219,9 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (cfg, cache, batch, k, v, table, w_k, q, w_q, q_out, stream) -> q_out or None
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 11, [&]() -> PyObject * {
-        const auto *c = address<engram_attn_config>(a[0]);
-        const auto *cache = address<engram_kv_cache>(a[1]);
-        const auto *batch = address<engram_kv_batch>(a[2]);
+        const auto *c = structure<engram_attn_config>(a[0], "cfg");
+        const auto *cache = structure<engram_kv_cache>(a[1], "cache");
+        const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *k = tensor(a[3], "k"), *v = tensor(a[4], "v"), *q = tensor(a[7], "q");
         if (!k || !v) fail(PyExc_ValueError, "k and v are needed");
         const int64_t T = batch->n_query;
@@ -230,9 +246,9 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (cfg, cache, batch, q, out, lse, workspace, stream) -> out
 PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 8, [&]() -> PyObject * {
-        const auto *c = address<engram_attn_config>(a[0]);
-        const auto *cache = address<engram_kv_cache>(a[1]);
-        const auto *batch = address<engram_kv_batch>(a[2]);
+        const auto *c = structure<engram_attn_config>(a[0], "cfg");
+        const auto *cache = structure<engram_kv_cache>(a[1], "cache");
+        const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *q = tensor(a[3], "q"), *lse = tensor(a[5], "lse"), *ws = tensor(a[6], "workspace");
         if (!q) fail(PyExc_ValueError, "q is needed");
         const int64_t T = batch->n_query;
