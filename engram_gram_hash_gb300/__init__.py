@@ -483,6 +483,8 @@ def engram_host_cache_new(cfg, slots, capacity, device=None, stream=None):
     cache = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     _check(lib().engram_host_cache_reset(ctypes.byref(cfg), _ptr(cache), int(slots), int(capacity), _stream(stream)),
            "engram_host_cache_reset")
+    if cache.device_index != batch.device_index:
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, the batch on cuda:{batch.device_index}")
     return cache
 
 
@@ -715,6 +717,11 @@ def rope_table(n_positions, rope_dim, theta=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+def _one_device(**tensors):
+    if len({t.device for t in tensors.values()}) > 1:
+        raise ValueError("on one device: " + ", ".join(f"{n} is on {t.device}" for n, t in tensors.items()))
+
+
 def kv_cache(k_pages, v_pages):
     """An engram_kv_cache over K and V pages [n_pages, page_size, n_kv_heads, head_dim] with the same
     strides (any, the head's values contiguous: permute for other orders).  It keeps the tensors alive."""
@@ -727,11 +734,12 @@ def kv_cache(k_pages, v_pages):
             raise ValueError(f"{name} must be a CUDA tensor")
     if k_pages.dtype != v_pages.dtype or k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
         raise ValueError("k_pages and v_pages must have the same type, shape and strides")
+    _one_device(k_pages=k_pages, v_pages=v_pages)
     c = engram_kv_cache()
     c.k, c.v = k_pages.data_ptr(), v_pages.data_ptr()
     c.n_pages, c.page_size = k_pages.shape[0], k_pages.shape[1]
     c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
-    c.tensors = (k_pages, v_pages)
+    c.tensors, c.device_index = (k_pages, v_pages), k_pages.get_device()
     c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), k_pages.dtype
     return c
 
@@ -751,12 +759,13 @@ def kv_batch(seq_offsets, kv_len, block_table, n_query):
         raise ValueError("block_table must have contiguous rows")
     if seq_offsets.numel() != n + 1:
         raise ValueError("seq_offsets must have one entry more than kv_len")
+    _one_device(seq_offsets=seq_offsets, kv_len=kv_len, block_table=block_table)
     b = engram_kv_batch()
     b.n_seqs, b.n_query = n, int(n_query)
     b.seq_offsets, b.kv_len, b.block_table = seq_offsets.data_ptr(), kv_len.data_ptr(), block_table.data_ptr()
     b.table_width = block_table.shape[1]
     b.table_stride = b.table_width if n <= 1 else block_table.stride(0)
-    b.tensors = (seq_offsets, kv_len, block_table)
+    b.tensors, b.device_index = (seq_offsets, kv_len, block_table), kv_len.get_device()
     return b
 
 
@@ -782,9 +791,11 @@ def _step():
     return _step_module
 
 
-def _cache_of(cache, cfg):
+def _cache_of(cache, cfg, batch):
     if cache.torch_dtype is not cfg.torch_dtype or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
         raise ValueError(f"the cache must hold {cfg.torch_dtype} heads {[cfg.n_kv_heads, cfg.head_dim]}")
+    if cache.device_index != batch.device_index:
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, the batch on cuda:{batch.device_index}")
     return cache
 
 
@@ -798,7 +809,8 @@ def engram_qk_norm_rope(cfg, q, k, positions, table, w_q=None, w_k=None, q_out=N
 def engram_kv_append(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
     """The step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] into their slots of the cache.
     With q [n_query, n_heads, D], also its norm and rotation in the same launch; returns q_out (None without)."""
-    return _step().kv_append(cfg, _cache_of(cache, cfg), batch, k, v, table, w_k, q, w_q, q_out, stream)
+    return _step().kv_append(cfg, _cache_of(cache, cfg, batch), batch, k, v, table, w_k, q, w_q, q_out, stream,
+                             cache.device_index)
 
 
 def engram_paged_attention_workspace_bytes(cfg, cache, batch):
@@ -809,4 +821,5 @@ def engram_paged_attention_workspace_bytes(cfg, cache, batch):
 def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
     """out [n_query, n_heads, D]: attention of the step's tokens over the paged cache (and lse fp32
     [n_query, n_heads] if a tensor for it is given)."""
-    return _step().paged_attention(cfg, _cache_of(cache, cfg), batch, q, out, lse, workspace, stream)
+    return _step().paged_attention(cfg, _cache_of(cache, cfg, batch), batch, q, out, lse, workspace, stream,
+                                   cache.device_index)

@@ -53,21 +53,32 @@ void need_type(const at::Tensor &t, at::ScalarType type, const char *name) {
         fail(PyExc_TypeError, std::string(name) + " must be " + toString(type) + ", got " + toString(t.scalar_type()));
 }
 
-// A contiguous CUDA tensor of the type.
-void need(const at::Tensor &t, at::ScalarType type, const char *name) {
+// On the call's device (its cache's or first tensor's; CUDA is checked before): pointers are handed on, and
+// another device's would fault there.
+[[noreturn, gnu::cold, gnu::noinline]] void wrong_device(const at::Tensor &t, at::Device dev, const char *name) {
+    fail(PyExc_ValueError, std::string(name) + " must be on " + dev.str() + ", got " + t.device().str());
+}
+void need_device(const at::Tensor &t, at::Device dev, const char *name) {
+    if (t.get_device() != dev.index()) wrong_device(t, dev, name);
+}
+
+// A contiguous CUDA tensor of the type on the device.
+void need(const at::Tensor &t, at::ScalarType type, at::Device dev, const char *name) {
     need_type(t, type, name);
     if (!t.is_contiguous()) fail(PyExc_ValueError, std::string(name) + " must be contiguous");
     if (!t.is_cuda()) fail(PyExc_ValueError, std::string(name) + " must be a CUDA tensor");
+    need_device(t, dev, name);
 }
 
 // A [tokens, heads, head_dim] tensor with contiguous heads.
-engram_heads heads(const at::Tensor &t, const engram_attn_config *c, int64_t tokens, int64_t n, const char *name) {
+engram_heads heads(const at::Tensor &t, const engram_attn_config *c, int64_t tokens, int64_t n, at::Device dev, const char *name) {
     need_type(t, type_of(c), name);
     const int64_t want[3] = {tokens, n, c->head_dim};
     if (t.sizes() != at::IntArrayRef(want, 3))
         fail(PyExc_ValueError, std::string(name) + " must be " + sizes({want, 3}) + ", got " + sizes(t.sizes()));
     if ((t.stride(2) != 1 && c->head_dim > 1) || !t.is_cuda())
         fail(PyExc_ValueError, std::string(name) + " must be a CUDA tensor with contiguous heads");
+    need_device(t, dev, name);
     // the stride of a size of one is never used, and torch may give it any value
     return {t.data_ptr(), tokens > 1 ? t.stride(0) : 0, n > 1 ? t.stride(1) : 0};
 }
@@ -76,22 +87,22 @@ at::Tensor new_heads(const at::Tensor &like, int64_t tokens, int64_t n, const en
     return at::empty({tokens, n, c->head_dim}, at::TensorOptions().dtype(type_of(c)).device(like.device()));
 }
 
-const void *weight(PyObject *o, const engram_attn_config *c, const char *name) {
+const void *weight(PyObject *o, const engram_attn_config *c, at::Device dev, const char *name) {
     const at::Tensor *w = tensor(o, name);
     if (!w) return nullptr;
-    need(*w, type_of(c), name);
+    need(*w, type_of(c), dev, name);
     if (w->numel() != c->head_dim) fail(PyExc_ValueError, std::string(name) + " must have " + std::to_string(c->head_dim) + " values");
     return w->data_ptr();
 }
 
-const float *table(PyObject *o, const engram_attn_config *c, int64_t &rows) {
+const float *table(PyObject *o, const engram_attn_config *c, at::Device dev, int64_t &rows) {
     const at::Tensor *t = tensor(o, "table");
     rows = 0;
     if (!t) {
         if (c->rope_dim) fail(PyExc_ValueError, "table is needed: rope_dim is not 0");
         return nullptr;
     }
-    need(*t, at::kFloat, "table");
+    need(*t, at::kFloat, dev, "table");
     if (t->dim() != 2 || t->size(1) != c->rope_dim)
         fail(PyExc_ValueError, "table must be [positions, " + std::to_string(c->rope_dim) + "]");
     rows = t->size(0);
@@ -119,6 +130,13 @@ const T *structure(PyObject *o, const char *name) {
     }
     if (view.len != (Py_ssize_t)sizeof(T)) fail(PyExc_TypeError, std::string(name) + " must be its engram.h structure");
     return static_cast<const T *>(view.buf);
+}
+
+// The CUDA device of an index.
+at::Device cache_device(PyObject *o) {
+    const long i = PyLong_AsLong(o);
+    if (i == -1 && PyErr_Occurred()) throw PyFailed();
+    return at::Device(at::kCUDA, (c10::DeviceIndex)i);
 }
 
 // The device of the call's tensors and its stream (a torch.cuda.Stream, or None
@@ -185,26 +203,27 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!some) fail(PyExc_ValueError, "q or k is needed");
         if (some->dim() != 3) fail(PyExc_ValueError, "q and k must be [tokens, heads, head_dim]");
         const int64_t T = some->size(0);
+        const at::Device dev = some->device();
         engram_heads hq, hk, hqo, hko;
         at::Tensor made_q, made_k;
-        if (q) hq = heads(*q, c, T, c->n_heads, "q");
-        if (k) hk = heads(*k, c, T, c->n_kv_heads, "k");
+        if (q) hq = heads(*q, c, T, c->n_heads, dev, "q");
+        if (k) hk = heads(*k, c, T, c->n_kv_heads, dev, "k");
         const Where where(a[9], *some);
         if (q) {
             if (a[7] == Py_None) made_q = new_heads(*q, T, c->n_heads, c);
-            hqo = heads(a[7] == Py_None ? made_q : *tensor(a[7], "q_out"), c, T, c->n_heads, "q_out");
+            hqo = heads(a[7] == Py_None ? made_q : *tensor(a[7], "q_out"), c, T, c->n_heads, dev, "q_out");
         }
         if (k) {
             if (a[8] == Py_None) made_k = new_heads(*k, T, c->n_kv_heads, c);
-            hko = heads(a[8] == Py_None ? made_k : *tensor(a[8], "k_out"), c, T, c->n_kv_heads, "k_out");
+            hko = heads(a[8] == Py_None ? made_k : *tensor(a[8], "k_out"), c, T, c->n_kv_heads, dev, "k_out");
         }
         if (pos) {
-            need(*pos, at::kInt, "positions");
+            need(*pos, at::kInt, dev, "positions");
             if (pos->numel() != T) fail(PyExc_ValueError, "positions must have " + std::to_string(T) + " entries");
         }
         int64_t rows;
-        const float *tab = table(a[4], c, rows);
-        const void *wq = weight(a[5], c, "w_q"), *wk = weight(a[6], c, "w_k");
+        const float *tab = table(a[4], c, dev, rows);
+        const void *wq = weight(a[5], c, dev, "w_q"), *wk = weight(a[6], c, dev, "w_k");
         check(fn_qk(c, T, q ? &hq : nullptr, k ? &hk : nullptr, pos ? pos->data_ptr<int32_t>() : nullptr, tab, rows, wq, wk,
                     q ? &hqo : nullptr, k ? &hko : nullptr, where.stream.stream()),
               "engram_qk_norm_rope");
@@ -216,56 +235,58 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// (cfg, cache, batch, k, v, table, w_k, q, w_q, q_out, stream) -> q_out or None
+// (cfg, cache, batch, k, v, table, w_k, q, w_q, q_out, stream, the cache's device) -> q_out or None
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 11, [&]() -> PyObject * {
+    return guarded(n, 12, [&]() -> PyObject * {
         const auto *c = structure<engram_attn_config>(a[0], "cfg");
         const auto *cache = structure<engram_kv_cache>(a[1], "cache");
         const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *k = tensor(a[3], "k"), *v = tensor(a[4], "v"), *q = tensor(a[7], "q");
         if (!k || !v) fail(PyExc_ValueError, "k and v are needed");
         const int64_t T = batch->n_query;
-        const engram_heads hk = heads(*k, c, T, c->n_kv_heads, "k"), hv = heads(*v, c, T, c->n_kv_heads, "v");
+        const at::Device dev = cache_device(a[11]);
+        const engram_heads hk = heads(*k, c, T, c->n_kv_heads, dev, "k"), hv = heads(*v, c, T, c->n_kv_heads, dev, "v");
         engram_heads hq, ho;
         at::Tensor made;
-        if (q) hq = heads(*q, c, T, c->n_heads, "q");
+        if (q) hq = heads(*q, c, T, c->n_heads, dev, "q");
         const Where where(a[10], *k);
         if (q) {
             if (a[9] == Py_None) made = new_heads(*q, T, c->n_heads, c);
-            ho = heads(a[9] == Py_None ? made : *tensor(a[9], "q_out"), c, T, c->n_heads, "q_out");
+            ho = heads(a[9] == Py_None ? made : *tensor(a[9], "q_out"), c, T, c->n_heads, dev, "q_out");
         }
         int64_t rows;
-        const float *tab = table(a[5], c, rows);
-        const void *wk = weight(a[6], c, "w_k"), *wq = weight(a[8], c, "w_q");
+        const float *tab = table(a[5], c, dev, rows);
+        const void *wk = weight(a[6], c, dev, "w_k"), *wq = weight(a[8], c, dev, "w_q");
         check(fn_append(c, cache, batch, &hk, &hv, wk, tab, rows, q ? &hq : nullptr, wq, q ? &ho : nullptr, where.stream.stream()),
               "engram_kv_append");
         return q ? give(a[9], made) : Py_NewRef(Py_None);
     });
 }
 
-// (cfg, cache, batch, q, out, lse, workspace, stream) -> out
+// (cfg, cache, batch, q, out, lse, workspace, stream, the cache's device) -> out
 PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 8, [&]() -> PyObject * {
+    return guarded(n, 9, [&]() -> PyObject * {
         const auto *c = structure<engram_attn_config>(a[0], "cfg");
         const auto *cache = structure<engram_kv_cache>(a[1], "cache");
         const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *q = tensor(a[3], "q"), *lse = tensor(a[5], "lse"), *ws = tensor(a[6], "workspace");
         if (!q) fail(PyExc_ValueError, "q is needed");
         const int64_t T = batch->n_query;
-        const engram_heads hq = heads(*q, c, T, c->n_heads, "q");
+        const at::Device dev = cache_device(a[8]);
+        const engram_heads hq = heads(*q, c, T, c->n_heads, dev, "q");
         const Where where(a[7], *q);
         at::Tensor made, made_ws;
         if (a[4] == Py_None) made = new_heads(*q, T, c->n_heads, c);
-        const engram_heads ho = heads(a[4] == Py_None ? made : *tensor(a[4], "out"), c, T, c->n_heads, "out");
+        const engram_heads ho = heads(a[4] == Py_None ? made : *tensor(a[4], "out"), c, T, c->n_heads, dev, "out");
         if (lse) {
-            need(*lse, at::kFloat, "lse");
+            need(*lse, at::kFloat, dev, "lse");
             const int64_t want[2] = {T, c->n_heads};
             if (lse->sizes() != at::IntArrayRef(want, 2)) fail(PyExc_ValueError, "lse must be " + sizes({want, 2}));
         }
         size_t bytes = 0;
         void *room = nullptr;
         if (ws) {
-            need(*ws, at::kByte, "workspace");
+            need(*ws, at::kByte, dev, "workspace");
             bytes = (size_t)ws->numel();
             room = ws->data_ptr();
         } else if ((bytes = fn_bytes(c, cache, batch)) > 0) {  // freed on return, to this stream's pool
