@@ -12,6 +12,7 @@ LIB_PATH = os.path.join(HERE, "libengram.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 STEP_SRC = os.path.join(SRC_DIR, "step_binding.cpp")
 STEP_PATH = os.path.join(HERE, "_step.so")
+STEP_STAMP = os.path.join(OBJ_DIR, "_step.torch")  # the torch and Python that it was built against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -29,6 +30,23 @@ def _stale(path, srcs):
         return True
     t = os.path.getmtime(path)
     return any(os.path.getmtime(s) > t for s in srcs)
+
+
+def _against():
+    import torch
+
+    return f"{torch.__version__} {sysconfig.get_config_var('EXT_SUFFIX')}"
+
+
+def step_stale():
+    """Whether the binding module is older than its sources or was built against another torch or Python (it uses
+    torch's C++ interface, which changes from one version to the next)."""
+    if _stale(STEP_PATH, [STEP_SRC, os.path.join(os.path.dirname(HERE), "include", "engram.h")]):
+        return True
+    if not os.path.exists(STEP_STAMP):
+        return True
+    with open(STEP_STAMP, encoding="utf-8") as f:
+        return f.read() != _against()
 
 
 def step_cmd():
@@ -54,12 +72,13 @@ def link_cmd(objs, out=LIB_PATH):
 
 def build(force=False, verbose=False):
     """Compile what is older than its sources; returns the library's path."""
-    cmds, objs = [], []
+    cmds, objs, step = [], [], force or step_stale()
     if force or _stale(LIB_PATH, sources()):
         os.makedirs(OBJ_DIR, exist_ok=True)
         objs = [os.path.join(OBJ_DIR, os.path.splitext(os.path.basename(s))[0] + ".o") for s in MAIN_SRCS]
         cmds += [compile_cmd(s, o) for s, o in zip(MAIN_SRCS, objs)]
-    if force or _stale(STEP_PATH, [STEP_SRC, os.path.join(os.path.dirname(HERE), "include", "engram.h")]):
+    if step:
+        os.makedirs(OBJ_DIR, exist_ok=True)
         cmds.append(step_cmd())
     if verbose:
         for cmd in cmds:
@@ -69,6 +88,9 @@ def build(force=False, verbose=False):
     for cmd, code in zip(cmds, codes):
         if code:
             raise subprocess.CalledProcessError(code, cmd)
+    if step:
+        with open(STEP_STAMP, "w", encoding="utf-8") as f:
+            f.write(_against())
     if objs:
         subprocess.check_call(link_cmd(objs))
     return LIB_PATH
