@@ -483,8 +483,6 @@ def engram_host_cache_new(cfg, slots, capacity, device=None, stream=None):
     cache = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
     _check(lib().engram_host_cache_reset(ctypes.byref(cfg), _ptr(cache), int(slots), int(capacity), _stream(stream)),
            "engram_host_cache_reset")
-    if cache.device_index != batch.device_index:
-        raise ValueError(f"the cache is on cuda:{cache.device_index}, the batch on cuda:{batch.device_index}")
     return cache
 
 
