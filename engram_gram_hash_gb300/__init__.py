@@ -744,8 +744,9 @@ def kv_cache(k_pages, v_pages):
 
 def kv_batch(seq_offsets, kv_len, block_table, n_query):
     """An engram_kv_batch: seq_offsets int64 [n_seqs + 1], kv_len int32 [n_seqs] (lengths with the new
-    tokens), block_table int32 [n_seqs, pages] (a slice of a wider one will do), n_query new tokens in all.  It keeps the tensors alive;
-    their contents may change from step to step."""
+    tokens), block_table int32 [n_seqs, pages] (a slice of a wider one will do: how keys are shared out
+    follows from its width), n_query new tokens in all.  It keeps the tensors alive; their contents may
+    change from step to step."""
     _need(seq_offsets, torch.int64, "seq_offsets")
     _need(kv_len, torch.int32, "kv_len")
     if block_table.dtype != torch.int32:

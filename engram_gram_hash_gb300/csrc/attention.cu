@@ -191,11 +191,12 @@ static int64_t rows_tiles_most(const engram_attn_config *cfg, const engram_kv_ca
 //     GPU at once.
 //   whole: no cut, no join; about one segment an SM, or so short that a cut cannot pay.
 //   cut: equal runs of tiles for every SM, then the join (a launch and about 5 us).
-// Measured, 8 key/value heads of 128, us a call in a CUDA graph, cluster of 8 / of 4 / whole or cut:
-//   1 sequence of 500 tokens 9.8 / 10.1 / 11.6, 2,000: 11.5 / 13.6 / 12.6, 4,000: 13.7 / 18.3 / 16.9,
-//     8,000: 18.5 / - / 16.5;  2 of 2,000: - / 13.6 / 12.9 (17.5 with the second launch's host time);
-//   4 of 2,000: - / 13.8 / 18.3, 4,000: - / 18.5 / 21.1;  16 of 500 whole 12.1, cut 19.5, 2,000: 27 / 33;
-//   64 of 1,000: cut 58, whole 55 with equal lengths, but unequal ones would wait for the longest.
+// Measured, 8 key/value heads of 128, us a call in a CUDA graph, cluster of 8 / of 4 / whole / cut:
+//   1 sequence of 500 tokens 7.0 / 7.3 / 9.2 / 9.1, 2,000: 8.4 / 10.4 / 21.7 / 11.0, 4,000: 10.4 / 14.5 / 38 / 14.2,
+//     8,000: 14.7 / 22.9 / 70 / 14.2;  2 of 2,000: 16.1 / 10.5 / 21.9 / 10.9;
+//   4 of 2,000: 24.2 / 10.7 / 21.9 / 15.2, 4,000: 30.3 / 14.9 / 38 / 18.0;  16 of 500: - / 29 / 9.8 / 15.0,
+//     2,000: - / 48 / 25.2 / 31.0;  64 of 1,000: whole 50.7, cut 53.6 with equal lengths, but unequal ones would
+//     wait for the longest.
 struct RowsShares {
     int32_t cluster, whole, runs;
     bool cut() const { return whole == 0 && runs > 1; }

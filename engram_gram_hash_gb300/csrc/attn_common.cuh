@@ -131,8 +131,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // weight 0 there, but 0 times an infinity is NaN, and the products run over
 // whole tiles.  So in tiles that some row sees only part of ("edge" tiles) such
 // values are cleared before the product (clear_nonfinite) and, where any was
-// found, added to the rows that do see their key afterwards (add_nonfinite):
-// the sum over the visible keys is infinite or NaN exactly where it should be.
+// found, added to the rows that do see their key afterwards (add_nonfinite).
+// No hidden value reaches a row; a row that sees one that is not finite has no
+// finite result either, but it may be NaN where the sum is an infinity: in the
+// other tiles, or when parts are joined, a weight that underflows to 0 meets it.
 
 // The infinities and NaN of the two values in w are set to zero.
 template <typename E>

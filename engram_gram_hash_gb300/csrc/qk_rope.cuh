@@ -9,7 +9,9 @@
 // the fp32 table row of a token (rope_dim * 4 bytes) is read once per warp and
 // serves all its heads.  32,768 tokens of 32 + 8 heads of 128: 120 us, 5.7 TB/s
 // (84 % of the copy rate); 15,026 tokens' keys and values into pages 27 us,
-// 4.8 TB/s (the chain offsets -> length -> page -> slot bounds it).
+// 4.8 TB/s (bound by the chain offsets -> length -> page -> slot of every token;
+// this form also spills, 72 bytes a thread at the 64 registers that four blocks
+// an SM leave).
 // Layout: a lane holds two 8-value pieces of a head, chosen so that both
 // values of every pair are in the same lane (HALVES: piece l and the piece
 // rope_dim/2 further on; INTERLEAVED: any two), so the rotation needs no

@@ -456,6 +456,9 @@ engram_status engram_forward_host_pipelined(const engram_config *cfg, const int3
  *
  * Values are bf16 or fp16 (cfg->dtype; pointers are void*); head sums, scores,
  * softmax statistics and accumulators are fp32, each output is rounded once.
+ * Attention also rounds its softmax weights to the 16-bit type on their way
+ * into the second product (the matrix instruction's operand type): about as
+ * much error again as the output's own rounding.
  * ======================================================================= */
 #define ENGRAM_BF16 0
 #define ENGRAM_FP16 1
@@ -568,7 +571,9 @@ engram_status engram_kv_append(const engram_attn_config *cfg, const engram_kv_ca
  *              read); where it is 0, NULL will do
  * A query without any key gets out = 0 and lse = -inf; one whose scores are all
  * -inf (infinite keys) out = NaN and lse = -inf.  Cache slots at or past a
- * sequence's length may hold anything, NaN included: they are not used.
+ * sequence's length may hold anything, NaN included: they are not used.  An
+ * infinite or NaN value reaches only the queries that see its position; there
+ * the result is not finite (NaN for an infinity whose weight underflows).
  * From one token per sequence to whole prompts, in any mix.  Long sequences
  * are split over the GPU by a rule on the batch's lengths, read on the
  * device; partial results are joined in a fixed order, so equal inputs give
