@@ -7,6 +7,7 @@ been built (``__graft_entry__.build()``), importing works but every call
 raises: there is no CPU path.
 """
 
+import collections
 import ctypes
 import os
 
@@ -126,6 +127,10 @@ def lib():
             "engram_kv_append": ([P, P, P, P, P, P, P, i64, P, P, P, P], ctypes.c_int),
             "engram_paged_attention_workspace_bytes": ([P, P, P], sz),
             "engram_paged_attention": ([P, P, P, P, P, P, P, sz, P], ctypes.c_int),
+            "engram_kv_plan": ([P, P], ctypes.c_int),
+            "engram_kv_append_q8": ([P, P, P, P, P, P, P, i64, P, P, P, P], ctypes.c_int),
+            "engram_paged_attention_q8_workspace_bytes": ([P, P, P], sz),
+            "engram_paged_attention_q8": ([P, P, P, P, P, P, P, sz, P], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             f = getattr(L, name)
@@ -671,6 +676,21 @@ class engram_kv_cache(ctypes.Structure):
     ]
 
 
+class engram_kv_cache_q8(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int32),
+        ("block_tokens", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
 class engram_kv_batch(ctypes.Structure):
     _fields_ = [
         ("n_seqs", ctypes.c_int64),
@@ -742,6 +762,36 @@ def kv_cache(k_pages, v_pages):
     return c
 
 
+def kv_cache_q8(k_pages, v_pages, k_scales, v_scales):
+    """An engram_kv_cache_q8 over K and V codes, torch.float8_e4m3fn [n_pages, page_size, n_kv_heads, head_dim] with
+    the same strides (any, the head's codes contiguous), and their scales, fp32 [n_pages, n_kv_heads, blocks]
+    contiguous: page_size / blocks consecutive tokens (16, 32, 64 or 128) share one.  It keeps the tensors alive."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if t.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"{name} must be torch.float8_e4m3fn, got {t.dtype}")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim] with contiguous heads")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same shape and strides")
+    pages, size, heads = k_pages.shape[:3]
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _need(t, torch.float32, name)
+        if t.dim() != 3 or t.shape[:2] != (pages, heads) or t.shape[2] < 1 or size % t.shape[2]:
+            raise ValueError(f"{name} must be [{pages}, {heads}, blocks] with blocks that divide the page's {size} tokens")
+    if k_scales.shape != v_scales.shape or size // k_scales.shape[2] not in (16, 32, 64, 128):
+        raise ValueError("k_scales and v_scales must be alike, with blocks of 16, 32, 64 or 128 tokens")
+    _one_device(k_pages=k_pages, v_pages=v_pages, k_scales=k_scales, v_scales=v_scales)
+    c = engram_kv_cache_q8()
+    c.k, c.v, c.k_scales, c.v_scales = (t.data_ptr() for t in (k_pages, v_pages, k_scales, v_scales))
+    c.n_pages, c.page_size, c.block_tokens = pages, size, size // k_scales.shape[2]
+    c.page_stride, c.token_stride, c.head_stride = k_pages.stride()[:3]
+    c.tensors, c.device_index = (k_pages, v_pages, k_scales, v_scales), k_pages.get_device()
+    c.heads_dim, c.torch_dtype = tuple(k_pages.shape[2:]), torch.float8_e4m3fn
+    return c
+
+
 def kv_batch(seq_offsets, kv_len, block_table, n_query):
     """An engram_kv_batch: seq_offsets int64 [n_seqs + 1], kv_len int32 [n_seqs] (lengths with the new
     tokens), block_table int32 [n_seqs, pages] (a slice of a wider one will do: how keys are shared out
@@ -785,7 +835,8 @@ def _step():
         L = lib()
         m.bind(EngramError, *[ctypes.cast(f, ctypes.c_void_p).value
                               for f in (L.engram_qk_norm_rope, L.engram_kv_append, L.engram_paged_attention,
-                                        L.engram_paged_attention_workspace_bytes)])
+                                        L.engram_paged_attention_workspace_bytes, L.engram_kv_plan, L.engram_kv_append_q8,
+                                        L.engram_paged_attention_q8, L.engram_paged_attention_q8_workspace_bytes)])
         _step_module = m
     return _step_module
 
@@ -822,3 +873,49 @@ def engram_paged_attention(cfg, cache, batch, q, out=None, lse=None, workspace=N
     [n_query, n_heads] if a tensor for it is given)."""
     return _step().paged_attention(cfg, _cache_of(cache, cfg, batch), batch, q, out, lse, workspace, stream,
                                    cache.device_index)
+
+
+# ------------------------------------------------------------- the 8-bit cache --
+
+
+KvPlan = collections.namedtuple("KvPlan", "seq_offsets kv_len n_free positions slots counts")
+
+
+def engram_kv_plan(new_len, kv_len, block_table, free_pages, n_free, page_size, max_tokens, keep_len=None,
+                   kv_len_out=None, n_free_out=None, seq_offsets=None, positions=None, slots=None, counts=None,
+                   stream=None):
+    """The step's batch from the requests' lengths (int32 [n_seqs]: new_len come, keep_len of the kv_len cached ones
+    stay; None: all): pages between block_table [n_seqs, pages] and the stack free_pages [n_pages], of which
+    n_free [1] are free.  Returns a KvPlan of seq_offsets int64 [n_seqs + 1], the new lengths and free pages, positions
+    int32 and slots int64 [max_tokens] (-1 past the step's tokens) and counts int32 [4] (new tokens, pages taken, given
+    back, missing); what is given as an output is written there (kv_len_out=kv_len and n_free_out=n_free: in
+    place), what is not is made."""
+    return KvPlan(*_step().kv_plan(new_len, kv_len, block_table, free_pages, n_free, page_size, max_tokens, keep_len,
+                                   kv_len_out, n_free_out, seq_offsets, positions, slots, counts, stream))
+
+
+def _cache_q8_of(cache, cfg, batch):
+    if not isinstance(cache, engram_kv_cache_q8) or cache.heads_dim != (cfg.n_kv_heads, cfg.head_dim):
+        raise ValueError(f"the cache must be a kv_cache_q8 of heads {[cfg.n_kv_heads, cfg.head_dim]}")
+    if cache.device_index != batch.device_index:
+        raise ValueError(f"the cache is on cuda:{cache.device_index}, the batch on cuda:{batch.device_index}")
+    return cache
+
+
+def engram_kv_append_q8(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
+    """engram_kv_append into a kv_cache_q8: the step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] as
+    codes, their blocks' scales set or raised.  With q, also its norm and rotation in the same launch; returns q_out
+    (None without)."""
+    return _step().kv_append_q8(cfg, _cache_q8_of(cache, cfg, batch), batch, k, v, table, w_k, q, w_q, q_out, stream,
+                                cache.device_index)
+
+
+def engram_paged_attention_q8_workspace_bytes(cfg, cache, batch):
+    """Bytes of workspace that engram_paged_attention_q8 needs for this batch (0: none)."""
+    return int(lib().engram_paged_attention_q8_workspace_bytes(*(ctypes.byref(x) for x in (cfg, cache, batch))))
+
+
+def engram_paged_attention_q8(cfg, cache, batch, q, out=None, lse=None, workspace=None, stream=None):
+    """engram_paged_attention over a kv_cache_q8."""
+    return _step().paged_attention_q8(cfg, _cache_q8_of(cache, cfg, batch), batch, q, out, lse, workspace, stream,
+                                      cache.device_index)

@@ -1,4 +1,4 @@
-"""Builds libengram.so in-tree with nvcc for sm_103a (two translation units, compiled side by side) and, with
+"""Builds libengram.so in-tree with nvcc for sm_103a (three translation units, compiled side by side) and, with
 the host compiler, the binding's marshalling module for the decode-step calls (against torch's headers)."""
 
 import os
@@ -7,7 +7,7 @@ import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
-MAIN_SRCS = [os.path.join(SRC_DIR, f) for f in ("engram_core.cu", "attention.cu")]
+MAIN_SRCS = [os.path.join(SRC_DIR, f) for f in ("engram_core.cu", "attention.cu", "cache8.cu")]
 LIB_PATH = os.path.join(HERE, "libengram.so")
 OBJ_DIR = os.path.join(HERE, "_build")
 STEP_SRC = os.path.join(SRC_DIR, "step_binding.cpp")

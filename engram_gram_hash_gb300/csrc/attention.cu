@@ -2,107 +2,16 @@
 // entry points, argument checks, tensor maps, launches.  A translation unit of
 // its own: it shares no device code with the Engram read but the helpers of
 // common.cuh, and the two compile side by side.
-#include <algorithm>
-#include <cmath>
-#include <cstring>
-#include <initializer_list>
 #include <type_traits>
 
-#include "common.cuh"
-#include "host.cuh"
-
-#include "attn_common.cuh"
+#include "attn_host.cuh"
 #include "attn_rows.cuh"
 #include "attn_tile.cuh"
-#include "qk_rope.cuh"
 
 namespace engram {
 namespace attn {
 
 cudaError_t take_error(unsigned int *w) { return take_error_word(w); }
-
-static bool finite_pos(float x) { return x > 0.f && x < INFINITY; }
-
-static engram_status check_attn_config(const engram_attn_config *c) {
-    if (!c) return ENGRAM_EINVAL;
-    if (c->n_kv_heads < 1 || c->n_heads < 1 || c->n_heads % c->n_kv_heads) return ENGRAM_EINVAL;
-    if (c->n_heads / c->n_kv_heads > 128 || c->n_heads > 65536) return ENGRAM_EINVAL;
-    if (c->head_dim < 8 || c->head_dim > 128 || c->head_dim % 8) return ENGRAM_EINVAL;
-    if (c->rope_dim < 0 || c->rope_dim > c->head_dim || c->rope_dim % 16) return ENGRAM_EINVAL;
-    if (c->rope_layout > ENGRAM_ROPE_INTERLEAVED || c->dtype > ENGRAM_FP16) return ENGRAM_EINVAL;
-    if (!(c->norm_eps >= 0.f) || !finite_pos(c->scale) || c->window < 0) return ENGRAM_EINVAL;
-    return ENGRAM_OK;
-}
-
-static bool view_ok(const engram_heads *h) {
-    return h && h->data && aligned(h->data, 16) && h->token_stride % 8 == 0 && h->head_stride % 8 == 0;
-}
-static HeadView view(const engram_heads *h) {
-    return h ? HeadView{static_cast<uint16_t *>(h->data), h->token_stride, h->head_stride} : HeadView{nullptr, 0, 0};
-}
-
-static engram_status check_cache(const engram_attn_config *cfg, const engram_kv_cache *c) {
-    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ENGRAM_EINVAL;
-    if (c->n_pages < 1 || c->n_pages > INT32_MAX) return ENGRAM_EINVAL;
-    if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16) return ENGRAM_EINVAL;
-    // strides positive (a size of one may still name any), so no value lies before the base
-    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
-        if (s < 8 || s % 8 || s >= (INT64_C(1) << 39)) return ENGRAM_EINVAL;
-    if (c->token_stride < cfg->head_dim || c->page_stride < cfg->head_dim) return ENGRAM_EINVAL;
-    if (cfg->n_kv_heads > 1 && c->head_stride < cfg->head_dim) return ENGRAM_EINVAL;
-    return ENGRAM_OK;
-}
-
-static engram_status check_batch(const engram_kv_batch *b) {
-    if (!b || b->n_query < 0 || b->n_seqs < 0) return ENGRAM_EINVAL;
-    if (b->n_query > INT32_MAX || b->n_seqs > INT32_MAX || b->table_stride < 0) return ENGRAM_EINVAL;
-    if (b->n_query == 0) return ENGRAM_OK;
-    if (b->n_seqs < 1 || b->table_stride < 1 || b->table_stride > INT32_MAX) return ENGRAM_EINVAL;
-    if (b->table_width < 0 || b->table_width > b->table_stride) return ENGRAM_EINVAL;
-    if (!b->seq_offsets || !b->kv_len || !b->block_table) return ENGRAM_EINVAL;
-    if (!aligned(b->seq_offsets, 8) || !aligned(b->kv_len, 4) || !aligned(b->block_table, 4)) return ENGRAM_EINVAL;
-    return ENGRAM_OK;
-}
-
-// Entries of a sequence's row of the block table.
-static int64_t table_width(const engram_kv_batch *b) { return b->table_width > 0 ? b->table_width : b->table_stride; }
-
-static Batch device_batch(const engram_kv_batch *b, const engram_kv_cache *c) {
-    Batch d;
-    d.offs = b->seq_offsets;
-    d.kv_len = b->kv_len;
-    d.block_table = b->block_table;
-    d.table_stride = b->table_stride;
-    d.table_width = table_width(b);
-    d.n_seqs = b->n_seqs;
-    d.n_query = b->n_query;
-    d.n_pages = c->n_pages;
-    d.page_size = c->page_size;
-    return d;
-}
-
-// An ordinary launch that may start while the kernel before it drains: every
-// kernel here waits for that kernel's completion before its first global
-// access, so this only hides launch latency.
-template <typename... P, typename... A>
-static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
-                                  const char *what, const A &...args) {
-    cudaLaunchConfig_t lc = {};
-    cudaLaunchAttribute attr[2];
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.gridDim = grid;
-    lc.blockDim = dim3(threads);
-    lc.dynamicSmemBytes = smem;
-    lc.stream = st;
-    lc.attrs = attr;
-    lc.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, kern, args...);
-    return e == cudaSuccess ? ENGRAM_OK : cuda_fail(e, what);
-}
 
 // ------------------------------------------------- norm, rotation, append ----
 
@@ -152,10 +61,6 @@ static bool page_map(CUtensorMap *m, const engram_attn_config *cfg, const engram
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }
-static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-static int padded_dim(const engram_attn_config *cfg) { return cfg->head_dim <= 64 ? 64 : 128; }
-
 static size_t rows_part_o_bytes(const engram_attn_config *cfg) {
     return up256((size_t)num_sms() * 2 * rows::ROWS * padded_dim(cfg) * sizeof(float));
 }
@@ -169,17 +74,6 @@ static int64_t rows_segs_most(const engram_attn_config *cfg, const engram_kv_bat
     const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
     return cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
                                       (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);
-}
-static int64_t keys_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    const int64_t room = table_width(batch) * cache->page_size;
-    return cfg->window > 0 ? std::min<int64_t>(room, (int64_t)cfg->window + 256) : room;
-}
-// The configuration with a window that hides nothing taken for plain causal attention (0): no position
-// reaches the block table's room or 2^31 - 1, so a window of that many tokens ends before every sequence.
-static engram_attn_config effective(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
-    engram_attn_config c = *cfg;
-    if (c.window >= std::min<int64_t>(table_width(batch) * cache->page_size, INT32_MAX)) c.window = 0;
-    return c;
 }
 static int64_t rows_tiles_most(const engram_attn_config *cfg, const engram_kv_cache *cache, const engram_kv_batch *batch) {
     return (keys_most(cfg, cache, batch) * padded_dim(cfg) + 8191) / 8192;

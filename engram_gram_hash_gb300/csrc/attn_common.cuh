@@ -213,20 +213,25 @@ __device__ __forceinline__ void add_nonfinite(const Batch &b, const ValuePages &
     }
 }
 
-// The last sequence s with offs[s] <= base + t (a whole warp looks at 32
-// offsets at a time, so up to 32 sequences take one load and 1,024 take two).
-__device__ __forceinline__ int64_t warp_find_seq(const int64_t *offs, int64_t n_seqs, int64_t p) {
+// The last i in [0, n) for which le(i) holds (it holds for 0 and, once it
+// fails, never again).  A whole warp asks 32 places at a time, so up to 32 take
+// one round of loads and 1,024 two.
+template <typename F>
+__device__ __forceinline__ int64_t warp_find(int64_t count, const F &le) {
     const int lane = threadIdx.x & 31;
-    int64_t lo = 0, n = n_seqs;  // the answer lies in [lo, lo + n)
+    int64_t lo = 0, n = count;  // the answer lies in [lo, lo + n)
     while (n > 1) {
         const int64_t step = (n + 31) / 32;
-        const int64_t at = lo + lane * step;
-        const bool le = lane == 0 || (lane * step < n && __ldg(offs + at) <= p);
-        const int k = 31 - __clz(__ballot_sync(0xffffffffu, le));  // offsets ascend: the last lane that holds
+        const bool holds = lane == 0 || (lane * step < n && le(lo + lane * step));
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, holds));  // the last lane that holds
         lo += k * step;
         n = n - k * step < step ? n - k * step : step;
     }
     return lo;
+}
+// The last sequence s with offs[s] <= p.
+__device__ __forceinline__ int64_t warp_find_seq(const int64_t *offs, int64_t n_seqs, int64_t p) {
+    return warp_find(n_seqs, [&](int64_t s) { return __ldg(offs + s) <= p; });
 }
 
 }  // namespace attn

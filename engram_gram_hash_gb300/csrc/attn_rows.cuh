@@ -300,8 +300,8 @@ __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;
 // (m, l) in base 2 -> ln sum; -inf where nothing was seen
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
 // A row's maximum and sum over the eight warps, in warp order.
-template <int DP>
-__device__ __forceinline__ void row_total(const Shared<DP> *sh, int r, float &m, float &l) {
+template <typename S>
+__device__ __forceinline__ void row_total(const S *sh, int r, float &m, float &l) {
     m = sh->m[0][r];
 #pragma unroll
     for (int w = 1; w < CONSUMERS; ++w) m = fmaxf(m, sh->m[w][r]);

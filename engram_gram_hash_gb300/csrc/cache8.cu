@@ -1,0 +1,300 @@
+// The serving step over the 8-bit cache (block tables from request lengths, the
+// quantising append, attention over codes): C entry points, argument checks,
+// tensor maps, launches.  A translation unit of its own beside the 16-bit
+// step's, whose plans and joins it instantiates again.
+#include "attn_host.cuh"
+#include "attn_rows.cuh"
+
+#include "append8.cuh"
+#include "attn8_common.cuh"
+#include "attn_rows8.cuh"
+#include "kv_plan.cuh"
+
+namespace engram {
+namespace attn {
+
+cudaError_t take_error8(unsigned int *w) { return take_error_word(w); }
+
+// What both calls over the 8-bit cache ask of the configuration and the cache.
+static engram_status check_cache8(const engram_attn_config *cfg, const engram_kv_cache_q8 *c) {
+    if (cfg->head_dim % 16) return ENGRAM_EINVAL;
+    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ENGRAM_EINVAL;
+    if (!c->k_scales || !c->v_scales || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4)) return ENGRAM_EINVAL;
+    if (c->n_pages < 1 || c->n_pages > INT32_MAX) return ENGRAM_EINVAL;
+    if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16) return ENGRAM_EINVAL;
+    const int32_t b = c->block_tokens;
+    if ((b != 16 && b != 32 && b != 64 && b != 128) || c->page_size % b) return ENGRAM_EINVAL;
+    // strides positive (a size of one may still name any), so no value lies before the base
+    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
+        if (s < 16 || s % 16 || s >= (INT64_C(1) << 40)) return ENGRAM_EINVAL;
+    if (c->token_stride < cfg->head_dim || c->page_stride < cfg->head_dim) return ENGRAM_EINVAL;
+    if (cfg->n_kv_heads > 1 && c->head_stride < cfg->head_dim) return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+// --------------------------------------------------------------------- plan --
+
+static engram_status check_plan(const engram_kv_plan_args *a) {
+    if (!a || a->n_seqs < 0 || a->n_seqs > INT32_MAX || a->max_tokens < 0 || a->max_tokens > INT32_MAX) return ENGRAM_EINVAL;
+    if (a->n_pages < 1 || a->n_pages > INT32_MAX) return ENGRAM_EINVAL;
+    if (a->page_size < 16 || a->page_size > 65536 || a->page_size % 16) return ENGRAM_EINVAL;
+    if (!a->seq_offsets || !aligned(a->seq_offsets, 8) || !a->counts || !aligned(a->counts, 4)) return ENGRAM_EINVAL;
+    if (!a->free_pages || !aligned(a->free_pages, 4) || !a->n_free || !aligned(a->n_free, 4) || !a->n_free_out ||
+        !aligned(a->n_free_out, 4))
+        return ENGRAM_EINVAL;
+    if (!aligned(a->positions, 4) || !aligned(a->slots, 8)) return ENGRAM_EINVAL;
+    if (a->n_seqs == 0) return ENGRAM_OK;
+    if (a->table_stride < 1 || a->table_stride > INT32_MAX || a->table_width < 0 || a->table_width > a->table_stride)
+        return ENGRAM_EINVAL;
+    if (!a->new_len || !aligned(a->new_len, 4) || !aligned(a->keep_len, 4) || !a->kv_len || !aligned(a->kv_len, 4) ||
+        !a->kv_len_out || !aligned(a->kv_len_out, 4) || !a->block_table || !aligned(a->block_table, 4))
+        return ENGRAM_EINVAL;
+    return ENGRAM_OK;
+}
+
+// ------------------------------------------------------------------- append --
+
+template <typename E, int LPH>
+static engram_status append8_launch(const engram_attn_config *cfg, const Append8 &a, cudaStream_t st) {
+    constexpr int per = 32 / LPH;
+    const int warps = a.block / TOKENS_PER_WARP;
+    const int64_t q_blocks = a.h.n_q ? (a.h.n_tokens + warps - 1) / warps : 0;
+    const dim3 grid((unsigned)std::max(a.units, q_blocks), 2 * ((a.n_kv + per - 1) / per) + (a.h.n_q + per - 1) / per);
+    if (grid.y > 65535) return ENGRAM_EINVAL;
+    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
+        return launch_after(append8_kernel<E, LPH, true>, grid, warps * 32, 0, 1, st, "append8_kernel", a);
+    return launch_after(append8_kernel<E, LPH, false>, grid, warps * 32, 0, 1, st, "append8_kernel", a);
+}
+
+// ---------------------------------------------------------------- attention --
+
+// A [page][head][token][D] view of K or V codes for TMA: boxes of the padded head (rows of 128 bytes, or 64) x
+// `rows` tokens, swizzled over the row; codes past head_dim read as zeros.
+static bool page_map8(CUtensorMap *m, const engram_attn_config *cfg, const engram_kv_cache_q8 *c, void *base, int rows) {
+    auto enc = tensormap_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)cfg->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)cfg->n_kv_heads,
+                          (cuuint64_t)c->n_pages};
+    cuuint64_t strides[3] = {(cuuint64_t)c->token_stride, (cuuint64_t)c->head_stride, (cuuint64_t)c->page_stride};
+    cuuint32_t box[4] = {(cuuint32_t)padded_dim(cfg), (cuuint32_t)rows, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               padded_dim(cfg) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static Scales scales_of(const engram_kv_cache_q8 *c) {
+    int log2 = 4;
+    while ((1 << log2) < c->block_tokens) ++log2;
+    return Scales{c->k_scales, c->v_scales, c->page_size / c->block_tokens, log2};
+}
+
+static size_t rows8_part_o_bytes(const engram_attn_config *cfg) {
+    return up256((size_t)num_sms() * 2 * rows::ROWS * padded_dim(cfg) * sizeof(float));
+}
+static size_t rows8_workspace_bytes(const engram_attn_config *cfg) {
+    return rows8_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
+}
+
+// Segments of the rows kernel (row tile x kv head) at most, and the tiles of 128 keys that the block table has
+// room for (in a window's reach).
+static int64_t rows8_segs_most(const engram_attn_config *cfg, const engram_kv_batch *batch) {
+    const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
+    return cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
+                                      (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);
+}
+static int64_t rows8_tiles_most(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    return (keys_most(cfg, cache, batch) + rows::KT8 - 1) / rows::KT8;
+}
+
+// How a segment's tiles are shared out, as for the 16-bit cache: clusters of CTAs for few segments and short
+// tables, whole segments where a cut cannot pay, else equal runs of tiles for every SM and the join.
+struct Rows8Shares {
+    int32_t cluster, whole, runs;
+    bool cut() const { return whole == 0 && runs > 1; }
+};
+static Rows8Shares rows8_shares(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    const int64_t tiles = rows8_tiles_most(cfg, cache, batch), segs = rows8_segs_most(cfg, batch);
+    const int sms = num_sms();
+    Rows8Shares p = {1, 0, sms};
+    if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
+        p.cluster = 8;
+    } else if (tiles > 2 && tiles <= (segs >= 24 ? 64 : 32) && segs * 4 <= sms - 8) {
+        p.cluster = 4;
+    } else if (tiles <= 8 || (tiles <= 32 && segs * 2 >= sms && segs <= sms)) {
+        p.whole = (int32_t)tiles;
+    }
+    if (p.cluster > 1) {
+        p.whole = 1;
+        p.runs = (int32_t)segs;
+    }
+    return p;
+}
+
+template <typename E, int DP>
+static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                  const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                  float *lse, void *workspace, cudaStream_t st) {
+    rows::Params8 a;
+    memset(&a, 0, sizeof(a));
+    rows::Params &p = a.r;
+    p.b = device_batch(batch, cache);
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.q_token_stride = q->token_stride;
+    p.q_head_stride = q->head_stride;
+    p.out = static_cast<uint16_t *>(out->data);
+    p.out_token_stride = out->token_stride;
+    p.out_head_stride = out->head_stride;
+    p.lse = lse;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + rows8_part_o_bytes(cfg));
+    p.n_heads = cfg->n_heads;
+    p.n_kv_heads = cfg->n_kv_heads;
+    p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.by_group = Divisor(p.group);
+    p.by_heads = Divisor(cfg->n_kv_heads);
+    p.head_dim = cfg->head_dim;
+    p.window = cfg->window;
+    p.kt_log2 = rows::Cfg8<DP>::KT_LOG2;
+    p.box = gcd(cache->page_size, rows::KT8);
+    const Rows8Shares shares = rows8_shares(cfg, cache, batch);
+    p.cluster = shares.cluster;
+    p.whole = shares.whole;
+    p.runs = shares.runs;
+    p.scale_log2 = cfg->scale * 1.4426950408889634f;
+    a.scales = scales_of(cache);
+    a.codes = CodePages{static_cast<const uint8_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
+    CUtensorMap km, vm;
+    if (!page_map8(&km, cfg, cache, cache->k, p.box) || !page_map8(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
+    constexpr int smem = rows::smem8_bytes<DP>();
+    static std::atomic<bool> attr_done[64];
+    const auto kern = rows::rows8_kernel<E, DP>;
+    engram_status s = ensure_smem((const void *)kern, smem, attr_done);
+    if (s != ENGRAM_OK) return s;
+    s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows8_kernel", km, vm, a);
+    if (s != ENGRAM_OK || !shares.cut()) return s;
+    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
+}
+
+static size_t workspace_bytes8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    return rows8_shares(cfg, cache, batch).cut() ? rows8_workspace_bytes(cfg) : 0;
+}
+
+}  // namespace attn
+}  // namespace engram
+
+using namespace engram;
+
+extern "C" engram_status engram_kv_plan(const engram_kv_plan_args *a, void *stream) {
+    using namespace engram::attn;
+    if (check_plan(a) != ENGRAM_OK) return ENGRAM_EINVAL;
+    plan::Params p;
+    memset(&p, 0, sizeof(p));
+    p.new_len = a->new_len;
+    p.keep_len = a->keep_len;
+    p.kv_len = a->kv_len;
+    p.kv_len_out = a->kv_len_out;
+    p.table = a->block_table;
+    p.table_stride = a->table_stride;
+    p.table_width = a->table_width > 0 ? a->table_width : a->table_stride;
+    p.free_pages = a->free_pages;
+    p.n_free = a->n_free;
+    p.n_free_out = a->n_free_out;
+    p.offs = a->seq_offsets;
+    p.positions = a->positions;
+    p.slots = a->slots;
+    p.counts = a->counts;
+    p.n_seqs = a->n_seqs;
+    p.max_tokens = a->max_tokens;
+    p.n_pages = a->n_pages;
+    p.page_size = a->page_size;
+    p.by_page = Divisor(a->page_size);
+    p.maps = a->max_tokens <= 4096;
+    cudaStream_t st = (cudaStream_t)stream;
+    const engram_status s = launch_after(plan::plan_kernel, dim3(1), plan::NT, 0, 1, st, "plan_kernel", p);
+    if (s != ENGRAM_OK || p.maps || (!p.positions && !p.slots)) return s;
+    const int64_t warps = p.max_tokens / plan::SPAN + p.n_seqs + 1;
+    return launch_after(plan::map_kernel, dim3((unsigned)((warps + 7) / 8)), 256, 0, 1, st, "map_kernel", p);
+}
+
+extern "C" engram_status engram_kv_append_q8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                             const engram_kv_batch *batch, const engram_heads *k, const engram_heads *v,
+                                             const void *w_k, const float *table, int64_t table_rows,
+                                             const engram_heads *q, const void *w_q, const engram_heads *q_out,
+                                             void *stream) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK) return ENGRAM_EINVAL;
+    if (batch->n_query == 0) return ENGRAM_OK;
+    if (check_cache8(cfg, cache) != ENGRAM_OK || !view_ok(k) || !view_ok(v)) return ENGRAM_EINVAL;
+    if (q && (!view_ok(q) || !view_ok(q_out))) return ENGRAM_EINVAL;
+    if (!aligned(w_q, 16) || !aligned(w_k, 16) || table_rows < 0) return ENGRAM_EINVAL;
+    if (cfg->rope_dim > 0 && (!table || !aligned(table, 16))) return ENGRAM_EINVAL;
+    Append8 a;
+    memset(&a, 0, sizeof(a));
+    HeadParams &p = a.h;
+    p.q = view(q);
+    p.k = view(k);
+    p.v = view(v);
+    p.q_out = view(q ? q_out : nullptr);
+    p.n_q = q ? cfg->n_heads : 0;  // keys and values go their own way
+    p.w_q = static_cast<const uint16_t *>(w_q);
+    p.w_k = static_cast<const uint16_t *>(w_k);
+    p.table = table;
+    p.table_rows = table_rows;
+    p.n_tokens = batch->n_query;
+    p.head_dim = cfg->head_dim;
+    p.rope_dim = cfg->rope_dim;
+    p.eps = cfg->norm_eps;
+    p.inv_dim = 1.f / (float)cfg->head_dim;
+    p.batch = device_batch(batch, cache);
+    p.by_page = Divisor(cache->page_size);
+    a.k_pages = static_cast<uint8_t *>(cache->k);
+    a.v_pages = static_cast<uint8_t *>(cache->v);
+    a.k_scales = cache->k_scales;
+    a.v_scales = cache->v_scales;
+    a.page_stride = cache->page_stride;
+    a.slot_stride = cache->token_stride;
+    a.head_stride = cache->head_stride;
+    a.n_kv = cfg->n_kv_heads;
+    a.block = cache->block_tokens;
+    a.per_page = cache->page_size / cache->block_tokens;
+    // sequence s has the units from row0 / block + 2 s on
+    a.units = batch->n_query / a.block + 2 * batch->n_seqs;
+    if (a.units > INT32_MAX) return ENGRAM_EINVAL;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (cfg->head_dim <= 64)
+        return cfg->dtype == ENGRAM_BF16 ? append8_launch<Bf16, 4>(cfg, a, st) : append8_launch<Fp16, 4>(cfg, a, st);
+    return cfg->dtype == ENGRAM_BF16 ? append8_launch<Bf16, 8>(cfg, a, st) : append8_launch<Fp16, 8>(cfg, a, st);
+}
+
+extern "C" size_t engram_paged_attention_q8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                                            const engram_kv_batch *batch) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK || batch->n_query == 0) return 0;
+    if (check_cache8(cfg, cache) != ENGRAM_OK) return 0;
+    const engram_attn_config eff = effective(cfg, cache, batch);
+    return workspace_bytes8(&eff, cache, batch);
+}
+
+extern "C" engram_status engram_paged_attention_q8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                                   const engram_kv_batch *batch, const engram_heads *q,
+                                                   const engram_heads *out, float *lse, void *workspace,
+                                                   size_t workspace_bytes, void *stream) {
+    using namespace engram::attn;
+    if (check_attn_config(cfg) != ENGRAM_OK || check_batch(batch) != ENGRAM_OK) return ENGRAM_EINVAL;
+    if (batch->n_query == 0) return ENGRAM_OK;
+    if (check_cache8(cfg, cache) != ENGRAM_OK || !view_ok(q) || !view_ok(out) || !aligned(lse, 4)) return ENGRAM_EINVAL;
+    if (batch->n_query > INT32_MAX / cfg->n_heads) return ENGRAM_EINVAL;
+    const engram_attn_config eff = effective(cfg, cache, batch);
+    cfg = &eff;
+    const size_t need = workspace_bytes8(cfg, cache, batch);
+    if (need > 0 && (!workspace || !aligned(workspace, 256))) return ENGRAM_EINVAL;
+    if (workspace_bytes < need) return ENGRAM_ENOMEM;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool bf16 = cfg->dtype == ENGRAM_BF16;
+    if (padded_dim(cfg) == 64)
+        return bf16 ? rows8_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
+                    : rows8_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);
+    return bf16 ? rows8_launch<Bf16, 128>(cfg, cache, batch, q, out, lse, workspace, st)
+                : rows8_launch<Fp16, 128>(cfg, cache, batch, q, out, lse, workspace, st);
+}

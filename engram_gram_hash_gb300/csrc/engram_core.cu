@@ -1499,9 +1499,11 @@ extern "C" const char *engram_status_string(engram_status st) {
 
 extern "C" engram_status engram_last_error(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return ENGRAM_ECUDA;
-    unsigned int w = 0, attention = 0;
-    if (take_error_word(&w) != cudaSuccess || attn::take_error(&attention) != cudaSuccess) return ENGRAM_ECUDA;
-    w |= attention;
+    unsigned int w = 0, attention = 0, cache8 = 0;
+    if (take_error_word(&w) != cudaSuccess || attn::take_error(&attention) != cudaSuccess ||
+        attn::take_error8(&cache8) != cudaSuccess)
+        return ENGRAM_ECUDA;
+    w |= attention | cache8;
     for (int k = 1; k < 32; ++k)
         if (w & (1u << k)) return (engram_status)k;
     return ENGRAM_OK;

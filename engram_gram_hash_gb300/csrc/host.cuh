@@ -1,4 +1,4 @@
-// Host helpers shared by the library's two translation units: device
+// Host helpers shared by the library's translation units: device
 // properties, error reporting, launch set-up, the tensor-map encoder.
 #pragma once
 
@@ -79,7 +79,8 @@ static inline cudaError_t take_error_word(unsigned int *w) {
 }
 
 namespace attn {
-cudaError_t take_error(unsigned int *w);  // the attention kernels' error word
+cudaError_t take_error(unsigned int *w);   // the attention kernels' error word
+cudaError_t take_error8(unsigned int *w);  // the 8-bit cache's
 }
 
 }  // namespace engram

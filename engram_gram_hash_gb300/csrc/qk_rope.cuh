@@ -90,20 +90,112 @@ __device__ __forceinline__ void from_pairs(const float2 (&f)[4], const float2 (&
     p1 = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
+// A lane's two 8-value pieces of a head, and which of them turn.
+struct HeadLane {
+    int c0, c1;
+    bool rot0, rot1, has0, has1;
+};
+template <int LPH, bool INTERLEAVED>
+__device__ __forceinline__ HeadLane head_lane(const HeadParams &p, int l) {
+    const int n_pieces = p.head_dim >> 3, rot_pieces = p.rope_dim >> 3;
+    HeadLane k;
+    if (INTERLEAVED) {
+        k.c0 = l;
+        k.c1 = l + LPH;
+        k.rot0 = k.c0 < rot_pieces;
+        k.rot1 = k.c1 < rot_pieces;
+    } else {
+        const int half = rot_pieces >> 1;
+        k.rot0 = k.rot1 = l < half;
+        k.c0 = k.rot0 ? l : rot_pieces + 2 * (l - half);
+        k.c1 = k.rot0 ? l + half : k.c0 + 1;
+    }
+    k.has0 = k.c0 < n_pieces;
+    k.has1 = k.c1 < n_pieces;
+    return k;
+}
+
+// The lane's 8 pairs (f, s) turn as f' = f A + s B, s' = s C + f D with the weights in the factors,
+// A = w_f cos, B = -w_s sin, C = w_s cos, D = w_f sin, made once for all its heads of a token.
+struct Turn {
+    float2 A[4], B[4], C[4], D[4];
+};
+// A and C to start from: the weights (1 without).
+template <typename E, bool INTERLEAVED>
+__device__ __forceinline__ void turn_weights(const HeadLane &k, const uint16_t *w, Turn &t) {
+    if (w)
+        to_pairs<E, INTERLEAVED>(k.has0 ? __ldg(reinterpret_cast<const uint4 *>(w + k.c0 * 8)) : make_uint4(0, 0, 0, 0),
+                                 k.has1 ? __ldg(reinterpret_cast<const uint4 *>(w + k.c1 * 8)) : make_uint4(0, 0, 0, 0), t.A, t.C);
+    else
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t.A[i] = t.C[i] = make_float2(1.f, 1.f);
+}
+template <bool INTERLEAVED>
+__device__ __forceinline__ void turn_angles(const HeadParams &p, const HeadLane &k, int64_t pos, Turn &t) {
+    const float *row = p.table + pos * p.rope_dim;
+    const int hr = p.rope_dim >> 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // pairs 4i .. 4i + 3
+        t.B[2 * i] = t.B[2 * i + 1] = t.D[2 * i] = t.D[2 * i + 1] = make_float2(0.f, 0.f);
+        if (i ? k.rot1 : k.rot0) {
+            const int at = INTERLEAVED ? (i ? k.c1 : k.c0) * 4 : k.c0 * 8 + i * 4;
+            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + at));
+            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + hr + at));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int q = 2 * i + j;
+                const float2 cs = j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
+                const float2 sn = j ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
+                t.B[q] = mul2(t.C[q], make_float2(-sn.x, -sn.y));
+                t.D[q] = mul2(t.A[q], sn);
+                t.A[q] = mul2(t.A[q], cs);
+                t.C[q] = mul2(t.C[q], cs);
+            }
+        }
+    }
+}
+// The lane's pieces of one head: normed (norm, over the LPH lanes of the head; the whole warp calls) and turned.
+template <typename E, int LPH, bool INTERLEAVED>
+__device__ __forceinline__ void turn_head(const HeadParams &p, const HeadLane &k, const Turn &t, bool norm, uint4 x0, uint4 x1,
+                                          float2 (&f)[4], float2 (&s)[4]) {
+    to_pairs<E, INTERLEAVED>(x0, x1, f, s);
+    float rinv = 1.f;
+    if (norm) {
+        float2 ss = mul2(f[0], f[0]);
+#pragma unroll
+        for (int i = 1; i < 4; ++i) ss = fma2(f[i], f[i], ss);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = fma2(s[i], s[i], ss);
+        float sum = ss.x + ss.y;
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        rinv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
+    }
+    const float2 r2 = make_float2(rinv, rinv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 a = mul2(f[i], t.A[i]), b = mul2(s[i], t.C[i]);
+        if (i < 2 ? k.rot0 : k.rot1) {  // values that do not turn never meet their neighbours'
+            a = fma2(s[i], t.B[i], a);
+            b = fma2(f[i], t.D[i], b);
+        }
+        f[i] = mul2(a, r2);
+        s[i] = mul2(b, r2);
+    }
+}
+
 // LPH lanes per head (4 up to 64 values, 8 up to 128), U heads per lane: a
-// warp takes up to U * 32 / LPH heads of one token, either queries or, in one
-// row, keys and values (the values are only copied).
+// warp takes up to U * 32 / LPH heads of token t, either queries or, in one
+// row, keys and values (the values are only copied).  `block` counts the
+// warps' shares of a token's heads, the queries' first.
 template <typename E, int LPH, int U, bool INTERLEAVED, bool APPEND>
-__global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ HeadParams p) {
+__device__ __forceinline__ void head_rows(const HeadParams &p, int64_t t, int block) {
     constexpr int GPW = 32 / LPH, PER = GPW * U;
-    grid_dependency_wait();
-    allow_dependent_launch();
     const int lane = threadIdx.x & 31;
     const int l = lane % LPH, grp = lane / LPH;
-    const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     if (t >= p.n_tokens) return;
+    const bool first = t == 0 && block == 0;
     // the warp's kind and its first head
-    int block = blockIdx.y;
     const int q_blocks = (p.n_q + PER - 1) / PER;
     const bool is_q = block < q_blocks;
     if (!is_q) block -= q_blocks;
@@ -111,22 +203,7 @@ __global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ He
     const HeadView in = is_q ? p.q : p.k;
     const int h0 = block * PER + grp;
     const bool turns = block * PER < n_rot;  // any of the warp's heads
-    const int n_pieces = p.head_dim >> 3, rot_pieces = p.rope_dim >> 3;
-
-    int c0, c1;
-    bool rot0, rot1;
-    if (INTERLEAVED) {
-        c0 = l;
-        c1 = l + LPH;
-        rot0 = c0 < rot_pieces;
-        rot1 = c1 < rot_pieces;
-    } else {
-        const int half = rot_pieces >> 1;
-        rot0 = rot1 = l < half;
-        c0 = rot0 ? l : rot_pieces + 2 * (l - half);
-        c1 = rot0 ? l + half : c0 + 1;
-    }
-    const bool has0 = c0 < n_pieces, has1 = c1 < n_pieces;
+    const HeadLane k = head_lane<LPH, INTERLEAVED>(p, l);
 
     // all of this lane's heads: loads first, the position's chain behind them
     uint4 x0[U], x1[U];
@@ -136,15 +213,15 @@ __global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ He
     for (int u = 0; u < U; ++u) {
         const int h = h0 + u * GPW;
         const uint16_t *a = APPEND && h >= n_rot ? src_v + (int64_t)(h - n_rot) * p.v.head_stride : src + (int64_t)h * in.head_stride;
-        x0[u] = h < n_heads && has0 ? *reinterpret_cast<const uint4 *>(a + c0 * 8) : make_uint4(0, 0, 0, 0);
-        x1[u] = h < n_heads && has1 ? *reinterpret_cast<const uint4 *>(a + c1 * 8) : make_uint4(0, 0, 0, 0);
+        x0[u] = h < n_heads && k.has0 ? *reinterpret_cast<const uint4 *>(a + k.c0 * 8) : make_uint4(0, 0, 0, 0);
+        x1[u] = h < n_heads && k.has1 ? *reinterpret_cast<const uint4 *>(a + k.c1 * 8) : make_uint4(0, 0, 0, 0);
     }
 
     int64_t pos = 0;
     int64_t slot = 0;  // element offset of the token's slot in the pages
     if (APPEND) {
         const int64_t base = __ldg(p.batch.offs);
-        if (t == 0 && blockIdx.y == 0 && lane == 0 && __ldg(p.batch.offs + p.batch.n_seqs) - base != p.n_tokens)
+        if (first && lane == 0 && __ldg(p.batch.offs + p.batch.n_seqs) - base != p.n_tokens)
             raise_error(ENGRAM_ERANGE);
         const int64_t s = warp_find_seq(p.batch.offs, p.batch.n_seqs, base + t);
         const int64_t after = __ldg(p.batch.offs + s + 1) - (base + t);  // new tokens from this one on
@@ -168,64 +245,14 @@ __global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ He
     }
 
     if (turns) {
-        // The lane's 8 pairs (f, s) turn as f' = f A + s B, s' = s C + f D with the weights in the
-        // factors, A = w_f cos, B = -w_s sin, C = w_s cos, D = w_f sin, made once for all its heads.
-        float2 A[4], B[4], C[4], D[4];
         const uint16_t *w = is_q ? p.w_q : p.w_k;
-        if (w)
-            to_pairs<E, INTERLEAVED>(has0 ? __ldg(reinterpret_cast<const uint4 *>(w + c0 * 8)) : make_uint4(0, 0, 0, 0),
-                                     has1 ? __ldg(reinterpret_cast<const uint4 *>(w + c1 * 8)) : make_uint4(0, 0, 0, 0), A, C);
-        else
-#pragma unroll
-            for (int i = 0; i < 4; ++i) A[i] = C[i] = make_float2(1.f, 1.f);
-        const float *row = p.table + pos * p.rope_dim;
-        const int hr = p.rope_dim >> 1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {  // pairs 4i .. 4i + 3
-            B[2 * i] = B[2 * i + 1] = D[2 * i] = D[2 * i + 1] = make_float2(0.f, 0.f);
-            if (i ? rot1 : rot0) {
-                const int at = INTERLEAVED ? (i ? c1 : c0) * 4 : c0 * 8 + i * 4;
-                const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + at));
-                const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + hr + at));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int k = 2 * i + j;
-                    const float2 cs = j ? make_float2(c4.z, c4.w) : make_float2(c4.x, c4.y);
-                    const float2 sn = j ? make_float2(s4.z, s4.w) : make_float2(s4.x, s4.y);
-                    B[k] = mul2(C[k], make_float2(-sn.x, -sn.y));
-                    D[k] = mul2(A[k], sn);
-                    A[k] = mul2(A[k], cs);
-                    C[k] = mul2(C[k], cs);
-                }
-            }
-        }
+        Turn turn;
+        turn_weights<E, INTERLEAVED>(k, w, turn);
+        turn_angles<INTERLEAVED>(p, k, pos, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float2 f[4], s[4];
-            to_pairs<E, INTERLEAVED>(x0[u], x1[u], f, s);
-            float rinv = 1.f;
-            if (w) {
-                float2 ss = mul2(f[0], f[0]);
-#pragma unroll
-                for (int i = 1; i < 4; ++i) ss = fma2(f[i], f[i], ss);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) ss = fma2(s[i], s[i], ss);
-                float sum = ss.x + ss.y;
-#pragma unroll
-                for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                rinv = rsqrtf(fmaf(sum, p.inv_dim, p.eps));
-            }
-            const float2 r2 = make_float2(rinv, rinv);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float2 a = mul2(f[i], A[i]), b = mul2(s[i], C[i]);
-                if (i < 2 ? rot0 : rot1) {  // values that do not turn never meet their neighbours'
-                    a = fma2(s[i], B[i], a);
-                    b = fma2(f[i], D[i], b);
-                }
-                f[i] = mul2(a, r2);
-                s[i] = mul2(b, r2);
-            }
+            turn_head<E, LPH, INTERLEAVED>(p, k, turn, w != nullptr, x0[u], x1[u], f, s);
             if (!APPEND || h0 + u * GPW < n_rot) from_pairs<E, INTERLEAVED>(f, s, x0[u], x1[u]);
         }
     }
@@ -240,9 +267,16 @@ __global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ He
             a = p.k_out.data + t * p.k_out.token_stride + (int64_t)h * p.k_out.head_stride;
         else
             a = (h < n_rot ? p.k_pages + (int64_t)h * p.page_head_stride : p.v_pages + (int64_t)(h - n_rot) * p.page_head_stride) + slot;
-        if (has0) *reinterpret_cast<uint4 *>(a + c0 * 8) = x0[u];
-        if (has1) *reinterpret_cast<uint4 *>(a + c1 * 8) = x1[u];
+        if (k.has0) *reinterpret_cast<uint4 *>(a + k.c0 * 8) = x0[u];
+        if (k.has1) *reinterpret_cast<uint4 *>(a + k.c1 * 8) = x1[u];
     }
+}
+
+template <typename E, int LPH, int U, bool INTERLEAVED, bool APPEND>
+__global__ void __launch_bounds__(256, 4) head_kernel(const __grid_constant__ HeadParams p) {
+    grid_dependency_wait();
+    allow_dependent_launch();
+    head_rows<E, LPH, U, INTERLEAVED, APPEND>(p, (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), blockIdx.y);
 }
 
 }  // namespace attn

@@ -1,5 +1,5 @@
-// The Python binding's marshalling for the calls of a decode step (head norm +
-// rotation, cache append, paged attention): tensors to the plain structures of
+// The Python binding's marshalling for the calls of a decode step (block
+// tables, head norm + rotation, cache append, paged attention): tensors to the plain structures of
 // engram.h and back.  These calls run several times per layer and token on
 // kernels of a few microseconds, so what a call costs the host decides how fast
 // small steps go; reading the tensors here costs about a tenth of what it does
@@ -24,6 +24,10 @@ decltype(&engram_qk_norm_rope) fn_qk = nullptr;
 decltype(&engram_kv_append) fn_append = nullptr;
 decltype(&engram_paged_attention) fn_attend = nullptr;
 decltype(&engram_paged_attention_workspace_bytes) fn_bytes = nullptr;
+decltype(&engram_kv_plan) fn_plan = nullptr;
+decltype(&engram_kv_append_q8) fn_append8 = nullptr;
+decltype(&engram_paged_attention_q8) fn_attend8 = nullptr;
+decltype(&engram_paged_attention_q8_workspace_bytes) fn_bytes8 = nullptr;
 PyObject *error_class = nullptr;  // EngramError(status, where)
 
 // Thrown with the Python error set.
@@ -236,10 +240,11 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // (cfg, cache, batch, k, v, table, w_k, q, w_q, q_out, stream, the cache's device) -> q_out or None
-PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+template <typename Cache, typename F>
+PyObject *append_into(const char *name, const F &fn, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 12, [&]() -> PyObject * {
         const auto *c = structure<engram_attn_config>(a[0], "cfg");
-        const auto *cache = structure<engram_kv_cache>(a[1], "cache");
+        const auto *cache = structure<Cache>(a[1], "cache");
         const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *k = tensor(a[3], "k"), *v = tensor(a[4], "v"), *q = tensor(a[7], "q");
         if (!k || !v) fail(PyExc_ValueError, "k and v are needed");
@@ -257,17 +262,18 @@ PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         int64_t rows;
         const float *tab = table(a[5], c, dev, rows);
         const void *wk = weight(a[6], c, dev, "w_k"), *wq = weight(a[8], c, dev, "w_q");
-        check(fn_append(c, cache, batch, &hk, &hv, wk, tab, rows, q ? &hq : nullptr, wq, q ? &ho : nullptr, where.stream.stream()),
-              "engram_kv_append");
+        check(fn(c, cache, batch, &hk, &hv, wk, tab, rows, q ? &hq : nullptr, wq, q ? &ho : nullptr, where.stream.stream()),
+              name);
         return q ? give(a[9], made) : Py_NewRef(Py_None);
     });
 }
 
 // (cfg, cache, batch, q, out, lse, workspace, stream, the cache's device) -> out
-PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+template <typename Cache, typename F, typename B>
+PyObject *attention_over(const char *name, const F &fn, const B &fn_size, PyObject *const *a, Py_ssize_t n) {
     return guarded(n, 9, [&]() -> PyObject * {
         const auto *c = structure<engram_attn_config>(a[0], "cfg");
-        const auto *cache = structure<engram_kv_cache>(a[1], "cache");
+        const auto *cache = structure<Cache>(a[1], "cache");
         const auto *batch = structure<engram_kv_batch>(a[2], "batch");
         const at::Tensor *q = tensor(a[3], "q"), *lse = tensor(a[5], "lse"), *ws = tensor(a[6], "workspace");
         if (!q) fail(PyExc_ValueError, "q is needed");
@@ -289,30 +295,137 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
             need(*ws, at::kByte, dev, "workspace");
             bytes = (size_t)ws->numel();
             room = ws->data_ptr();
-        } else if ((bytes = fn_bytes(c, cache, batch)) > 0) {  // freed on return, to this stream's pool
+        } else if ((bytes = fn_size(c, cache, batch)) > 0) {  // freed on return, to this stream's pool
             made_ws = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(q->device()));
             room = made_ws.data_ptr();
         }
-        check(fn_attend(c, cache, batch, &hq, &ho, lse ? lse->data_ptr<float>() : nullptr, room, bytes, where.stream.stream()),
-              "engram_paged_attention");
+        check(fn(c, cache, batch, &hq, &ho, lse ? lse->data_ptr<float>() : nullptr, room, bytes, where.stream.stream()),
+              name);
         return give(a[4], made);
     });
 }
 
-// (EngramError, addresses of the four entry points)
+PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return append_into<engram_kv_cache>("engram_kv_append", fn_append, a, n);
+}
+PyObject *kv_append_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return append_into<engram_kv_cache_q8>("engram_kv_append_q8", fn_append8, a, n);
+}
+PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return attention_over<engram_kv_cache>("engram_paged_attention", fn_attend, fn_bytes, a, n);
+}
+PyObject *paged_attention_q8(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return attention_over<engram_kv_cache_q8>("engram_paged_attention_q8", fn_attend8, fn_bytes8, a, n);
+}
+
+int64_t integer(PyObject *o, const char *name) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) {
+        PyErr_Clear();
+        fail(PyExc_TypeError, std::string(name) + " must be an integer");
+    }
+    return v;
+}
+
+// A contiguous tensor of the type and number of values on the device; nullptr for None.
+template <typename T>
+T *values(PyObject *o, at::ScalarType type, int64_t count, at::Device dev, const char *name) {
+    const at::Tensor *t = tensor(o, name);
+    if (!t) return nullptr;
+    need(*t, type, dev, name);
+    if (t->numel() != count) fail(PyExc_ValueError, std::string(name) + " must have " + std::to_string(count) + " values");
+    return t->data_ptr<T>();
+}
+
+// (new_len, kv_len, block_table, free_pages, n_free, page_size, max_tokens, keep_len, kv_len_out, n_free_out, seq_offsets,
+// positions, slots, counts, stream) -> (seq_offsets, kv_len_out, n_free_out, positions, slots, counts)
+PyObject *kv_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject * {
+        const at::Tensor *fresh = tensor(a[0], "new_len"), *table = tensor(a[2], "block_table"), *stack = tensor(a[3], "free_pages");
+        if (!fresh || !table || !stack) fail(PyExc_ValueError, "new_len, block_table and free_pages are needed");
+        const at::Device dev = stack->device();
+        engram_kv_plan_args p = {};
+        p.n_seqs = fresh->numel();
+        p.max_tokens = integer(a[6], "max_tokens");
+        const int64_t size = integer(a[5], "page_size");
+        if (size < 1 || size > INT32_MAX) fail(PyExc_ValueError, "page_size must be a multiple of 16, at most 65536");
+        p.page_size = (int32_t)size;
+        if (p.max_tokens < 0 || p.max_tokens > INT32_MAX) fail(PyExc_ValueError, "max_tokens must be from 0 to 2^31 - 1");
+        need(*stack, at::kInt, dev, "free_pages");
+        p.n_pages = stack->numel();
+        p.free_pages = stack->data_ptr<int32_t>();
+        p.new_len = values<int32_t>(a[0], at::kInt, p.n_seqs, dev, "new_len");
+        p.kv_len = values<int32_t>(a[1], at::kInt, p.n_seqs, dev, "kv_len");
+        if (!p.kv_len && p.n_seqs) fail(PyExc_ValueError, "kv_len is needed");
+        p.keep_len = values<int32_t>(a[7], at::kInt, p.n_seqs, dev, "keep_len");
+        p.n_free = values<int32_t>(a[4], at::kInt, 1, dev, "n_free");
+        if (!p.n_free) fail(PyExc_ValueError, "n_free is needed");
+        need_type(*table, at::kInt, "block_table");
+        if (!table->is_cuda() || table->dim() != 2 || table->size(0) != p.n_seqs)
+            fail(PyExc_ValueError, "block_table must be a CUDA tensor [" + std::to_string(p.n_seqs) + ", pages]");
+        need_device(*table, dev, "block_table");
+        p.table_width = table->size(1);
+        if (p.n_seqs && ((p.table_width > 1 && table->stride(1) != 1) || (p.n_seqs > 1 && table->stride(0) < p.table_width)))
+            fail(PyExc_ValueError, "block_table must have contiguous rows");
+        p.table_stride = p.n_seqs > 1 ? table->stride(0) : p.table_width;
+        p.block_table = table->data_ptr<int32_t>();
+        const Where where(a[14], *stack);
+        // what is not given is made: offsets, lengths, free pages, positions, slots, counts
+        static const char *const names[6] = {"seq_offsets", "kv_len_out", "n_free_out", "positions", "slots", "counts"};
+        const int from[6] = {10, 8, 9, 11, 12, 13};
+        const int64_t counts[6] = {p.n_seqs + 1, p.n_seqs, 1, p.max_tokens, p.max_tokens, 4};
+        at::Tensor made[6];
+        void *data[6];
+        for (int i = 0; i < 6; ++i) {
+            const at::ScalarType type = i == 0 || i == 4 ? at::kLong : at::kInt;
+            if (a[from[i]] == Py_None) {
+                made[i] = at::empty({counts[i]}, at::TensorOptions().dtype(type).device(dev));
+                data[i] = made[i].data_ptr();
+            } else {
+                data[i] = type == at::kLong ? (void *)values<int64_t>(a[from[i]], type, counts[i], dev, names[i])
+                                            : (void *)values<int32_t>(a[from[i]], type, counts[i], dev, names[i]);
+            }
+        }
+        p.seq_offsets = static_cast<int64_t *>(data[0]);
+        p.kv_len_out = static_cast<int32_t *>(data[1]);
+        p.n_free_out = static_cast<int32_t *>(data[2]);
+        p.positions = static_cast<int32_t *>(data[3]);
+        p.slots = static_cast<int64_t *>(data[4]);
+        p.counts = static_cast<int32_t *>(data[5]);
+        check(fn_plan(&p, where.stream.stream()), "engram_kv_plan");
+        PyObject *r = PyTuple_New(6);
+        if (!r) throw PyFailed();
+        for (int i = 0; i < 6; ++i) {
+            PyObject *x = give(a[from[i]], made[i]);
+            if (!x) {
+                Py_DECREF(r);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(r, i, x);
+        }
+        return r;
+    });
+}
+
+// (EngramError, addresses of the entry points)
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded(n, 5, [&]() -> PyObject * {
+    return guarded(n, 9, [&]() -> PyObject * {
         Py_XSETREF(error_class, Py_NewRef(a[0]));
         fn_qk = reinterpret_cast<decltype(fn_qk)>(address<void>(a[1]));
         fn_append = reinterpret_cast<decltype(fn_append)>(address<void>(a[2]));
         fn_attend = reinterpret_cast<decltype(fn_attend)>(address<void>(a[3]));
         fn_bytes = reinterpret_cast<decltype(fn_bytes)>(address<void>(a[4]));
+        fn_plan = reinterpret_cast<decltype(fn_plan)>(address<void>(a[5]));
+        fn_append8 = reinterpret_cast<decltype(fn_append8)>(address<void>(a[6]));
+        fn_attend8 = reinterpret_cast<decltype(fn_attend8)>(address<void>(a[7]));
+        fn_bytes8 = reinterpret_cast<decltype(fn_bytes8)>(address<void>(a[8]));
         return Py_NewRef(Py_None);
     });
 }
 
 #define STEP_CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {STEP_CALL(bind), STEP_CALL(qk_norm_rope), STEP_CALL(kv_append), STEP_CALL(paged_attention),
+                         STEP_CALL(kv_plan), STEP_CALL(kv_append_q8), STEP_CALL(paged_attention_q8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -587,6 +587,125 @@ engram_status engram_paged_attention(const engram_attn_config *cfg, const engram
                                      const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
                                      float *lse, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ======================================================================= *
+ * Serving from an 8-bit cache: the block tables made on the device from the
+ * requests' lengths, the append that quantises, attention over the codes.
+ * Conventions as above; the batch is engram_kv_batch, the queries, keys and
+ * values are of cfg->dtype (bf16 or fp16).
+ * ======================================================================= */
+
+/* The paged 8-bit cache of one layer.  k and v hold e4m3 codes (1 sign, 4
+ * exponent, 3 mantissa bits; 448 the largest, 0x7F NaN, no infinity), code (p,
+ * token, head, c) at p*page_stride + token*token_stride + head*head_stride + c.
+ * A block of block_tokens consecutive tokens of a page has one scale per head:
+ * a code stands for its value times the scale at ((p*n_kv_heads + head) *
+ * (page_size / block_tokens)) + token / block_tokens of k_scales and v_scales.
+ * Scales are finite and not negative; engram_kv_append_q8 makes powers of two
+ * from 2^-48 to 2^48, others (largest value / 448, say) are read as well.  In
+ * v_scales, values below 2^-48 count as 2^-48 and those above 2^48 as 2^48.
+ * head_dim must be a multiple of 16. */
+typedef struct {
+    void *k;
+    void *v;
+    float *k_scales;      /* fp32 [n_pages][n_kv_heads][page_size / block_tokens] */
+    float *v_scales;
+    int64_t n_pages;      /* 1 .. 2^31 - 1 */
+    int32_t page_size;    /* tokens per page: a multiple of 16, at most 65536 */
+    int32_t block_tokens; /* tokens that share a scale: 16, 32, 64 or 128, a divisor of page_size */
+    int64_t page_stride;  /* bytes, multiples of 16; data 16-byte aligned */
+    int64_t token_stride;
+    int64_t head_stride;
+} engram_kv_cache_q8;
+
+/*
+ * A step's batch from the requests' lengths: pages for the tokens that come,
+ * pages back from those that went, the batch's offsets and the tokens' maps.
+ * Request s has kv_len[s] tokens in the cache, keeps the first keep_len[s] of
+ * them (rejected drafts go; 0: the request has ended, its row may serve a new
+ * one) and brings new_len[s]; kv_len_out[s] = keep_len[s] + new_len[s].  With P
+ * = page_size it had ceil(kv_len / P) pages and needs ceil(kv_len_out / P): the
+ * pages of the entries past those needed go on top of the stack free_pages
+ * (*n_free of them are free, free_pages[*n_free - 1] the top) in the order of
+ * (request, entry); then those missing come off its top in the same order.
+ * Entries given back stay in the table, unused.
+ * Outputs:
+ *   seq_offsets   int64 [n_seqs + 1]: new tokens before each request
+ *   positions     int32 [max_tokens] (or NULL): token i of request s has
+ *                 position keep_len[s] + i; -1 past the step's tokens
+ *   slots         int64 [max_tokens] (or NULL): its row in the cache, page *
+ *                 page_size + position % page_size; -1 past the step's tokens
+ *   counts        int32 [4]: new tokens, pages taken, pages given back, pages
+ *                 missing
+ * kv_len_out may be kv_len and n_free_out n_free (in place); other buffers are
+ * apart.  All or nothing: a length that is negative, kept beyond what is
+ * there, past the table's width or 2^31 - 1024, or a stack that does not fit
+ * n_pages sets ENGRAM_ERANGE; more new tokens than max_tokens or more pages
+ * than are free (counts[3] says how many are missing) set ENGRAM_ECAPACITY; in
+ * both cases lengths, table and stack stay as they are and the step has no
+ * tokens (offsets 0, counts 0).  Page ids are moved, not looked at.
+ */
+typedef struct {
+    int64_t n_seqs;
+    int64_t max_tokens;      /* room in positions and slots, < 2^31 */
+    int64_t n_pages;         /* room in free_pages: the cache's pages, < 2^31 */
+    int32_t page_size;       /* a multiple of 16, at most 65536 */
+    const int32_t *new_len;  /* int32 [n_seqs] */
+    const int32_t *keep_len; /* int32 [n_seqs], or NULL: everything is kept */
+    const int32_t *kv_len;   /* int32 [n_seqs] */
+    int32_t *kv_len_out;     /* int32 [n_seqs] */
+    int32_t *block_table;    /* int32 [n_seqs][table_stride] */
+    int64_t table_stride;
+    int64_t table_width;     /* entries of a row, 1 .. table_stride (0: table_stride) */
+    int32_t *free_pages;     /* int32 [n_pages] */
+    const int32_t *n_free;   /* int32 [1] */
+    int32_t *n_free_out;     /* int32 [1] */
+    int64_t *seq_offsets;
+    int32_t *positions;
+    int64_t *slots;
+    int32_t *counts;
+} engram_kv_plan_args;
+engram_status engram_kv_plan(const engram_kv_plan_args *args, void *stream);
+
+/*
+ * engram_kv_append into an 8-bit cache, in one launch: k normed, rotated and
+ * rounded to cfg->dtype (what the 16-bit cache would hold), k and v then
+ * quantised.  The scale of a block and head is the least power of two, from
+ * 2^-48 to 2^48, whose 448-fold holds the largest finite magnitude of its new
+ * tokens; where the block holds earlier tokens of the sequence it is at least
+ * their scale (rounded up to a power of two), and if that grows, their codes
+ * are rounded again to the new one.  Each value becomes the code nearest to
+ * value / scale (ties to even), at most 448 in magnitude; NaN and infinities
+ * become NaN.  So the codes depend on which tokens were appended together; all
+ * of one call's tokens of a block are one step.
+ * A position >= table_rows, a page id outside [0, n_pages) or a position past
+ * the block table sets ENGRAM_ERANGE and writes nothing for that token; tokens
+ * before position 0 are padding.  Two sequences that write to one block in the
+ * same call race.
+ */
+engram_status engram_kv_append_q8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                  const engram_kv_batch *batch, const engram_heads *k, const engram_heads *v,
+                                  const void *w_k, const float *table, int64_t table_rows, const engram_heads *q,
+                                  const void *w_q, const engram_heads *q_out, void *stream);
+
+/*
+ * engram_paged_attention over an 8-bit cache: scores from q (in its own 16
+ * bits) and the codes times their scale, weights rounded to fp16, sums in fp32.
+ * As there: a query without any key gets out = 0 and lse = -inf; slots at or
+ * past a sequence's length may hold anything, scales of blocks without any of
+ * its tokens too; a NaN code reaches only the queries that see its position; a
+ * page id outside [0, n_pages) sets ENGRAM_ERANGE and reads as zeros; kv_len
+ * beyond the block table or 2^31 - 1024 sets ENGRAM_ERANGE and is cut there;
+ * equal inputs give equal bits.  Weights relative to 1 / v scale below 2^-100 of
+ * a row's largest may count as 0.
+ *   workspace  >= engram_paged_attention_q8_workspace_bytes(cfg, cache, batch)
+ *              bytes, 256-byte aligned; scratch, nothing to clear
+ */
+size_t engram_paged_attention_q8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                                 const engram_kv_batch *batch);
+engram_status engram_paged_attention_q8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                        const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                        float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
