@@ -1,0 +1,778 @@
+// Attention over the 8-bit cache for many query rows per key/value head
+// (prompts, chunks): the tile kernel's items, plan, products and join, on tiles
+// that four more warps make from the codes.
+//
+// Bound: as the 16-bit tile kernel, by the softmax's instructions beside the
+// tensor pipe.  Why the codes become fp16 tiles first: the fp8 matrix
+// instruction wants both operands in 8 bits, so queries and weights would have
+// to be split into two or three pieces each; a tile's codes are converted once
+// for 256 rows instead (32,768 codes a pair of row tiles, 12 instructions for
+// 256 of them, on warps that the softmax leaves idle slots).
+//
+// Beside the roles of the 16-bit kernel (softmax, products, loads, items):
+//   warps 12-15   wait for a tile of codes (two stages of 16 KB, keys and values by
+//                 turns), convert a quarter of its keys each and store them as
+//                 the products read them (three stages of 32 KB: the values in
+//                 use, the next keys, the next values).  They also clear what
+//                 the products must not meet: values of keys that no row
+//                 reaches, NaN in tiles that some row sees only part of.
+//   Scales come with their tile of keys (asynchronous copies, counted by its
+//   barrier); a converter turns them into the factor, log2 and inverse that the
+//   softmax reads, a strip of 16 keys at a time.
+#pragma once
+
+#include <type_traits>
+
+namespace engram {
+namespace attn {
+namespace tile {
+
+constexpr int NUM_THREADS8 = 512;
+constexpr int CONVERTERS = 4;
+constexpr int STRIPS = KT / STRIP;  // scales of a tile
+// Tiles whose factors are kept.  A slot is written again only when the values of the tile two later have been
+// used by both row tiles, so by then both have read it.
+constexpr int FACTORS = 4;
+
+template <int DP>
+struct Cfg8 : Cfg<DP> {
+    static constexpr int STAGES = DP == 128 ? 3 : 6;
+    static constexpr int RAW_BYTES = KT * DP;  // codes of K or V of a tile
+    static constexpr int RAW_STAGES = DP == 128 ? 2 : 4;
+    static_assert(RAW_STAGES % 2 == 0, "keys and values by turns");
+};
+
+template <int DP>
+struct Shared8 {
+    uint64_t kv_full[Cfg8<DP>::STAGES];
+    uint64_t kv_empty[Cfg8<DP>::STAGES];
+    uint64_t raw_full[Cfg8<DP>::RAW_STAGES];
+    uint64_t raw_empty[Cfg8<DP>::RAW_STAGES];
+    uint64_t fac_full[FACTORS];
+    uint64_t q_full[2];
+    uint64_t s_full[2];
+    uint64_t p_ready[2][P_PARTS];
+    uint64_t s_free[2];   // APART: the scores have been read
+    uint64_t pv_done[2];  // APART: the weights have been used, O is up to date
+    uint64_t o_full[2];
+    uint64_t turn[2];
+    uint64_t drained[2];
+    uint64_t item_full[ITEMS];
+    uint64_t item_empty[ITEMS];
+    float4 fac[FACTORS][STRIPS];  // of a strip: the scores' factor, log2 of the value scale, its inverse
+    float scales[Cfg8<DP>::RAW_STAGES / 2][2][STRIPS];
+    Item items[ITEMS];
+    uint32_t tmem_base;
+    int abort;
+    PlanShared plan;
+};
+
+template <int DP>
+constexpr int smem8_bytes() {
+    return 2 * Cfg8<DP>::Q_BYTES + Cfg8<DP>::STAGES * Cfg8<DP>::STAGE_BYTES + Cfg8<DP>::RAW_STAGES * Cfg8<DP>::RAW_BYTES +
+           Cfg8<DP>::SWAP_BYTES + (int)sizeof(Shared8<DP>);
+}
+static_assert(smem8_bytes<128>() <= 232448 && smem8_bytes<64>() <= 232448, "tile kernel shared memory over the per-CTA limit");
+
+struct Params8 {
+    Params t;  // values: unused
+    Scales scales;
+    CodePages codes;
+};
+
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+// A strip's factor for a row.  Not 0 (a key scale may be): a hidden score, -inf, must stay that.
+__device__ __forceinline__ float factor(float strip, float row) { return fmaxf(strip * row, 7.5231638452626401e-37f); }
+
+template <typename E, int DP>
+__global__ void __launch_bounds__(NUM_THREADS8, 1)
+    tile8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const __grid_constant__ Params8 p8) {
+    using C = Cfg8<DP>;
+    using H = Fp16;  // of the products
+    const Params &p = p8.t;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *q_smem = smem;
+    uint8_t *kv_smem = smem + 2 * C::Q_BYTES;
+    uint8_t *raw_smem = kv_smem + C::STAGES * C::STAGE_BYTES;
+    uint8_t *swap_smem = raw_smem + C::RAW_STAGES * C::RAW_BYTES;
+    Shared8<DP> *sh = reinterpret_cast<Shared8<DP> *>(swap_smem + C::SWAP_BYTES);
+    volatile int *abort = &sh->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
+        grid_dependency_wait();
+        if (threadIdx.x == 0) raise_error(ENGRAM_EUNSUPPORTED);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&sh->kv_full[i], CONVERTERS);
+            mbar_init(&sh->kv_empty[i], 2);  // both row tiles' products
+        }
+        for (int i = 0; i < C::RAW_STAGES; ++i) {
+            mbar_init(&sh->raw_full[i], i % 2 == 0 ? 1 + 2 * STRIPS : 1);  // keys bring both scales
+            mbar_init(&sh->raw_empty[i], CONVERTERS);
+        }
+        for (int i = 0; i < FACTORS; ++i) mbar_init(&sh->fac_full[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->q_full[i], 4);
+            mbar_init(&sh->s_full[i], 1);
+            for (int c = 0; c < P_PARTS; ++c) mbar_init(&sh->p_ready[i][c], 4);
+            mbar_init(&sh->s_free[i], 4);
+            mbar_init(&sh->pv_done[i], 1);
+            mbar_init(&sh->turn[i], 1);
+            mbar_init(&sh->drained[i], 1);
+            mbar_init(&sh->o_full[i], 1);
+        }
+        for (int i = 0; i < ITEMS; ++i) {
+            mbar_init(&sh->item_full[i], 1);
+            mbar_init(&sh->item_empty[i], 11 + CONVERTERS);  // eight softmax warps, two MMA warps, the load warp and the converters
+        }
+        sh->abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&k_map);
+        prefetch_tensormap(&v_map);
+    }
+    if (warp == 8) {
+        tmem_alloc(&sh->tmem_base, C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t base = __ldg(p.b.offs);
+    if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.b.offs + p.b.n_seqs) - base != p.b.n_query)
+        raise_error(ENGRAM_ERANGE);
+    tc_fence_before();
+    const bool few = p.b.n_seqs <= 32;  // then the items' warp plans alone, below
+    if (few) {
+        __syncthreads();
+    } else {
+        make_plan<NUM_THREADS8>(p, base, &sh->plan);  // synchronises the block
+        if (blockIdx.x == 0 && threadIdx.x == 0 && p.cut) *p.cut = sh->plan.cut;
+    }
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+
+    // Item number i of this CTA, for a whole warp: every role takes all of them in order (null after a time-out).
+    const auto take = [&](uint32_t i) -> const Item * {
+        return warp_wait(&sh->item_full[i % ITEMS], (i / ITEMS) & 1, abort) ? &sh->items[i % ITEMS] : nullptr;
+    };
+
+    // Registers move from the other warps to the softmax warps, which hold a row of 128 scores each:
+    // 256 x 192 + 128 x 72 + 128 x 56 = the launch's 512 x 128.
+    if (warp < 8) {  // ------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        const int t = warp >> 2;                  // row tile
+        const int row = (warp & 3) * 32 + lane;   // row of the tile: this thread's TMEM lane
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_tm = tmem + lanes + t * KT, o_tm = tmem + lanes + C::O_COL + t * DP;
+        const uint32_t p_tm = C::APART ? tmem + lanes + C::P_COL + t * 64 : s_tm;
+        constexpr float LIFT = H::LIFT - H::RESCALE;  // of a weight at the running maximum
+        uint32_t s_ph = 0, o_ph = 0, it = 0, pv_ph = 0;  // it: tiles before the item
+        float rf = 1.f;  // what this thread's row of queries was divided by
+        bool ok = true;
+
+        // The tile's query rows into shared memory by asynchronous copies, 16 bytes a lane and round
+        // (rows past the item's are zero): fetch_q starts them, hand_q waits for them and tells the
+        // MMA warp.
+        constexpr int PIECES = DP / 8, PER = 32 / PIECES;  // 16-byte pieces of a row, rows a warp loads at once
+        const auto fetch_q = [&](const Item &w) {
+            const int ch = lane % PIECES;
+            const int32_t rr = w.r0 + t * MT + row, tok = p.by_group.quotient(rr), n_rows = w.n_rows;
+            const int64_t mine = ((int64_t)w.q.row0 + tok) * p.q_token_stride +
+                                 (int64_t)(w.head * p.group + rr - tok * p.group) * p.q_head_stride;
+            const uint32_t dst = smem_u32(q_smem) + t * C::Q_BYTES + (ch >> 3) * (MT * 128);
+#pragma unroll 4
+            for (int i = 0; i < 32; i += PER) {
+                const int r = (warp & 3) * 32 + i + lane / PIECES;
+                const int64_t at = __shfl_sync(0xffffffffu, mine, r & 31);
+                const bool in = t * MT + r < n_rows && ch * 8 < p.head_dim;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)),
+                             "l"(p.q + (in ? at + ch * 8 : 0)), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+        };
+        const auto hand_q = [&] {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            if (std::is_same<E, Bf16>::value) {  // this thread's row as fp16, times a power of two
+                __syncwarp();  // the warp's lanes have copied each other's rows
+                const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
+                const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
+                float most = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < DP / 8; ++i) {
+                    const uint4 v = lds16(piece(i));
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) most = max3(most, fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k])));
+                }
+                const int e = row_exponent(most);
+                const float up = exp2i(e);
+                rf = exp2i(-e);
+#pragma unroll 4
+                for (int i = 0; i < DP / 8; ++i) {
+                    const uint4 v = lds16(piece(i));
+                    const auto half = [&](uint32_t x) { return H::pack(bf16_lo(x) * up, bf16_hi(x) * up); };
+                    sts16(piece(i), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->q_full[t]);
+        };
+
+        const Item *w = take(0);
+        if (w && w->n > 0 && w->n_rows > t * MT) {
+            fetch_q(*w);
+            hand_q();
+        }
+        for (uint32_t k = 0; w && w->n_rows > 0 && ok; ++k) {
+            const bool mine = w->n_rows > t * MT;
+            const int32_t n = w->n;
+            const Item *next = nullptr;
+            float m = -INFINITY, l = 0.f;  // m: the exponent that the weights refer to
+            if (mine && n > 0) {
+                const int32_t item_key0 = w->key0;
+                const int32_t pos = w->pos0 + p.by_group.quotient(w->r0 + t * MT + row);
+                const int32_t row_lo = first_seen(pos, p.window);
+                // keys in reach of every row of the tile
+                const int32_t last = (w->n_rows < (t + 1) * MT ? w->n_rows : (t + 1) * MT) - 1;
+                const int32_t full_hi = w->pos0 + p.by_group.quotient(w->r0 + t * MT) + 1;
+                const int32_t full_lo = first_seen(w->pos0 + p.by_group.quotient(w->r0 + last), p.window);
+                for (int32_t j = 0; j < n; ++j) {
+                    const int32_t key0 = item_key0 + j * KT;
+                    ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t f = it + j;
+                    ok = warp_wait(&sh->fac_full[f % FACTORS], (f / FACTORS) & 1, abort);
+                    if (!ok) break;
+                    const float4 *const fac = sh->fac[f % FACTORS];
+                    // the second half of the scores arrives under the first half's maximum
+                    uint32_t raw[4][32];
+                    tmem_ld_32x32b_x32(s_tm, raw[0]);
+                    tmem_ld_32x32b_x32(s_tm + 32, raw[1]);
+                    tmem_ld_wait();
+                    tmem_ld_32x32b_x32(s_tm + 64, raw[2]);
+                    tmem_ld_32x32b_x32(s_tm + 96, raw[3]);
+                    const bool edge = key0 < full_lo || key0 + KT > full_hi;
+                    const int32_t a = row_lo - key0, b = pos - key0;  // this row's keys: [a, b] of the tile
+                    float s[KT];
+                    float mx = -INFINITY;  // of the exponents u = s F + log2 vs
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h) {
+                            tmem_ld_wait();
+                            if (C::APART) {
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(&sh->s_free[t]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = h * 64; i < h * 64 + 64; ++i) s[i] = __uint_as_float(raw[i >> 5][i & 31]);
+                        if (edge) {
+#pragma unroll
+                            for (int c = h * 2; c < h * 2 + 2; ++c) {
+                                const uint32_t in = bits_from(a - c * 32) & ~bits_from(b - c * 32 + 1);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(in & (1u << i))) s[c * 32 + i] = -INFINITY;
+                            }
+                        }
+                        float part[4];  // a strip each: independent chains
+#pragma unroll
+                        for (int i = 0; i < STRIP; i += 2)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const float u = s[h * 64 + c * STRIP + i], v = s[h * 64 + c * STRIP + i + 1];
+                                part[c] = i == 0 ? fmaxf(u, v) : max3(part[c], u, v);
+                            }
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float4 g = fac[h * 4 + c];
+                            part[c] = fmaf(part[c], factor(g.x, rf), g.y);
+                        }
+                        mx = max3(mx, part[0], part[1]);
+                        mx = max3(mx, part[2], part[3]);
+                    }
+                    if (C::APART) {  // the tile before is in O, its weights are used (before the first there is none)
+                        ok = warp_wait(&sh->pv_done[t], pv_ph ^ 1, abort);
+                        pv_ph ^= 1;
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    float up = 1.f;
+                    if (mx - m > H::RESCALE) {  // also from -inf
+                        up = rows::exp2_approx(m - mx);
+                        m = mx;
+                    }
+                    if (j > 0 && __any_sync(0xffffffffu, up != 1.f)) {
+                        l *= up;
+#pragma unroll
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(o_tm + c * 16, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
+                            tmem_st_32x32b_x16(o_tm + c * 16, o);
+                        }
+                    }
+                    const float mref = m == -INFINITY ? 0.f : m - LIFT;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {  // a strip: one factor, one scale
+                            const float4 fa = fac[2 * c + g];
+                            const float k = factor(fa.x, rf), at = fa.y - mref;
+                            const float2 sc = make_float2(k, k), off = make_float2(at, at);
+                            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                            for (int i = 8 * g; i < 8 * g + 8; ++i) {
+                                float2 x = fma2(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), sc, off);
+                                x.x = rows::exp2_approx(x.x);
+                                x.y = rows::exp2_approx(x.y);
+                                sum = i == 8 * g ? x : add2(sum, x);
+                                pk[i] = H::pack(x.x, x.y);  // 16-bit operands of the second product
+                            }
+                            l = fmaf(sum.x + sum.y, fa.z, l);
+                        }
+                        tmem_st_32x32b_x16(p_tm + c * 16, pk);
+                        if ((c + 1) % (4 / P_PARTS) == 0) {  // the second product may start on these keys
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&sh->p_ready[t][c * P_PARTS / 4]);
+                        }
+                    }
+                }
+                if (!ok) break;
+            }
+            it += n;
+            if (mine && n > 0) {
+                // The last scores were there, so the queries' memory is free: the next item's are fetched
+                // under this item's last product, and its scores computed under this item's epilogue.
+                next = take(k + 1);
+                const bool next_mine = next && next->n > 0 && next->n_rows > t * MT;
+                if (next_mine) fetch_q(*next);
+                ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
+                if (!ok) break;
+                if (next_mine) hand_q();
+                tc_fence_after();
+            } else {
+                next = take(k + 1);
+                if (next && next->n > 0 && next->n_rows > t * MT) {
+                    fetch_q(*next);
+                    hand_q();
+                }
+            }
+            if (mine) {
+                const bool whole = w->splits == 1, live = t * MT + row < w->n_rows;
+                const int64_t slot = whole ? 0 : w->slot;
+                const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
+                const int64_t out_row = (int64_t)w->q.row0 + tok;
+                const float inv = whole ? inverse(l, w->pos0 + tok) : 1.f;
+                // A lane has a row in TMEM, but lanes that store to 32 rows at once cost an access to L1 each:
+                // the rows change hands in shared memory, 128 bytes of each at a time (the pieces permuted,
+                // so neither way meets a bank twice), and eight lanes store a row's piece.
+                const uint32_t swap = smem_u32(swap_smem) + warp * (32 * 128);
+                const int64_t dst = out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
+                float *part = p.part_o + (slot * ROWS + t * MT + row - lane) * DP;
+                const int32_t warp_rows = w->n_rows - (t * MT + row - lane);  // this warp's rows of the item
+                const auto read_o = [&](int c, uint32_t (&o)[32]) {  // 32 columns of this lane's row
+                    if (n > 0) {
+                        tmem_ld_32x32b_x32(o_tm + c, o);
+                        tmem_ld_wait();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = 0;
+                    }
+                    if (w->bad_hi >= 0 && live) {
+                        const int32_t pos = w->pos0 + tok;
+                        float x[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
+                        add_nan<32>(p.b, p8.codes, w->s, w->head, max(first_seen(pos, p.window), w->key0 + w->bad_lo * KT),
+                                    min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c, p.head_dim, x);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
+                    }
+                };
+                const auto put = [&](int i, const uint32_t *v) {
+                    sts16(swap + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(v[0], v[1], v[2], v[3]));
+                };
+                const auto get = [&](int r) { return lds16(swap + r * 128 + (((lane ^ r) & 7) << 4)); };
+                if (whole) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 64) {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t o[32], u[16];
+                            read_o(c + half * 32, o);
+#pragma unroll
+                            for (int h = 0; h < 16; ++h)
+                                u[h] = E::pack(__uint_as_float(o[2 * h]) * inv, __uint_as_float(o[2 * h + 1]) * inv);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) put(half * 4 + i, u + 4 * i);
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = k * 4 + (lane >> 3), at = c + (lane & 7) * 8;
+                            const int64_t to = __shfl_sync(0xffffffffu, dst, r);
+                            if (r < warp_rows && at < p.head_dim) *reinterpret_cast<uint4 *>(p.out + to + at) = get(r);
+                        }
+                        __syncwarp();
+                    }
+                } else if (n > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        read_o(c, o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) put(i, o + 4 * i);
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int r = k * 4 + (lane >> 3);
+                            if (r < warp_rows) *reinterpret_cast<uint4 *>(part + r * DP + c + (lane & 7) * 4) = get(r);
+                        }
+                        __syncwarp();
+                    }
+                }
+                tc_fence_before();  // O has been read before the next item's first product is allowed
+                if (live) {
+                    const float m2 = m == -INFINITY ? -INFINITY : m - LIFT;
+                    if (!whole) {
+                        p.part_ml[slot * (2 * ROWS) + t * MT + row] = m2;
+                        p.part_ml[slot * (2 * ROWS) + ROWS + t * MT + row] = l;
+                    } else if (p.lse) {
+                        p.lse[out_row * p.n_heads + head] = rows::lse_of(m2, l);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->item_empty[k % ITEMS]);
+            w = next;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // after a time-out queries may still be on their way
+    } else if (warp >= 12) {  // -------------------------------- codes to fp16 tiles
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        const int part = warp - 12;  // a quarter of each tile's keys
+        constexpr int LPK = DP / 8, KEYS = 32 / LPK;  // lanes a key (8 codes each), keys at a time
+        const int ch = lane % LPK, key = part * 32 + lane / LPK;
+        const uint32_t src = smem_u32(raw_smem) + key * DP + ch * 8;
+        const uint32_t dst = smem_u32(kv_smem) + (ch >> 3) * (KT * 128) + key * 128;
+        uint32_t it = 0;  // tiles of keys and values by turns
+        bool ok = true;
+        for (uint32_t i = 0; ok; ++i) {
+            const Item *const item = take(i);
+            if (!item || item->n_rows == 0) break;
+            const int32_t n = item->n, lo = item->lo, hi = item->hi, full_lo = item->full_lo, full_hi = item->full_hi;
+            for (int32_t j = 0; ok && j < n; ++j) {
+                const int32_t key0 = item->key0 + j * KT;
+                const bool edge = key0 < full_lo || key0 + KT > full_hi;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv, ++it) {
+                    const uint32_t r = it % C::RAW_STAGES, st = it % C::STAGES;
+                    ok = warp_wait(&sh->raw_full[r], (it / C::RAW_STAGES) & 1, abort);
+                    if (!ok) break;
+                    ok = it < C::STAGES || warp_wait(&sh->kv_empty[st], ((it / C::STAGES) - 1) & 1, abort);
+                    if (!ok) break;
+                    if (kv == 0 && part == 0) {  // the tile's factors
+                        const uint32_t f = it / 2;
+                        if (lane < STRIPS) {
+                            const float2 vs = value_scale(sh->scales[r / 2][1][lane]);
+                            sh->fac[f % FACTORS][lane] = make_float4(sh->scales[r / 2][0][lane] * p.scale_log2, vs.x, vs.y, 0.f);
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh->fac_full[f % FACTORS]);
+                    }
+                    const uint32_t from = src + r * C::RAW_BYTES, to = dst + st * C::STAGE_BYTES;
+                    uint32_t bad = 0;
+#pragma unroll 8
+                    for (int g = 0; g < 32; g += KEYS) {
+                        uint2 c = lds8(from + g * DP);
+                        // Values that must not meet a weight of zero: those of keys that no row reaches (they may be
+                        // anything), NaN of keys that some row does not see (the epilogue adds it to the rows that do).
+                        if (kv && edge) {
+                            if (key0 + key + g < lo || key0 + key + g >= hi) c = make_uint2(0, 0);
+                            bad |= nan_codes(c.x) | nan_codes(c.y);
+                            c = make_uint2(without_nan(c.x), without_nan(c.y));
+                        }
+                        sts16(to + g * 128 + (((ch ^ (key + g)) & 7) << 4),
+                              make_uint4(codes_lo(c.x), codes_hi(c.x), codes_lo(c.y), codes_hi(c.y)));
+                    }
+                    if (bad) {
+                        Item *const note = const_cast<Item *>(item);
+                        atomicMin(&note->bad_lo, j);
+                        atomicMax(&note->bad_hi, j);
+                        __threadfence_block();
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&sh->kv_full[st]);
+                        mbar_arrive(&sh->raw_empty[r]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 10) {  // --------------------------------------------- items
+            // Rounds of one item per CTA, every other one in reverse: the items come longest first, and
+            // the CTAs at one end would get the longer one of every round.  A lane finds one of the
+            // next 32 items (several divisions each), then they are handed out in order.
+            const auto prefetch_q = [&](const Item &w) {  // an item's queries on their way into L2
+                const int64_t row0 = w.q.row0;
+                const int32_t r0 = w.r0, n_rows = w.n > 0 ? w.n_rows : 0, head0 = w.head * p.group;
+                for (int r = lane; r < n_rows; r += 32) {
+                    const int32_t tok = p.by_group.quotient(r0 + r), hh = r0 + r - tok * p.group;
+                    const uint16_t *q = p.q + (row0 + tok) * p.q_token_stride + (int64_t)(head0 + hh) * p.q_head_stride;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+                    if (p.head_dim > 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+                }
+            };
+            WarpPlan plan;
+            if (few) {
+                plan = plan_warp(p, base);
+                if (blockIdx.x == 0 && lane == 0 && p.cut) *p.cut = plan.cut;
+            } else {
+                plan.total = sh->plan.items[CHUNKS];
+            }
+            bool ok = true, more = true;
+            for (uint32_t i0 = 0; ok && more; i0 += 32) {
+                const uint32_t i = i0 + lane;
+                const int64_t index = (int64_t)i * gridDim.x + (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                Item mine;
+                mine.n_rows = 0;
+                if (few)
+                    mine = find_item_warp(p, base, plan, index);
+                else if (index < plan.total)
+                    mine = find_item(p, base, &sh->plan, index);
+                for (int k = 0; ok && more && k < 32; ++k) {
+                    if (lane == k) {
+                        if (i >= ITEMS) ok = mbar_wait(&sh->item_empty[i % ITEMS], ((i / ITEMS) - 1) & 1, abort);
+                        if (ok) {
+                            sh->items[i % ITEMS] = mine;
+                            mbar_arrive(&sh->item_full[i % ITEMS]);
+                        }
+                        more = mine.n_rows != 0;
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, k);
+                    more = __shfl_sync(0xffffffffu, more, k);
+                    if (ok && more) prefetch_q(sh->items[(i0 + k) % ITEMS]);
+                }
+            }
+        } else if (warp == 9) {  // --------------------------------------- K, V loads
+            const int boxes = KT / p.box;
+            const uint32_t box_bytes = (uint32_t)p.box * DP;
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t i = 0; ok; ++i) {
+                const Item *const item = take(i);
+                if (!item || item->n_rows == 0) break;
+                const struct {
+                    int64_t s;
+                    int32_t head, key0, n, lo, hi;
+                } w = {item->s, item->head, item->key0, item->n, item->lo, item->hi};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
+                int64_t window0 = -1;
+                int32_t page = -1;
+                for (int32_t j = 0; ok && j < w.n; ++j) {
+                    const int64_t b0 = w.key0 / p.box + (int64_t)j * boxes;
+                    if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
+                        window0 = b0;
+                        const int64_t key = (b0 + lane) * p.box;
+                        page = -1;
+                        if (key < w.hi) {
+                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + (uint32_t)key / (uint32_t)p.b.page_size);
+                            if (page < 0 || page >= p.b.n_pages) {
+                                if (key + p.box > w.lo) raise_error(ENGRAM_ERANGE);
+                                page = -1;  // out of range: the copy fills zeros
+                            }
+                        }
+                    }
+                    const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
+                    const int64_t key = (b0 + lane) * p.box;
+                    const bool load = lane < boxes && key < w.hi && key + p.box > w.lo;
+                    const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
+                    const int y = (int)((uint32_t)key % (uint32_t)p.b.page_size);
+                    // lanes 0..7 copy the strips' key scales, 8..15 their value scales
+                    const int sl = lane & (STRIPS - 1);
+                    const int32_t strip_page = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + sl * STRIP / p.box);
+                    const int64_t strip = b0 * p.box + sl * STRIP;
+                    const bool has_scale = strip < w.hi && strip + STRIP > w.lo && strip_page >= 0;
+                    const int32_t block = (int32_t)((uint32_t)strip % (uint32_t)p.b.page_size) >> p8.scales.block_log2;
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const int st = it % C::RAW_STAGES;
+                        if (lane == 0) {
+                            if (it >= C::RAW_STAGES) ok = mbar_wait(&sh->raw_empty[st], ((it / C::RAW_STAGES) - 1) & 1, abort);
+                            if (ok) mbar_arrive_expect_tx(&sh->raw_full[st], loads * box_bytes);
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                        if (load)
+                            rows::tma_load_4d(raw_smem + st * C::RAW_BYTES + lane * p.box * DP, kv ? &v_map : &k_map,
+                                              &sh->raw_full[st], 0, y, w.head, mine);
+                        if (kv == 0 && lane < 2 * STRIPS) {
+                            copy4_async(smem_u32(&sh->scales[st / 2][lane / STRIPS][sl]),
+                                        (lane < STRIPS ? p8.scales.k : p8.scales.v) +
+                                            (has_scale ? ((int64_t)strip_page * p.n_kv_heads + w.head) * p8.scales.per_page + block : 0),
+                                        has_scale);
+                            arrive_when_copied(&sh->raw_full[st]);
+                        }
+                    }
+                }
+            }
+            if (lane == 0) {  // never leave with a copy still landing (also after an abort elsewhere)
+                int no_abort = 0;
+                for (uint32_t i = it < C::RAW_STAGES ? 0 : it - C::RAW_STAGES; i < it; ++i)
+                    mbar_wait(&sh->raw_full[i % C::RAW_STAGES], (i / C::RAW_STAGES) & 1, &no_abort, 200000000ull);
+            }
+        } else {  // warps 8, 11 ---------------------------------- MMAs of row tile t
+            // The whole warp walks the tiles with warp-uniform values (the instruction takes its
+            // descriptors from uniform registers) and one elected lane issues.  Issuing blocks while
+            // the tensor pipe has a few products waiting, so each row tile has a warp of its own that
+            // waits for weights and keys meanwhile; the two take strict turns (turn[t]).  Without the
+            // turns their products interleave, both softmaxes then run at once and both wait for the
+            // tensor pipe at once (65,536-token chunk: 1.99 ms; one warp for both tiles 1.64 ms).
+            const int t = warp == 8 ? 0 : 1;
+            constexpr uint32_t ID_S = idesc_16(false, MT, KT, false), ID_O = idesc_16(false, MT, DP, true);
+            const bool leader = elect_one();
+            const uint32_t kva = smem_u32(kv_smem);
+            const uint64_t q_desc = smem_desc(smem_u32(q_smem) + t * C::Q_BYTES, 16, 1024, kSwizzle128B);
+            const uint64_t k_desc = smem_desc(kva, 16, 1024, kSwizzle128B);
+            const uint64_t v_desc = smem_desc(kva, KT * 128, 1024, kSwizzle128B);
+            const uint32_t s_tm = __shfl_sync(0xffffffffu, tmem, 0) + t * KT;
+            const uint32_t o_tm = __shfl_sync(0xffffffffu, tmem, 0) + C::O_COL + t * DP;
+            const uint32_t p_tm = C::APART ? __shfl_sync(0xffffffffu, tmem, 0) + C::P_COL + t * 64 : s_tm;
+            uint32_t st = 0, st_ph = 0;  // ring entry to consume next, and its phase
+            uint32_t q_ph = 0, p_ph = 0, turn_ph = 0, s_ph = 0;
+            bool ok = true;
+            const auto advance = [&] {
+                if (++st == C::STAGES) st = 0, st_ph ^= 1;
+            };
+            const auto scores = [&] {  // S = Q K^T, K in ring entry st
+                const uint64_t k0 = k_desc + st * (C::STAGE_BYTES >> 4);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t off = ((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4;
+                    mma_ss(s_tm, q_desc + off, k0 + off, ID_S, k != 0);
+                }
+                mma_commit(&sh->s_full[t]);
+                mma_commit(&sh->kv_empty[st]);
+            };
+            // Row tile 0 has the first turn: its first wait finds the phase before the first complete.
+            const auto my_turn = [&](bool both) {
+                if (C::APART || !both) return true;
+                const bool r = warp_wait(&sh->turn[t], turn_ph ^ (t == 0), abort);
+                turn_ph ^= 1;
+                return r;
+            };
+            // APART: the scores before have been read (before the first there are none).
+            const auto scores_free = [&] {
+                if (!C::APART) return true;
+                const bool r = warp_wait(&sh->s_free[t], s_ph ^ 1, abort);
+                s_ph ^= 1;
+                return r;
+            };
+            for (uint32_t i = 0; ok; ++i) {
+                const Item *const item = take(i);
+                ok = item != nullptr;
+                if (!ok) break;
+                const int32_t n_rows = __shfl_sync(0xffffffffu, item->n_rows, 0);
+                const int32_t n = __shfl_sync(0xffffffffu, item->n, 0);
+                if (n_rows == 0) break;
+                __syncwarp();
+                if (leader) mbar_arrive(&sh->item_empty[i % ITEMS]);
+                if (n == 0) continue;
+                const bool both = n_rows > MT;
+                if (!both && t == 1) {  // no rows here: give every ring entry back as it fills
+                    for (int32_t j = 0; ok && j < 2 * n; ++j) {
+                        ok = warp_wait(&sh->kv_full[st], st_ph, abort);
+                        if (leader) mbar_arrive(&sh->kv_empty[st]);
+                        advance();
+                    }
+                    continue;
+                }
+                ok = warp_wait(&sh->q_full[t], q_ph, abort) && warp_wait(&sh->kv_full[st], st_ph, abort) && scores_free() &&
+                     my_turn(both);
+                if (!ok) break;
+                q_ph ^= 1;
+                tc_fence_after();
+                if (leader) {
+                    scores();
+                    if (!C::APART && both) mbar_arrive(&sh->turn[t ^ 1]);
+                }
+                advance();
+                for (int32_t j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const uint32_t v = st;
+                    const uint64_t v0 = v_desc + v * (C::STAGE_BYTES >> 4);
+                    ok = warp_wait(&sh->kv_full[v], st_ph, abort);
+                    advance();
+                    ok = ok && (!more || warp_wait(&sh->kv_full[st], st_ph, abort));
+                    if (C::APART && more && ok) {
+                        ok = scores_free();
+                        tc_fence_after();
+                        if (ok && leader) scores();
+                    }
+                    ok = ok && warp_wait(&sh->p_ready[t][0], p_ph, abort) && my_turn(both);
+#pragma unroll
+                    for (int c = 0; c < P_PARTS; ++c) {
+                        if (c) ok = ok && warp_wait(&sh->p_ready[t][c], p_ph, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (leader) {
+#pragma unroll
+                            for (int k = c * (KT / 16 / P_PARTS); k < (c + 1) * (KT / 16 / P_PARTS); ++k)
+                                mma_ts(o_tm, p_tm + k * 8, v0 + k * (2048 >> 4), ID_O, (j | k) != 0);
+                        }
+                    }
+                    if (!ok) break;
+                    p_ph ^= 1;
+                    if (leader) {
+                        if (C::APART) mma_commit(&sh->pv_done[t]);
+                        if (!more)
+                            mma_commit(&sh->o_full[t]);
+                        else if (!C::APART)
+                            scores();
+                        if (!C::APART && both) mbar_arrive(&sh->turn[t ^ 1]);
+                        mma_commit(&sh->kv_empty[v]);
+                    }
+                    if (more) advance();
+                }
+            }
+            // Leave only when every MMA and the arrivals that follow them are done: one more commit of the
+            // issuing lane, on a barrier that nothing else uses.
+            if (leader) {
+                int no_abort = 0;
+                mma_commit(&sh->drained[t]);
+                mbar_wait(&sh->drained[t], 0, &no_abort, 200000000ull);
+            }
+            __syncwarp();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+}  // namespace tile
+}  // namespace attn
+}  // namespace engram

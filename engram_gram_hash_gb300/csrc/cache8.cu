@@ -4,10 +4,12 @@
 // step's, whose plans and joins it instantiates again.
 #include "attn_host.cuh"
 #include "attn_rows.cuh"
+#include "attn_tile.cuh"
 
 #include "append8.cuh"
 #include "attn8_common.cuh"
 #include "attn_rows8.cuh"
+#include "attn_tile8.cuh"
 #include "kv_plan.cuh"
 
 namespace engram {
@@ -69,8 +71,8 @@ static engram_status append8_launch(const engram_attn_config *cfg, const Append8
 // ---------------------------------------------------------------- attention --
 
 // A [page][head][token][D] view of K or V codes for TMA: boxes of the padded head (rows of 128 bytes, or 64) x
-// `rows` tokens, swizzled over the row; codes past head_dim read as zeros.
-static bool page_map8(CUtensorMap *m, const engram_attn_config *cfg, const engram_kv_cache_q8 *c, void *base, int rows) {
+// `rows` tokens, swizzled over the row where asked; codes past head_dim read as zeros.
+static bool page_map8(CUtensorMap *m, const engram_attn_config *cfg, const engram_kv_cache_q8 *c, void *base, int rows, bool swizzle) {
     auto enc = tensormap_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)cfg->head_dim, (cuuint64_t)c->page_size, (cuuint64_t)cfg->n_kv_heads,
@@ -79,7 +81,7 @@ static bool page_map8(CUtensorMap *m, const engram_attn_config *cfg, const engra
     cuuint32_t box[4] = {(cuuint32_t)padded_dim(cfg), (cuuint32_t)rows, 1, 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               padded_dim(cfg) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : padded_dim(cfg) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -165,7 +167,7 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     a.scales = scales_of(cache);
     a.codes = CodePages{static_cast<const uint8_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
     CUtensorMap km, vm;
-    if (!page_map8(&km, cfg, cache, cache->k, p.box) || !page_map8(&vm, cfg, cache, cache->v, p.box)) return ENGRAM_ECUDA;
+    if (!page_map8(&km, cfg, cache, cache->k, p.box, true) || !page_map8(&vm, cfg, cache, cache->v, p.box, true)) return ENGRAM_ECUDA;
     constexpr int smem = rows::smem8_bytes<DP>();
     static std::atomic<bool> attr_done[64];
     const auto kern = rows::rows8_kernel<E, DP>;
@@ -176,7 +178,90 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
+// Row blocks x kv heads of a batch at most, and the slots for partial results, as for the 16-bit cache.
+static int64_t tile8_items_most(const engram_attn_config *cfg, int64_t n_seqs, int64_t n_query) {
+    const int64_t rows = n_query * (cfg->n_heads / cfg->n_kv_heads);
+    const int64_t seqs = n_seqs < n_query ? n_seqs : n_query;
+    return (rows / tile::ROWS + seqs) * cfg->n_kv_heads;
+}
+static int64_t tile8_slots(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    const int64_t n_seqs = batch->n_seqs, n_query = batch->n_query;
+    if (keys_most(cfg, cache, batch) <= 6 * tile::KT) return 0;
+    const int64_t least = (n_query * (cfg->n_heads / cfg->n_kv_heads) + tile::ROWS - 1) / tile::ROWS * cfg->n_kv_heads;
+    if (least >= (int64_t)num_sms() * 6) return 0;
+    return std::min<int64_t>((int64_t)num_sms() * tile::SLOTS_PER_SM, tile8_items_most(cfg, n_seqs, n_query) * tile::MAX_SPLIT);
+}
+static size_t tile8_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
+    return up256((size_t)slots * tile::ROWS * padded_dim(cfg) * sizeof(float));
+}
+static size_t tile8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    const int64_t slots = tile8_slots(cfg, cache, batch);
+    if (slots == 0) return 0;
+    return tile8_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
+}
+
+// Rows kernel or tile kernel: the one whose estimate, in us on this GPU, is less.
+static bool use_tiles8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    const double sms = num_sms();
+    const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
+    const double mean = (double)rows / (double)seqs, parts = (double)seqs * cfg->n_kv_heads;
+    const double segs = parts * ceil(mean / rows::ROWS), items = parts * ceil(mean / tile::ROWS);
+    const double seg_us = 2.5 + 1.0 * (double)rows8_tiles_most(cfg, cache, batch);
+    const double item_us = 3.7 + 1.6 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
+    const double rows_us = std::min(9.0 + segs * seg_us / sms, 3.5 + ceil(segs / sms) * seg_us);
+    const double tile_us = tile8_slots(cfg, cache, batch) > 0 ? 24.0 + items * item_us / sms : 4.0 + ceil(items / sms) * item_us;
+    return tile_us < rows_us;
+}
+
+template <typename E, int DP>
+static engram_status tile8_launch(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
+                                  const engram_kv_batch *batch, const engram_heads *q, const engram_heads *out,
+                                  float *lse, void *workspace, cudaStream_t st) {
+    tile::Params8 a;
+    memset(&a, 0, sizeof(a));
+    tile::Params &p = a.t;
+    const int64_t slots = tile8_slots(cfg, cache, batch);
+    p.b = device_batch(batch, cache);
+    p.q = static_cast<const uint16_t *>(q->data);
+    p.q_token_stride = q->token_stride;
+    p.q_head_stride = q->head_stride;
+    p.out = static_cast<uint16_t *>(out->data);
+    p.out_token_stride = out->token_stride;
+    p.out_head_stride = out->head_stride;
+    p.lse = lse;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + tile8_part_o_bytes(cfg, slots));
+    p.n_heads = cfg->n_heads;
+    p.n_kv_heads = cfg->n_kv_heads;
+    p.group = cfg->n_heads / cfg->n_kv_heads;
+    p.by_group = Divisor(p.group);
+    p.by_heads = Divisor(cfg->n_kv_heads);
+    p.head_dim = cfg->head_dim;
+    p.window = cfg->window;
+    p.box = gcd(cache->page_size, tile::KT);
+    p.ctas = num_sms();
+    p.max_slots = (int32_t)slots;
+    p.cut = slots == 0 ? nullptr
+                       : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
+                                                     tile8_workspace_bytes(cfg, cache, batch) - 256);
+    p.scale_log2 = cfg->scale * 1.4426950408889634f;
+    a.scales = scales_of(cache);
+    a.codes = CodePages{static_cast<const uint8_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
+    CUtensorMap km, vm;
+    if (!page_map8(&km, cfg, cache, cache->k, p.box, false) || !page_map8(&vm, cfg, cache, cache->v, p.box, false))
+        return ENGRAM_ECUDA;
+    constexpr int smem = tile::smem8_bytes<DP>();
+    static std::atomic<bool> attr_done[64];
+    const auto kern = tile::tile8_kernel<E, DP>;
+    engram_status s = ensure_smem((const void *)kern, smem, attr_done);
+    if (s != ENGRAM_OK) return s;
+    s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS8, smem, 1, st, "tile8_kernel", km, vm, a);
+    if (s != ENGRAM_OK || slots == 0) return s;
+    return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * tile::JOIN_PER_SM), 128, 0, 1, st, "tile_join_kernel", p);
+}
+
 static size_t workspace_bytes8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    if (use_tiles8(cfg, cache, batch)) return tile8_workspace_bytes(cfg, cache, batch);
     return rows8_shares(cfg, cache, batch).cut() ? rows8_workspace_bytes(cfg) : 0;
 }
 
@@ -292,6 +377,13 @@ extern "C" engram_status engram_paged_attention_q8(const engram_attn_config *cfg
     if (workspace_bytes < need) return ENGRAM_ENOMEM;
     cudaStream_t st = (cudaStream_t)stream;
     const bool bf16 = cfg->dtype == ENGRAM_BF16;
+    if (use_tiles8(cfg, cache, batch)) {
+        if (padded_dim(cfg) == 64)
+            return bf16 ? tile8_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
+                        : tile8_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);
+        return bf16 ? tile8_launch<Bf16, 128>(cfg, cache, batch, q, out, lse, workspace, st)
+                    : tile8_launch<Fp16, 128>(cfg, cache, batch, q, out, lse, workspace, st);
+    }
     if (padded_dim(cfg) == 64)
         return bf16 ? rows8_launch<Bf16, 64>(cfg, cache, batch, q, out, lse, workspace, st)
                     : rows8_launch<Fp16, 64>(cfg, cache, batch, q, out, lse, workspace, st);
