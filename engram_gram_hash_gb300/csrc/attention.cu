@@ -153,7 +153,7 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows_kernel", km, vm, p);
     if (s != ENGRAM_OK || !shares.cut()) return s;
-    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
+    return launch_after(rows::rows_join_kernel<E, DP, rows::ROWS>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
 // Row blocks x kv heads of a batch at most.

@@ -10,9 +10,8 @@
 // made of (weight times scale), so weights rounded to fp16 keep their bits
 // whatever the scales are; l, in fp32, takes the scale out again, a block at a
 // time.  (m, l, O) of two parts join as in the 16-bit kernels, with R for m.
-// Codes are exact in fp16, so both products run on fp16 whatever the type of
-// the queries: a row of bf16 queries is multiplied by a power of two that puts
-// its largest value at 2^14 .. 2^15 (below 2^-28 of it values lose bits).
+// Codes are exact in fp16 and weights keep 11 bits there, so the second product
+// runs on fp16 whatever the type of the queries.
 #pragma once
 
 namespace engram {
@@ -28,10 +27,15 @@ struct Scales {
 };
 
 // log2 vs and 1 / vs of a strip's value scale.  Below 2^-48 it counts as 2^-48, so a block of zeros may have
-// scale 0; above 2^48 as that.  NaN stays.
+// scale 0; above 2^48 as that.  The logarithm is the exponent, exact, and that of the mantissa, off by 2^-22 at
+// most; the same number weighs a key's values and, taken out of l by the inverse, hardly its weight.
 __device__ __forceinline__ float2 value_scale(float vs) {
-    const float x = vs < 3.5527136788005009e-15f ? 3.5527136788005009e-15f : (vs > 281474976710656.f ? 281474976710656.f : vs);
-    return make_float2(log2f(x), __frcp_rn(x));
+    const float x = fminf(fmaxf(vs, 3.5527136788005009e-15f), 281474976710656.f);
+    const uint32_t b = __float_as_uint(x);
+    float lg, inv;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(lg) : "f"(__uint_as_float((b & 0x7FFFFFu) | 0x3F800000u)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(x));
+    return make_float2(lg + (float)((int)(b >> 23) - 127), inv);
 }
 
 // Two codes (the low or high half of w) as an fp16 pair.
@@ -50,12 +54,13 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xFFu); }
 
-// The power of two that brings a row's largest magnitude to 2^14 .. 2^15, as its exponent; 0 for a row of
-// zeros or with an infinity or NaN.
+// The power of two that brings a row's largest magnitude to 2^TO .. 2^(TO + 1), as its exponent (at most 124); 0 for
+// a row of zeros or with an infinity or NaN.
+template <int TO>
 __device__ __forceinline__ int row_exponent(float most) {
     if (!(most > 0.f) || !(most < INFINITY)) return 0;
-    const int e = (int)(__float_as_uint(most) >> 23) - 127;
-    return e < -110 ? 124 : 14 - e;
+    const int e = TO + 127 - (int)(__float_as_uint(most) >> 23);
+    return e > 124 ? 124 : e;
 }
 // 2^e for -126 <= e <= 127.
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }

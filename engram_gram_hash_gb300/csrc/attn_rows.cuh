@@ -88,8 +88,8 @@ struct Params {
     int64_t out_token_stride, out_head_stride;
     float *lse;         // [n_query][n_heads] or null
     ValuePages values;
-    float *part_o;      // [grid][2][ROWS][DP]
-    float *part_ml;     // [grid][2][2][ROWS]
+    float *part_o;      // [grid][2][rows of a segment][DP]
+    float *part_ml;     // [grid][2][2][rows of a segment]
     int32_t n_heads, n_kv_heads, group, head_dim;
     Divisor by_group, by_heads;  // the query heads of a kv head; the kv heads
     int32_t window;
@@ -103,22 +103,25 @@ struct Params {
 
 // ------------------------------------------------------------------- plan ----
 
-// Key tiles that a segment of sequence q is given on the line (at least one,
-// so that rows without keys are written too), and its segments per kv head.
+// Key tiles that a segment (R rows) of sequence q is given on the line (at
+// least one, so that rows without keys are written too), and its segments per
+// kv head.
+template <int R>
 __device__ __forceinline__ int32_t seg_tiles(const Params &p, const Seq &q) {
     if (p.whole > 0) return p.whole;
     const int32_t kt = 1 << p.kt_log2;
     int32_t n = (q.kv + kt - 1) >> p.kt_log2;
     if (p.window > 0) {
-        const int32_t tokens = (ROWS - 2) / p.group + 2;  // most tokens that 16 consecutive rows touch
+        const int32_t tokens = (R - 2) / p.group + 2;  // most tokens that R consecutive rows touch
         const int64_t reach = (int64_t)p.window + tokens - 1;
         const int64_t w = ((reach + kt - 2) >> p.kt_log2) + 1;
         if (w < n) n = (int32_t)w;
     }
     return n > 0 ? n : 1;
 }
+template <int R>
 __device__ __forceinline__ int32_t seg_rows(const Params &p, const Seq &q) {
-    return (int32_t)(((int64_t)q.q_len * p.group + ROWS - 1) / ROWS);
+    return (int32_t)(((int64_t)q.q_len * p.group + R - 1) / R);
 }
 
 struct Plan {
@@ -135,7 +138,7 @@ __device__ __forceinline__ int64_t run_of(const Params &p, int64_t total) {
 // All threads of a block of NT: the length of the line, the tiles per CTA,
 // and for f(run) = the place asked for the sequence it lies in (sh_s, with
 // the tiles before that sequence in sh_before; sh_s = -1 past the end).
-template <int NT>
+template <int NT, int R>
 __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t *scan, int64_t *sh_s, int64_t *sh_before) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t per = (p.b.n_seqs + NT - 1) / NT;
@@ -143,7 +146,7 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
     int64_t sum = 0;
     for (int64_t s = s0; s < s1; ++s) {
         const Seq q = load_seq(p.b, s, base);
-        sum += (int64_t)seg_rows(p, q) * p.n_kv_heads * seg_tiles(p, q);
+        sum += (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
     }
     int64_t incl = sum;
 #pragma unroll
@@ -168,7 +171,7 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
         int64_t at = before;
         for (int64_t s = s0; s < s1; ++s) {
             const Seq q = load_seq(p.b, s, base);
-            const int64_t c = (int64_t)seg_rows(p, q) * p.n_kv_heads * seg_tiles(p, q);
+            const int64_t c = (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
             if (f < at + c) {
                 *sh_s = s;
                 *sh_before = at;
@@ -183,12 +186,13 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
 
 // The same for at most 32 sequences, by every warp for itself: one round of
 // loads and no block barrier.
+template <int R>
 __device__ __forceinline__ Plan plan_find_small(const Params &p, int64_t base, int64_t index, int64_t &s, int64_t &before) {
     const int lane = threadIdx.x & 31;
     int64_t cost = 0;
     if (lane < p.b.n_seqs) {
         const Seq q = load_seq(p.b, lane, base);
-        cost = (int64_t)seg_rows(p, q) * p.n_kv_heads * seg_tiles(p, q);
+        cost = (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
     }
     int64_t incl = cost;
 #pragma unroll
@@ -207,6 +211,7 @@ __device__ __forceinline__ Plan plan_find_small(const Params &p, int64_t base, i
 }
 
 // A place on the line: the segment and the tile within it.
+template <int R>
 struct Walk {
     int64_t s;       // sequence
     int32_t seg;     // segment within the sequence: row tile * n_kv_heads + kv head
@@ -218,8 +223,8 @@ struct Walk {
     __device__ __forceinline__ void enter(const Params &p, int64_t base, int64_t s_) {
         s = s_;
         q = load_seq(p.b, s, base);
-        tiles = seg_tiles(p, q);
-        n_segs = seg_rows(p, q) * p.n_kv_heads;
+        tiles = seg_tiles<R>(p, q);
+        n_segs = seg_rows<R>(p, q) * p.n_kv_heads;
     }
     __device__ __forceinline__ void start(const Params &p, int64_t base, int64_t s_, int64_t offset) {
         enter(p, base, s_);
@@ -242,20 +247,21 @@ struct Walk {
 struct Segment {
     int32_t head;       // kv head
     int32_t r0;         // first row (token * group + query head within the group)
-    int32_t n_rows;     // 1..16
+    int32_t n_rows;     // 1..R
     int32_t pos0;       // position of the sequence's first new token
     int32_t lo, hi;     // keys in reach of any row: [lo, hi)
     int32_t full_lo, full_hi;  // keys in reach of every row
     int32_t tile0, n_tiles;
 };
 
-__device__ __forceinline__ Segment segment(const Params &p, const Walk &w) {
+template <int R>
+__device__ __forceinline__ Segment segment(const Params &p, const Walk<R> &w) {
     Segment g;
     const int32_t block = p.by_heads.quotient(w.seg);
     g.head = w.seg - block * p.n_kv_heads;
-    g.r0 = block * ROWS;
+    g.r0 = block * R;
     const int32_t left = w.q.q_len * p.group - g.r0;
-    g.n_rows = left < ROWS ? left : ROWS;
+    g.n_rows = left < R ? left : R;
     g.pos0 = w.q.kv - w.q.q_len;
     const int32_t first = g.pos0 + p.by_group.quotient(g.r0), last = g.pos0 + p.by_group.quotient(g.r0 + g.n_rows - 1);
     g.hi = last + 1;  // <= kv
@@ -295,7 +301,8 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // e^(x - m) in base 2, 0 where nothing was seen (m = -inf only with x = -inf)
 __device__ __forceinline__ float weight(float x, float m) { return exp2_approx(x - (m == -INFINITY ? 0.f : m)); }
 
-__device__ __forceinline__ int64_t w_row(const Walk &w, int32_t token) { return (int64_t)w.q.row0 + token; }
+template <int R>
+__device__ __forceinline__ int64_t w_row(const Walk<R> &w, int32_t token) { return (int64_t)w.q.row0 + token; }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); }
 // (m, l) in base 2 -> ln sum; -inf where nothing was seen
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
@@ -333,15 +340,16 @@ __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_saddr) {
 // ---------------------------------------------------------------- kernel ----
 
 // Values c .. c + 3 of row r of the segment, v / l, and the row's lse.
-template <typename E>
-__device__ __forceinline__ void write_out(const Params &p, const Walk &w, const Segment &g, int r, int c, float4 v, float l) {
+template <typename E, int R>
+__device__ __forceinline__ void write_out(const Params &p, const Walk<R> &w, const Segment &g, int r, int c, float4 v, float l) {
     if (c >= p.head_dim) return;
     const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
     const float inv = inverse(l, g.pos0 + tok);
     uint16_t *dst = p.out + (int64_t)w_row(w, tok) * p.out_token_stride + (int64_t)(g.head * p.group + hh) * p.out_head_stride + c;
     *reinterpret_cast<uint2 *>(dst) = make_uint2(E::pack(v.x * inv, v.y * inv), E::pack(v.z * inv, v.w * inv));
 }
-__device__ __forceinline__ void write_lse(const Params &p, const Walk &w, const Segment &g, int r, float m, float l) {
+template <int R>
+__device__ __forceinline__ void write_lse(const Params &p, const Walk<R> &w, const Segment &g, int r, float m, float l) {
     const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
     p.lse[(int64_t)w_row(w, tok) * p.n_heads + g.head * p.group + hh] = lse_of(m, l);
 }
@@ -386,17 +394,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Plan plan;
     int64_t at_s, at_before;
     if (p.b.n_seqs <= 32) {
-        plan = plan_find_small(p, base, index, at_s, at_before);
+        plan = plan_find_small<ROWS>(p, base, index, at_s, at_before);
         __syncthreads();  // the barriers are initialised
     } else {
-        plan = plan_find<NUM_THREADS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+        plan = plan_find<NUM_THREADS, ROWS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
         at_s = sh->find_s;
         at_before = sh->find_before;
     }
     const int64_t f0 = index * plan.run;
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
-    Walk walk;
+    Walk<ROWS> walk;
     walk.start(p, base, at_s, f0 - at_before);
     uint32_t it = 0;  // tiles through the ring
     // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
@@ -765,7 +773,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // Adds up the parts of the segments that the line's cuts went through.  Block
 // x looks at the cut between CTAs x and x + 1 and acts on it if it is the
 // first inside its segment; a warp takes one row, its lanes 4 values each.
-template <typename E, int DP>
+template <typename E, int DP, int R>
 __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ Params p) {
     __shared__ int64_t scan[4], find_s, find_before;
     // The plan reads the batch only, which was final before the attention kernel let this one start
@@ -775,9 +783,9 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     Plan plan;
     int64_t at_s, at_before;
     if (p.b.n_seqs <= 32) {
-        plan = plan_find_small(p, base, cut, at_s, at_before);
+        plan = plan_find_small<R>(p, base, cut, at_s, at_before);
     } else {
-        plan = plan_find<128>(p, base, cut, scan, &find_s, &find_before);
+        plan = plan_find<128, R>(p, base, cut, scan, &find_s, &find_before);
         at_s = find_s;
         at_before = find_before;
     }
@@ -785,7 +793,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     allow_dependent_launch();
     const int64_t f = cut * plan.run;
     if (f >= plan.total) return;
-    Walk w;
+    Walk<R> w;
     w.start(p, base, at_s, f - at_before);
     const int64_t first = f - w.j;  // the segment's first tile on the line
     if (w.j == 0 || (cut - 1) * plan.run > first) return;
@@ -798,7 +806,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     const auto slot_of = [&](int k) { return k == 0 ? slot0 : (cut - 1 + k) * 2; };
 
     float m = -INFINITY;
-    for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(k) * (2 * ROWS) + r));
+    for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(k) * (2 * R) + r));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.f;
@@ -807,16 +815,16 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     for (int k0 = 0; k0 < parts; k0 += 32) {
         float wk = 0.f;
         if (k0 + lane < parts) {
-            const float *ml = p.part_ml + slot_of(k0 + lane) * (2 * ROWS) + r;
+            const float *ml = p.part_ml + slot_of(k0 + lane) * (2 * R) + r;
             wk = weight(__ldcg(ml), m);
-            l += wk * __ldcg(ml + ROWS);
+            l += wk * __ldcg(ml + R);
         }
         const int n = parts - k0 < 32 ? parts - k0 : 32;
 #pragma unroll 8
         for (int k = 0; k < n; ++k) {
             const float x = __shfl_sync(0xffffffffu, wk, k);
             if (on) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot_of(k0 + k) * (ROWS * DP) + r * DP) + lane);
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot_of(k0 + k) * (R * DP) + r * DP) + lane);
                 acc.x = fmaf(x, v.x, acc.x);
                 acc.y = fmaf(x, v.y, acc.y);
                 acc.z = fmaf(x, v.z, acc.z);

@@ -1,22 +1,31 @@
 // Attention over the 8-bit cache for few query rows per key/value head (single
 // tokens and short chunks): the rows kernel's plan, ring and joins over tiles
-// of codes.
+// of codes, 8 rows a segment.
 //
-// Bound: the bytes of the codes, half the 16-bit cache's.  A tile is 128 keys
-// (32 KB of K and V at 128 values); a warp has a quarter of one, turns the
-// codes it needs into fp16 pairs on their way from shared memory into the
-// matrix instruction (one conversion a pair, beside a byte permutation for V,
-// whose pairs lie across keys) and multiplies them with mma.sync m16n8k16.  The
-// order of a head's values within the products is chosen so that a lane's four
-// codes are neighbours in memory; nothing is exchanged.  The strips' scales
-// travel with their tile: 4-byte asynchronous copies that the tile's barrier
-// counts, so their latency is hidden as the codes' is.
+// Bound: the bytes of the codes, half the 16-bit cache's, if a tile costs the
+// warps few enough instructions.  So the codes of K are not converted: the
+// queries are split into two (bf16) or three (fp16) e4m3 pieces, each the
+// rounding of what the ones before leave times 16, and multiplied by mma.sync
+// m16n8k32 on e4m3; the first two pieces of 8 rows are the 16 rows of one
+// instruction, and a score is s0 + s1 / 16 (+ s2 / 256).  Two pieces hold the 8
+// bits of bf16, three the 11 of fp16 exactly, in a row whose largest value is
+// brought to 2^7 .. 2^8; values far below it are off by at most 2^-21 of it
+// (2^-25 with three).  Weights want more range than two pieces
+// have (a long tail beside a large key), so the second product is on fp16, as
+// O^T = V^T P^T: 16 values x 8 rows an instruction, the pairs of weights where
+// the scores' accumulators left them.  Codes of V become fp16 pairs on their way
+// from shared memory (a byte permutation and two conversions for four).
+// A warp has a quarter of a tile (128 keys, 32 KB of K and V at 128 values) and
+// every value's order within the products is free, so a lane's codes are
+// neighbours in memory.  The strips' scales travel with their tile: 4-byte
+// asynchronous copies that the tile's barrier counts.
 #pragma once
 
 namespace engram {
 namespace attn {
 namespace rows {
 
+constexpr int ROWS8 = 8;               // query rows per segment
 constexpr int KT8 = 128;               // keys per tile
 constexpr int STRIPS = KT8 / STRIP;    // scales of a tile
 
@@ -28,7 +37,7 @@ struct Cfg8 {
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     static constexpr int STAGES = 196608 / STAGE_BYTES;
     static_assert(STAGES % 2 == 0, "each ring stage must belong to one consumer group");
-    static constexpr int JOIN_FLOATS = 4 * ROWS * DP;
+    static constexpr int JOIN_FLOATS = 4 * ROWS8 * DP;
 };
 
 // Shared memory of piece ch (16 codes) of a tile's key, swizzled by TMA: rows of 128 bytes, or two of 64.
@@ -36,23 +45,43 @@ template <int DP>
 __device__ __forceinline__ uint32_t piece_at(int key, int ch) {
     return DP == 128 ? key * 128 + (((ch ^ key) & 7) << 4) : key * 64 + (((ch ^ (key >> 1)) & 3) << 4);
 }
-// Float c of row r in a join buffer: neighbouring rows' 64-byte halves are exchanged (a store's two rows of four
-// lanes meet different banks).
+// Float c of row r in a join buffer: the rows' 32-byte pieces are rotated, so that the accumulators' layout (4
+// rows x 4 pairs of values a half warp) meets different banks.
 template <int DP>
-__device__ __forceinline__ int join8_at(int r, int c) { return r * DP + (c ^ ((r & 1) * 16)); }
+__device__ __forceinline__ int join8_at(int r, int c) { return r * DP + (c ^ (((r >> 1) & 3) * 8)); }
+
+// d += A B with e4m3 operands, 16 rows x 32 values x 8 keys.
+__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Four values as codes; x becomes 16 times what they leave (NaN and infinities leave NaN).
+__device__ __forceinline__ uint32_t take_codes(float (&x)[4]) {
+    const uint32_t c = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
+                       (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+    const float2 lo = e4m3x2_to_float2((uint16_t)c), hi = e4m3x2_to_float2((uint16_t)(c >> 16));
+    x[0] = (x[0] - lo.x) * 16.f;
+    x[1] = (x[1] - lo.y) * 16.f;
+    x[2] = (x[2] - hi.x) * 16.f;
+    x[3] = (x[3] - hi.y) * 16.f;
+    return c;
+}
 
 template <int DP>
 struct Shared8 {
     uint64_t full[Cfg8<DP>::STAGES];
     uint64_t empty[Cfg8<DP>::STAGES];
     float scales[Cfg8<DP>::STAGES][2][STRIPS];
-    float m[CONSUMERS][ROWS];
-    float l[CONSUMERS][ROWS];
+    float m[CONSUMERS][ROWS8];
+    float l[CONSUMERS][ROWS8];
     int64_t scan[NUM_THREADS / 32];
     int64_t find_s;
     int64_t find_before;
     uint64_t ready, done;
-    float tm[ROWS], tl[ROWS];
+    float tm[ROWS8], tl[ROWS8];
     int32_t bad_lo[2], bad_hi[2];  // tiles in which NaN was cleared; two segments in turn
     int abort;
 };
@@ -109,17 +138,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     Plan plan;
     int64_t at_s, at_before;
     if (p.b.n_seqs <= 32) {
-        plan = plan_find_small(p, base, index, at_s, at_before);
+        plan = plan_find_small<ROWS8>(p, base, index, at_s, at_before);
         __syncthreads();  // the barriers are initialised
     } else {
-        plan = plan_find<NUM_THREADS>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+        plan = plan_find<NUM_THREADS, ROWS8>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
         at_s = sh->find_s;
         at_before = sh->find_before;
     }
     const int64_t f0 = index * plan.run;
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
-    Walk walk;
+    Walk<ROWS8> walk;
     walk.start(p, base, at_s, f0 - at_before);
     uint32_t it = 0;  // tiles through the ring
     // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
@@ -207,7 +236,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {  // ------------------------------------------------------ consumers
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int grp = warp >> 2, wq = warp & 3;
-        const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's rows qr, qr + 8 and first column
+        const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's row of scores and its first key of each 8
         int turn = 0;  // segments alternate
         uint32_t exchange_ph = 0;
         for (int64_t f = f0; f < f1; turn ^= 1) {
@@ -215,20 +244,18 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int32_t first, end;
             const int32_t n = tiles_of(g, f, first, end);
 
-            // The 16 query rows as fp16 A fragments, and each row's reach.  Of every 16 values a lane has four
-            // neighbours (those of the four codes that it gets of a key): the products' order of summation is free.
-            uint32_t qf[DP / 16][4];
-            float rf[2];  // what a row was divided by, times the scores' factor
-            int32_t row_lo[2], row_hi[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int r = qr + i * 8;
-                const bool live = r < g.n_rows;
-                const int32_t tok = p.by_group.quotient(g.r0 + r), hh = (g.r0 + r) - tok * p.group;
-                const int32_t pos = g.pos0 + tok;
-                row_hi[i] = live ? pos : -1;
-                row_lo[i] = first_seen(pos, p.window);
-                const uint16_t *src = p.q + (int64_t)(w_row(walk, tok)) * p.q_token_stride +
+            // The lane's query row in pieces, four neighbours of every 16 values, and the row's reach.
+            constexpr int KS = DP / 32;  // steps of the first product
+            constexpr bool THREE = std::is_same<E, Fp16>::value;
+            uint32_t qf[KS][4];  // as the instruction wants them: piece 0 and 1 of values 32 k .. + 15, then of the next 16
+            uint32_t qg[THREE ? KS : 1][2];  // piece 2
+            float rf;  // what the row was divided by, times the scores' factor
+            const bool live = qr < g.n_rows;
+            const int32_t q_tok = p.by_group.quotient(g.r0 + qr);
+            const int32_t row_hi = live ? g.pos0 + q_tok : -1, row_lo = first_seen(g.pos0 + q_tok, p.window);
+            {
+                const int32_t hh = (g.r0 + qr) - q_tok * p.group;
+                const uint16_t *src = p.q + (int64_t)(w_row(walk, q_tok)) * p.q_token_stride +
                                       (int64_t)(g.head * p.group + hh) * p.q_head_stride;
                 uint2 x[DP / 16];
 #pragma unroll
@@ -245,21 +272,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                const int k = row_exponent(most);
+                const int k = row_exponent<7>(most);
                 const float up = exp2i(k);
-                rf[i] = exp2i(-k) * p.scale_log2;
+                // a row with an infinity has no finite score; as codes it would have
+                rf = most < INFINITY ? exp2i(-k) * p.scale_log2 : NAN;
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
                     const float2 u = E::unpack(x[c].x), v = E::unpack(x[c].y);
-                    qf[c][i] = Fp16::pack(u.x * up, u.y * up);
-                    qf[c][2 + i] = Fp16::pack(v.x * up, v.y * up);
+                    float y[4] = {u.x * up, u.y * up, v.x * up, v.y * up};
+                    qf[c / 2][(c & 1) * 2] = take_codes(y);
+                    qf[c / 2][(c & 1) * 2 + 1] = take_codes(y);
+                    if (THREE) qg[c / 2][c & 1] = take_codes(y);
                 }
             }
 
-            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-            float o[DP / 8][4];
+            // m, l: this lane's row.  O^T: values 16 c + 2 qr (0, 1) and + 1 (2, 3) of rows qc (0, 2) and qc + 1.
+            float m = -INFINITY, l = 0.f;
+            float o[DP / 16][4];
 #pragma unroll
-            for (int i = 0; i < DP / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            for (int i = 0; i < DP / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            const auto of_row = [&](float x, int r) { return __shfl_sync(0xffffffffu, x, r * 4); };  // a row's number
 
             for (int32_t j = first; j < end; ++j, ++it) {
                 if ((int)(it & 1) != grp) continue;
@@ -297,91 +329,90 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         fence_proxy_async_smem();  // before the ring's next copy over it
                         __syncwarp();
                     }
-                    float s[KPW / 8][4];  // rows qr (0, 1) and qr + 8 (2, 3), keys 8 t + qc, + 1
+                    float s[KPW / 8][4];  // keys 8 t + qc, + 1: pieces 0 (0, 1) and 1 (2, 3)
+                    float s2[THREE ? KPW / 8 : 1][4];
 #pragma unroll
-                    for (int t = 0; t < KPW / 8; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                    for (int t = 0; t < KPW / 8; ++t) {
+                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+                        if (THREE) s2[t][0] = s2[t][1] = s2[t][2] = s2[t][3] = 0.f;
+                    }
                     {
                         const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
 #pragma unroll
-                        for (int c = 0; c < DP / 16; c += 2) {
+                        for (int k = 0; k < KS; ++k) {
 #pragma unroll
                             for (int b16 = 0; b16 < KPW / 16; ++b16) {
-                                uint32_t b[4];  // 8 keys x 16 codes: keys 0..7 and 8..15 of pieces c and c + 1
-                                ldmatrix_x4(b, kb + piece_at<DP>(b16 * 16 + key, c + half));
-                                Fp16::mma(s[2 * b16], qf[c], codes_lo(b[0]), codes_hi(b[0]));
-                                Fp16::mma(s[2 * b16 + 1], qf[c], codes_lo(b[2]), codes_hi(b[2]));
-                                Fp16::mma(s[2 * b16], qf[c + 1], codes_lo(b[1]), codes_hi(b[1]));
-                                Fp16::mma(s[2 * b16 + 1], qf[c + 1], codes_lo(b[3]), codes_hi(b[3]));
+                                uint32_t b[4];  // 8 keys x 16 codes: keys 0..7 and 8..15 of pieces 2 k and 2 k + 1
+                                ldmatrix_x4(b, kb + piece_at<DP>(b16 * 16 + key, 2 * k + half));
+                                mma_codes(s[2 * b16], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
+                                mma_codes(s[2 * b16 + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+                                if (THREE) {
+                                    mma_codes(s2[2 * b16], qg[k][0], 0u, qg[k][1], 0u, b[0], b[1]);
+                                    mma_codes(s2[2 * b16 + 1], qg[k][0], 0u, qg[k][1], 0u, b[2], b[3]);
+                                }
                             }
                         }
                     }
                     float rs[KPW / STRIP];  // 1 / value scale of a strip
+                    float mx = m;
 #pragma unroll
                     for (int b16 = 0; b16 < KPW / STRIP; ++b16) {
-                        const float ks = sh->scales[st][0][wq * (KPW / STRIP) + b16];
+                        const float f = rf * sh->scales[st][0][wq * (KPW / STRIP) + b16];
                         const float2 vs = value_scale(sh->scales[st][1][wq * (KPW / STRIP) + b16]);
                         rs[b16] = vs.y;
 #pragma unroll
                         for (int t = 2 * b16; t < 2 * b16 + 2; ++t)
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                s[t][c] = fmaf(s[t][c], rf[c >> 1] * ks, vs.x);
+                            for (int c = 0; c < 2; ++c) {
+                                float x = fmaf(s[t][2 + c], 0.0625f, s[t][c]);
+                                if (THREE) x = fmaf(s2[t][c], 0.00390625f, x);
+                                x = fmaf(x, f, vs.x);
                                 if (edge) {
-                                    const int32_t key = key0 + t * 8 + qc + (c & 1);
-                                    if (key > row_hi[c >> 1] || key < row_lo[c >> 1]) s[t][c] = -INFINITY;
+                                    const int32_t key = key0 + t * 8 + qc + c;
+                                    if (key > row_hi || key < row_lo) x = -INFINITY;
                                 }
+                                s[t][c] = x;
+                                mx = fmaxf(mx, x);
                             }
                     }
-                    float up[2], ref[2];
-                    bool same = true;
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    if (!__all_sync(0xffffffffu, mx == m)) {
+                        const float up = weight(m, mx);
+                        l *= up;
+                        m = mx;
+                        const float u0 = of_row(up, qc), u1 = of_row(up, qc + 1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(s[0][2 * i], s[0][2 * i + 1]);
-#pragma unroll
-                        for (int t = 1; t < KPW / 8; ++t) mx = fmaxf(mx, fmaxf(s[t][2 * i], s[t][2 * i + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        mx = fmaxf(mx, m[i]);
-                        up[i] = weight(m[i], mx);
-                        same = same && mx == m[i];
-                        m[i] = mx;
-                        ref[i] = mx - Fp16::LIFT;
-                    }
-                    if (!__all_sync(0xffffffffu, same)) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) l[i] *= up[i];
-#pragma unroll
-                        for (int i = 0; i < DP / 8; ++i) {
-                            o[i][0] *= up[0];
-                            o[i][1] *= up[0];
-                            o[i][2] *= up[1];
-                            o[i][3] *= up[1];
+                        for (int i = 0; i < DP / 16; ++i) {
+                            o[i][0] *= u0;
+                            o[i][1] *= u1;
+                            o[i][2] *= u0;
+                            o[i][3] *= u1;
                         }
                     }
+                    const float ref = m == -INFINITY ? 0.f : m - Fp16::LIFT;
 #pragma unroll
-                    for (int t = 0; t < KPW / 8; ++t)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            s[t][c] = weight(s[t][c], ref[c >> 1]);
-                            l[c >> 1] = fmaf(s[t][c], rs[t / (STRIP / 8)], l[c >> 1]);
-                        }
+                    for (int t = 0; t < KPW / 8; ++t) {
+                        s[t][0] = exp2_approx(s[t][0] - ref);
+                        s[t][1] = exp2_approx(s[t][1] - ref);
+                        l = fmaf(s[t][0] + s[t][1], rs[t / (STRIP / 8)], l);
+                    }
                     const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
                     for (int b16 = 0; b16 < KPW / 16; ++b16) {
                         // the weights rounded to fp16 (the matrix instruction takes 16-bit operands): at most 2^-11
-                        // of each, half a bf16 output's own rounding and as much as an fp16 one's
-                        const float(&u)[4] = s[2 * b16], (&v)[4] = s[2 * b16 + 1];
-                        const uint32_t pa[4] = {Fp16::pack(u[0], u[1]), Fp16::pack(u[2], u[3]), Fp16::pack(v[0], v[1]), Fp16::pack(v[2], v[3])};
+                        // of each, an eighth of a bf16 output's own rounding and as much as an fp16 one's
+                        const uint32_t p0 = Fp16::pack(s[2 * b16][0], s[2 * b16][1]), p1 = Fp16::pack(s[2 * b16 + 1][0], s[2 * b16 + 1][1]);
 #pragma unroll
                         for (int c = 0; c < DP / 16; c += 2) {
                             uint32_t b[4];  // pairs of values of keys 0..7 and 8..15, pieces c and c + 1
                             ldmatrix_x4_trans(b, kb + C::KV_BYTES + piece_at<DP>(b16 * 16 + key, c + (lane >> 4)));
 #pragma unroll
                             for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0, 0x3120);  // even values of two keys, then odd ones
-                            Fp16::mma(o[2 * c], pa, codes_lo(b[0]), codes_lo(b[1]));
-                            Fp16::mma(o[2 * c + 1], pa, codes_hi(b[0]), codes_hi(b[1]));
-                            Fp16::mma(o[2 * c + 2], pa, codes_lo(b[2]), codes_lo(b[3]));
-                            Fp16::mma(o[2 * c + 3], pa, codes_hi(b[2]), codes_hi(b[3]));
+                            const uint32_t v0[4] = {codes_lo(b[0]), codes_hi(b[0]), codes_lo(b[1]), codes_hi(b[1])};
+                            const uint32_t v1[4] = {codes_lo(b[2]), codes_hi(b[2]), codes_lo(b[3]), codes_hi(b[3])};
+                            Fp16::mma(o[c], v0, p0, p1);
+                            Fp16::mma(o[c + 1], v1, p0, p1);
                         }
                     }
                 }
@@ -390,43 +421,35 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
 
             // the eight warps' parts of the segment, joined in warp order; from here on m is what the weights refer to
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                m[i] -= Fp16::LIFT;
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-                if ((lane & 3) == 0) {
-                    sh->m[warp][qr + i * 8] = m[i];
-                    sh->l[warp][qr + i * 8] = l[i];
-                }
+            m -= Fp16::LIFT;
+            l += __shfl_xor_sync(0xffffffffu, l, 1);
+            l += __shfl_xor_sync(0xffffffffu, l, 2);
+            if ((lane & 3) == 0) {
+                sh->m[warp][qr] = m;
+                sh->l[warp][qr] = l;
             }
             consumers_sync();
             if (threadIdx.x == 0) {  // the segment before is done with its turn
                 sh->bad_lo[turn ^ 1] = INT32_MAX;
                 sh->bad_hi[turn ^ 1] = -1;
             }
-            float all[2], fac[2];
+            float all = sh->m[0][qr];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                all[i] = sh->m[0][qr + i * 8];
-#pragma unroll
-                for (int w = 1; w < CONSUMERS; ++w) all[i] = fmaxf(all[i], sh->m[w][qr + i * 8]);
-                fac[i] = weight(m[i], all[i]);
-            }
-            float *mine = join + wq * (ROWS * DP);
+            for (int w = 1; w < CONSUMERS; ++w) all = fmaxf(all, sh->m[w][qr]);
+            const float mine_fac = weight(m, all), fac[2] = {of_row(mine_fac, qc), of_row(mine_fac, qc + 1)};
+            float *mine = join + wq * (ROWS8 * DP);
 #pragma unroll
             for (int half = 1; half >= 0; --half) {
                 if (grp == half) {
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {  // four neighbours: even and odd values by turns
-                            float4 *at = reinterpret_cast<float4 *>(mine + join8_at<DP>(qr + i * 8, c * 16 + (lane & 3) * 4));
-                            const float(&x)[4] = o[2 * c], (&y)[4] = o[2 * c + 1];
-                            float4 v = make_float4(x[2 * i] * fac[i], y[2 * i] * fac[i], x[2 * i + 1] * fac[i], y[2 * i + 1] * fac[i]);
+                        for (int i = 0; i < 2; ++i) {
+                            float2 *at = reinterpret_cast<float2 *>(mine + join8_at<DP>(qc + i, c * 16 + qr * 2));
+                            float2 v = make_float2(o[c][i] * fac[i], o[c][2 + i] * fac[i]);
                             if (half == 0) {
-                                const float4 w = *at;
-                                v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+                                const float2 w = *at;
+                                v.x += w.x, v.y += w.y;
                             }
                             *at = v;
                         }
@@ -436,14 +459,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const bool whole = walk.j == 0 && n == walk.tiles;
             const int slot = (int)blockIdx.x * 2 + (f == f0 ? 0 : 1);
             // a thread takes 4 values of a row at a time
-            for (int e = threadIdx.x * 4; e < ROWS * DP; e += 32 * CONSUMERS * 4) {
+            for (int e = threadIdx.x * 4; e < ROWS8 * DP; e += 32 * CONSUMERS * 4) {
                 const int r = e / DP, c = e - r * DP;
                 if (r >= g.n_rows) continue;
                 const int at = join8_at<DP>(r, c);
                 float4 v = *reinterpret_cast<const float4 *>(join + at);
 #pragma unroll
                 for (int w = 1; w < 4; ++w) {
-                    const float4 t = *reinterpret_cast<const float4 *>(join + w * (ROWS * DP) + at);
+                    const float4 t = *reinterpret_cast<const float4 *>(join + w * (ROWS8 * DP) + at);
                     v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
                 }
                 if (sh->bad_hi[turn] >= 0 && c < p.head_dim) {
@@ -458,7 +481,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     continue;
                 }
                 if (!whole) {
-                    *reinterpret_cast<float4 *>(p.part_o + (int64_t)slot * (ROWS * DP) + e) = v;
+                    *reinterpret_cast<float4 *>(p.part_o + (int64_t)slot * (ROWS8 * DP) + e) = v;
                     continue;
                 }
                 float mm, ll;
@@ -473,8 +496,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     sh->tm[r] = mm;
                     sh->tl[r] = ll;
                 } else if (!whole) {
-                    p.part_ml[slot * (2 * ROWS) + r] = mm;
-                    p.part_ml[slot * (2 * ROWS) + ROWS + r] = ll;
+                    p.part_ml[slot * (2 * ROWS8) + r] = mm;
+                    p.part_ml[slot * (2 * ROWS8) + ROWS8 + r] = ll;
                 } else if (p.lse) {
                     write_lse(p, walk, g, r, mm, ll);
                 }
@@ -483,7 +506,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 consumers_sync();
                 if (threadIdx.x < p.cluster) arrive_at(&sh->ready, threadIdx.x);
                 const bool ok = mbar_wait_cluster(&sh->ready, exchange_ph, abort);
-                const int share = ROWS * DP / p.cluster;
+                const int share = ROWS8 * DP / p.cluster;
                 for (int e = rank * share + threadIdx.x * 4; ok && e < (rank + 1) * share; e += 32 * CONSUMERS * 4) {
                     const int r = e / DP, c = e - r * DP;
                     if (r >= g.n_rows) continue;

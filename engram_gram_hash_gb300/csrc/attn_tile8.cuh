@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
         };
         const auto hand_q = [&] {
             asm volatile("cp.async.wait_all;" ::: "memory");
-            if (std::is_same<E, Bf16>::value) {  // this thread's row as fp16, times a power of two
+            if (std::is_same<E, Bf16>::value) {  // this thread's row as fp16: exact but for values below 2^-28 of its largest
                 __syncwarp();  // the warp's lanes have copied each other's rows
                 const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
                 const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) most = max3(most, fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k])));
                 }
-                const int e = row_exponent(most);
+                const int e = row_exponent<14>(most);
                 const float up = exp2i(e);
                 rf = exp2i(-e);
 #pragma unroll 4

@@ -92,18 +92,18 @@ static Scales scales_of(const engram_kv_cache_q8 *c) {
 }
 
 static size_t rows8_part_o_bytes(const engram_attn_config *cfg) {
-    return up256((size_t)num_sms() * 2 * rows::ROWS * padded_dim(cfg) * sizeof(float));
+    return up256((size_t)num_sms() * 2 * rows::ROWS8 * padded_dim(cfg) * sizeof(float));
 }
 static size_t rows8_workspace_bytes(const engram_attn_config *cfg) {
-    return rows8_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS * sizeof(float));
+    return rows8_part_o_bytes(cfg) + up256((size_t)num_sms() * 2 * 2 * rows::ROWS8 * sizeof(float));
 }
 
 // Segments of the rows kernel (row tile x kv head) at most, and the tiles of 128 keys that the block table has
 // room for (in a window's reach).
 static int64_t rows8_segs_most(const engram_attn_config *cfg, const engram_kv_batch *batch) {
     const int64_t group = cfg->n_heads / cfg->n_kv_heads, seqs = std::min(batch->n_seqs, batch->n_query);
-    return cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS - 1) / rows::ROWS),
-                                      (batch->n_query * group + (rows::ROWS - 1) * seqs) / rows::ROWS);
+    return cfg->n_kv_heads * std::min(batch->n_query * ((group + rows::ROWS8 - 1) / rows::ROWS8),
+                                      (batch->n_query * group + (rows::ROWS8 - 1) * seqs) / rows::ROWS8);
 }
 static int64_t rows8_tiles_most(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
     return (keys_most(cfg, cache, batch) + rows::KT8 - 1) / rows::KT8;
@@ -175,7 +175,7 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     if (s != ENGRAM_OK) return s;
     s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows8_kernel", km, vm, a);
     if (s != ENGRAM_OK || !shares.cut()) return s;
-    return launch_after(rows::rows_join_kernel<E, DP>, dim3(p.runs - 1, rows::ROWS / 4), 128, 0, 1, st, "rows_join_kernel", p);
+    return launch_after(rows::rows_join_kernel<E, DP, rows::ROWS8>, dim3(p.runs - 1, rows::ROWS8 / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
 // Row blocks x kv heads of a batch at most, and the slots for partial results, as for the 16-bit cache.
@@ -205,7 +205,7 @@ static bool use_tiles8(const engram_attn_config *cfg, const engram_kv_cache_q8 *
     const double sms = num_sms();
     const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
     const double mean = (double)rows / (double)seqs, parts = (double)seqs * cfg->n_kv_heads;
-    const double segs = parts * ceil(mean / rows::ROWS), items = parts * ceil(mean / tile::ROWS);
+    const double segs = parts * ceil(mean / rows::ROWS8), items = parts * ceil(mean / tile::ROWS);
     const double seg_us = 2.5 + 1.0 * (double)rows8_tiles_most(cfg, cache, batch);
     const double item_us = 3.7 + 1.6 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
     const double rows_us = std::min(9.0 + segs * seg_us / sms, 3.5 + ceil(segs / sms) * seg_us);
