@@ -95,6 +95,7 @@ struct Params8 {
     Params r;  // values: unused
     Scales scales;
     CodePages codes;
+    Divisor by_page;
 };
 
 template <typename E, int DP>
@@ -171,38 +172,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (warp < CONSUMERS + 2) {  // ---------------------- producers: one warp loads K, the next V
             const bool is_v = warp == CONSUMERS + 1;
             const CUtensorMap *const map = is_v ? &v_map : &k_map;
-            const int boxes = KT / p.box;
+            const int box_log2 = 31 - __clz(p.box), boxes = KT >> box_log2;  // the box divides 128
             const uint32_t box_bytes = (uint32_t)p.box * DP;
             const float *const scales = is_v ? p8.scales.v : p8.scales.k;
             for (int64_t f = f0; f < f1;) {
                 const Segment g = segment(p, walk);
                 int32_t first, end;
                 const int32_t n = tiles_of(g, f, first, end);
-                int64_t window0 = -1;  // first box whose page lane 0 holds
+                // keys in 32 bits without sign: the boxes looked up ahead may lie past 2^31
+                int32_t window0 = -1;  // first box whose page lane 0 holds
                 int32_t page = -1;
                 for (int32_t j = first; j < end; ++j, ++it) {
-                    const int32_t tile = g.tile0 + j;
-                    const int64_t b0 = (int64_t)tile * boxes;
+                    const int32_t tile = g.tile0 + j, b0 = tile * boxes;
                     if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
                         window0 = b0;
-                        const int64_t key = (b0 + lane) * p.box;
+                        const uint32_t ahead = (uint32_t)(b0 + lane) * p.box;
                         page = -1;
-                        if (key < g.hi) {
-                            page = __ldg(p.b.block_table + walk.s * p.b.table_stride + key / p.b.page_size);
+                        if (ahead < (uint32_t)g.hi) {
+                            page = __ldg(p.b.block_table + walk.s * p.b.table_stride + p8.by_page.quotient((int32_t)ahead));
                             if (page < 0 || page >= p.b.n_pages) {
-                                if (key + p.box > g.lo) raise_error(ENGRAM_ERANGE);
+                                if (ahead + p.box > (uint32_t)g.lo) raise_error(ENGRAM_ERANGE);
                                 page = -1;  // out of range: the copy fills zeros
                             }
                         }
                     }
-                    const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
-                    const int64_t key = (b0 + lane) * p.box;
-                    const bool load = lane < boxes && key < g.hi && key + p.box > g.lo;
+                    const int32_t mine = __shfl_sync(0xffffffffu, page, (b0 - window0) + (lane < boxes ? lane : 0));
+                    const uint32_t key = (uint32_t)(b0 + lane) * p.box;
+                    const bool load = lane < boxes && key < (uint32_t)g.hi && key + p.box > (uint32_t)g.lo;
                     const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
                     // this lane's strip of keys, whose scale it copies
-                    const int32_t strip_page = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane & (STRIPS - 1)) * STRIP / p.box);
-                    const int64_t strip = (int64_t)tile * KT + lane * STRIP;
-                    const bool has_scale = strip < g.hi && strip + STRIP > g.lo && strip_page >= 0;
+                    const int32_t strip_page = __shfl_sync(0xffffffffu, page, (b0 - window0) + (((lane & (STRIPS - 1)) * STRIP) >> box_log2));
+                    const uint32_t strip = (uint32_t)tile * KT + lane * STRIP;
+                    const bool has_scale = strip < (uint32_t)g.hi && strip + STRIP > (uint32_t)g.lo && strip_page >= 0;
                     const int st = it % C::STAGES;
                     bool ok = true;
                     if (lane == 0) {
@@ -212,13 +213,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     ok = __shfl_sync(0xffffffffu, ok, 0);
                     if (ok && load) {
                         uint8_t *dst = smem + st * C::STAGE_BYTES + (is_v ? C::KV_BYTES : 0) + lane * p.box * DP;
-                        const int y = (int)(key % p.b.page_size);
+                        const int y = load ? (int)key - p8.by_page.quotient((int32_t)key) * p.b.page_size : 0;
                         tma_load_4d(dst, map, &sh->full[st], 0, y, g.head, mine);
                     }
                     if (ok && lane < STRIPS) {
-                        const int32_t block = (int32_t)(strip % p.b.page_size) >> p8.scales.block_log2;
+                        const int32_t at = (int32_t)strip - p8.by_page.quotient((int32_t)strip) * p.b.page_size;
                         copy4_async(smem_u32(&sh->scales[st][is_v][lane]),
-                                    scales + (has_scale ? ((int64_t)strip_page * p.n_kv_heads + g.head) * p8.scales.per_page + block : 0),
+                                    scales + (has_scale ? ((int64_t)strip_page * p.n_kv_heads + g.head) * p8.scales.per_page + (at >> p8.scales.block_log2) : 0),
                                     has_scale);
                         arrive_when_copied(&sh->full[st]);
                     }

@@ -78,6 +78,7 @@ struct Params8 {
     Params t;  // values: unused
     Scales scales;
     CodePages codes;
+    Divisor by_page;
 };
 
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
@@ -574,7 +575,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 }
             }
         } else if (warp == 9) {  // --------------------------------------- K, V loads
-            const int boxes = KT / p.box;
+            const int box_log2 = 31 - __clz(p.box), boxes = KT >> box_log2;  // the box divides 128
             const uint32_t box_bytes = (uint32_t)p.box * DP;
             uint32_t it = 0;
             bool ok = true;
@@ -587,33 +588,34 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 } w = {item->s, item->head, item->key0, item->n, item->lo, item->hi};
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
-                int64_t window0 = -1;
+                // keys in 32 bits without sign: the boxes looked up ahead may lie past 2^31
+                int32_t window0 = -1;
                 int32_t page = -1;
                 for (int32_t j = 0; ok && j < w.n; ++j) {
-                    const int64_t b0 = w.key0 / p.box + (int64_t)j * boxes;
+                    const int32_t b0 = (w.key0 >> box_log2) + j * boxes;
                     if (window0 < 0 || b0 + boxes > window0 + 32) {  // the pages of the next 32 boxes, a lane each
                         window0 = b0;
-                        const int64_t key = (b0 + lane) * p.box;
+                        const uint32_t ahead = (uint32_t)(b0 + lane) << box_log2;
                         page = -1;
-                        if (key < w.hi) {
-                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + (uint32_t)key / (uint32_t)p.b.page_size);
+                        if (ahead < (uint32_t)w.hi) {
+                            page = __ldg(p.b.block_table + w.s * p.b.table_stride + p8.by_page.quotient((int32_t)ahead));
                             if (page < 0 || page >= p.b.n_pages) {
-                                if (key + p.box > w.lo) raise_error(ENGRAM_ERANGE);
+                                if (ahead + p.box > (uint32_t)w.lo) raise_error(ENGRAM_ERANGE);
                                 page = -1;  // out of range: the copy fills zeros
                             }
                         }
                     }
-                    const int32_t mine = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + (lane < boxes ? lane : 0));
-                    const int64_t key = (b0 + lane) * p.box;
-                    const bool load = lane < boxes && key < w.hi && key + p.box > w.lo;
+                    const int32_t mine = __shfl_sync(0xffffffffu, page, (b0 - window0) + (lane < boxes ? lane : 0));
+                    const uint32_t key = (uint32_t)(b0 + lane) << box_log2;
+                    const bool load = lane < boxes && key < (uint32_t)w.hi && key + p.box > (uint32_t)w.lo;
                     const uint32_t loads = __popc(__ballot_sync(0xffffffffu, load));
-                    const int y = (int)((uint32_t)key % (uint32_t)p.b.page_size);
+                    const int y = load ? (int)key - p8.by_page.quotient((int32_t)key) * p.b.page_size : 0;
                     // lanes 0..7 copy the strips' key scales, 8..15 their value scales
                     const int sl = lane & (STRIPS - 1);
-                    const int32_t strip_page = __shfl_sync(0xffffffffu, page, (int)(b0 - window0) + sl * STRIP / p.box);
-                    const int64_t strip = b0 * p.box + sl * STRIP;
-                    const bool has_scale = strip < w.hi && strip + STRIP > w.lo && strip_page >= 0;
-                    const int32_t block = (int32_t)((uint32_t)strip % (uint32_t)p.b.page_size) >> p8.scales.block_log2;
+                    const int32_t strip_page = __shfl_sync(0xffffffffu, page, (b0 - window0) + ((sl * STRIP) >> box_log2));
+                    const uint32_t strip = ((uint32_t)b0 << box_log2) + sl * STRIP;
+                    const bool has_scale = strip < (uint32_t)w.hi && strip + STRIP > (uint32_t)w.lo && strip_page >= 0;
+                    const int32_t block = ((int32_t)strip - p8.by_page.quotient((int32_t)strip) * p.b.page_size) >> p8.scales.block_log2;
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv, ++it) {
                         const int st = it % C::RAW_STAGES;

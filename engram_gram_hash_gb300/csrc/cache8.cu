@@ -82,7 +82,7 @@ static bool page_map8(CUtensorMap *m, const engram_attn_config *cfg, const engra
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : padded_dim(cfg) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 static Scales scales_of(const engram_kv_cache_q8 *c) {
@@ -165,6 +165,7 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     p.runs = shares.runs;
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     a.scales = scales_of(cache);
+    a.by_page = Divisor(cache->page_size);
     a.codes = CodePages{static_cast<const uint8_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
     CUtensorMap km, vm;
     if (!page_map8(&km, cfg, cache, cache->k, p.box, true) || !page_map8(&vm, cfg, cache, cache->v, p.box, true)) return ENGRAM_ECUDA;
@@ -246,6 +247,7 @@ static engram_status tile8_launch(const engram_attn_config *cfg, const engram_kv
                                                      tile8_workspace_bytes(cfg, cache, batch) - 256);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     a.scales = scales_of(cache);
+    a.by_page = Divisor(cache->page_size);
     a.codes = CodePages{static_cast<const uint8_t *>(cache->v), cache->page_stride, cache->token_stride, cache->head_stride};
     CUtensorMap km, vm;
     if (!page_map8(&km, cfg, cache, cache->k, p.box, false) || !page_map8(&vm, cfg, cache, cache->v, p.box, false))
