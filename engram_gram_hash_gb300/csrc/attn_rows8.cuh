@@ -3,22 +3,22 @@
 // of codes, 8 rows a segment.
 //
 // Bound: the bytes of the codes, half the 16-bit cache's, if a tile costs the
-// warps few enough instructions.  So the codes of K are not converted: the
-// queries are split into two (bf16) or three (fp16) e4m3 pieces, each the
-// rounding of what the ones before leave times 16, and multiplied by mma.sync
-// m16n8k32 on e4m3; the first two pieces of 8 rows are the 16 rows of one
-// instruction, and a score is s0 + s1 / 16 (+ s2 / 256).  Two pieces hold the 8
-// bits of bf16, three the 11 of fp16 exactly, in a row whose largest value is
-// brought to 2^7 .. 2^8; values far below it are off by at most 2^-21 of it
-// (2^-25 with three).  Weights want more range than two pieces
-// have (a long tail beside a large key), so the second product is on fp16, as
-// O^T = V^T P^T: 16 values x 8 rows an instruction, the pairs of weights where
-// the scores' accumulators left them.  Codes of V become fp16 pairs on their way
-// from shared memory (a byte permutation and two conversions for four).
+// warps few enough instructions: the conversion of the codes is most of them.
+// Both products therefore have the cache as the matrix instruction's first
+// operand (mma.sync m16n8k16 on fp16), S^T = K Q^T and O^T = V^T P^T, whose 16 rows
+// are all keys or values, and the 8 query rows as the second: 8 rows instead of
+// 16 in the accumulators of the softmax, and no row of an instruction is empty.
+// (mma.sync on e4m3 itself is no way around it: it took as long as two fp16
+// ones and the conversions of both operands.)  Between the products the
+// weights change from keys by lanes to rows by lanes, 8 x 8 at a time, by
+// movmatrix.  Queries are exact in fp16: a row is multiplied by the power of two
+// that brings its largest value to 2^14 .. 2^15 (below 2^-28 of it values lose
+// bits).
 // A warp has a quarter of a tile (128 keys, 32 KB of K and V at 128 values) and
-// every value's order within the products is free, so a lane's codes are
-// neighbours in memory.  The strips' scales travel with their tile: 4-byte
-// asynchronous copies that the tile's barrier counts.
+// every value's order within the products is free, so a lane's four codes are
+// neighbours in memory: two conversions for them, and for V, whose pairs lie
+// across keys, a byte permutation.  The strips' scales travel with their tile:
+// 4-byte asynchronous copies that the tile's barrier counts.
 #pragma once
 
 namespace engram {
@@ -50,24 +50,11 @@ __device__ __forceinline__ uint32_t piece_at(int key, int ch) {
 template <int DP>
 __device__ __forceinline__ int join8_at(int r, int c) { return r * DP + (c ^ (((r >> 1) & 3) * 8)); }
 
-// d += A B with e4m3 operands, 16 rows x 32 values x 8 keys.
-__device__ __forceinline__ void mma_codes(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Four values as codes; x becomes 16 times what they leave (NaN and infinities leave NaN).
-__device__ __forceinline__ uint32_t take_codes(float (&x)[4]) {
-    const uint32_t c = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
-                       (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3) << 16;
-    const float2 lo = e4m3x2_to_float2((uint16_t)c), hi = e4m3x2_to_float2((uint16_t)(c >> 16));
-    x[0] = (x[0] - lo.x) * 16.f;
-    x[1] = (x[1] - lo.y) * 16.f;
-    x[2] = (x[2] - hi.x) * 16.f;
-    x[3] = (x[3] - hi.y) * 16.f;
-    return c;
+// An 8 x 8 matrix of 16-bit values, two neighbours of row lane / 4 a lane: transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 template <int DP>
@@ -237,7 +224,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {  // ------------------------------------------------------ consumers
         asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int grp = warp >> 2, wq = warp & 3;
-        const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's row of scores and its first key of each 8
+        const int qr = lane >> 2, qc = (lane & 3) * 2;  // this lane's key of each 8; the rows qc and qc + 1 are its own
         int turn = 0;  // segments alternate
         uint32_t exchange_ph = 0;
         for (int64_t f = f0; f < f1; turn ^= 1) {
@@ -245,24 +232,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             int32_t first, end;
             const int32_t n = tiles_of(g, f, first, end);
 
-            // The lane's query row in pieces, four neighbours of every 16 values, and the row's reach.
-            constexpr int KS = DP / 32;  // steps of the first product
-            constexpr bool THREE = std::is_same<E, Fp16>::value;
-            uint32_t qf[KS][4];  // as the instruction wants them: piece 0 and 1 of values 32 k .. + 15, then of the next 16
-            uint32_t qg[THREE ? KS : 1][2];  // piece 2
-            float rf;  // what the row was divided by, times the scores' factor
-            const bool live = qr < g.n_rows;
-            const int32_t q_tok = p.by_group.quotient(g.r0 + qr);
-            const int32_t row_hi = live ? g.pos0 + q_tok : -1, row_lo = first_seen(g.pos0 + q_tok, p.window);
+            // Query row qr in fp16, of every 16 values the four neighbours that the lane gets of a key.
+            uint32_t qf[DP / 16][2];
+            // The lane's own rows: what they were divided by, times the scores' factor, and their reach.
+            float rf[2];
+            int32_t row_lo[2], row_hi[2];
             {
-                const int32_t hh = (g.r0 + qr) - q_tok * p.group;
-                const uint16_t *src = p.q + (int64_t)(w_row(walk, q_tok)) * p.q_token_stride +
+                const int32_t tok = p.by_group.quotient(g.r0 + qr), hh = (g.r0 + qr) - tok * p.group;
+                const uint16_t *src = p.q + (int64_t)(w_row(walk, tok)) * p.q_token_stride +
                                       (int64_t)(g.head * p.group + hh) * p.q_head_stride;
                 uint2 x[DP / 16];
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
                     const int at = c * 16 + (lane & 3) * 4;
-                    x[c] = live && at < p.head_dim ? __ldg(reinterpret_cast<const uint2 *>(src + at)) : make_uint2(0, 0);
+                    x[c] = qr < g.n_rows && at < p.head_dim ? __ldg(reinterpret_cast<const uint2 *>(src + at)) : make_uint2(0, 0);
                 }
                 float most = 0.f;
 #pragma unroll
@@ -273,26 +256,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                const int k = row_exponent<7>(most);
+                const int k = row_exponent<14>(most);
                 const float up = exp2i(k);
-                // a row with an infinity has no finite score; as codes it would have
-                rf = most < INFINITY ? exp2i(-k) * p.scale_log2 : NAN;
 #pragma unroll
                 for (int c = 0; c < DP / 16; ++c) {
                     const float2 u = E::unpack(x[c].x), v = E::unpack(x[c].y);
-                    float y[4] = {u.x * up, u.y * up, v.x * up, v.y * up};
-                    qf[c / 2][(c & 1) * 2] = take_codes(y);
-                    qf[c / 2][(c & 1) * 2 + 1] = take_codes(y);
-                    if (THREE) qg[c / 2][c & 1] = take_codes(y);
+                    qf[c][0] = Fp16::pack(u.x * up, u.y * up);
+                    qf[c][1] = Fp16::pack(v.x * up, v.y * up);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    rf[i] = exp2i(-__shfl_sync(0xffffffffu, k, (qc + i) * 4)) * p.scale_log2;
+                    const int32_t pos = g.pos0 + p.by_group.quotient(g.r0 + qc + i);
+                    row_hi[i] = qc + i < g.n_rows ? pos : -1;
+                    row_lo[i] = first_seen(pos, p.window);
                 }
             }
 
-            // m, l: this lane's row.  O^T: values 16 c + 2 qr (0, 1) and + 1 (2, 3) of rows qc (0, 2) and qc + 1.
-            float m = -INFINITY, l = 0.f;
+            // m, l: of the lane's rows (l its own keys').  O^T: values 16 c + 2 qr (0, 1) and + 1 (2, 3) of these rows.
+            float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
             float o[DP / 16][4];
 #pragma unroll
             for (int i = 0; i < DP / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            const auto of_row = [&](float x, int r) { return __shfl_sync(0xffffffffu, x, r * 4); };  // a row's number
 
             for (int32_t j = first; j < end; ++j, ++it) {
                 if ((int)(it & 1) != grp) continue;
@@ -330,84 +315,74 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         fence_proxy_async_smem();  // before the ring's next copy over it
                         __syncwarp();
                     }
-                    float s[KPW / 8][4];  // keys 8 t + qc, + 1: pieces 0 (0, 1) and 1 (2, 3)
-                    float s2[THREE ? KPW / 8 : 1][4];
+                    float s[KPW / 16][4];  // keys 16 t + qr (0, 1) and + 8 (2, 3) of rows qc (0, 2) and qc + 1
 #pragma unroll
-                    for (int t = 0; t < KPW / 8; ++t) {
-                        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-                        if (THREE) s2[t][0] = s2[t][1] = s2[t][2] = s2[t][3] = 0.f;
-                    }
+                    for (int t = 0; t < KPW / 16; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
                     {
                         const int key = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
 #pragma unroll
-                        for (int k = 0; k < KS; ++k) {
+                        for (int c = 0; c < DP / 16; c += 2) {
 #pragma unroll
-                            for (int b16 = 0; b16 < KPW / 16; ++b16) {
-                                uint32_t b[4];  // 8 keys x 16 codes: keys 0..7 and 8..15 of pieces 2 k and 2 k + 1
-                                ldmatrix_x4(b, kb + piece_at<DP>(b16 * 16 + key, 2 * k + half));
-                                mma_codes(s[2 * b16], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-                                mma_codes(s[2 * b16 + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
-                                if (THREE) {
-                                    mma_codes(s2[2 * b16], qg[k][0], 0u, qg[k][1], 0u, b[0], b[1]);
-                                    mma_codes(s2[2 * b16 + 1], qg[k][0], 0u, qg[k][1], 0u, b[2], b[3]);
-                                }
+                            for (int t = 0; t < KPW / 16; ++t) {
+                                uint32_t b[4];  // 8 keys x 16 codes: keys 0..7 and 8..15 of pieces c and c + 1
+                                ldmatrix_x4(b, kb + piece_at<DP>(t * 16 + key, c + half));
+                                const uint32_t k0[4] = {codes_lo(b[0]), codes_lo(b[2]), codes_hi(b[0]), codes_hi(b[2])};
+                                const uint32_t k1[4] = {codes_lo(b[1]), codes_lo(b[3]), codes_hi(b[1]), codes_hi(b[3])};
+                                Fp16::mma(s[t], k0, qf[c][0], qf[c][1]);
+                                Fp16::mma(s[t], k1, qf[c + 1][0], qf[c + 1][1]);
                             }
                         }
                     }
                     float rs[KPW / STRIP];  // 1 / value scale of a strip
-                    float mx = m;
+                    float mx[2] = {m[0], m[1]};
 #pragma unroll
-                    for (int b16 = 0; b16 < KPW / STRIP; ++b16) {
-                        const float f = rf * sh->scales[st][0][wq * (KPW / STRIP) + b16];
-                        const float2 vs = value_scale(sh->scales[st][1][wq * (KPW / STRIP) + b16]);
-                        rs[b16] = vs.y;
+                    for (int t = 0; t < KPW / STRIP; ++t) {
+                        const float ks = sh->scales[st][0][wq * (KPW / STRIP) + t];
+                        const float2 vs = value_scale(sh->scales[st][1][wq * (KPW / STRIP) + t]);
+                        rs[t] = vs.y;
+                        const float f[2] = {rf[0] * ks, rf[1] * ks};
 #pragma unroll
-                        for (int t = 2 * b16; t < 2 * b16 + 2; ++t)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                float x = fmaf(s[t][2 + c], 0.0625f, s[t][c]);
-                                if (THREE) x = fmaf(s2[t][c], 0.00390625f, x);
-                                x = fmaf(x, f, vs.x);
-                                if (edge) {
-                                    const int32_t key = key0 + t * 8 + qc + c;
-                                    if (key > row_hi || key < row_lo) x = -INFINITY;
-                                }
-                                s[t][c] = x;
-                                mx = fmaxf(mx, x);
+                        for (int c = 0; c < 4; ++c) {
+                            s[t][c] = fmaf(s[t][c], f[c & 1], vs.x);
+                            if (edge) {
+                                const int32_t key = key0 + t * 16 + (c >> 1) * 8 + qr;
+                                if (key > row_hi[c & 1] || key < row_lo[c & 1]) s[t][c] = -INFINITY;
                             }
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    if (!__all_sync(0xffffffffu, mx == m)) {
-                        const float up = weight(m, mx);
-                        l *= up;
-                        m = mx;
-                        const float u0 = of_row(up, qc), u1 = of_row(up, qc + 1);
-#pragma unroll
-                        for (int i = 0; i < DP / 16; ++i) {
-                            o[i][0] *= u0;
-                            o[i][1] *= u1;
-                            o[i][2] *= u0;
-                            o[i][3] *= u1;
+                            mx[c & 1] = fmaxf(mx[c & 1], s[t][c]);
                         }
                     }
-                    const float ref = m == -INFINITY ? 0.f : m - Fp16::LIFT;
 #pragma unroll
-                    for (int t = 0; t < KPW / 8; ++t) {
-                        s[t][0] = exp2_approx(s[t][0] - ref);
-                        s[t][1] = exp2_approx(s[t][1] - ref);
-                        l = fmaf(s[t][0] + s[t][1], rs[t / (STRIP / 8)], l);
+                    for (int w = 4; w < 32; w *= 2) {
+                        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], w));
+                        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], w));
                     }
+                    if (!__all_sync(0xffffffffu, mx[0] == m[0] && mx[1] == m[1])) {
+                        const float up[2] = {weight(m[0], mx[0]), weight(m[1], mx[1])};
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            l[i] *= up[i];
+                            m[i] = mx[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < DP / 16; ++i)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[i][c] *= up[c & 1];
+                    }
+                    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - Fp16::LIFT, m[1] == -INFINITY ? 0.f : m[1] - Fp16::LIFT};
                     const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
-                    for (int b16 = 0; b16 < KPW / 16; ++b16) {
+                    for (int t = 0; t < KPW / 16; ++t) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) s[t][c] = exp2_approx(s[t][c] - ref[c & 1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) l[i] = fmaf(s[t][i] + s[t][2 + i], rs[t], l[i]);
                         // the weights rounded to fp16 (the matrix instruction takes 16-bit operands): at most 2^-11
                         // of each, an eighth of a bf16 output's own rounding and as much as an fp16 one's
-                        const uint32_t p0 = Fp16::pack(s[2 * b16][0], s[2 * b16][1]), p1 = Fp16::pack(s[2 * b16 + 1][0], s[2 * b16 + 1][1]);
+                        const uint32_t p0 = transpose8(Fp16::pack(s[t][0], s[t][1])), p1 = transpose8(Fp16::pack(s[t][2], s[t][3]));
 #pragma unroll
                         for (int c = 0; c < DP / 16; c += 2) {
                             uint32_t b[4];  // pairs of values of keys 0..7 and 8..15, pieces c and c + 1
-                            ldmatrix_x4_trans(b, kb + C::KV_BYTES + piece_at<DP>(b16 * 16 + key, c + (lane >> 4)));
+                            ldmatrix_x4_trans(b, kb + C::KV_BYTES + piece_at<DP>(t * 16 + key, c + (lane >> 4)));
 #pragma unroll
                             for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0, 0x3120);  // even values of two keys, then odd ones
                             const uint32_t v0[4] = {codes_lo(b[0]), codes_hi(b[0]), codes_lo(b[1]), codes_hi(b[1])};
@@ -422,22 +397,29 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
 
             // the eight warps' parts of the segment, joined in warp order; from here on m is what the weights refer to
-            m -= Fp16::LIFT;
-            l += __shfl_xor_sync(0xffffffffu, l, 1);
-            l += __shfl_xor_sync(0xffffffffu, l, 2);
-            if ((lane & 3) == 0) {
-                sh->m[warp][qr] = m;
-                sh->l[warp][qr] = l;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[i] -= Fp16::LIFT;
+#pragma unroll
+                for (int w = 4; w < 32; w *= 2) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+                if (qr == 0) {
+                    sh->m[warp][qc + i] = m[i];
+                    sh->l[warp][qc + i] = l[i];
+                }
             }
             consumers_sync();
             if (threadIdx.x == 0) {  // the segment before is done with its turn
                 sh->bad_lo[turn ^ 1] = INT32_MAX;
                 sh->bad_hi[turn ^ 1] = -1;
             }
-            float all = sh->m[0][qr];
+            float fac[2];
 #pragma unroll
-            for (int w = 1; w < CONSUMERS; ++w) all = fmaxf(all, sh->m[w][qr]);
-            const float mine_fac = weight(m, all), fac[2] = {of_row(mine_fac, qc), of_row(mine_fac, qc + 1)};
+            for (int i = 0; i < 2; ++i) {
+                float all = sh->m[0][qc + i];
+#pragma unroll
+                for (int w = 1; w < CONSUMERS; ++w) all = fmaxf(all, sh->m[w][qc + i]);
+                fac[i] = weight(m[i], all);
+            }
             float *mine = join + wq * (ROWS8 * DP);
 #pragma unroll
             for (int half = 1; half >= 0; --half) {

@@ -3,9 +3,8 @@
 The plan is whole numbers, in Python lists.  The append rounds values that are given in 16 bits: its codes are the
 nearest ones, found from the grid's steps in 64 bits, so they have to be equal.  Bounds of the attention, with u the
 half step of the output's type (bf16 2^-8, fp16 2^-11):
- * A score is a D-term fp32 sum times one factor; q is exact in e4m3 pieces of 4 bits each but for values far below
-   the row's largest, which the last piece's subnormal step (two pieces: 2^-9 / 16 where the largest is at least 2^7) puts
-   off by at most 2^-21 of that: |ds| <= (D + 4) 2^-23 scale sum|q k| + 2^-21 scale max|q| sum|k|.
+ * A score is a D-term fp32 sum times one factor; q is exact in fp16 but for values below 2^-28 of the row's largest
+   (off by at most 2^-39 of that): |ds| <= (D + 4) 2^-23 scale sum|q k| + 2^-39 scale max|q| sum|k|.
  * The exponent u_j = log2(e) s_j + log2 vs_j is rounded (2^-24 of its size), log2 vs_j is off by 2^-22 and 2^-24 of its
    size, and exp2 and its argument add 2^-21 + 2^-22 times the row's largest |u_j - R|.  With e the sum of these, a weight is off
    by 1 +- 2e, a normalised one by 4e.
@@ -144,7 +143,7 @@ def attention(q, k_pages, v_pages, k_scales, v_scales, block_table, new, total, 
                     R = torch.where(any_key, uj.amax(1), zero)
                     spread = torch.where(ok, (uj - R[:, None]).abs().clamp(max=127.0), 0.0).amax(1)
                     size = torch.where(ok, uj.abs(), 0.0).amax(1)
-                    e = ((D + 4) * 2.0**-23 * mag + 2.0**-21 * scale * x.abs().amax(1) * k.abs().sum(1).amax()
+                    e = ((D + 4) * 2.0**-23 * mag + 2.0**-39 * scale * x.abs().amax(1) * k.abs().sum(1).amax()
                          + 2.0**-21 + spread * 2.0**-22 + size * 2.0**-24 + 2.0**-22 + lv.abs().amax() * 2.0**-24)
                     out[t0:t0 + a, h] = o
                     lse[t0:t0 + a, h] = torch.where(any_key, m + torch.log(safe), zero - math.inf)
