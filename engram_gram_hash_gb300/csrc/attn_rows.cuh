@@ -306,15 +306,16 @@ __device__ __forceinline__ int64_t w_row(const Walk<R> &w, int32_t token) { retu
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS) : "memory"); }
 // (m, l) in base 2 -> ln sum; -inf where nothing was seen
 __device__ __forceinline__ float lse_of(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f; }
-// A row's maximum and sum over the eight warps, in warp order.
+// A row's maximum and sum over the consumer warps, in warp order.
 template <typename S>
 __device__ __forceinline__ void row_total(const S *sh, int r, float &m, float &l) {
+    constexpr int WARPS = sizeof(sh->m) / sizeof(sh->m[0]);
     m = sh->m[0][r];
 #pragma unroll
-    for (int w = 1; w < CONSUMERS; ++w) m = fmaxf(m, sh->m[w][r]);
+    for (int w = 1; w < WARPS; ++w) m = fmaxf(m, sh->m[w][r]);
     l = 0.f;
 #pragma unroll
-    for (int w = 0; w < CONSUMERS; ++w) l += sh->l[w][r] * weight(sh->m[w][r], m);
+    for (int w = 0; w < WARPS; ++w) l += sh->l[w][r] * weight(sh->m[w][r], m);
 }
 
 // One arrival on this barrier's counterpart in CTA `rank` of the cluster,

@@ -26,6 +26,9 @@ namespace attn {
 namespace rows {
 
 constexpr int ROWS8 = 8;               // query rows per segment
+constexpr int GROUPS = 2;              // groups of four consumer warps, which take tiles in turn
+constexpr int CONSUMERS8 = 4 * GROUPS;
+constexpr int NUM_THREADS8 = 32 * (CONSUMERS8 + 4);
 constexpr int KT8 = 128;               // keys per tile
 constexpr int STRIPS = KT8 / STRIP;    // scales of a tile
 
@@ -36,7 +39,7 @@ struct Cfg8 {
     static constexpr int KV_BYTES = KT * DP;    // K (or V) of a tile
     static constexpr int STAGE_BYTES = 2 * KV_BYTES;
     static constexpr int STAGES = 196608 / STAGE_BYTES;
-    static_assert(STAGES % 2 == 0, "each ring stage must belong to one consumer group");
+    static_assert(STAGES % GROUPS == 0, "each ring stage must belong to one consumer group");
     static constexpr int JOIN_FLOATS = 4 * ROWS8 * DP;
 };
 
@@ -62,9 +65,9 @@ struct Shared8 {
     uint64_t full[Cfg8<DP>::STAGES];
     uint64_t empty[Cfg8<DP>::STAGES];
     float scales[Cfg8<DP>::STAGES][2][STRIPS];
-    float m[CONSUMERS][ROWS8];
-    float l[CONSUMERS][ROWS8];
-    int64_t scan[NUM_THREADS / 32];
+    float m[CONSUMERS8][ROWS8];
+    float l[CONSUMERS8][ROWS8];
+    int64_t scan[NUM_THREADS8 / 32];
     int64_t find_s;
     int64_t find_before;
     uint64_t ready, done;
@@ -72,6 +75,8 @@ struct Shared8 {
     int32_t bad_lo[2], bad_hi[2];  // tiles in which NaN was cleared; two segments in turn
     int abort;
 };
+__device__ __forceinline__ void consumers8_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * CONSUMERS8) : "memory"); }
+
 template <int DP>
 constexpr int smem8_bytes() {
     return Cfg8<DP>::STAGES * Cfg8<DP>::STAGE_BYTES + Cfg8<DP>::JOIN_FLOATS * 4 + (int)sizeof(Shared8<DP>);
@@ -86,7 +91,7 @@ struct Params8 {
 };
 
 template <typename E, int DP>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS8, 1)
     rows8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ Params8 p8) {
     const Params &p = p8.r;
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         plan = plan_find_small<ROWS8>(p, base, index, at_s, at_before);
         __syncthreads();  // the barriers are initialised
     } else {
-        plan = plan_find<NUM_THREADS, ROWS8>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
+        plan = plan_find<NUM_THREADS8, ROWS8>(p, base, index, sh->scan, &sh->find_s, &sh->find_before);
         at_s = sh->find_s;
         at_before = sh->find_before;
     }
@@ -152,12 +157,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         return n;
     };
 
-    // Registers move to the consumers, which hold 16 rows' queries and outputs: 256 x 192 + 128 x 120 =
-    // the launch's 384 x 168.
-    if (warp >= CONSUMERS) {
+    // Registers move to the consumers: 256 x 192 + 128 x 120 = the launch's 384 x 168.
+    if (warp >= CONSUMERS8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-        if (warp < CONSUMERS + 2) {  // ---------------------- producers: one warp loads K, the next V
-            const bool is_v = warp == CONSUMERS + 1;
+        if (warp < CONSUMERS8 + 2) {  // ---------------------- producers: one warp loads K, the next V
+            const bool is_v = warp == CONSUMERS8 + 1;
             const CUtensorMap *const map = is_v ? &v_map : &k_map;
             const int box_log2 = 31 - __clz(p.box), boxes = KT >> box_log2;  // the box divides 128
             const uint32_t box_bytes = (uint32_t)p.box * DP;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < DP / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
             for (int32_t j = first; j < end; ++j, ++it) {
-                if ((int)(it & 1) != grp) continue;
+                if ((int)(it % GROUPS) != grp) continue;
                 const int st = it % C::STAGES;
                 const bool ok = warp_wait(&sh->full[st], (it / C::STAGES) & 1, abort);
                 const int32_t key0 = (g.tile0 + j) * KT + wq * KPW;
@@ -333,17 +337,33 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             }
                         }
                     }
+                    // The tile's values and scales into registers, and its stage back to the ring before the softmax: what
+                    // is in flight decides the rate.
+                    uint32_t vr[KPW / 16][DP / 32][4];  // pairs of values of keys 0..7 and 8..15, pieces 2 c and 2 c + 1
+                    const int vkey = (((lane >> 3) & 1) << 3) + (lane & 7);
+#pragma unroll
+                    for (int t = 0; t < KPW / 16; ++t)
+#pragma unroll
+                        for (int c = 0; c < DP / 32; ++c)
+                            ldmatrix_x4_trans(vr[t][c], kb + C::KV_BYTES + piece_at<DP>(t * 16 + vkey, 2 * c + (lane >> 4)));
+                    float ks[KPW / STRIP], vs[KPW / STRIP];
+#pragma unroll
+                    for (int t = 0; t < KPW / STRIP; ++t) {
+                        ks[t] = sh->scales[st][0][wq * (KPW / STRIP) + t];
+                        vs[t] = sh->scales[st][1][wq * (KPW / STRIP) + t];
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->empty[st]);
                     float rs[KPW / STRIP];  // 1 / value scale of a strip
                     float mx[2] = {m[0], m[1]};
 #pragma unroll
                     for (int t = 0; t < KPW / STRIP; ++t) {
-                        const float ks = sh->scales[st][0][wq * (KPW / STRIP) + t];
-                        const float2 vs = value_scale(sh->scales[st][1][wq * (KPW / STRIP) + t]);
-                        rs[t] = vs.y;
-                        const float f[2] = {rf[0] * ks, rf[1] * ks};
+                        const float2 v = value_scale(vs[t]);
+                        rs[t] = v.y;
+                        const float f[2] = {rf[0] * ks[t], rf[1] * ks[t]};
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            s[t][c] = fmaf(s[t][c], f[c & 1], vs.x);
+                            s[t][c] = fmaf(s[t][c], f[c & 1], v.x);
                             if (edge) {
                                 const int32_t key = key0 + t * 16 + (c >> 1) * 8 + qr;
                                 if (key > row_hi[c & 1] || key < row_lo[c & 1]) s[t][c] = -INFINITY;
@@ -369,7 +389,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             for (int c = 0; c < 4; ++c) o[i][c] *= up[c & 1];
                     }
                     const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0] - Fp16::LIFT, m[1] == -INFINITY ? 0.f : m[1] - Fp16::LIFT};
-                    const int key = (((lane >> 3) & 1) << 3) + (lane & 7);
 #pragma unroll
                     for (int t = 0; t < KPW / 16; ++t) {
 #pragma unroll
@@ -381,8 +400,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                         const uint32_t p0 = transpose8(Fp16::pack(s[t][0], s[t][1])), p1 = transpose8(Fp16::pack(s[t][2], s[t][3]));
 #pragma unroll
                         for (int c = 0; c < DP / 16; c += 2) {
-                            uint32_t b[4];  // pairs of values of keys 0..7 and 8..15, pieces c and c + 1
-                            ldmatrix_x4_trans(b, kb + C::KV_BYTES + piece_at<DP>(t * 16 + key, c + (lane >> 4)));
+                            uint32_t(&b)[4] = vr[t][c / 2];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i], 0, 0x3120);  // even values of two keys, then odd ones
                             const uint32_t v0[4] = {codes_lo(b[0]), codes_hi(b[0]), codes_lo(b[1]), codes_hi(b[1])};
@@ -391,12 +409,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                             Fp16::mma(o[c + 1], v1, p0, p1);
                         }
                     }
+                } else if (lane == 0) {
+                    mbar_arrive(&sh->empty[st]);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->empty[st]);
             }
 
-            // the eight warps' parts of the segment, joined in warp order; from here on m is what the weights refer to
+            // the warps' parts of the segment, joined in warp order; from here on m is what the weights refer to
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[i] -= Fp16::LIFT;
@@ -407,7 +425,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     sh->l[warp][qc + i] = l[i];
                 }
             }
-            consumers_sync();
+            consumers8_sync();
             if (threadIdx.x == 0) {  // the segment before is done with its turn
                 sh->bad_lo[turn ^ 1] = INT32_MAX;
                 sh->bad_hi[turn ^ 1] = -1;
@@ -417,32 +435,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 float all = sh->m[0][qc + i];
 #pragma unroll
-                for (int w = 1; w < CONSUMERS; ++w) all = fmaxf(all, sh->m[w][qc + i]);
+                for (int w = 1; w < CONSUMERS8; ++w) all = fmaxf(all, sh->m[w][qc + i]);
                 fac[i] = weight(m[i], all);
             }
             float *mine = join + wq * (ROWS8 * DP);
 #pragma unroll
-            for (int half = 1; half >= 0; --half) {
-                if (grp == half) {
+            for (int turns = GROUPS - 1; turns >= 0; --turns) {  // the last group's first
+                if (grp == turns) {
 #pragma unroll
                     for (int c = 0; c < DP / 16; ++c)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float2 *at = reinterpret_cast<float2 *>(mine + join8_at<DP>(qc + i, c * 16 + qr * 2));
                             float2 v = make_float2(o[c][i] * fac[i], o[c][2 + i] * fac[i]);
-                            if (half == 0) {
+                            if (turns != GROUPS - 1) {
                                 const float2 w = *at;
                                 v.x += w.x, v.y += w.y;
                             }
                             *at = v;
                         }
                 }
-                consumers_sync();
+                consumers8_sync();
             }
             const bool whole = walk.j == 0 && n == walk.tiles;
             const int slot = (int)blockIdx.x * 2 + (f == f0 ? 0 : 1);
             // a thread takes 4 values of a row at a time
-            for (int e = threadIdx.x * 4; e < ROWS8 * DP; e += 32 * CONSUMERS * 4) {
+            for (int e = threadIdx.x * 4; e < ROWS8 * DP; e += 32 * CONSUMERS8 * 4) {
                 const int r = e / DP, c = e - r * DP;
                 if (r >= g.n_rows) continue;
                 const int at = join8_at<DP>(r, c);
@@ -486,11 +504,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 }
             }
             if (p.cluster > 1) {  // each CTA joins its share of the values from all shares of the keys, in rank order
-                consumers_sync();
+                consumers8_sync();
                 if (threadIdx.x < p.cluster) arrive_at(&sh->ready, threadIdx.x);
                 const bool ok = mbar_wait_cluster(&sh->ready, exchange_ph, abort);
                 const int share = ROWS8 * DP / p.cluster;
-                for (int e = rank * share + threadIdx.x * 4; ok && e < (rank + 1) * share; e += 32 * CONSUMERS * 4) {
+                for (int e = rank * share + threadIdx.x * 4; ok && e < (rank + 1) * share; e += 32 * CONSUMERS8 * 4) {
                     const int r = e / DP, c = e - r * DP;
                     if (r >= g.n_rows) continue;
                     float mk[MAX_CLUSTER], lk[MAX_CLUSTER], mm = -INFINITY, ll = 0.f;
@@ -521,13 +539,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                     if (p.lse && c == 0) write_lse(p, walk, g, r, mm, ll);
                 }
                 if (f + n < f1) {  // (more segments than clusters only with offsets that overlap)
-                    consumers_sync();
+                    consumers8_sync();
                     if (threadIdx.x < p.cluster) arrive_at(&sh->done, threadIdx.x);
                     mbar_wait_cluster(&sh->done, exchange_ph, abort);  // nobody reads this CTA's memory any more
                 }
                 exchange_ph ^= 1;
             }
-            consumers_sync();  // the join's memory is free again
+            consumers8_sync();  // the join's memory is free again
             f += n;
             if (f < f1) walk.next(p, base);
         }

@@ -174,7 +174,7 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     const auto kern = rows::rows8_kernel<E, DP>;
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
-    s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS, smem, p.cluster, st, "rows8_kernel", km, vm, a);
+    s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS8, smem, p.cluster, st, "rows8_kernel", km, vm, a);
     if (s != ENGRAM_OK || !shares.cut()) return s;
     return launch_after(rows::rows_join_kernel<E, DP, rows::ROWS8>, dim3(p.runs - 1, rows::ROWS8 / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
