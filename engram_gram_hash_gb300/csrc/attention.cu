@@ -135,6 +135,8 @@ static engram_status rows_launch(const engram_attn_config *cfg, const engram_kv_
     p.group = cfg->n_heads / cfg->n_kv_heads;
     p.by_group = Divisor(p.group);
     p.by_heads = Divisor(cfg->n_kv_heads);
+    p.side = 1;
+    p.line_heads = cfg->n_kv_heads;
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.kt_log2 = rows::Cfg<DP>::KT_LOG2;

@@ -91,11 +91,14 @@ struct Params {
     float *part_o;      // [grid][2][rows of a segment][DP]
     float *part_ml;     // [grid][2][2][rows of a segment]
     int32_t n_heads, n_kv_heads, group, head_dim;
-    Divisor by_group, by_heads;  // the query heads of a kv head; the kv heads
+    // The kv heads lie on `side` lines beside each other (head h on line h % side), each cut at the same places: CTAs
+    // on different lines then read the same pages at about the same time.
+    int32_t side, line_heads;    // side * line_heads = n_kv_heads
+    Divisor by_group, by_heads;  // the query heads of a kv head; a line's heads
     int32_t window;
     int32_t kt_log2;    // Cfg<DP>::KT_LOG2
     int32_t box;        // tokens per TMA box: gcd(page_size, KT)
-    int32_t runs;       // CTAs of the attention launch
+    int32_t runs;       // CTAs of a line (all CTAs of the attention launch: times side, times cluster)
     int32_t cluster;    // CTAs that share a segment through distributed shared memory (1: none; then whole = 1)
     int32_t whole;      // > 0: every segment is given this many tiles and none is cut (no join follows)
     float scale_log2;   // scale * log2(e)
@@ -146,7 +149,7 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
     int64_t sum = 0;
     for (int64_t s = s0; s < s1; ++s) {
         const Seq q = load_seq(p.b, s, base);
-        sum += (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
+        sum += (int64_t)seg_rows<R>(p, q) * p.line_heads * seg_tiles<R>(p, q);
     }
     int64_t incl = sum;
 #pragma unroll
@@ -171,7 +174,7 @@ __device__ Plan plan_find(const Params &p, int64_t base, int64_t index, int64_t 
         int64_t at = before;
         for (int64_t s = s0; s < s1; ++s) {
             const Seq q = load_seq(p.b, s, base);
-            const int64_t c = (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
+            const int64_t c = (int64_t)seg_rows<R>(p, q) * p.line_heads * seg_tiles<R>(p, q);
             if (f < at + c) {
                 *sh_s = s;
                 *sh_before = at;
@@ -192,7 +195,7 @@ __device__ __forceinline__ Plan plan_find_small(const Params &p, int64_t base, i
     int64_t cost = 0;
     if (lane < p.b.n_seqs) {
         const Seq q = load_seq(p.b, lane, base);
-        cost = (int64_t)seg_rows<R>(p, q) * p.n_kv_heads * seg_tiles<R>(p, q);
+        cost = (int64_t)seg_rows<R>(p, q) * p.line_heads * seg_tiles<R>(p, q);
     }
     int64_t incl = cost;
 #pragma unroll
@@ -214,7 +217,8 @@ __device__ __forceinline__ Plan plan_find_small(const Params &p, int64_t base, i
 template <int R>
 struct Walk {
     int64_t s;       // sequence
-    int32_t seg;     // segment within the sequence: row tile * n_kv_heads + kv head
+    int32_t line;    // the line: heads line, line + side, ...
+    int32_t seg;     // segment within the sequence: row tile * line_heads + head of the line
     int32_t n_segs;  // (n_query * n_heads < 2^31)
     int32_t tiles;   // tiles per segment of this sequence
     int32_t j;       // tile within the segment
@@ -224,9 +228,10 @@ struct Walk {
         s = s_;
         q = load_seq(p.b, s, base);
         tiles = seg_tiles<R>(p, q);
-        n_segs = seg_rows<R>(p, q) * p.n_kv_heads;
+        n_segs = seg_rows<R>(p, q) * p.line_heads;
     }
-    __device__ __forceinline__ void start(const Params &p, int64_t base, int64_t s_, int64_t offset) {
+    __device__ __forceinline__ void start(const Params &p, int64_t base, int64_t s_, int64_t offset, int32_t line_) {
+        line = line_;
         enter(p, base, s_);
         seg = (int32_t)(offset < INT32_MAX ? (int32_t)offset / tiles : offset / tiles);
         j = (int32_t)(offset - (int64_t)seg * tiles);
@@ -258,7 +263,7 @@ template <int R>
 __device__ __forceinline__ Segment segment(const Params &p, const Walk<R> &w) {
     Segment g;
     const int32_t block = p.by_heads.quotient(w.seg);
-    g.head = w.seg - block * p.n_kv_heads;
+    g.head = (w.seg - block * p.line_heads) * p.side + w.line;
     g.r0 = block * R;
     const int32_t left = w.q.q_len * p.group - g.r0;
     g.n_rows = left < R ? left : R;
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
     Walk<ROWS> walk;
-    walk.start(p, base, at_s, f0 - at_before);
+    walk.start(p, base, at_s, f0 - at_before, 0);
     uint32_t it = 0;  // tiles through the ring
     // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
     const auto tiles_of = [&](const Segment &g, int64_t f, int32_t &first, int32_t &end) -> int32_t {
@@ -772,7 +777,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 // Adds up the parts of the segments that the line's cuts went through.  Block
-// x looks at the cut between CTAs x and x + 1 and acts on it if it is the
+// x looks at a cut of a line and acts on it if it is the
 // first inside its segment; a warp takes one row, its lanes 4 values each.
 template <typename E, int DP, int R>
 __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ Params p) {
@@ -780,7 +785,8 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     // The plan reads the batch only, which was final before the attention kernel let this one start
     // (it does so after its own wait); the partial results need the wait below.
     const int64_t base = __ldg(p.b.offs);
-    const int64_t cut = (int64_t)blockIdx.x + 1;
+    const int32_t line = blockIdx.x % p.side;
+    const int64_t cut = (int64_t)(blockIdx.x / p.side) + 1;
     Plan plan;
     int64_t at_s, at_before;
     if (p.b.n_seqs <= 32) {
@@ -795,7 +801,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     const int64_t f = cut * plan.run;
     if (f >= plan.total) return;
     Walk<R> w;
-    w.start(p, base, at_s, f - at_before);
+    w.start(p, base, at_s, f - at_before, line);
     const int64_t first = f - w.j;  // the segment's first tile on the line
     if (w.j == 0 || (cut - 1) * plan.run > first) return;
     const Segment g = segment(p, w);
@@ -803,8 +809,8 @@ __global__ void __launch_bounds__(128) rows_join_kernel(const __grid_constant__ 
     if (r >= g.n_rows) return;
     const int64_t end = first + w.tiles;
     const int parts = (int)((end - 1) / plan.run - (cut - 1)) + 1;
-    const int64_t slot0 = (cut - 1) * 2 + ((cut - 1) * plan.run == first ? 0 : 1);
-    const auto slot_of = [&](int k) { return k == 0 ? slot0 : (cut - 1 + k) * 2; };
+    const int after = (cut - 1) * plan.run == first ? 0 : 1;  // the first part's slot of its CTA
+    const auto slot_of = [&](int k) { return ((cut - 1 + k) * p.side + line) * 2 + (k == 0 ? after : 0); };
 
     float m = -INFINITY;
     for (int k = lane; k < parts; k += 32) m = fmaxf(m, __ldcg(p.part_ml + slot_of(k) * (2 * R) + r));

@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
     const int64_t base = __ldg(p.b.offs);
     if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.b.offs + p.b.n_seqs) - base != p.b.n_query)
         raise_error(ENGRAM_ERANGE);
-    const int64_t index = blockIdx.x / p.cluster;
+    const int32_t line = blockIdx.x / p.cluster % p.side;
+    const int64_t index = blockIdx.x / p.cluster / p.side;
     const int rank = p.cluster > 1 ? (int)cluster_ctarank() : 0;
     Plan plan;
     int64_t at_s, at_before;
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
     const int64_t f1 = f0 + plan.run < plan.total ? f0 + plan.run : plan.total;
     if (f0 >= f1) return;
     Walk<ROWS8> walk;
-    walk.start(p, base, at_s, f0 - at_before);
+    walk.start(p, base, at_s, f0 - at_before, line);
     uint32_t it = 0;  // tiles through the ring
     // This CTA's tiles [first, end) of a segment, and the places on the line that it covers.
     const auto tiles_of = [&](const Segment &g, int64_t f, int32_t &first, int32_t &end) -> int32_t {

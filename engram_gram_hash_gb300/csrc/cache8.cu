@@ -111,14 +111,22 @@ static int64_t rows8_tiles_most(const engram_attn_config *cfg, const engram_kv_c
 
 // How a segment's tiles are shared out, as for the 16-bit cache: clusters of CTAs for few segments and short
 // tables, whole segments where a cut cannot pay, else equal runs of tiles for every SM and the join.
+// Cut, the heads lie side by side (as many as divide them and leave hardly an SM out): the CTAs that share a page
+// read it at the same time, which DRAM likes better than 128 bytes of every 1,024.
 struct Rows8Shares {
-    int32_t cluster, whole, runs;
+    int32_t cluster, whole, runs, side;
     bool cut() const { return whole == 0 && runs > 1; }
 };
+static int32_t heads_aside(int n_kv_heads, int sms) {
+    int32_t side = 1;
+    for (int d = 2; d <= n_kv_heads && d <= 16; ++d)
+        if (n_kv_heads % d == 0 && sms / d * d * 32 >= sms * 31) side = d;
+    return side;
+}
 static Rows8Shares rows8_shares(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
     const int64_t tiles = rows8_tiles_most(cfg, cache, batch), segs = rows8_segs_most(cfg, batch);
     const int sms = num_sms();
-    Rows8Shares p = {1, 0, sms};
+    Rows8Shares p = {1, 0, sms, 1};
     if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
         p.cluster = 8;
     } else if (tiles > 2 && tiles <= (segs >= 24 ? 64 : 32) && segs * 4 <= sms - 8) {
@@ -129,6 +137,10 @@ static Rows8Shares rows8_shares(const engram_attn_config *cfg, const engram_kv_c
     if (p.cluster > 1) {
         p.whole = 1;
         p.runs = (int32_t)segs;
+    }
+    if (p.whole == 0) {
+        p.side = heads_aside(cfg->n_kv_heads, sms);
+        p.runs = sms / p.side;
     }
     return p;
 }
@@ -154,7 +166,6 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     p.n_kv_heads = cfg->n_kv_heads;
     p.group = cfg->n_heads / cfg->n_kv_heads;
     p.by_group = Divisor(p.group);
-    p.by_heads = Divisor(cfg->n_kv_heads);
     p.head_dim = cfg->head_dim;
     p.window = cfg->window;
     p.kt_log2 = rows::Cfg8<DP>::KT_LOG2;
@@ -163,6 +174,9 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     p.cluster = shares.cluster;
     p.whole = shares.whole;
     p.runs = shares.runs;
+    p.side = shares.side;
+    p.line_heads = cfg->n_kv_heads / shares.side;
+    p.by_heads = Divisor(p.line_heads);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     a.scales = scales_of(cache);
     a.by_page = Divisor(cache->page_size);
@@ -174,9 +188,9 @@ static engram_status rows8_launch(const engram_attn_config *cfg, const engram_kv
     const auto kern = rows::rows8_kernel<E, DP>;
     engram_status s = ensure_smem((const void *)kern, smem, attr_done);
     if (s != ENGRAM_OK) return s;
-    s = launch_after(kern, dim3(p.runs * p.cluster), rows::NUM_THREADS8, smem, p.cluster, st, "rows8_kernel", km, vm, a);
+    s = launch_after(kern, dim3(p.runs * p.side * p.cluster), rows::NUM_THREADS8, smem, p.cluster, st, "rows8_kernel", km, vm, a);
     if (s != ENGRAM_OK || !shares.cut()) return s;
-    return launch_after(rows::rows_join_kernel<E, DP, rows::ROWS8>, dim3(p.runs - 1, rows::ROWS8 / 4), 128, 0, 1, st, "rows_join_kernel", p);
+    return launch_after(rows::rows_join_kernel<E, DP, rows::ROWS8>, dim3((p.runs - 1) * p.side, rows::ROWS8 / 4), 128, 0, 1, st, "rows_join_kernel", p);
 }
 
 // Row blocks x kv heads of a batch at most, and the slots for partial results, as for the 16-bit cache.
