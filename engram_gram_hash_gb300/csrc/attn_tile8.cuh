@@ -30,16 +30,15 @@ namespace tile {
 constexpr int NUM_THREADS8 = 512;
 constexpr int CONVERTERS = 4;
 constexpr int STRIPS = KT / STRIP;  // scales of a tile
-// Tiles whose factors are kept.  A slot is written again only when the values of the tile two later have been
-// used by both row tiles, so by then both have read it.
-constexpr int FACTORS = 4;
-
 template <int DP>
 struct Cfg8 : Cfg<DP> {
-    static constexpr int STAGES = DP == 128 ? 3 : 6;
     static constexpr int RAW_BYTES = KT * DP;  // codes of K or V of a tile
     static constexpr int RAW_STAGES = DP == 128 ? 2 : 4;
     static_assert(RAW_STAGES % 2 == 0, "keys and values by turns");
+    // Tiles whose factors are kept.  Tile f's are written when the ring has room for its keys: the values up to tile
+    // f - (STAGES + 2) / 2 have then been used by both row tiles, so their softmaxes are done with the factors.
+    static constexpr int FACTORS = DP == 128 ? 4 : 8;
+    static_assert(FACTORS >= (Cfg<DP>::STAGES + 2) / 2, "factors' ring");
 };
 
 template <int DP>
@@ -48,7 +47,7 @@ struct Shared8 {
     uint64_t kv_empty[Cfg8<DP>::STAGES];
     uint64_t raw_full[Cfg8<DP>::RAW_STAGES];
     uint64_t raw_empty[Cfg8<DP>::RAW_STAGES];
-    uint64_t fac_full[FACTORS];
+    uint64_t fac_full[Cfg8<DP>::FACTORS];
     uint64_t q_full[2];
     uint64_t s_full[2];
     uint64_t p_ready[2][P_PARTS];
@@ -59,7 +58,7 @@ struct Shared8 {
     uint64_t drained[2];
     uint64_t item_full[ITEMS];
     uint64_t item_empty[ITEMS];
-    float4 fac[FACTORS][STRIPS];  // of a strip: the scores' factor, log2 of the value scale, its inverse
+    float4 fac[Cfg8<DP>::FACTORS][STRIPS];  // of a strip: the scores' factor, log2 of the value scale, its inverse
     float scales[Cfg8<DP>::RAW_STAGES / 2][2][STRIPS];
     Item items[ITEMS];
     uint32_t tmem_base;
@@ -70,7 +69,7 @@ struct Shared8 {
 template <int DP>
 constexpr int smem8_bytes() {
     return 2 * Cfg8<DP>::Q_BYTES + Cfg8<DP>::STAGES * Cfg8<DP>::STAGE_BYTES + Cfg8<DP>::RAW_STAGES * Cfg8<DP>::RAW_BYTES +
-           Cfg8<DP>::SWAP_BYTES + (int)sizeof(Shared8<DP>);
+           (int)sizeof(Shared8<DP>);
 }
 static_assert(smem8_bytes<128>() <= 232448 && smem8_bytes<64>() <= 232448, "tile kernel shared memory over the per-CTA limit");
 
@@ -86,6 +85,17 @@ __device__ __forceinline__ uint2 lds8(uint32_t addr) {
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
+// 32 bytes to global memory, as one piece (32-byte aligned) or two.
+__device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                     "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<uint4 *>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
 // A strip's factor for a row.  Not 0 (a key scale may be): a hidden score, -inf, must stay that.
 __device__ __forceinline__ float factor(float strip, float row) { return fmaxf(strip * row, 7.5231638452626401e-37f); }
 
@@ -95,13 +105,13 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 const __grid_constant__ Params8 p8) {
     using C = Cfg8<DP>;
     using H = Fp16;  // of the products
+    constexpr int FACTORS = C::FACTORS;
     const Params &p = p8.t;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_smem = smem;
     uint8_t *kv_smem = smem + 2 * C::Q_BYTES;
     uint8_t *raw_smem = kv_smem + C::STAGES * C::STAGE_BYTES;
-    uint8_t *swap_smem = raw_smem + C::RAW_STAGES * C::RAW_BYTES;
-    Shared8<DP> *sh = reinterpret_cast<Shared8<DP> *>(swap_smem + C::SWAP_BYTES);
+    Shared8<DP> *sh = reinterpret_cast<Shared8<DP> *>(raw_smem + C::RAW_STAGES * C::RAW_BYTES);
     volatile int *abort = &sh->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
@@ -379,13 +389,8 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 const int32_t rr = w->r0 + t * MT + row, tok = p.by_group.quotient(rr), head = w->head * p.group + rr - tok * p.group;
                 const int64_t out_row = (int64_t)w->q.row0 + tok;
                 const float inv = whole ? inverse(l, w->pos0 + tok) : 1.f;
-                // A lane has a row in TMEM, but lanes that store to 32 rows at once cost an access to L1 each:
-                // the rows change hands in shared memory, 128 bytes of each at a time (the pieces permuted,
-                // so neither way meets a bank twice), and eight lanes store a row's piece.
-                const uint32_t swap = smem_u32(swap_smem) + warp * (32 * 128);
                 const int64_t dst = out_row * p.out_token_stride + (int64_t)head * p.out_head_stride;
-                float *part = p.part_o + (slot * ROWS + t * MT + row - lane) * DP;
-                const int32_t warp_rows = w->n_rows - (t * MT + row - lane);  // this warp's rows of the item
+                float *part = p.part_o + (slot * ROWS + t * MT + row) * DP;
                 const auto read_o = [&](int c, uint32_t (&o)[32]) {  // 32 columns of this lane's row
                     if (n > 0) {
                         tmem_ld_32x32b_x32(o_tm + c, o);
@@ -405,31 +410,23 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
                     }
                 };
-                const auto put = [&](int i, const uint32_t *v) {
-                    sts16(swap + lane * 128 + (((i ^ lane) & 7) << 4), make_uint4(v[0], v[1], v[2], v[3]));
-                };
-                const auto get = [&](int r) { return lds16(swap + r * 128 + (((lane ^ r) & 7) << 4)); };
+                // A lane stores its row's values itself, 32 bytes at a time where the rows begin on such a boundary: the
+                // ring takes the memory through which the 16-bit kernel's rows change hands.
                 if (whole) {
+                    const bool wide = ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)(p.out_token_stride * 2) |
+                                        (uintptr_t)(p.out_head_stride * 2)) & 31) == 0;
 #pragma unroll 1
-                    for (int c = 0; c < DP; c += 64) {
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            uint32_t o[32], u[16];
-                            read_o(c + half * 32, o);
+                    for (int c = 0; c < DP; c += 32) {
+                        uint32_t o[32];
+                        read_o(c, o);
 #pragma unroll
-                            for (int h = 0; h < 16; ++h)
-                                u[h] = E::pack(__uint_as_float(o[2 * h]) * inv, __uint_as_float(o[2 * h + 1]) * inv);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t u[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) put(half * 4 + i, u + 4 * i);
+                            for (int i = 0; i < 8; ++i)
+                                u[i] = E::pack(__uint_as_float(o[h * 16 + 2 * i]) * inv, __uint_as_float(o[h * 16 + 2 * i + 1]) * inv);
+                            if (live && c + h * 16 < p.head_dim) store32(p.out + dst + c + h * 16, u, wide);  // head_dim % 16 == 0
                         }
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = k * 4 + (lane >> 3), at = c + (lane & 7) * 8;
-                            const int64_t to = __shfl_sync(0xffffffffu, dst, r);
-                            if (r < warp_rows && at < p.head_dim) *reinterpret_cast<uint4 *>(p.out + to + at) = get(r);
-                        }
-                        __syncwarp();
                     }
                 } else if (n > 0) {
 #pragma unroll 1
@@ -437,14 +434,8 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                         uint32_t o[32];
                         read_o(c, o);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) put(i, o + 4 * i);
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int r = k * 4 + (lane >> 3);
-                            if (r < warp_rows) *reinterpret_cast<uint4 *>(part + r * DP + c + (lane & 7) * 4) = get(r);
-                        }
-                        __syncwarp();
+                        for (int i = 0; i < 4; ++i)
+                            if (live) store32(part + c + i * 8, o + i * 8, true);
                     }
                 }
                 tc_fence_before();  // O has been read before the next item's first product is allowed
@@ -747,12 +738,12 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                     p_ph ^= 1;
                     if (leader) {
                         if (C::APART) mma_commit(&sh->pv_done[t]);
+                        mma_commit(&sh->kv_empty[v]);  // before the scores: the keys after next wait for it
                         if (!more)
                             mma_commit(&sh->o_full[t]);
                         else if (!C::APART)
                             scores();
                         if (!C::APART && both) mbar_arrive(&sh->turn[t ^ 1]);
-                        mma_commit(&sh->kv_empty[v]);
                     }
                     if (more) advance();
                 }
