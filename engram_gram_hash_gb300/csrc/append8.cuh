@@ -32,6 +32,8 @@ struct Append8 {
     int64_t page_stride, slot_stride, head_stride;
     int64_t units;               // blocks of tokens that the batch can touch
     int32_t n_kv, block, per_page;
+    int32_t kv_blocks;           // CTAs for keys and values; those for the queries follow
+    int32_t q_groups;            // warps' shares of a token's query heads
 };
 
 // The unbiased exponent of the least power of two >= x, cut to -48 .. 48; -48 unless x > 0.
@@ -79,31 +81,34 @@ __device__ __forceinline__ uint32_t nan_for_inf(uint32_t w) {
     return w;
 }
 
-template <typename E, int LPH, bool INTERLEAVED>
-__global__ void __launch_bounds__(32 * MAX_BLOCK / TOKENS_PER_WARP) append8_kernel(const __grid_constant__ Append8 a) {
+template <typename E, int LPH, bool INTERLEAVED, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) append8_kernel(const __grid_constant__ Append8 a) {
     constexpr int GPW = 32 / LPH, N = TOKENS_PER_WARP;
-    __shared__ uint32_t most[MAX_BLOCK / N][GPW];
+    __shared__ uint32_t most[THREADS / 32][GPW];
     grid_dependency_wait();
     allow_dependent_launch();
     const HeadParams &p = a.h;
     const Batch &b = p.batch;
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
     const int l = lane % LPH, grp = lane / LPH, groups = (a.n_kv + GPW - 1) / GPW;
-    if ((int)blockIdx.y >= 2 * groups) {  // queries
-        head_rows<E, LPH, 1, INTERLEAVED, true>(p, (int64_t)blockIdx.x * warps + warp, (int)blockIdx.y - 2 * groups);
+    if ((int)blockIdx.x >= a.kv_blocks) {  // queries
+        const int at = (int)blockIdx.x - a.kv_blocks;
+        head_rows<E, LPH, 1, INTERLEAVED, true>(p, (int64_t)(at / a.q_groups) * warps + warp, at % a.q_groups);
         return;
     }
-    const int64_t u = blockIdx.x;
-    if (u >= a.units) return;
-    const bool is_v = (int)blockIdx.y >= groups;
-    const int h = ((int)blockIdx.y - (is_v ? groups : 0)) * GPW + grp;
+    const int part = (int)blockIdx.x % (2 * groups);
+    const int64_t u = (int)blockIdx.x / (2 * groups);
+    const bool is_v = part >= groups;
+    const int h = (is_v ? part - groups : part) * GPW + grp;
     const bool live = h < a.n_kv;
 
-    // Sequence s has the units from row0 / B + 2 s on: its rows touch at most one block more than they fill.
+    // Sequence s has the units from min(row0 / B + 2 s, row0) on: its rows touch at most one block more than they fill,
+    // and no more blocks than there are rows.
     const int32_t B = a.block;
     const int64_t base = __ldg(b.offs);
-    if (u == 0 && blockIdx.y == 0 && threadIdx.x == 0 && __ldg(b.offs + b.n_seqs) - base != p.n_tokens) raise_error(ENGRAM_ERANGE);
-    const int64_t s = warp_find(b.n_seqs, [&](int64_t i) { return (__ldg(b.offs + i) - base) / B + 2 * i <= u; });
+    if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(b.offs + b.n_seqs) - base != p.n_tokens) raise_error(ENGRAM_ERANGE);
+    const auto first_unit = [&](int64_t i, int64_t row) { return min(row / B + 2 * i, row); };
+    const int64_t s = warp_find(b.n_seqs, [&](int64_t i) { return first_unit(i, __ldg(b.offs + i) - base) <= u; });
     const int64_t r0 = __ldg(b.offs + s) - base, r1 = __ldg(b.offs + s + 1) - base;
     if (r0 < 0 || r1 < r0 || r1 > p.n_tokens) {
         if (threadIdx.x == 0) raise_error(ENGRAM_ERANGE);
@@ -111,7 +116,7 @@ __global__ void __launch_bounds__(32 * MAX_BLOCK / TOKENS_PER_WARP) append8_kern
     }
     const int64_t kv = __ldg(b.kv_len + s), first = kv - (r1 - r0);  // the first new token's position; before 0: padding
     const int64_t begin = first > 0 ? first : 0;
-    const int64_t block0 = (begin / B + (u - (r0 / B + 2 * s))) * B;
+    const int64_t block0 = (begin / B + (u - first_unit(s, r0))) * B;
     const int64_t lo = begin > block0 ? begin : block0;
     int64_t hi = kv < block0 + B ? kv : block0 + B;
     if (lo >= hi) return;
@@ -123,14 +128,8 @@ __global__ void __launch_bounds__(32 * MAX_BLOCK / TOKENS_PER_WARP) append8_kern
     const int32_t entry = p.by_page.quotient((int32_t)block0), slot0 = (int32_t)block0 - entry * b.page_size;
     int32_t page = -1;
     if (entry < b.table_width) page = __ldg(b.block_table + s * b.table_stride + entry);
-    if (page < 0 || page >= b.n_pages) {
-        if (threadIdx.x == 0) raise_error(ENGRAM_ERANGE);
-        return;
-    }
     const int32_t n_old = (int32_t)(lo - block0), n_end = (int32_t)(hi - block0);  // new tokens: [n_old, n_end) of the block
 
-    float *scale = (is_v ? a.v_scales : a.k_scales) + ((int64_t)page * a.n_kv + h) * a.per_page + slot0 / B;
-    const float was = live && n_old > 0 ? *scale : 0.f;
     HeadLane k;
     if (is_v) {  // any pieces do
         k.c0 = 2 * l;
@@ -152,6 +151,13 @@ __global__ void __launch_bounds__(32 * MAX_BLOCK / TOKENS_PER_WARP) append8_kern
         x0[i] = on && k.has0 ? *reinterpret_cast<const uint4 *>(src + t * in.token_stride + k.c0 * 8) : make_uint4(0, 0, 0, 0);
         x1[i] = on && k.has1 ? *reinterpret_cast<const uint4 *>(src + t * in.token_stride + k.c1 * 8) : make_uint4(0, 0, 0, 0);
     }
+    // (the page's number has been on its way meanwhile)
+    if (page < 0 || page >= b.n_pages) {
+        if (threadIdx.x == 0) raise_error(ENGRAM_ERANGE);
+        return;
+    }
+    float *scale = (is_v ? a.v_scales : a.k_scales) + ((int64_t)page * a.n_kv + h) * a.per_page + slot0 / B;
+    const float was = live && n_old > 0 ? *scale : 0.f;
     if (!is_v) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {

@@ -56,16 +56,23 @@ static engram_status check_plan(const engram_kv_plan_args *a) {
 
 // ------------------------------------------------------------------- append --
 
+template <typename E, int LPH, int THREADS>
+static engram_status append8_launch_t(const engram_attn_config *cfg, const Append8 &a, int64_t blocks, int threads, cudaStream_t st) {
+    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
+        return launch_after(append8_kernel<E, LPH, true, THREADS>, dim3((unsigned)blocks), threads, 0, 1, st, "append8_kernel", a);
+    return launch_after(append8_kernel<E, LPH, false, THREADS>, dim3((unsigned)blocks), threads, 0, 1, st, "append8_kernel", a);
+}
 template <typename E, int LPH>
-static engram_status append8_launch(const engram_attn_config *cfg, const Append8 &a, cudaStream_t st) {
+static engram_status append8_launch(const engram_attn_config *cfg, Append8 &a, cudaStream_t st) {
     constexpr int per = 32 / LPH;
     const int warps = a.block / TOKENS_PER_WARP;
-    const int64_t q_blocks = a.h.n_q ? (a.h.n_tokens + warps - 1) / warps : 0;
-    const dim3 grid((unsigned)std::max(a.units, q_blocks), 2 * ((a.n_kv + per - 1) / per) + (a.h.n_q + per - 1) / per);
-    if (grid.y > 65535) return ENGRAM_EINVAL;
-    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
-        return launch_after(append8_kernel<E, LPH, true>, grid, warps * 32, 0, 1, st, "append8_kernel", a);
-    return launch_after(append8_kernel<E, LPH, false>, grid, warps * 32, 0, 1, st, "append8_kernel", a);
+    a.q_groups = (a.h.n_q + per - 1) / per;
+    const int64_t kv_blocks = a.units * 2 * ((a.n_kv + per - 1) / per);
+    const int64_t blocks = kv_blocks + (a.h.n_tokens + warps - 1) / warps * a.q_groups;
+    if (blocks > INT32_MAX) return ENGRAM_EINVAL;
+    a.kv_blocks = (int32_t)kv_blocks;
+    return warps <= 8 ? append8_launch_t<E, LPH, 256>(cfg, a, blocks, warps * 32, st)
+                      : append8_launch_t<E, LPH, 512>(cfg, a, blocks, warps * 32, st);
 }
 
 // ---------------------------------------------------------------- attention --
@@ -312,7 +319,8 @@ extern "C" engram_status engram_kv_plan(const engram_kv_plan_args *a, void *stre
     p.by_page = Divisor(a->page_size);
     p.maps = a->max_tokens <= 4096;
     cudaStream_t st = (cudaStream_t)stream;
-    const engram_status s = launch_after(plan::plan_kernel, dim3(1), plan::NT, 0, 1, st, "plan_kernel", p);
+    const engram_status s = p.n_seqs <= 256 ? launch_after(plan::plan_kernel<256>, dim3(1), 256, 0, 1, st, "plan_kernel", p)
+                                            : launch_after(plan::plan_kernel<plan::MOST>, dim3(1), plan::MOST, 0, 1, st, "plan_kernel", p);
     if (s != ENGRAM_OK || p.maps || (!p.positions && !p.slots)) return s;
     const int64_t warps = p.max_tokens / plan::SPAN + p.n_seqs + 1;
     return launch_after(plan::map_kernel, dim3((unsigned)((warps + 7) / 8)), 256, 0, 1, st, "map_kernel", p);
@@ -359,9 +367,7 @@ extern "C" engram_status engram_kv_append_q8(const engram_attn_config *cfg, cons
     a.n_kv = cfg->n_kv_heads;
     a.block = cache->block_tokens;
     a.per_page = cache->page_size / cache->block_tokens;
-    // sequence s has the units from row0 / block + 2 s on
-    a.units = batch->n_query / a.block + 2 * batch->n_seqs;
-    if (a.units > INT32_MAX) return ENGRAM_EINVAL;
+    a.units = std::min(batch->n_query / a.block + 2 * batch->n_seqs, batch->n_query);
     cudaStream_t st = (cudaStream_t)stream;
     if (cfg->head_dim <= 64)
         return cfg->dtype == ENGRAM_BF16 ? append8_launch<Bf16, 4>(cfg, a, st) : append8_launch<Fp16, 4>(cfg, a, st);

@@ -8,17 +8,20 @@
 //
 // Bound: a decode step's plan by latency (a chain of loads, a scan, the page
 // moves), a prompt's by the 12 bytes written for each token.  One block scans
-// the requests (1,024 at a time) and moves the pages, so the whole step is
-// checked before anything changes and the stack's order does not depend on
-// timing.  The maps of many tokens are a second kernel over the whole GPU.
+// the requests (1,024 at a time, 256 where that is all) and moves the pages, so
+// the whole step is checked before anything changes and the stack's order does
+// not depend on timing.  Pages and tokens go to the block's threads one each,
+// whosever they are (a search in the scan's sums finds the request): a warp a
+// request, its 16 requests' loads one after another, took 19 us for 512 mixed
+// requests.  The maps of many tokens are a second kernel over the whole GPU.
 #pragma once
 
 namespace engram {
 namespace attn {
 namespace plan {
 
-constexpr int NT = 1024;   // requests at a time
-constexpr int SPAN = 256;  // tokens of a warp of the map kernel
+constexpr int MOST = 1024;  // requests at a time
+constexpr int SPAN = 256;   // tokens of a warp of the map kernel
 
 struct Params {
     const int32_t *new_len, *keep_len, *kv_len;  // keep_len null: all is kept
@@ -62,34 +65,51 @@ __device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) {
     return Sums{a.tokens + b.tokens, a.back + b.back, a.take + b.take};
 }
 
+template <int NT>
 struct Shared {
     Sums warp[NT / 32];
-    int64_t tokens[NT];           // before each request of the chunk
-    int32_t back[NT], take[NT];   // in a plan that is carried out both fit: they are at most n_pages
-    int32_t had[NT], need[NT], keep[NT], fresh[NT];
+    // before each request of the chunk and after the last; pages: in a plan that is carried out the sums are at most n_pages
+    int64_t tokens[NT + 1];
+    int32_t back[NT + 1], take[NT + 1];
+    int32_t had[NT], need[NT], keep[NT];
 };
 
 // Exclusive sums over the block's threads, and their total.
+template <int NT>
 __device__ __forceinline__ Sums block_scan(Sums v, Sums *warps, Sums &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums x = v;
+    const auto scan = [&](Sums x, int n) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const Sums u = {__shfl_up_sync(0xffffffffu, x.tokens, o), __shfl_up_sync(0xffffffffu, x.back, o),
-                        __shfl_up_sync(0xffffffffu, x.take, o)};
-        if (lane >= o) x = x + u;
-    }
+        for (int o = 1; o < 32; o <<= 1) {
+            if (o >= n) break;
+            const Sums u = {__shfl_up_sync(0xffffffffu, x.tokens, o), __shfl_up_sync(0xffffffffu, x.back, o),
+                            __shfl_up_sync(0xffffffffu, x.take, o)};
+            if (lane >= o) x = x + u;
+        }
+        return x;
+    };
+    const Sums x = scan(v, 32);
     __syncthreads();  // the last call's sums have been read
     if (lane == 31) warps[warp] = x;
     __syncthreads();
-    Sums before = {0, 0, 0};
-    total = before;
-#pragma unroll 4
-    for (int w = 0; w < NT / 32; ++w) {
-        if (w < warp) before = before + warps[w];
-        total = total + warps[w];
-    }
+    const Sums y = scan(lane < NT / 32 ? warps[lane] : Sums{0, 0, 0}, NT / 32);
+    const auto at = [&](int w) {
+        return Sums{__shfl_sync(0xffffffffu, y.tokens, w), __shfl_sync(0xffffffffu, y.back, w), __shfl_sync(0xffffffffu, y.take, w)};
+    };
+    total = at(NT / 32 - 1);
+    const Sums before = warp > 0 ? at(warp - 1) : Sums{0, 0, 0};
     return Sums{before.tokens + x.tokens - v.tokens, before.back + x.back - v.back, before.take + x.take - v.take};
+}
+
+// The request of the chunk that holds place x: the last i < n with v[i] <= x.
+template <typename T>
+__device__ __forceinline__ int request_of(const T *v, int n, T x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
 }
 
 __device__ __forceinline__ void write_token(const Params &p, int64_t s, int64_t t, int32_t pos) {
@@ -104,11 +124,12 @@ __device__ __forceinline__ void write_none(const Params &p, int64_t t) {
     if (p.slots) p.slots[t] = -1;
 }
 
+template <int NT>
 __global__ void __launch_bounds__(NT) plan_kernel(const __grid_constant__ Params p) {
-    __shared__ Shared sh;
+    __shared__ Shared<NT> sh;
     grid_dependency_wait();
     allow_dependent_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     const bool single = p.n_seqs <= NT;
     const int64_t n_free = *p.n_free;
     Sums done = {0, 0, 0};  // before the chunk
@@ -120,16 +141,20 @@ __global__ void __launch_bounds__(NT) plan_kernel(const __grid_constant__ Params
         bad = bad || !r.ok;
         const Sums mine = {r.fresh, r.had > r.need ? r.had - r.need : 0, r.need > r.had ? r.need - r.had : 0};
         Sums total;
-        const Sums at = done + block_scan(mine, sh.warp, total);
+        const Sums at = done + block_scan<NT>(mine, sh.warp, total);
         sh.tokens[tid] = at.tokens;
         sh.back[tid] = (int32_t)at.back;
         sh.take[tid] = (int32_t)at.take;
         sh.had[tid] = r.had;
         sh.need[tid] = r.need;
         sh.keep[tid] = r.keep;
-        sh.fresh[tid] = r.fresh;
-        __syncthreads();
         done = done + total;
+        if (tid == NT - 1) {
+            sh.tokens[NT] = done.tokens;
+            sh.back[NT] = (int32_t)done.back;
+            sh.take[NT] = (int32_t)done.take;
+        }
+        __syncthreads();
     };
     for (int64_t c0 = 0; c0 < p.n_seqs; c0 += NT) enter(c0);
     const Sums all = done;
@@ -158,9 +183,11 @@ __global__ void __launch_bounds__(NT) plan_kernel(const __grid_constant__ Params
         for (int64_t c0 = 0; c0 < p.n_seqs; c0 += NT) {
             if (!single) enter(c0);
             const int n = (int)(p.n_seqs - c0 < NT ? p.n_seqs - c0 : NT);
-            for (int i = warp; i < n; i += NT / 32)
-                for (int32_t e = sh.need[i] + lane; e < sh.had[i]; e += 32)
-                    p.free_pages[n_free + sh.back[i] + e - sh.need[i]] = p.table[(c0 + i) * p.table_stride + e];
+#pragma unroll 4
+            for (int32_t k = sh.back[0] + tid; k < sh.back[NT]; k += NT) {
+                const int i = request_of(sh.back, n, k);
+                p.free_pages[n_free + k] = p.table[(c0 + i) * p.table_stride + sh.need[i] + k - sh.back[i]];
+            }
         }
         __syncthreads();
     }
@@ -170,21 +197,22 @@ __global__ void __launch_bounds__(NT) plan_kernel(const __grid_constant__ Params
         if (!single) enter(c0);
         const int n = (int)(p.n_seqs - c0 < NT ? p.n_seqs - c0 : NT);
         if (all.take > 0) {
-            for (int i = warp; i < n; i += NT / 32)
-                for (int32_t e = sh.had[i] + lane; e < sh.need[i]; e += 32)
-                    p.table[(c0 + i) * p.table_stride + e] = p.free_pages[top - (sh.take[i] + e - sh.had[i])];
+#pragma unroll 4
+            for (int32_t k = sh.take[0] + tid; k < sh.take[NT]; k += NT) {
+                const int i = request_of(sh.take, n, k);
+                p.table[(c0 + i) * p.table_stride + sh.had[i] + k - sh.take[i]] = p.free_pages[top - k];
+            }
         }
         if (tid < n) {
-            p.kv_len_out[c0 + tid] = sh.keep[tid] + sh.fresh[tid];
+            p.kv_len_out[c0 + tid] = sh.keep[tid] + (int32_t)(sh.tokens[tid + 1] - sh.tokens[tid]);
             p.offs[c0 + tid] = sh.tokens[tid];
         }
         if (p.maps) {
             __syncthreads();  // the pages are in the table
-            if (tid < n && sh.fresh[tid] <= 4)
-                for (int32_t i = 0; i < sh.fresh[tid]; ++i) write_token(p, c0 + tid, sh.tokens[tid] + i, sh.keep[tid] + i);
-            for (int i = warp; i < n; i += NT / 32)
-                if (sh.fresh[i] > 4)
-                    for (int32_t j = lane; j < sh.fresh[i]; j += 32) write_token(p, c0 + i, sh.tokens[i] + j, sh.keep[i] + j);
+            for (int64_t t = sh.tokens[0] + tid; t < sh.tokens[NT]; t += NT) {
+                const int i = request_of(sh.tokens, n, t);
+                write_token(p, c0 + i, t, sh.keep[i] + (int32_t)(t - sh.tokens[i]));
+            }
         }
     }
     if (p.maps)

@@ -12,6 +12,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/TensorImpl.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -374,16 +376,31 @@ PyObject *kv_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
         static const char *const names[6] = {"seq_offsets", "kv_len_out", "n_free_out", "positions", "slots", "counts"};
         const int from[6] = {10, 8, 9, 11, 12, 13};
         const int64_t counts[6] = {p.n_seqs + 1, p.n_seqs, 1, p.max_tokens, p.max_tokens, 4};
+        // one allocation for all of them, a 16-byte boundary for each (six would cost the host more than the plan the GPU)
+        int64_t at[6], bytes = 0;
+        for (int i = 0; i < 6; ++i) {
+            at[i] = bytes;
+            if (a[from[i]] == Py_None) bytes += (counts[i] * (i == 0 || i == 4 ? 8 : 4) + 15) / 16 * 16;
+        }
         at::Tensor made[6];
         void *data[6];
+        c10::Storage storage;
+        if (bytes > 0) {
+            c10::Allocator *const pool = c10::cuda::CUDACachingAllocator::get();
+            storage = c10::Storage(c10::Storage::use_byte_size_t(), bytes, pool->allocate(bytes), pool, /*resizable=*/false);
+        }
         for (int i = 0; i < 6; ++i) {
-            const at::ScalarType type = i == 0 || i == 4 ? at::kLong : at::kInt;
+            const bool wide = i == 0 || i == 4;
             if (a[from[i]] == Py_None) {
-                made[i] = at::empty({counts[i]}, at::TensorOptions().dtype(type).device(dev));
-                data[i] = made[i].data_ptr();
+                made[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                                   c10::scalarTypeToTypeMeta(wide ? at::kLong : at::kInt));
+                c10::TensorImpl *const impl = made[i].unsafeGetTensorImpl();
+                impl->set_sizes_contiguous(c10::IntArrayRef(&counts[i], 1));
+                impl->set_storage_offset(at[i] / (wide ? 8 : 4));
+                data[i] = static_cast<char *>(storage.mutable_data()) + at[i];
             } else {
-                data[i] = type == at::kLong ? (void *)values<int64_t>(a[from[i]], type, counts[i], dev, names[i])
-                                            : (void *)values<int32_t>(a[from[i]], type, counts[i], dev, names[i]);
+                data[i] = wide ? (void *)values<int64_t>(a[from[i]], at::kLong, counts[i], dev, names[i])
+                               : (void *)values<int32_t>(a[from[i]], at::kInt, counts[i], dev, names[i]);
             }
         }
         p.seq_offsets = static_cast<int64_t *>(data[0]);
