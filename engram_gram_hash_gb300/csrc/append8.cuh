@@ -15,7 +15,9 @@
 // chain offsets -> length -> page -> scale.  A CTA has one block of tokens, the
 // keys or the values of the 4 or 8 heads that a warp holds side by side, and a
 // warp for every 8 tokens: each value is read once, stays in registers while
-// the block's maximum is found, and is written once.
+// the block's maximum is found, and is written once.  The angles of a block's
+// tokens come into shared memory beside the keys (from the table, token by
+// token, each waited for: 32,768 tokens TTTT).
 #pragma once
 
 namespace engram {
@@ -85,6 +87,7 @@ template <typename E, int LPH, bool INTERLEAVED, int THREADS>
 __global__ void __launch_bounds__(THREADS, 512 / THREADS) append8_kernel(const __grid_constant__ Append8 a) {
     constexpr int GPW = 32 / LPH, N = TOKENS_PER_WARP;
     __shared__ uint32_t most[THREADS / 32][GPW];
+    extern __shared__ __align__(16) float rows[];  // the table's rows of the block's tokens, for keys
     grid_dependency_wait();
     allow_dependent_launch();
     const HeadParams &p = a.h;
@@ -96,8 +99,8 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) append8_kernel(const _
         head_rows<E, LPH, 1, INTERLEAVED, true>(p, (int64_t)(at / a.q_groups) * warps + warp, at % a.q_groups);
         return;
     }
-    const int part = (int)blockIdx.x % (2 * groups);
-    const int64_t u = (int)blockIdx.x / (2 * groups);
+    const int part = (int)blockIdx.x / (int)a.units;
+    const int64_t u = (int)blockIdx.x - part * (int)a.units;
     const bool is_v = part >= groups;
     const int h = (is_v ? part - groups : part) * GPW + grp;
     const bool live = h < a.n_kv;
@@ -130,6 +133,17 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) append8_kernel(const _
     if (entry < b.table_width) page = __ldg(b.block_table + s * b.table_stride + entry);
     const int32_t n_old = (int32_t)(lo - block0), n_end = (int32_t)(hi - block0);  // new tokens: [n_old, n_end) of the block
 
+    if (page < 0 || page >= b.n_pages) {
+        if (threadIdx.x == 0) raise_error(ENGRAM_ERANGE);
+        return;
+    }
+    float *scale = (is_v ? a.v_scales : a.k_scales) + ((int64_t)page * a.n_kv + h) * a.per_page + slot0 / B;
+    const float was = live && n_old > 0 ? *scale : 0.f;
+    if (!is_v && p.rope_dim > 0) {
+        const float *from = p.table + block0 * p.rope_dim;
+        for (int i = n_old * p.rope_dim + threadIdx.x * 4; i < n_end * p.rope_dim; i += blockDim.x * 4)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(rows + i)), "l"(from + i) : "memory");
+    }
     HeadLane k;
     if (is_v) {  // any pieces do
         k.c0 = 2 * l;
@@ -151,21 +165,17 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) append8_kernel(const _
         x0[i] = on && k.has0 ? *reinterpret_cast<const uint4 *>(src + t * in.token_stride + k.c0 * 8) : make_uint4(0, 0, 0, 0);
         x1[i] = on && k.has1 ? *reinterpret_cast<const uint4 *>(src + t * in.token_stride + k.c1 * 8) : make_uint4(0, 0, 0, 0);
     }
-    // (the page's number has been on its way meanwhile)
-    if (page < 0 || page >= b.n_pages) {
-        if (threadIdx.x == 0) raise_error(ENGRAM_ERANGE);
-        return;
-    }
-    float *scale = (is_v ? a.v_scales : a.k_scales) + ((int64_t)page * a.n_kv + h) * a.per_page + slot0 / B;
-    const float was = live && n_old > 0 ? *scale : 0.f;
     if (!is_v) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int t = i * warps + warp;
             if (t < n_old || t >= n_end) continue;
             Turn turn;
             turn_weights<E, INTERLEAVED>(k, p.w_k, turn);
-            turn_angles<INTERLEAVED>(p, k, block0 + t, turn);
+            const float *row = rows + t * p.rope_dim;
+            turn_angles<INTERLEAVED>(p, k, [&](int j) { return *reinterpret_cast<const float4 *>(row + j); }, turn);
             float2 f[4], g[4];
             turn_head<E, LPH, INTERLEAVED>(p, k, turn, p.w_k != nullptr, x0[i], x1[i], f, g);
             from_pairs<E, INTERLEAVED>(f, g, x0[i], x1[i]);

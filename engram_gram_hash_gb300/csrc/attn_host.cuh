@@ -37,18 +37,6 @@ static HeadView view(const engram_heads *h) {
     return h ? HeadView{static_cast<uint16_t *>(h->data), h->token_stride, h->head_stride} : HeadView{nullptr, 0, 0};
 }
 
-static engram_status check_cache(const engram_attn_config *cfg, const engram_kv_cache *c) {
-    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return ENGRAM_EINVAL;
-    if (c->n_pages < 1 || c->n_pages > INT32_MAX) return ENGRAM_EINVAL;
-    if (c->page_size < 16 || c->page_size > 65536 || c->page_size % 16) return ENGRAM_EINVAL;
-    // strides positive (a size of one may still name any), so no value lies before the base
-    for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
-        if (s < 8 || s % 8 || s >= (INT64_C(1) << 39)) return ENGRAM_EINVAL;
-    if (c->token_stride < cfg->head_dim || c->page_stride < cfg->head_dim) return ENGRAM_EINVAL;
-    if (cfg->n_kv_heads > 1 && c->head_stride < cfg->head_dim) return ENGRAM_EINVAL;
-    return ENGRAM_OK;
-}
-
 static engram_status check_batch(const engram_kv_batch *b) {
     if (!b || b->n_query < 0 || b->n_seqs < 0) return ENGRAM_EINVAL;
     if (b->n_query > INT32_MAX || b->n_seqs > INT32_MAX || b->table_stride < 0) return ENGRAM_EINVAL;
@@ -99,6 +87,36 @@ static engram_status launch_after(void (*kern)(P...), dim3 grid, int threads, in
     lc.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&lc, kern, args...);
     return e == cudaSuccess ? ENGRAM_OK : cuda_fail(e, what);
+}
+
+// Norm and rotation of heads, with the append to the 16-bit cache or without.
+template <typename E, int LPH, int U, bool APPEND>
+static engram_status head_launch_u(const engram_attn_config *cfg, HeadParams &p, cudaStream_t st) {
+    constexpr int per = 32 / LPH * U;  // heads per warp; a block takes 8 tokens
+    const int64_t blocks = (p.n_tokens + 7) / 8;
+    const dim3 grid((unsigned)blocks, (p.n_q + per - 1) / per + (p.n_k + p.n_v + per - 1) / per);
+    if (grid.y > 65535) return ENGRAM_EINVAL;
+    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
+        return launch_after(head_kernel<E, LPH, U, true, APPEND>, grid, 256, 0, 1, st, "head_kernel", p);
+    return launch_after(head_kernel<E, LPH, U, false, APPEND>, grid, 256, 0, 1, st, "head_kernel", p);
+}
+
+static bool many_heads(const HeadParams &p) {
+    return p.n_tokens * ((p.n_q + p.n_k + p.n_v + 3) / 4) >= (int64_t)num_sms() * 64;
+}
+template <typename E, bool APPEND>
+static engram_status head_launch(const engram_attn_config *cfg, HeadParams &p, cudaStream_t st) {
+    p.head_dim = cfg->head_dim;
+    p.rope_dim = cfg->rope_dim;
+    p.eps = cfg->norm_eps;
+    p.inv_dim = 1.f / (float)cfg->head_dim;
+    // One head per lane while the batch leaves SMs idle (a shorter chain per warp), two once there are
+    // 64 warps per SM without it: 32,768 tokens of 32 + 8 heads of 128 take 120 us with two, 140 with
+    // one, 117 to 145 with four (more registers, fewer warps); 64 tokens 1.8 us with one or two.
+    const bool wide = many_heads(p);
+    if (cfg->head_dim <= 64)
+        return wide ? head_launch_u<E, 4, 2, APPEND>(cfg, p, st) : head_launch_u<E, 4, 1, APPEND>(cfg, p, st);
+    return wide ? head_launch_u<E, 8, 2, APPEND>(cfg, p, st) : head_launch_u<E, 8, 1, APPEND>(cfg, p, st);
 }
 
 static int gcd(int a, int b) { return b == 0 ? a : gcd(b, a % b); }

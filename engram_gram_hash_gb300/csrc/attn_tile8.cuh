@@ -213,22 +213,23 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 __syncwarp();  // the warp's lanes have copied each other's rows
                 const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
                 const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
+                uint4 v[DP / 8];  // (no scores are held here)
+#pragma unroll
+                for (int i = 0; i < DP / 8; ++i) v[i] = lds16(piece(i));
                 float most = 0.f;
-#pragma unroll 4
+#pragma unroll
                 for (int i = 0; i < DP / 8; ++i) {
-                    const uint4 v = lds16(piece(i));
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) most = max3(most, fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k])));
                 }
                 const int e = row_exponent<14>(most);
                 const float up = exp2i(e);
                 rf = exp2i(-e);
-#pragma unroll 4
+#pragma unroll
                 for (int i = 0; i < DP / 8; ++i) {
-                    const uint4 v = lds16(piece(i));
                     const auto half = [&](uint32_t x) { return H::pack(bf16_lo(x) * up, bf16_hi(x) * up); };
-                    sts16(piece(i), make_uint4(half(v.x), half(v.y), half(v.z), half(v.w)));
+                    sts16(piece(i), make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w)));
                 }
             }
             fence_proxy_async_smem();
@@ -367,14 +368,16 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
             }
             it += n;
             if (mine && n > 0) {
-                // The last scores were there, so the queries' memory is free: the next item's are fetched
-                // under this item's last product, and its scores computed under this item's epilogue.
+                // The last scores were there, so the queries' memory is free: the next item's are fetched and turned
+                // into fp16 under this item's last product, and its scores computed under this item's epilogue.
                 next = take(k + 1);
                 const bool next_mine = next && next->n > 0 && next->n_rows > t * MT;
-                if (next_mine) fetch_q(*next);
+                if (next_mine) {
+                    fetch_q(*next);
+                    hand_q();
+                }
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
                 if (!ok) break;
-                if (next_mine) hand_q();
                 tc_fence_after();
             } else {
                 next = take(k + 1);

@@ -56,23 +56,36 @@ static engram_status check_plan(const engram_kv_plan_args *a) {
 
 // ------------------------------------------------------------------- append --
 
-template <typename E, int LPH, int THREADS>
-static engram_status append8_launch_t(const engram_attn_config *cfg, const Append8 &a, int64_t blocks, int threads, cudaStream_t st) {
-    if (cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED)
-        return launch_after(append8_kernel<E, LPH, true, THREADS>, dim3((unsigned)blocks), threads, 0, 1, st, "append8_kernel", a);
-    return launch_after(append8_kernel<E, LPH, false, THREADS>, dim3((unsigned)blocks), threads, 0, 1, st, "append8_kernel", a);
+template <typename E, int LPH, bool INTERLEAVED, int THREADS>
+static engram_status append8_launch_t(const Append8 &a, int64_t blocks, int threads, cudaStream_t st) {
+    const int smem = a.block * a.h.rope_dim * (int)sizeof(float);
+    const auto kern = append8_kernel<E, LPH, INTERLEAVED, THREADS>;
+    static std::atomic<bool> attr_done[64];
+    const engram_status s = ensure_smem((const void *)kern, THREADS / 32 * TOKENS_PER_WARP * 128 * (int)sizeof(float), attr_done);
+    if (s != ENGRAM_OK) return s;
+    return launch_after(kern, dim3((unsigned)blocks), threads, smem, 1, st, "append8_kernel", a);
 }
 template <typename E, int LPH>
 static engram_status append8_launch(const engram_attn_config *cfg, Append8 &a, cudaStream_t st) {
     constexpr int per = 32 / LPH;
+    // The queries of many tokens go in a launch of their own: beside the keys' registers half as many of their warps
+    // run (32,768 tokens of 32 + 8 heads 297 us in one launch).
+    if (a.h.n_tokens * ((a.h.n_q + 3) / 4) >= (int64_t)num_sms() * 256) {
+        HeadParams q = a.h;
+        a.h.n_q = 0;
+        const engram_status s = head_launch<E, true>(cfg, q, st);
+        if (s != ENGRAM_OK) return s;
+    }
     const int warps = a.block / TOKENS_PER_WARP;
     a.q_groups = (a.h.n_q + per - 1) / per;
     const int64_t kv_blocks = a.units * 2 * ((a.n_kv + per - 1) / per);
     const int64_t blocks = kv_blocks + (a.h.n_tokens + warps - 1) / warps * a.q_groups;
     if (blocks > INT32_MAX) return ENGRAM_EINVAL;
     a.kv_blocks = (int32_t)kv_blocks;
-    return warps <= 8 ? append8_launch_t<E, LPH, 256>(cfg, a, blocks, warps * 32, st)
-                      : append8_launch_t<E, LPH, 512>(cfg, a, blocks, warps * 32, st);
+    const bool pairs = cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED;
+    if (warps <= 8)
+        return pairs ? append8_launch_t<E, LPH, true, 256>(a, blocks, warps * 32, st) : append8_launch_t<E, LPH, false, 256>(a, blocks, warps * 32, st);
+    return pairs ? append8_launch_t<E, LPH, true, 512>(a, blocks, warps * 32, st) : append8_launch_t<E, LPH, false, 512>(a, blocks, warps * 32, st);
 }
 
 // ---------------------------------------------------------------- attention --
@@ -116,12 +129,23 @@ static int64_t rows8_tiles_most(const engram_attn_config *cfg, const engram_kv_c
     return (keys_most(cfg, cache, batch) + rows::KT8 - 1) / rows::KT8;
 }
 
-// How a segment's tiles are shared out, as for the 16-bit cache: clusters of CTAs for few segments and short
-// tables, whole segments where a cut cannot pay, else equal runs of tiles for every SM and the join.
+// How a segment's tiles are shared out, and about how long that takes (us on this GPU): the least of
+//   whole: no cut, no join; a round of segments over the SMs costs 2.9 and 0.61 a tile (64 values: 0.54), the first 2.4 more;
+//   cluster of 8 or 4: a segment's tiles over that many CTAs, joined through distributed shared memory, one launch;
+//     15 clusters of 8 and 36 of 4 fit the GPU at once;
+//   cut: equal runs of tiles for every SM, then the join: 9.5, and 0.78 a tile.  Several sequences seldom have the room
+//     that their tables give them; here alone that shortens the work, so it counts for less (unequal lengths make the
+//     others wait for the longest).
+// Measured, 32 / 8 heads of 128, us a call in a CUDA graph, cluster of 8 / of 4 / whole / cut:
+//   1 sequence of 100 tokens 7.3 / 7.1 / 5.8 / 6.8, 1,000 7.3 / 7.7 / 9.8 / 9.1, 8,000 11.1 / 15.5 / 41 / 12.5, 32,000
+//   25 / 43 / 153 / 18.8;  4 of 2,000 - / 9.1 / 14.7 / 11.3;  8 of 500 - / - / 8.0 / 9.9, 8,000 43 / 31;  64 of 100
+//   16.5 / 19.4, 2,000 53 / 55, 8,000 169 / 164.
 // Cut, the heads lie side by side (as many as divide them and leave hardly an SM out): the CTAs that share a page
-// read it at the same time, which DRAM likes better than 128 bytes of every 1,024.
+// read it at the same time, which DRAM likes better than 128 bytes of every 1,024 (64 sequences of up to 16,384 tokens
+// 173 us instead of 197).
 struct Rows8Shares {
     int32_t cluster, whole, runs, side;
+    double us;
     bool cut() const { return whole == 0 && runs > 1; }
 };
 static int32_t heads_aside(int n_kv_heads, int sms) {
@@ -131,22 +155,17 @@ static int32_t heads_aside(int n_kv_heads, int sms) {
     return side;
 }
 static Rows8Shares rows8_shares(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
-    const int64_t tiles = rows8_tiles_most(cfg, cache, batch), segs = rows8_segs_most(cfg, batch);
+    const int64_t tiles = std::max<int64_t>(rows8_tiles_most(cfg, cache, batch), 1), segs = rows8_segs_most(cfg, batch);
     const int sms = num_sms();
-    Rows8Shares p = {1, 0, sms, 1};
-    if (tiles > 2 && tiles <= 64 && segs * 12 <= sms) {
-        p.cluster = 8;
-    } else if (tiles > 2 && tiles <= (segs >= 24 ? 64 : 32) && segs * 4 <= sms - 8) {
-        p.cluster = 4;
-    } else if (tiles <= 8 || (tiles <= 32 && segs * 2 >= sms && segs <= sms)) {
-        p.whole = (int32_t)tiles;
+    const double tile_us = padded_dim(cfg) == 64 ? 0.54 : 0.61, t = (double)tiles, g = (double)segs;
+    Rows8Shares p = {1, (int32_t)std::min<int64_t>(tiles, INT32_MAX), sms, 1, 2.4 + ceil(g / sms) * (2.9 + tile_us * t)};
+    for (int c = 8; c >= 4; c -= 4) {
+        const double us = 6.7 + tile_us * t / c;
+        if (segs <= (c == 8 ? sms / 10 : sms / 4 - 2) && us < p.us) p = {c, 1, (int32_t)segs, 1, us};
     }
-    if (p.cluster > 1) {
-        p.whole = 1;
-        p.runs = (int32_t)segs;
-    }
-    if (p.whole == 0) {
-        p.side = heads_aside(cfg->n_kv_heads, sms);
+    const double cut = 9.5 + (batch->n_seqs > 1 ? 0.85 : 1.0) * 0.78 * g * std::max(t, 1.5) / sms;
+    if (cut < p.us) {
+        p = {1, 0, sms, heads_aside(cfg->n_kv_heads, sms), cut};
         p.runs = sms / p.side;
     }
     return p;
@@ -222,17 +241,19 @@ static size_t tile8_workspace_bytes(const engram_attn_config *cfg, const engram_
     return tile8_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
 }
 
-// Rows kernel or tile kernel: the one whose estimate, in us on this GPU, is less.
+// Rows kernel or tile kernel: the one whose estimate is less.  An item of 256 rows costs 3.2 us and 2.2 a tile of 128
+// keys; whole rounds of them, or equal shares after a later start (split and joined).  Fitted to 545 measured pairs
+// (32 / 8 and 16 / 16 heads of 128, 32 / 4 of 64; 1 to 40 sequences of 1 to 256 new tokens over 1 to 16,000): the
+// choice costs 0.2 % over the better kernel in the mean and 25 % at worst.  Of them, 32 / 8 heads of 128, us rows kernel /
+// tile kernel, new tokens over cached ones: 8 sequences of 8 over 8,000 78 / 98; 40 of 16 prompts 61 / 21, 8 over 2,000
+// 107 / 128.
 static bool use_tiles8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
     const double sms = num_sms();
     const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
-    const double mean = (double)rows / (double)seqs, parts = (double)seqs * cfg->n_kv_heads;
-    const double segs = parts * ceil(mean / rows::ROWS8), items = parts * ceil(mean / tile::ROWS);
-    const double seg_us = 2.5 + 1.0 * (double)rows8_tiles_most(cfg, cache, batch);
-    const double item_us = 3.7 + 1.6 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
-    const double rows_us = std::min(9.0 + segs * seg_us / sms, 3.5 + ceil(segs / sms) * seg_us);
-    const double tile_us = tile8_slots(cfg, cache, batch) > 0 ? 24.0 + items * item_us / sms : 4.0 + ceil(items / sms) * item_us;
-    return tile_us < rows_us;
+    const double items = (double)seqs * cfg->n_kv_heads * ceil((double)rows / (double)seqs / tile::ROWS);
+    const double item_us = 3.2 + 2.2 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
+    const double tile_us = tile8_slots(cfg, cache, batch) > 0 ? 28.8 + items * item_us / sms : 5.2 + ceil(items / sms) * item_us;
+    return tile_us < rows8_shares(cfg, cache, batch).us;
 }
 
 template <typename E, int DP>
@@ -319,7 +340,8 @@ extern "C" engram_status engram_kv_plan(const engram_kv_plan_args *a, void *stre
     p.by_page = Divisor(a->page_size);
     p.maps = a->max_tokens <= 4096;
     cudaStream_t st = (cudaStream_t)stream;
-    const engram_status s = p.n_seqs <= 256 ? launch_after(plan::plan_kernel<256>, dim3(1), 256, 0, 1, st, "plan_kernel", p)
+    // 256 threads where requests and pages to take are few (a decode step 2.9 us, 4.2 with 1,024), else 1,024
+    const engram_status s = p.n_seqs <= 256 && p.max_tokens / p.page_size <= 1024 ? launch_after(plan::plan_kernel<256>, dim3(1), 256, 0, 1, st, "plan_kernel", p)
                                             : launch_after(plan::plan_kernel<plan::MOST>, dim3(1), plan::MOST, 0, 1, st, "plan_kernel", p);
     if (s != ENGRAM_OK || p.maps || (!p.positions && !p.slots)) return s;
     const int64_t warps = p.max_tokens / plan::SPAN + p.n_seqs + 1;

@@ -130,17 +130,16 @@ __device__ __forceinline__ void turn_weights(const HeadLane &k, const uint16_t *
 #pragma unroll
         for (int i = 0; i < 4; ++i) t.A[i] = t.C[i] = make_float2(1.f, 1.f);
 }
-template <bool INTERLEAVED>
-__device__ __forceinline__ void turn_angles(const HeadParams &p, const HeadLane &k, int64_t pos, Turn &t) {
-    const float *row = p.table + pos * p.rope_dim;
+// `angles(i)`: four numbers of the position's table row from the i-th on.
+template <bool INTERLEAVED, typename F>
+__device__ __forceinline__ void turn_angles(const HeadParams &p, const HeadLane &k, const F &angles, Turn &t) {
     const int hr = p.rope_dim >> 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // pairs 4i .. 4i + 3
         t.B[2 * i] = t.B[2 * i + 1] = t.D[2 * i] = t.D[2 * i + 1] = make_float2(0.f, 0.f);
         if (i ? k.rot1 : k.rot0) {
             const int at = INTERLEAVED ? (i ? k.c1 : k.c0) * 4 : k.c0 * 8 + i * 4;
-            const float4 c4 = __ldg(reinterpret_cast<const float4 *>(row + at));
-            const float4 s4 = __ldg(reinterpret_cast<const float4 *>(row + hr + at));
+            const float4 c4 = angles(at), s4 = angles(hr + at);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int q = 2 * i + j;
@@ -248,7 +247,8 @@ __device__ __forceinline__ void head_rows(const HeadParams &p, int64_t t, int bl
         const uint16_t *w = is_q ? p.w_q : p.w_k;
         Turn turn;
         turn_weights<E, INTERLEAVED>(k, w, turn);
-        turn_angles<INTERLEAVED>(p, k, pos, turn);
+        const float *row = p.table + pos * p.rope_dim;
+        turn_angles<INTERLEAVED>(p, k, [&](int i) { return __ldg(reinterpret_cast<const float4 *>(row + i)); }, turn);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             float2 f[4], s[4];
