@@ -19,6 +19,9 @@
 // neighbours in memory: two conversions for them, and for V, whose pairs lie
 // across keys, a byte permutation.  The strips' scales travel with their tile:
 // 4-byte asynchronous copies that the tile's barrier counts.
+// 64 sequences of up to 16,384 tokens, 32 / 8 heads of 128: 173-176 us, 96-97 % of
+// the copy rate; 131,072 tokens of one 51 us, 77 % (launch, first loads and the
+// join take 11); 512 tokens, 4 / 2 heads of 64, 5.9 us in a CUDA graph.
 #pragma once
 
 namespace engram {

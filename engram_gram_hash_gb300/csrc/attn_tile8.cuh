@@ -2,23 +2,36 @@
 // (prompts, chunks): the tile kernel's items, plan, products and join, on tiles
 // that four more warps make from the codes.
 //
-// Bound: as the 16-bit tile kernel, by the softmax's instructions beside the
-// tensor pipe.  Why the codes become fp16 tiles first: the fp8 matrix
-// instruction wants both operands in 8 bits, so queries and weights would have
-// to be split into two or three pieces each; a tile's codes are converted once
-// for 256 rows instead (32,768 codes a pair of row tiles, 12 instructions for
-// 256 of them, on warps that the softmax leaves idle slots).
+// Bound: neither the tensor pipe (a prompt of 8,192 tokens, 32 / 8 heads of 128:
+// 541 us, 1,020 TFLOP/s, 54 % of the burst rate; over 63,488 cached tokens
+// 2,048 more 2,090 us) nor memory, but the converters and the softmax beside
+// them: a pair of row tiles takes 4,600 cycles of an SM, 3,000 on 16-bit tiles.
+// By a clock trace the converters are busy all that time (1,500 cycles a tile of
+// keys or values, most of it the latency of one load and store after another);
+// loading eight pieces ahead takes them to 950, but both softmaxes then fall
+// into step, share the issue slots and the period grows to 5,400 (566 us).
+// Why the codes become fp16 tiles first: the fp8 matrix instruction wants both
+// operands in 8 bits, so queries and weights would have to be split into two or
+// three pieces each; a tile's codes are converted once for 256 rows instead
+// (32,768 codes a pair of row tiles).
+// Tried and left: codes from global memory straight into the converters'
+// registers (649 us: too few bytes in flight), two threads a row in the softmax
+// (732), scores read twice from TMEM in rolled loops (572), factors kept in
+// registers (575), strips brought to one scale while converting (546, and
+// inexact), row tile 1 held half a period behind (592).
 //
 // Beside the roles of the 16-bit kernel (softmax, products, loads, items):
-//   warps 12-15   wait for a tile of codes (two stages of 16 KB, keys and values by
-//                 turns), convert a quarter of its keys each and store them as
-//                 the products read them (three stages of 32 KB: the values in
-//                 use, the next keys, the next values).  They also clear what
-//                 the products must not meet: values of keys that no row
-//                 reaches, NaN in tiles that some row sees only part of.
+//   warps 12-15   wait for a tile of codes (a stage of keys and one of values, 16 KB
+//                 each), convert a quarter of its keys each and store them as
+//                 the products read them (four stages of 32 KB; three: 565 us).
+//                 They also clear what the products must not meet: values of
+//                 keys that no row reaches, NaN in tiles that some row sees
+//                 only part of.
 //   Scales come with their tile of keys (asynchronous copies, counted by its
 //   barrier); a converter turns them into the factor, log2 and inverse that the
 //   softmax reads, a strip of 16 keys at a time.
+// The memory through which the 16-bit kernel's rows change hands on their way
+// out went to the ring: a lane stores its own row, 32 bytes at a time.
 #pragma once
 
 #include <type_traits>
@@ -213,23 +226,34 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 __syncwarp();  // the warp's lanes have copied each other's rows
                 const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
                 const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
-                uint4 v[DP / 8];  // (no scores are held here)
-#pragma unroll
-                for (int i = 0; i < DP / 8; ++i) v[i] = lds16(piece(i));
+                // Pieces loaded together: one after another each waits out its load (5,000 cycles an item).  All at
+                // once is best at 128 values (a prompt of 8,192 tokens 541 us; four 548); at 64 it costs the softmax
+                // registers (470 us; four 428).
+                constexpr int BATCH = C::APART ? 4 : DP / 8;
                 float most = 0.f;
+#pragma unroll 1
+                for (int i = 0; i < DP / 8; i += BATCH) {
+                    uint4 v[BATCH];
 #pragma unroll
-                for (int i = 0; i < DP / 8; ++i) {
-                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    for (int k = 0; k < BATCH; ++k) v[k] = lds16(piece(i + k));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) most = max3(most, fabsf(bf16_lo(x[k])), fabsf(bf16_hi(x[k])));
+                    for (int k = 0; k < BATCH; ++k) {
+                        const uint32_t x[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) most = max3(most, fabsf(bf16_lo(x[c])), fabsf(bf16_hi(x[c])));
+                    }
                 }
                 const int e = row_exponent<14>(most);
                 const float up = exp2i(e);
                 rf = exp2i(-e);
+                const auto half = [&](uint32_t x) { return H::pack(bf16_lo(x) * up, bf16_hi(x) * up); };
+#pragma unroll 1
+                for (int i = 0; i < DP / 8; i += BATCH) {
+                    uint4 v[BATCH];
 #pragma unroll
-                for (int i = 0; i < DP / 8; ++i) {
-                    const auto half = [&](uint32_t x) { return H::pack(bf16_lo(x) * up, bf16_hi(x) * up); };
-                    sts16(piece(i), make_uint4(half(v[i].x), half(v[i].y), half(v[i].z), half(v[i].w)));
+                    for (int k = 0; k < BATCH; ++k) v[k] = lds16(piece(i + k));
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) sts16(piece(i + k), make_uint4(half(v[k].x), half(v[k].y), half(v[k].z), half(v[k].w)));
                 }
             }
             fence_proxy_async_smem();
@@ -368,16 +392,15 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
             }
             it += n;
             if (mine && n > 0) {
-                // The last scores were there, so the queries' memory is free: the next item's are fetched and turned
-                // into fp16 under this item's last product, and its scores computed under this item's epilogue.
+                // The last scores were there, so the queries' memory is free: the next item's are fetched
+                // under this item's last product, and its scores computed under this item's epilogue.  (Handed over before
+                // that product too they were worth 1 % of a long prompt and cost 9 % of a window of 128 tokens.)
                 next = take(k + 1);
                 const bool next_mine = next && next->n > 0 && next->n_rows > t * MT;
-                if (next_mine) {
-                    fetch_q(*next);
-                    hand_q();
-                }
+                if (next_mine) fetch_q(*next);
                 ok = warp_wait(&sh->o_full[t], o_ph++ & 1, abort);
                 if (!ok) break;
+                if (next_mine) hand_q();
                 tc_fence_after();
             } else {
                 next = take(k + 1);
