@@ -1,7 +1,7 @@
 """Python binding of libengram.so, the Engram memory read for one GB300.
 
 Argument marshalling only: every step runs in the CUDA kernels of
-``csrc/engram_core.cu``; PyTorch supplies device memory and streams.  The
+``csrc/``; PyTorch supplies device memory and streams.  The
 names and semantics are those of ``include/engram.h``.  If the library has not
 been built (``__graft_entry__.build()``), importing works but every call
 raises: there is no CPU path.
@@ -904,7 +904,7 @@ def _cache_q8_of(cache, cfg, batch):
 
 def engram_kv_append_q8(cfg, cache, batch, k, v, table, w_k=None, q=None, w_q=None, q_out=None, stream=None):
     """engram_kv_append into a kv_cache_q8: the step's k (normed with w_k, rotated) and v [n_query, n_kv_heads, D] as
-    codes, their blocks' scales set or raised.  With q, also its norm and rotation in the same launch; returns q_out
+    codes, their blocks' scales set or raised.  With q, also its norm and rotation in the same call; returns q_out
     (None without)."""
     return _step().kv_append_q8(cfg, _cache_q8_of(cache, cfg, batch), batch, k, v, table, w_k, q, w_q, q_out, stream,
                                 cache.device_index)

@@ -2,25 +2,28 @@
 // (prompts, chunks): the tile kernel's items, plan, products and join, on tiles
 // that four more warps make from the codes.
 //
-// Bound: neither the tensor pipe (a prompt of 8,192 tokens, 32 / 8 heads of 128:
-// 541 us, 1,020 TFLOP/s, 54 % of the burst rate; over 63,488 cached tokens
-// 2,048 more 2,090 us) nor memory, but the converters and the softmax beside
-// them: a pair of row tiles takes 4,600 cycles of an SM, 3,000 on 16-bit tiles.
-// By a clock trace the converters are busy all that time (1,500 cycles a tile of
-// keys or values, most of it the latency of one load and store after another);
-// loading eight pieces ahead takes them to 950, but both softmaxes then fall
-// into step, share the issue slots and the period grows to 5,400 (566 us).
-// Why the codes become fp16 tiles first: the fp8 matrix instruction wants both
-// operands in 8 bits, so queries and weights would have to be split into two or
-// three pieces each; a tile's codes are converted once for 256 rows instead
-// (32,768 codes a pair of row tiles).
-// Tried and left: codes from global memory straight into the converters'
-// registers (649 us: too few bytes in flight), two threads a row in the softmax
-// (732), scores read twice from TMEM in rolled loops (572), factors kept in
-// registers (575), strips brought to one scale while converting (546, and
-// inexact), row tile 1 held half a period behind (592).
+// The products run on fp16 (codes are exact there), so a tile's codes become an fp16 tile first: the fp8 matrix
+// instruction wants both operands in 8 bits, and queries and weights would have to be split into two or three
+// pieces each.  Two forms:
+//   opened   for work with many row blocks over the same keys a kernel makes the tiles of every sequence and head
+//            once, in the workspace, in the order of the ring's stages, and a stage is two plain bulk copies (a prompt
+//            of 8,192 tokens has 128 row blocks a head: its tiles are converted once instead of 65 times in the mean);
+//   in place for fewer, four more warps convert each tile that the CTA meets.
+// Opened, bound as the 16-bit kernel by the softmax's chain beside the tensor pipe, longer by the strips' factors:
+// a prompt of 8,192 tokens, 32 / 8 heads of 128, 434 us (1,270 TFLOP/s, 67 % of the burst rate; about 12 are the
+// opening; fp16 queries 416: bf16 ones are converted between items), 2,048 more over 63,488 cached 1,635 (1,325
+// TFLOP/s); the 16-bit kernel takes 360 and 1,400.  Tried and left there: factors loaded ahead of the scores 446-451,
+// ahead of the exponentials 445; codes brought to one scale a tile and a second form of the softmax for such tiles 465.
+// In place, bound by the converters and the softmax beside them: 541 and 2,090 us; a pair of row tiles takes 4,600
+// cycles of an SM, 3,000 on 16-bit tiles.  By a clock trace the converters are busy all that time (1,500 cycles a
+// tile of keys or values, most of it the latency of one load and store after another); loading eight pieces ahead
+// takes them to 950, but both softmaxes then fall into step, share the issue slots and the period grows to 5,400.
+// Tried and left: codes from global memory straight into the converters' registers (649 us: too few bytes in
+// flight), two threads a row in the softmax (732), scores read twice from TMEM in rolled loops (572), factors kept in
+// registers (575), strips brought to one scale while converting (546, and inexact), row tile 1 held half a period
+// behind (592).
 //
-// Beside the roles of the 16-bit kernel (softmax, products, loads, items):
+// Beside the roles of the 16-bit kernel (softmax, products, loads, items), in place:
 //   warps 12-15   wait for a tile of codes (a stage of keys and one of values, 16 KB
 //                 each), convert a quarter of its keys each and store them as
 //                 the products read them (four stages of 32 KB; three: 565 us).
@@ -79,18 +82,28 @@ struct Shared8 {
     PlanShared plan;
 };
 
-template <int DP>
+template <int DP, bool OPEN>
 constexpr int smem8_bytes() {
-    return 2 * Cfg8<DP>::Q_BYTES + Cfg8<DP>::STAGES * Cfg8<DP>::STAGE_BYTES + Cfg8<DP>::RAW_STAGES * Cfg8<DP>::RAW_BYTES +
-           (int)sizeof(Shared8<DP>);
+    return 2 * Cfg8<DP>::Q_BYTES + Cfg8<DP>::STAGES * Cfg8<DP>::STAGE_BYTES +
+           (OPEN ? 0 : Cfg8<DP>::RAW_STAGES * Cfg8<DP>::RAW_BYTES) + (int)sizeof(Shared8<DP>);
 }
-static_assert(smem8_bytes<128>() <= 232448 && smem8_bytes<64>() <= 232448, "tile kernel shared memory over the per-CTA limit");
+static_assert(smem8_bytes<128, false>() <= 232448 && smem8_bytes<64, false>() <= 232448, "tile kernel shared memory over the per-CTA limit");
+
+// The sequences' keys and values as fp16, in the order of the ring's stages: for each sequence and head the keys' 64
+// values at a time (rows of 128 bytes, swizzled over 8 keys), the values' likewise, then the strips' factors.
+struct Opened {
+    uint8_t *at;
+    int64_t keys;  // of a sequence and head: the block table's room, rounded up to tiles, and a tile of zeros
+};
+template <int DP>
+__host__ __device__ constexpr int64_t opened_bytes(int64_t keys) { return keys * (4 * DP + (int)sizeof(float4) / STRIP); }
 
 struct Params8 {
     Params t;  // values: unused
     Scales scales;
     CodePages codes;
     Divisor by_page;
+    Opened opened;  // at null: none
 };
 
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
@@ -112,19 +125,120 @@ __device__ __forceinline__ void store32(void *to, const uint32_t *v, bool wide) 
 // A strip's factor for a row.  Not 0 (a key scale may be): a hidden score, -inf, must stay that.
 __device__ __forceinline__ float factor(float strip, float row) { return fmaxf(strip * row, 7.5231638452626401e-37f); }
 
-template <typename E, int DP>
-__global__ void __launch_bounds__(NUM_THREADS8, 1)
+// 16-byte aligned global memory into shared memory, asynchronously, counted in bytes by the barrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+struct OpenParams {
+    Batch b;
+    const uint8_t *k, *v;
+    int64_t page_stride, slot_stride, head_stride;
+    Scales scales;
+    Divisor by_page;
+    Opened opened;
+    int64_t units;  // sequences x tiles x kv heads x 2
+    int32_t tiles, n_kv_heads, head_dim, window;
+    float scale_log2;
+};
+constexpr int OPEN_THREADS = 256;
+constexpr int OPEN_PER_SM = 6;
+// A tile of keys, or of values, of one sequence and head as fp16 into the opened memory; with the values the strips'
+// factors, log2 and inverse, and whether a value was NaN.  Keys that no token of the sequence sees become zeros, NaN
+// values too.  Bound: memory (1 byte in, 2 out a code).
+template <int DP>
+__global__ void __launch_bounds__(OPEN_THREADS, OPEN_PER_SM) open_kernel(const OpenParams p) {
+    __shared__ int bad[STRIPS];
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const int64_t base = __ldg(p.b.offs);
+    constexpr int PIECES = DP / 16;                   // 16 codes each, of a key
+    constexpr int EACH = KT * PIECES / OPEN_THREADS;  // a thread's
+    const int ch = threadIdx.x % PIECES;
+    for (int64_t u = blockIdx.x; u < p.units; u += gridDim.x) {
+        const int kv = (int)(u & 1);
+        const int64_t tile_of = (u >> 1) / p.n_kv_heads, s = tile_of / p.tiles;
+        const int32_t head = (int32_t)((u >> 1) - tile_of * p.n_kv_heads), key0 = (int32_t)(tile_of - s * p.tiles) * KT;
+        const Seq q = load_seq(p.b, s, base);
+        const int32_t lo = first_seen(q.kv - q.q_len, p.window), hi = q.kv;
+        // With a window an item's tiles begin on any box of a page, so its last one may end in the tile after the last key.
+        if (q.q_len == 0 || hi <= 0 || key0 >= hi + (p.window > 0 ? KT : 0) || key0 + KT <= lo) continue;
+        const auto page_of = [&](int32_t entry) { return __ldg(p.b.block_table + s * p.b.table_stride + entry); };
+        uint8_t *const to = p.opened.at + (s * p.n_kv_heads + head) * opened_bytes<DP>(p.opened.keys);
+        const uint8_t *const codes = (kv ? p.v : p.k) + head * p.head_stride + ch * 16;
+        uint4 c[EACH];
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int32_t key = key0 + (i * OPEN_THREADS + threadIdx.x) / PIECES;
+            c[i] = make_uint4(0, 0, 0, 0);
+            if (key >= lo && key < hi) {
+                const int32_t entry = p.by_page.quotient(key), page = page_of(entry);
+                if (page < 0 || page >= p.b.n_pages)
+                    raise_error(ENGRAM_ERANGE);
+                else if (ch * 16 < p.head_dim)
+                    c[i] = *reinterpret_cast<const uint4 *>(codes + page * p.page_stride + (key - entry * p.b.page_size) * p.slot_stride);
+            }
+        }
+        float ks = 0.f, vs = 0.f;
+        if (kv) {  // the same for the block
+            if (threadIdx.x < STRIPS) {
+                const int32_t key = key0 + threadIdx.x * STRIP;
+                if (key < hi && key + STRIP > lo) {
+                    const int32_t entry = p.by_page.quotient(key), page = page_of(entry);
+                    if (page >= 0 && page < p.b.n_pages) {
+                        const int64_t at = ((int64_t)page * p.n_kv_heads + head) * p.scales.per_page +
+                                           ((key - entry * p.b.page_size) >> p.scales.block_log2);
+                        ks = p.scales.k[at];
+                        vs = p.scales.v[at];
+                    }
+                }
+                bad[threadIdx.x] = 0;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < EACH; ++i) {
+                if (nan_codes(c[i].x) | nan_codes(c[i].y) | nan_codes(c[i].z) | nan_codes(c[i].w))
+                    bad[(i * OPEN_THREADS + threadIdx.x) / PIECES / STRIP] = 1;
+                c[i] = make_uint4(without_nan(c[i].x), without_nan(c[i].y), without_nan(c[i].z), without_nan(c[i].w));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int32_t key = key0 + (i * OPEN_THREADS + threadIdx.x) / PIECES;
+            uint8_t *const row = to + ((int64_t)(kv * (DP / 64) + (ch >> 2)) * p.opened.keys + key) * 128;
+            const int at = (ch & 3) * 2, swizzle = key & 7;
+            *reinterpret_cast<uint4 *>(row + ((at ^ swizzle) << 4)) =
+                make_uint4(codes_lo(c[i].x), codes_hi(c[i].x), codes_lo(c[i].y), codes_hi(c[i].y));
+            *reinterpret_cast<uint4 *>(row + (((at + 1) ^ swizzle) << 4)) =
+                make_uint4(codes_lo(c[i].z), codes_hi(c[i].z), codes_lo(c[i].w), codes_hi(c[i].w));
+        }
+        if (kv) {
+            __syncthreads();
+            if (threadIdx.x < STRIPS) {
+                const float2 f = value_scale(vs);
+                reinterpret_cast<float4 *>(to + p.opened.keys * 4 * DP)[key0 / STRIP + threadIdx.x] =
+                    make_float4(ks * p.scale_log2, f.x, f.y, bad[threadIdx.x] ? 1.f : 0.f);
+            }
+            // (a thread clears its own mark next)
+        }
+    }
+}
+
+template <typename E, int DP, bool OPEN>
+__global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
     tile8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ Params8 p8) {
     using C = Cfg8<DP>;
     using H = Fp16;  // of the products
-    constexpr int FACTORS = C::FACTORS;
+    constexpr int FACTORS = C::FACTORS, MAKERS = OPEN ? 0 : CONVERTERS;
     const Params &p = p8.t;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_smem = smem;
     uint8_t *kv_smem = smem + 2 * C::Q_BYTES;
     uint8_t *raw_smem = kv_smem + C::STAGES * C::STAGE_BYTES;
-    Shared8<DP> *sh = reinterpret_cast<Shared8<DP> *>(raw_smem + C::RAW_STAGES * C::RAW_BYTES);
+    Shared8<DP> *sh = reinterpret_cast<Shared8<DP> *>(raw_smem + (OPEN ? 0 : C::RAW_STAGES * C::RAW_BYTES));
     volatile int *abort = &sh->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if ((smem_u32(smem) & 1023u) != 0) {  // the same for every CTA
@@ -134,7 +248,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(&sh->kv_full[i], CONVERTERS);
+            mbar_init(&sh->kv_full[i], OPEN ? 1 : CONVERTERS);
             mbar_init(&sh->kv_empty[i], 2);  // both row tiles' products
         }
         for (int i = 0; i < C::RAW_STAGES; ++i) {
@@ -154,7 +268,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
         }
         for (int i = 0; i < ITEMS; ++i) {
             mbar_init(&sh->item_full[i], 1);
-            mbar_init(&sh->item_empty[i], 11 + CONVERTERS);  // eight softmax warps, two MMA warps, the load warp and the converters
+            mbar_init(&sh->item_empty[i], 11 + MAKERS);  // eight softmax warps, two MMA warps, the load warp and the converters
         }
         sh->abort = 0;
         fence_mbar_init();
@@ -175,7 +289,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
     if (few) {
         __syncthreads();
     } else {
-        make_plan<NUM_THREADS8>(p, base, &sh->plan);  // synchronises the block
+        make_plan<OPEN ? NUM_THREADS : NUM_THREADS8>(p, base, &sh->plan);  // synchronises the block
         if (blockIdx.x == 0 && threadIdx.x == 0 && p.cut) *p.cut = sh->plan.cut;
     }
     tc_fence_after();
@@ -187,9 +301,12 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
     };
 
     // Registers move from the other warps to the softmax warps, which hold a row of 128 scores each:
-    // 256 x 192 + 128 x 72 + 128 x 56 = the launch's 512 x 128.
+    // 256 x 192 + 128 x 72 + 128 x 56 = the launch's 512 x 128, 256 x 208 + 128 x 88 = 384 x 168.
     if (warp < 8) {  // ------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        if (OPEN)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int t = warp >> 2;                  // row tile
         const int row = (warp & 3) * 32 + lane;   // row of the tile: this thread's TMEM lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -227,8 +344,8 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                 const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
                 const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
                 // Pieces loaded together: one after another each waits out its load (5,000 cycles an item).  All at
-                // once is best at 128 values (a prompt of 8,192 tokens 541 us; four 548); at 64 it costs the softmax
-                // registers (470 us; four 428).
+                // once is best at 128 values (a prompt of 8,192 tokens, in place, 541 us; four 548); at 64 it costs the
+                // softmax registers (470 us; four 428).
                 constexpr int BATCH = C::APART ? 4 : DP / 8;
                 float most = 0.f;
 #pragma unroll 1
@@ -288,6 +405,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                     ok = warp_wait(&sh->fac_full[f % FACTORS], (f / FACTORS) & 1, abort);
                     if (!ok) break;
                     const float4 *const fac = sh->fac[f % FACTORS];
+                    float nan_in = 0.f;  // OPEN: whether values of the tile were NaN
                     // the second half of the scores arrives under the first half's maximum
                     uint32_t raw[4][32];
                     tmem_ld_32x32b_x32(s_tm, raw[0]);
@@ -332,6 +450,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                         for (int c = 0; c < 4; ++c) {
                             const float4 g = fac[h * 4 + c];
                             part[c] = fmaf(part[c], factor(g.x, rf), g.y);
+                            if (OPEN) nan_in += g.w;
                         }
                         mx = max3(mx, part[0], part[1]);
                         mx = max3(mx, part[2], part[3]);
@@ -358,6 +477,15 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * up);
                             tmem_st_32x32b_x16(o_tm + c * 16, o);
                         }
+                    }
+                    if (OPEN && nan_in != 0.f) {  // the same in every lane
+                        if (lane == 0) {
+                            Item *const note = const_cast<Item *>(w);
+                            atomicMin(&note->bad_lo, j);
+                            atomicMax(&note->bad_hi, j);
+                            __threadfence_block();
+                        }
+                        __syncwarp();
                     }
                     const float mref = m == -INFINITY ? 0.f : m - LIFT;
 #pragma unroll
@@ -430,8 +558,17 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                         float x[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(o[i]);
-                        add_nan<32>(p.b, p8.codes, w->s, w->head, max(first_seen(pos, p.window), w->key0 + w->bad_lo * KT),
-                                    min(pos + 1, w->key0 + (w->bad_hi + 1) * KT), c, p.head_dim, x);
+                        const int32_t key_lo = max(first_seen(pos, p.window), w->key0 + w->bad_lo * KT);
+                        const int32_t key_hi = min(pos + 1, w->key0 + (w->bad_hi + 1) * KT);
+                        if (OPEN) {
+                            const float4 *const strips = reinterpret_cast<const float4 *>(
+                                p8.opened.at + (w->s * p.n_kv_heads + w->head) * opened_bytes<DP>(p8.opened.keys) + p8.opened.keys * 4 * DP);
+                            for (int32_t k0 = key_lo & ~(STRIP - 1); k0 < key_hi; k0 += STRIP)
+                                if (strips[k0 / STRIP].w != 0.f)
+                                    add_nan<32>(p.b, p8.codes, w->s, w->head, max(key_lo, k0), min(key_hi, k0 + STRIP), c, p.head_dim, x);
+                        } else {
+                            add_nan<32>(p.b, p8.codes, w->s, w->head, key_lo, key_hi, c, p.head_dim, x);
+                        }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(x[i]);
                     }
@@ -480,7 +617,7 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
             w = next;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");  // after a time-out queries may still be on their way
-    } else if (warp >= 12) {  // -------------------------------- codes to fp16 tiles
+    } else if (!OPEN && warp >= 12) {  // ----------------------- codes to fp16 tiles
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const int part = warp - 12;  // a quarter of each tile's keys
         constexpr int LPK = DP / 8, KEYS = 32 / LPK;  // lanes a key (8 codes each), keys at a time
@@ -545,7 +682,10 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
             if (ok && lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (OPEN)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 10) {  // --------------------------------------------- items
             // Rounds of one item per CTA, every other one in reverse: the items come longest first, and
             // the CTAs at one end would get the longer one of every round.  A lane finds one of the
@@ -591,7 +731,50 @@ __global__ void __launch_bounds__(NUM_THREADS8, 1)
                     if (ok && more) prefetch_q(sh->items[(i0 + k) % ITEMS]);
                 }
             }
-        } else if (warp == 9) {  // --------------------------------------- K, V loads
+        } else if (OPEN && warp == 9) {  // ------------------------------- opened K, V, factors
+            uint32_t it = 0;
+            bool ok = true;
+            for (uint32_t i = 0; ok; ++i) {
+                const Item *const item = take(i);
+                if (!item || item->n_rows == 0) break;
+                const int32_t n = item->n;
+                const uint8_t *const from = p8.opened.at + (item->s * p.n_kv_heads + item->head) * opened_bytes<DP>(p8.opened.keys);
+                const int64_t key0 = item->key0;  // on a strip: boxes are whole strips
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh->item_empty[i % ITEMS]);
+                for (int32_t j = 0; ok && j < n; ++j) {
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; ++kv, ++it) {
+                        const int st = it % C::STAGES;
+                        if (lane == 0) {
+                            if (it >= C::STAGES) ok = mbar_wait(&sh->kv_empty[st], ((it / C::STAGES) - 1) & 1, abort);
+                            if (ok) {
+                                mbar_arrive_expect_tx(&sh->kv_full[st], C::STAGE_BYTES);
+#pragma unroll
+                                for (int c = 0; c < DP / 64; ++c)
+                                    bulk_load(smem_u32(kv_smem) + st * C::STAGE_BYTES + c * KT * 128,
+                                              from + ((kv * (DP / 64) + c) * p8.opened.keys + key0 + j * KT) * 128, KT * 128, &sh->kv_full[st]);
+                                if (kv == 0) {
+                                    const uint32_t f = it / 2 % FACTORS;
+                                    mbar_arrive_expect_tx(&sh->fac_full[f], STRIPS * (int)sizeof(float4));
+                                    bulk_load(smem_u32(sh->fac[f]), from + p8.opened.keys * 4 * DP + (key0 + j * KT) / STRIP * (int)sizeof(float4),
+                                              STRIPS * (int)sizeof(float4), &sh->fac_full[f]);
+                                }
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
+                    }
+                }
+            }
+            if (lane == 0) {  // never leave with a copy still landing (also after an abort elsewhere)
+                int no_abort = 0;
+                for (uint32_t i = it < C::STAGES ? 0 : it - C::STAGES; i < it; ++i) {
+                    mbar_wait(&sh->kv_full[i % C::STAGES], (i / C::STAGES) & 1, &no_abort, 200000000ull);
+                    if (i % 2 == 0) mbar_wait(&sh->fac_full[i / 2 % FACTORS], (i / 2 / FACTORS) & 1, &no_abort, 200000000ull);
+                }
+            }
+        } else if (warp == 9) {  // --------------------------------------- codes of K, V
             const int box_log2 = 31 - __clz(p.box), boxes = KT >> box_log2;  // the box divides 128
             const uint32_t box_bytes = (uint32_t)p.box * DP;
             uint32_t it = 0;

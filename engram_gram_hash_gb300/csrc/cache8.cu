@@ -235,10 +235,41 @@ static int64_t tile8_slots(const engram_attn_config *cfg, const engram_kv_cache_
 static size_t tile8_part_o_bytes(const engram_attn_config *cfg, int64_t slots) {
     return up256((size_t)slots * tile::ROWS * padded_dim(cfg) * sizeof(float));
 }
+// The parts' results and the plan's cut, the latter at the end.
+static size_t tile8_parts_bytes(const engram_attn_config *cfg, int64_t slots) {
+    return slots == 0 ? 0 : tile8_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;
+}
+
+// Items of the tile kernel at most, about.
+static double tile8_items(const engram_attn_config *cfg, const engram_kv_batch *batch) {
+    const double seqs = (double)std::min(batch->n_seqs, batch->n_query), rows = (double)batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
+    return seqs * cfg->n_kv_heads * ceil(rows / seqs / tile::ROWS);
+}
+
+// Bytes for the sequences' codes as fp16 tiles, made before the tile kernel; 0: its own warps convert each tile that it
+// meets.  Opened, a tile of an item takes 0.62 us less (64 values: 0.4); opening costs 8 us and 0.16 (0.08) a thousand
+// keys and heads.  Measured, us opened / not, 32 / 8 heads of 128, new tokens over cached ones: a prompt of 8,192 434 / 541,
+// 1,024 33 / 32; 2,048 over 63,488 1,632 / 2,078; 512 over 16,000 167 / 167, 64 74 / 46; 8 sequences of 256 over 4,000
+// 186 / 178; 8 prompts of up to 4,096, a window of 1,000 308 / 351, of 128 184 / 172; 64 values, a prompt of 8,192 357 / 430.
+// Up to 1 GiB: 4 bytes a key's value for the table's room of every sequence.
+constexpr int64_t OPEN_MOST = 1ll << 30;
+static int64_t opened_keys(const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    return (table_width(batch) * cache->page_size + tile::KT - 1) / tile::KT * tile::KT + tile::KT;
+}
+static size_t opened_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
+    const int64_t keys = opened_keys(cache, batch);
+    if (keys > OPEN_MOST / 256) return 0;
+    const bool narrow = padded_dim(cfg) == 64;
+    const int64_t one = (narrow ? tile::opened_bytes<64>(keys) : tile::opened_bytes<128>(keys)) * cfg->n_kv_heads;
+    if (one > OPEN_MOST || batch->n_seqs > OPEN_MOST / one) return 0;
+    const double seqs = (double)std::min(batch->n_seqs, batch->n_query), thousands = (double)keys * seqs * cfg->n_kv_heads / 1000;
+    const double reach = std::min((double)keys_most(cfg, cache, batch),
+                                  std::max((double)(table_width(batch) * cache->page_size) - batch->n_query / seqs / 2, 1.0));
+    const double saved = tile8_items(cfg, batch) * reach / tile::KT * (narrow ? 0.4 : 0.62) / num_sms();
+    return saved > 8 + thousands * (narrow ? 0.08 : 0.16) ? up256((size_t)(one * batch->n_seqs)) : 0;
+}
 static size_t tile8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
-    const int64_t slots = tile8_slots(cfg, cache, batch);
-    if (slots == 0) return 0;
-    return tile8_part_o_bytes(cfg, slots) + up256((size_t)slots * 2 * tile::ROWS * sizeof(float)) + 256;  // the plan's cut last
+    return tile8_parts_bytes(cfg, tile8_slots(cfg, cache, batch)) + opened_bytes(cfg, cache, batch);
 }
 
 // Rows kernel or tile kernel: the one whose estimate is less.  An item of 256 rows costs 3.2 us and 2.2 a tile of 128
@@ -248,12 +279,20 @@ static size_t tile8_workspace_bytes(const engram_attn_config *cfg, const engram_
 // tile kernel, new tokens over cached ones: 8 sequences of 8 over 8,000 78 / 98; 40 of 16 prompts 61 / 21, 8 over 2,000
 // 107 / 128.
 static bool use_tiles8(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
-    const double sms = num_sms();
-    const int64_t seqs = std::min(batch->n_seqs, batch->n_query), rows = batch->n_query * (cfg->n_heads / cfg->n_kv_heads);
-    const double items = (double)seqs * cfg->n_kv_heads * ceil((double)rows / (double)seqs / tile::ROWS);
+    const double sms = num_sms(), items = tile8_items(cfg, batch);
     const double item_us = 3.2 + 2.2 * (double)((keys_most(cfg, cache, batch) + tile::KT - 1) / tile::KT);
     const double tile_us = tile8_slots(cfg, cache, batch) > 0 ? 28.8 + items * item_us / sms : 5.2 + ceil(items / sms) * item_us;
     return tile_us < rows8_shares(cfg, cache, batch).us;
+}
+
+template <typename E, int DP, bool OPEN>
+static engram_status tile8_run(const CUtensorMap &km, const CUtensorMap &vm, const tile::Params8 &a, cudaStream_t st) {
+    constexpr int smem = tile::smem8_bytes<DP, OPEN>();
+    static std::atomic<bool> attr_done[64];
+    const auto kern = tile::tile8_kernel<E, DP, OPEN>;
+    const engram_status s = ensure_smem((const void *)kern, smem, attr_done);
+    if (s != ENGRAM_OK) return s;
+    return launch_after(kern, dim3(a.t.ctas), OPEN ? tile::NUM_THREADS : tile::NUM_THREADS8, smem, 1, st, "tile8_kernel", km, vm, a);
 }
 
 template <typename E, int DP>
@@ -285,8 +324,7 @@ static engram_status tile8_launch(const engram_attn_config *cfg, const engram_kv
     p.ctas = num_sms();
     p.max_slots = (int32_t)slots;
     p.cut = slots == 0 ? nullptr
-                       : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) +
-                                                     tile8_workspace_bytes(cfg, cache, batch) - 256);
+                       : reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + tile8_parts_bytes(cfg, slots) - 256);
     p.scale_log2 = cfg->scale * 1.4426950408889634f;
     a.scales = scales_of(cache);
     a.by_page = Divisor(cache->page_size);
@@ -294,12 +332,31 @@ static engram_status tile8_launch(const engram_attn_config *cfg, const engram_kv
     CUtensorMap km, vm;
     if (!page_map8(&km, cfg, cache, cache->k, p.box, false) || !page_map8(&vm, cfg, cache, cache->v, p.box, false))
         return ENGRAM_ECUDA;
-    constexpr int smem = tile::smem8_bytes<DP>();
-    static std::atomic<bool> attr_done[64];
-    const auto kern = tile::tile8_kernel<E, DP>;
-    engram_status s = ensure_smem((const void *)kern, smem, attr_done);
-    if (s != ENGRAM_OK) return s;
-    s = launch_after(kern, dim3(p.ctas), tile::NUM_THREADS8, smem, 1, st, "tile8_kernel", km, vm, a);
+    engram_status s;
+    if (opened_bytes(cfg, cache, batch) > 0) {
+        tile::OpenParams o;
+        memset(&o, 0, sizeof(o));
+        o.b = p.b;
+        o.k = static_cast<const uint8_t *>(cache->k);
+        o.v = static_cast<const uint8_t *>(cache->v);
+        o.page_stride = cache->page_stride;
+        o.slot_stride = cache->token_stride;
+        o.head_stride = cache->head_stride;
+        o.scales = a.scales;
+        o.by_page = a.by_page;
+        o.opened = a.opened = tile::Opened{static_cast<uint8_t *>(workspace) + tile8_parts_bytes(cfg, slots), opened_keys(cache, batch)};
+        o.tiles = (int32_t)(o.opened.keys / tile::KT);
+        o.units = batch->n_seqs * o.tiles * cfg->n_kv_heads * 2;
+        o.n_kv_heads = cfg->n_kv_heads;
+        o.head_dim = cfg->head_dim;
+        o.window = cfg->window;
+        o.scale_log2 = p.scale_log2;
+        s = launch_after(tile::open_kernel<DP>, dim3((unsigned)std::min<int64_t>(o.units, (int64_t)num_sms() * tile::OPEN_PER_SM)),
+                         tile::OPEN_THREADS, 0, 1, st, "open_kernel", o);
+        if (s == ENGRAM_OK) s = tile8_run<E, DP, true>(km, vm, a, st);
+    } else {
+        s = tile8_run<E, DP, false>(km, vm, a, st);
+    }
     if (s != ENGRAM_OK || slots == 0) return s;
     return launch_after(tile::tile_join_kernel<E, DP>, dim3(p.ctas * tile::JOIN_PER_SM), 128, 0, 1, st, "tile_join_kernel", p);
 }

@@ -667,7 +667,7 @@ typedef struct {
 engram_status engram_kv_plan(const engram_kv_plan_args *args, void *stream);
 
 /*
- * engram_kv_append into an 8-bit cache, in one launch: k normed, rotated and
+ * engram_kv_append into an 8-bit cache: k normed, rotated and
  * rounded to cfg->dtype (what the 16-bit cache would hold), k and v then
  * quantised.  The scale of a block and head is the least power of two, from
  * 2^-48 to 2^48, whose 448-fold holds the largest finite magnitude of its new
@@ -698,7 +698,10 @@ engram_status engram_kv_append_q8(const engram_attn_config *cfg, const engram_kv
  * equal inputs give equal bits.  Weights relative to 1 / v scale below 2^-100 of
  * a row's largest may count as 0.
  *   workspace  >= engram_paged_attention_q8_workspace_bytes(cfg, cache, batch)
- *              bytes, 256-byte aligned; scratch, nothing to clear
+ *              bytes, 256-byte aligned; scratch, nothing to clear.  For long
+ *              prompts and chunks it holds the sequences' codes as fp16 tiles
+ *              (4 bytes a key's value, for the room of the block table's width)
+ *              as long as those are at most 1 GiB
  */
 size_t engram_paged_attention_q8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache,
                                                  const engram_kv_batch *batch);

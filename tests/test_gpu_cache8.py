@@ -456,7 +456,7 @@ def test_attention_follows_small_values(eg):
             c.k_scales[p] = 0.01
             c.v_scales[p] = 2.0**-30 if i == 1 else 1.0
         c.k_pages.view(torch.uint8)[used[1]] = torch.full((16, 1, 64), 240.0, device="cuda").to(E4M3).view(torch.uint8)
-        c.q.fill_(20.0)  # q.k = 3072 * scale 1/8 at block 1, under 200 at the others
+        c.q.fill_(20.0)  # far above the others at block 1
         cfg = eg.make_attn_config(2, 1, 64, rope_dim=0)
         got = eg.engram_paged_attention_q8(cfg, c.cache, c.batch, c.q).double()
         ref = plain.attention(c.q, c.k_pages, c.v_pages, c.k_scales, c.v_scales, c.block_table, c.new, c.total, 1, cfg.scale, 0)[0]
