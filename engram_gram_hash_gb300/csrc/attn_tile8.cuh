@@ -145,10 +145,10 @@ struct OpenParams {
 };
 constexpr int OPEN_THREADS = 256;
 constexpr int OPEN_PER_SM = 6;
-// A tile of keys, or of values, of one sequence and head as fp16 into the opened memory; with the values the strips'
+// A tile of keys (in the queries' type), or of values (fp16), of one sequence and head into the opened memory; with the values the strips'
 // factors, log2 and inverse, and whether a value was NaN.  Keys that no token of the sequence sees become zeros, NaN
 // values too.  Bound: memory (1 byte in, 2 out a code).
-template <int DP>
+template <typename E, int DP>
 __global__ void __launch_bounds__(OPEN_THREADS, OPEN_PER_SM) open_kernel(const OpenParams p) {
     __shared__ int bad[STRIPS];
     grid_dependency_wait();
@@ -209,17 +209,24 @@ __global__ void __launch_bounds__(OPEN_THREADS, OPEN_PER_SM) open_kernel(const O
             const int32_t key = key0 + (i * OPEN_THREADS + threadIdx.x) / PIECES;
             uint8_t *const row = to + ((int64_t)(kv * (DP / 64) + (ch >> 2)) * p.opened.keys + key) * 128;
             const int at = (ch & 3) * 2, swizzle = key & 7;
-            *reinterpret_cast<uint4 *>(row + ((at ^ swizzle) << 4)) =
-                make_uint4(codes_lo(c[i].x), codes_hi(c[i].x), codes_lo(c[i].y), codes_hi(c[i].y));
-            *reinterpret_cast<uint4 *>(row + (((at + 1) ^ swizzle) << 4)) =
-                make_uint4(codes_lo(c[i].z), codes_hi(c[i].z), codes_lo(c[i].w), codes_hi(c[i].w));
+            uint32_t x[8] = {codes_lo(c[i].x), codes_hi(c[i].x), codes_lo(c[i].y), codes_hi(c[i].y),
+                             codes_lo(c[i].z), codes_hi(c[i].z), codes_lo(c[i].w), codes_hi(c[i].w)};
+            if (std::is_same<E, Bf16>::value && !kv) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float2 f = Fp16::unpack(x[k]);
+                    x[k] = E::pack(f.x, f.y);
+                }
+            }
+            *reinterpret_cast<uint4 *>(row + ((at ^ swizzle) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4 *>(row + (((at + 1) ^ swizzle) << 4)) = make_uint4(x[4], x[5], x[6], x[7]);
         }
         if (kv) {
             __syncthreads();
             if (threadIdx.x < STRIPS) {
                 const float2 f = value_scale(vs);
                 reinterpret_cast<float4 *>(to + p.opened.keys * 4 * DP)[key0 / STRIP + threadIdx.x] =
-                    make_float4(ks * p.scale_log2, f.x, f.y, bad[threadIdx.x] ? 1.f : 0.f);
+                    make_float4(factor(ks, p.scale_log2), f.x, f.y, bad[threadIdx.x] ? 1.f : 0.f);
             }
             // (a thread clears its own mark next)
         }
@@ -315,6 +322,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
         constexpr float LIFT = H::LIFT - H::RESCALE;  // of a weight at the running maximum
         uint32_t s_ph = 0, o_ph = 0, it = 0, pv_ph = 0;  // it: tiles before the item
         float rf = 1.f;  // what this thread's row of queries was divided by
+        const auto of_row = [&](float strip) { return OPEN ? strip : factor(strip, rf); };
         bool ok = true;
 
         // The tile's query rows into shared memory by asynchronous copies, 16 bytes a lane and round
@@ -339,7 +347,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
         };
         const auto hand_q = [&] {
             asm volatile("cp.async.wait_all;" ::: "memory");
-            if (std::is_same<E, Bf16>::value) {  // this thread's row as fp16: exact but for values below 2^-28 of its largest
+            if (!OPEN && std::is_same<E, Bf16>::value) {  // this thread's row as fp16: exact but for values below 2^-28 of its largest
                 __syncwarp();  // the warp's lanes have copied each other's rows
                 const uint32_t at = smem_u32(q_smem) + t * C::Q_BYTES + row * 128;
                 const auto piece = [&](int i) { return at + (i >> 3) * (MT * 128) + (((i ^ row) & 7) << 4); };
@@ -449,7 +457,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const float4 g = fac[h * 4 + c];
-                            part[c] = fmaf(part[c], factor(g.x, rf), g.y);
+                            part[c] = fmaf(part[c], of_row(g.x), g.y);
                             if (OPEN) nan_in += g.w;
                         }
                         mx = max3(mx, part[0], part[1]);
@@ -494,7 +502,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {  // a strip: one factor, one scale
                             const float4 fa = fac[2 * c + g];
-                            const float k = factor(fa.x, rf), at = fa.y - mref;
+                            const float k = of_row(fa.x), at = fa.y - mref;
                             const float2 sc = make_float2(k, k), off = make_float2(at, at);
                             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -851,7 +859,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
             // turns their products interleave, both softmaxes then run at once and both wait for the
             // tensor pipe at once (65,536-token chunk: 1.99 ms; one warp for both tiles 1.64 ms).
             const int t = warp == 8 ? 0 : 1;
-            constexpr uint32_t ID_S = idesc_16(false, MT, KT, false), ID_O = idesc_16(false, MT, DP, true);
+            constexpr uint32_t ID_S = idesc_16(OPEN && std::is_same<E, Bf16>::value, MT, KT, false), ID_O = idesc_16(false, MT, DP, true);
             const bool leader = elect_one();
             const uint32_t kva = smem_u32(kv_smem);
             const uint64_t q_desc = smem_desc(smem_u32(q_smem) + t * C::Q_BYTES, 16, 1024, kSwizzle128B);

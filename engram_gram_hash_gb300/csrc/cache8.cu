@@ -351,7 +351,7 @@ static engram_status tile8_launch(const engram_attn_config *cfg, const engram_kv
         o.head_dim = cfg->head_dim;
         o.window = cfg->window;
         o.scale_log2 = p.scale_log2;
-        s = launch_after(tile::open_kernel<DP>, dim3((unsigned)std::min<int64_t>(o.units, (int64_t)num_sms() * tile::OPEN_PER_SM)),
+        s = launch_after(tile::open_kernel<E, DP>, dim3((unsigned)std::min<int64_t>(o.units, (int64_t)num_sms() * tile::OPEN_PER_SM)),
                          tile::OPEN_THREADS, 0, 1, st, "open_kernel", o);
         if (s == ENGRAM_OK) s = tile8_run<E, DP, true>(km, vm, a, st);
     } else {
