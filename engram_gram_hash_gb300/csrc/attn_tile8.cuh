@@ -2,7 +2,7 @@
 // (prompts, chunks): the tile kernel's items, plan, products and join, on tiles
 // that four more warps make from the codes.
 //
-// The products run on fp16 (codes are exact there), so a tile's codes become an fp16 tile first: the fp8 matrix
+// The products run on 16-bit tiles (codes are exact in both types), so a tile's codes are converted first: the fp8 matrix
 // instruction wants both operands in 8 bits, and queries and weights would have to be split into two or three
 // pieces each.  Two forms:
 //   opened   for work with many row blocks over the same keys a kernel makes the tiles of every sequence and head
@@ -10,10 +10,11 @@
 //            of 8,192 tokens has 128 row blocks a head: its tiles are converted once instead of 65 times in the mean);
 //   in place for fewer, four more warps convert each tile that the CTA meets.
 // Opened, bound as the 16-bit kernel by the softmax's chain beside the tensor pipe, longer by the strips' factors:
-// a prompt of 8,192 tokens, 32 / 8 heads of 128, 434 us (1,270 TFLOP/s, 67 % of the burst rate; about 12 are the
-// opening; fp16 queries 416: bf16 ones are converted between items), 2,048 more over 63,488 cached 1,635 (1,325
-// TFLOP/s); the 16-bit kernel takes 360 and 1,400.  Tried and left there: factors loaded ahead of the scores 446-451,
-// ahead of the exponentials 445; codes brought to one scale a tile and a second form of the softmax for such tiles 465.
+// a prompt of 8,192 tokens, 32 / 8 heads of 128, 415 us (1,325 TFLOP/s, 70 % of the burst rate; about 12 are the
+// opening), 2,048 more over 63,488 cached 1,515 (1,430 TFLOP/s), 64 values 335; the 16-bit kernel takes 360, 1,400 and
+// 317.  Keys are opened in the queries' type, values as fp16: with keys in fp16 too, bf16 queries had to be converted
+// between items (434 us).  Tried and left: half of a tile's factors in registers 422-427, codes brought to one
+// scale a tile and a second form of the softmax for such tiles 465 (then 440).
 // In place, bound by the converters and the softmax beside them: 541 and 2,090 us; a pair of row tiles takes 4,600
 // cycles of an SM, 3,000 on 16-bit tiles.  By a clock trace the converters are busy all that time (1,500 cycles a
 // tile of keys or values, most of it the latency of one load and store after another); loading eight pieces ahead
@@ -89,7 +90,7 @@ constexpr int smem8_bytes() {
 }
 static_assert(smem8_bytes<128, false>() <= 232448 && smem8_bytes<64, false>() <= 232448, "tile kernel shared memory over the per-CTA limit");
 
-// The sequences' keys and values as fp16, in the order of the ring's stages: for each sequence and head the keys' 64
+// The sequences' keys (in the queries' type) and values (fp16), in the order of the ring's stages: for each sequence and head the keys' 64
 // values at a time (rows of 128 bytes, swizzled over 8 keys), the values' likewise, then the strips' factors.
 struct Opened {
     uint8_t *at;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
     tile8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                 const __grid_constant__ Params8 p8) {
     using C = Cfg8<DP>;
-    using H = Fp16;  // of the products
+    using H = Fp16;  // of the second product (in place, of both)
     constexpr int FACTORS = C::FACTORS, MAKERS = OPEN ? 0 : CONVERTERS;
     const Params &p = p8.t;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -321,6 +322,9 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
         const uint32_t p_tm = C::APART ? tmem + lanes + C::P_COL + t * 64 : s_tm;
         constexpr float LIFT = H::LIFT - H::RESCALE;  // of a weight at the running maximum
         uint32_t s_ph = 0, o_ph = 0, it = 0, pv_ph = 0;  // it: tiles before the item
+        // Factors in registers: 853 -> 817 us (2,048 new over 30,720); at 64 values, beside the second score buffer's
+        // registers, 336 -> 364 (a prompt of 8,192).
+        constexpr bool AHEAD = OPEN && !C::APART;
         float rf = 1.f;  // what this thread's row of queries was divided by
         const auto of_row = [&](float strip) { return OPEN ? strip : factor(strip, rf); };
         bool ok = true;
@@ -406,14 +410,35 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
                 const int32_t full_lo = first_seen(w->pos0 + p.by_group.quotient(w->r0 + last), p.window);
                 for (int32_t j = 0; j < n; ++j) {
                     const int32_t key0 = item_key0 + j * KT;
+                    const uint32_t f = it + j;
+                    const float4 *const fac = sh->fac[f % FACTORS];
+                    float nan_in = 0.f;  // OPEN: whether values of the tile were NaN
+                    // AHEAD: the strips' factors come into registers before the scores are waited for.  (Not an item's
+                    // first: a row tile that passed items over may be phases behind the factors' barriers until its
+                    // scores are there.)
+                    float kf[STRIPS], yf[STRIPS];
+                    const auto fetch = [&] {
+                        ok = warp_wait(&sh->fac_full[f % FACTORS], (f / FACTORS) & 1, abort);
+                        if constexpr (AHEAD) {
+#pragma unroll
+                            for (int c = 0; c < STRIPS; ++c) {
+                                const float4 g = fac[c];
+                                kf[c] = g.x, yf[c] = g.y;
+                                nan_in += g.w;
+                            }
+                        }
+                    };
+                    if (AHEAD && j > 0) {
+                        fetch();
+                        if (!ok) break;
+                    }
                     ok = warp_wait(&sh->s_full[t], s_ph++ & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t f = it + j;
-                    ok = warp_wait(&sh->fac_full[f % FACTORS], (f / FACTORS) & 1, abort);
-                    if (!ok) break;
-                    const float4 *const fac = sh->fac[f % FACTORS];
-                    float nan_in = 0.f;  // OPEN: whether values of the tile were NaN
+                    if (!AHEAD || j == 0) {
+                        fetch();
+                        if (!ok) break;
+                    }
                     // the second half of the scores arrives under the first half's maximum
                     uint32_t raw[4][32];
                     tmem_ld_32x32b_x32(s_tm, raw[0]);
@@ -456,9 +481,13 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
                             }
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            const float4 g = fac[h * 4 + c];
-                            part[c] = fmaf(part[c], of_row(g.x), g.y);
-                            if (OPEN) nan_in += g.w;
+                            if constexpr (AHEAD) {
+                                part[c] = fmaf(part[c], kf[h * 4 + c], yf[h * 4 + c]);
+                            } else {
+                                const float4 g = fac[h * 4 + c];
+                                part[c] = fmaf(part[c], of_row(g.x), g.y);
+                                if (OPEN) nan_in += g.w;
+                            }
                         }
                         mx = max3(mx, part[0], part[1]);
                         mx = max3(mx, part[2], part[3]);
@@ -502,7 +531,7 @@ __global__ void __launch_bounds__(OPEN ? NUM_THREADS : NUM_THREADS8, 1)
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {  // a strip: one factor, one scale
                             const float4 fa = fac[2 * c + g];
-                            const float k = of_row(fa.x), at = fa.y - mref;
+                            const float k = AHEAD ? kf[2 * c + g] : of_row(fa.x), at = (AHEAD ? yf[2 * c + g] : fa.y) - mref;
                             const float2 sc = make_float2(k, k), off = make_float2(at, at);
                             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll

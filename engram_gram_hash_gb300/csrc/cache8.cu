@@ -246,11 +246,11 @@ static double tile8_items(const engram_attn_config *cfg, const engram_kv_batch *
     return seqs * cfg->n_kv_heads * ceil(rows / seqs / tile::ROWS);
 }
 
-// Bytes for the sequences' codes as fp16 tiles, made before the tile kernel; 0: its own warps convert each tile that it
-// meets.  Opened, a tile of an item takes 0.62 us less (64 values: 0.4); opening costs 8 us and 0.16 (0.08) a thousand
-// keys and heads.  Measured, us opened / not, 32 / 8 heads of 128, new tokens over cached ones: a prompt of 8,192 434 / 541,
-// 1,024 33 / 32; 2,048 over 63,488 1,632 / 2,078; 512 over 16,000 167 / 167, 64 74 / 46; 8 sequences of 256 over 4,000
-// 186 / 178; 8 prompts of up to 4,096, a window of 1,000 308 / 351, of 128 184 / 172; 64 values, a prompt of 8,192 357 / 430.
+// Bytes for the sequences' codes as 16-bit tiles, made before the tile kernel; 0: its own warps convert each tile that it
+// meets.  Opened, a tile of an item takes 0.7 us less (64 values: 0.45); opening costs 8 us and 0.16 (0.08) a thousand
+// keys and heads.  Measured, us opened / not, 32 / 8 heads of 128, new tokens over cached ones: a prompt of 8,192 415 / 541,
+// 1,024 33 / 32; 2,048 over 63,488 1,515 / 2,078; 512 over 16,000 157 / 167, 64 74 / 46; 8 sequences of 256 over 4,000
+// 186 / 178; 8 prompts of up to 4,096, a window of 1,000 304 / 351, of 128 184 / 172; 64 values, a prompt of 8,192 335 / 430.
 // Up to 1 GiB: 4 bytes a key's value for the table's room of every sequence.
 constexpr int64_t OPEN_MOST = 1ll << 30;
 static int64_t opened_keys(const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {
@@ -265,7 +265,7 @@ static size_t opened_bytes(const engram_attn_config *cfg, const engram_kv_cache_
     const double seqs = (double)std::min(batch->n_seqs, batch->n_query), thousands = (double)keys * seqs * cfg->n_kv_heads / 1000;
     const double reach = std::min((double)keys_most(cfg, cache, batch),
                                   std::max((double)(table_width(batch) * cache->page_size) - batch->n_query / seqs / 2, 1.0));
-    const double saved = tile8_items(cfg, batch) * reach / tile::KT * (narrow ? 0.4 : 0.62) / num_sms();
+    const double saved = tile8_items(cfg, batch) * reach / tile::KT * (narrow ? 0.45 : 0.7) / num_sms();
     return saved > 8 + thousands * (narrow ? 0.08 : 0.16) ? up256((size_t)(one * batch->n_seqs)) : 0;
 }
 static size_t tile8_workspace_bytes(const engram_attn_config *cfg, const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {

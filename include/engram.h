@@ -699,7 +699,7 @@ engram_status engram_kv_append_q8(const engram_attn_config *cfg, const engram_kv
  * a row's largest may count as 0.
  *   workspace  >= engram_paged_attention_q8_workspace_bytes(cfg, cache, batch)
  *              bytes, 256-byte aligned; scratch, nothing to clear.  For long
- *              prompts and chunks it holds the sequences' codes as fp16 tiles
+ *              prompts and chunks it holds the sequences' codes as 16-bit tiles
  *              (4 bytes a key's value, for the room of the block table's width)
  *              as long as those are at most 1 GiB
  */
