@@ -235,12 +235,14 @@ __global__ void __launch_bounds__(256) map_kernel(const __grid_constant__ Params
     allow_dependent_launch();
     const int lane = threadIdx.x & 31;
     const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t s = warp_find(p.n_seqs, [&](int64_t i) { return p.offs[i] / SPAN + i <= u; });
-    const int64_t t0 = p.offs[s], t1 = p.offs[s + 1], j0 = (u - t0 / SPAN - s) * SPAN;
-    const int64_t end = t1 - t0 < j0 + SPAN ? t1 - t0 : j0 + SPAN;
-    const int32_t keep = p.kv_len_out[s] - (int32_t)(t1 - t0);
+    if (p.n_seqs > 0) {  // without requests there are no lengths, no rows of the table and one offset
+        const int64_t s = warp_find(p.n_seqs, [&](int64_t i) { return p.offs[i] / SPAN + i <= u; });
+        const int64_t t0 = p.offs[s], t1 = p.offs[s + 1], j0 = (u - t0 / SPAN - s) * SPAN;
+        const int64_t end = t1 - t0 < j0 + SPAN ? t1 - t0 : j0 + SPAN;
+        const int32_t keep = p.kv_len_out[s] - (int32_t)(t1 - t0);
 #pragma unroll 4
-    for (int64_t j = j0 + lane; j < end; j += 32) write_token(p, s, t0 + j, keep + (int32_t)j);
+        for (int64_t j = j0 + lane; j < end; j += 32) write_token(p, s, t0 + j, keep + (int32_t)j);
+    }
     for (int64_t t = p.offs[p.n_seqs] + u * 32 + lane; t < p.max_tokens; t += (int64_t)gridDim.x * 256) write_none(p, t);
 }
 
