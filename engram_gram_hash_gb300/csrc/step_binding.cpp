@@ -378,14 +378,17 @@ PyObject *kv_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const int64_t counts[6] = {p.n_seqs + 1, p.n_seqs, 1, p.max_tokens, p.max_tokens, 4};
         // one allocation for all of them, a 16-byte boundary for each (six would cost the host more than the plan the GPU)
         int64_t at[6], bytes = 0;
+        bool makes = false;
         for (int i = 0; i < 6; ++i) {
             at[i] = bytes;
-            if (a[from[i]] == Py_None) bytes += (counts[i] * (i == 0 || i == 4 ? 8 : 4) + 15) / 16 * 16;
+            if (a[from[i]] != Py_None) continue;
+            bytes += (counts[i] * (i == 0 || i == 4 ? 8 : 4) + 15) / 16 * 16;
+            makes = true;
         }
         at::Tensor made[6];
         void *data[6];
         c10::Storage storage;
-        if (bytes > 0) {
+        if (makes) {  // also of no bytes: an output without values has a storage too
             c10::Allocator *const pool = c10::cuda::CUDACachingAllocator::get();
             storage = c10::Storage(c10::Storage::use_byte_size_t(), bytes, pool->allocate(bytes), pool, /*resizable=*/false);
         }
