@@ -68,19 +68,20 @@ static engram_status append8_launch_t(const Append8 &a, int64_t blocks, int thre
 template <typename E, int LPH>
 static engram_status append8_launch(const engram_attn_config *cfg, Append8 &a, cudaStream_t st) {
     constexpr int per = 32 / LPH;
+    const int warps = a.block / TOKENS_PER_WARP;
+    const int64_t kv_blocks = a.units * 2 * ((a.n_kv + per - 1) / per);
     // The queries of many tokens go in a launch of their own: beside the keys' registers half as many of their warps
     // run (32,768 tokens of 32 + 8 heads 297 us in one launch).
-    if (a.h.n_tokens * ((a.h.n_q + 3) / 4) >= (int64_t)num_sms() * 256) {
+    const bool apart = a.h.n_tokens * ((a.h.n_q + 3) / 4) >= (int64_t)num_sms() * 256;
+    a.q_groups = apart ? 0 : (a.h.n_q + per - 1) / per;
+    const int64_t blocks = kv_blocks + (a.h.n_tokens + warps - 1) / warps * a.q_groups;
+    if (blocks > INT32_MAX) return ENGRAM_EINVAL;  // before the first launch
+    if (apart) {
         HeadParams q = a.h;
         a.h.n_q = 0;
         const engram_status s = head_launch<E, true>(cfg, q, st);
         if (s != ENGRAM_OK) return s;
     }
-    const int warps = a.block / TOKENS_PER_WARP;
-    a.q_groups = (a.h.n_q + per - 1) / per;
-    const int64_t kv_blocks = a.units * 2 * ((a.n_kv + per - 1) / per);
-    const int64_t blocks = kv_blocks + (a.h.n_tokens + warps - 1) / warps * a.q_groups;
-    if (blocks > INT32_MAX) return ENGRAM_EINVAL;
     a.kv_blocks = (int32_t)kv_blocks;
     const bool pairs = cfg->rope_layout == ENGRAM_ROPE_INTERLEAVED;
     if (warps <= 8)
