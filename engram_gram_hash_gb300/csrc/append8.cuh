@@ -27,7 +27,6 @@ namespace engram {
 namespace attn {
 
 constexpr int TOKENS_PER_WARP = 8;
-constexpr int MAX_BLOCK = 128;  // tokens that share a scale
 constexpr int MAX_EXP = 48;     // of a scale: 2^-48 .. 2^48
 
 struct Append8 {
