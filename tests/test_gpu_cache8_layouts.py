@@ -147,3 +147,36 @@ def test_plan_maps_left_out(eg, left_out, tokens):  # noqa: F811
     for name, t in outs.items():
         assert t.tolist() == ([7] * tokens if name in left_out else want[name]), name
     assert r.t_table.tolist() == table and r.t_stack.tolist() == stack
+
+
+# ------------------------------------------------------------- parts of a step ----
+
+@pytest.mark.parametrize("first", [1, 1000, 1 << 40])
+@pytest.mark.parametrize("name", FORMS)
+def test_offsets_from_anywhere(eg, name, first, tmp_path):  # noqa: F811
+    """A step's offsets need not begin at 0: appends and results are the same bit for bit."""
+    c, d = (form(eg, name, tmp_path) for _ in range(2))
+    d.seq_offsets += first
+    cfg = config(eg, c)
+    for x in (c, d):
+        eg.engram_kv_append_q8(cfg, x.cache, x.batch, x.k, x.v, None)
+    out, other = (eg.engram_paged_attention_q8(cfg, x.cache, x.batch, x.q) for x in (c, d))
+    assert eg.engram_last_error() == 0 and torch.equal(out, other)
+    for x, y in ((c.k_pages, d.k_pages), (c.v_pages, d.v_pages), (c.k_scales, d.k_scales), (c.v_scales, d.v_scales)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_a_step_in_two_calls(eg):  # noqa: F811
+    """Single tokens and a chunk of one step, a call for each: slices of its offsets, lengths, table and queries."""
+    new, total = [1] * 12 + [400], [50 * s + 1 for s in range(12)] + [1500]
+    c = Cache(eg, BF16, 32, 8, 128, 64, 64, new, total)
+    cfg, whole = config(eg, c), check_attention(eg, c)
+    ref, _, bound, _ = plain.attention(c.q, c.k_pages, c.v_pages, c.k_scales, c.v_scales, c.block_table, new, total, 8, cfg.scale, 0)
+    for lo, hi in ((0, 12), (12, 13)):
+        rows = slice(sum(new[:lo]), sum(new[:hi]))
+        width = -(-max(total[lo:hi]) // 64)
+        batch = eg.kv_batch(c.seq_offsets[lo:hi + 1], c.kv_len[lo:hi], c.block_table[lo:hi, :width], sum(new[lo:hi]))
+        part = eg.engram_paged_attention_q8(cfg, c.cache, batch, c.q[rows])
+        assert eg.engram_last_error() == 0
+        assert bool(((part.double() - ref[rows]).abs() <= bound[rows]).all())
+        assert bool(((part.double() - whole[rows].double()).abs() <= 2 * bound[rows]).all())
