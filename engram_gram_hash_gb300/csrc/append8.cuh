@@ -18,9 +18,14 @@
 // the block's maximum is found, and is written once.  The angles of a block's
 // tokens come into shared memory beside the keys (from the table token by
 // token, each waited for, 32,768 tokens took 62 us instead of 56).  56 us are
-// 57 % of the copy rate, 14,436 tokens of 8 sequences 27 us (55 %): by the
+// 57 % of the copy rate, 15,026 tokens of 8 sequences 27-28 us (53-55 %): by the
 // counters instructions (262 a warp and token) at the 16 warps an SM that 128
-// registers leave.  64 tokens with their queries 5.4 us in a CUDA graph.
+// registers leave; the maxima are packed 16-bit ones already.  64 tokens with
+// their queries 5.4-6.1 us in a CUDA graph.
+// The queries' CTAs of the same launch have as many warps as those of the
+// blocks, at the same 128 registers: two for blocks of 16.  2,407 tokens of 24
+// + 4 heads of 96 in blocks of 16 take 14.7 us, 7.7 without the queries, whose
+// rotation alone takes 5.4: 7,224 such CTAs run in about six waves.
 #pragma once
 
 namespace engram {

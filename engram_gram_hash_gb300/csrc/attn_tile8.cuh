@@ -11,7 +11,7 @@
 //   in place for fewer, four more warps convert each tile that the CTA meets.
 // Opened, bound as the 16-bit kernel by the softmax's chain beside the tensor pipe, longer by the strips' factors:
 // a prompt of 8,192 tokens, 32 / 8 heads of 128, 415 us (1,325 TFLOP/s, 70 % of the burst rate; about 12 are the
-// opening), 2,048 more over 63,488 cached 1,515 (1,430 TFLOP/s), 64 values 335; the 16-bit kernel takes 360, 1,400 and
+// opening), 2,048 more over 63,488 cached 1,515-1,580 (1,430-1,370 TFLOP/s, the clock falls in long runs), 64 values 335; the 16-bit kernel takes 360, 1,400 and
 // 317.  Keys are opened in the queries' type, values as fp16: with keys in fp16 too, bf16 queries had to be converted
 // between items (434 us).  Tried and left: half of a tile's factors in registers 422-427, codes brought to one
 // scale a tile and a second form of the softmax for such tiles 465 (then 440).

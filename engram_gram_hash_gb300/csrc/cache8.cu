@@ -133,7 +133,8 @@ static int64_t rows8_tiles_most(const engram_attn_config *cfg, const engram_kv_c
 // How a segment's tiles are shared out, and about how long that takes (us on this GPU): the least of
 //   whole: no cut, no join; a round of segments over the SMs costs 2.9 and 0.61 a tile (64 values: 0.54), the first 2.4 more;
 //   cluster of 8 or 4: a segment's tiles over that many CTAs, joined through distributed shared memory, one launch;
-//     15 clusters of 8 and 36 of 4 fit the GPU at once;
+//     15 clusters of 8 and 36 of 4 run at once on this GPU's 152 SMs, as observed; beyond that some wait, so more
+//     segments than sms / 10 and sms / 4 - 2 do not go this way;
 //   cut: equal runs of tiles for every SM, then the join: 9.5, and 0.78 a tile.  Several sequences seldom have the room
 //     that their tables give them; here alone that shortens the work, so it counts for less (unequal lengths make the
 //     others wait for the longest).
@@ -252,6 +253,7 @@ static double tile8_items(const engram_attn_config *cfg, const engram_kv_batch *
 // keys and heads.  Measured, us opened / not, 32 / 8 heads of 128, new tokens over cached ones: a prompt of 8,192 415 / 541,
 // 1,024 33 / 32; 2,048 over 63,488 1,515 / 2,078; 512 over 16,000 157 / 167, 64 74 / 46; 8 sequences of 256 over 4,000
 // 186 / 178; 8 prompts of up to 4,096, a window of 1,000 304 / 351, of 128 184 / 172; 64 values, a prompt of 8,192 335 / 430.
+// Keys are counted by the table's width: a prompt of 1,024 in a table with room for 131,072 opens (45 us, 34 in a tight one).
 // Up to 1 GiB: 4 bytes a key's value for the table's room of every sequence.
 constexpr int64_t OPEN_MOST = 1ll << 30;
 static int64_t opened_keys(const engram_kv_cache_q8 *cache, const engram_kv_batch *batch) {

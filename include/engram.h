@@ -642,7 +642,8 @@ typedef struct {
  * n_pages sets ENGRAM_ERANGE; more new tokens than max_tokens or more pages
  * than are free (counts[3] says how many are missing) set ENGRAM_ECAPACITY; in
  * both cases lengths, table and stack stay as they are and the step has no
- * tokens (offsets 0, counts 0).  Page ids are moved, not looked at.
+ * tokens (offsets 0, counts 0).  Page ids are moved, not looked at.  With
+ * n_seqs 0 lengths and table are not read and may be NULL.
  */
 typedef struct {
     int64_t n_seqs;
